@@ -1,0 +1,93 @@
+// e4m3 pages -> bf16 K and V in token order, for the key blocks that a BlockMask lists: the first step of the
+// forward over an 8-bit paged cache. The tcgen05 forward then reads bf16 tiles as it always does.
+//
+// Bound: HBM, 1 byte read and 2 written a value (and read again by the forward, mostly from L2 for short contexts).
+// Against the forward's 4 Q_LEN Hq / Hkv operations a value this is small once Q_LEN * Hq / Hkv is in the hundreds,
+// which is what a prompt chunk has; single tokens go through the decode kernel, which reads the bytes themselves.
+//
+// Positions that no query row may see (past the last key of a causal or prefix term) become zero, so what a page
+// holds behind its sequence does not matter.
+#include "fa_launch.h"
+#include "fp8.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 256;
+
+// first key position that no row of batch b sees, by the causal and prefix bounds of the rule's terms
+__device__ __forceinline__ int64_t key_end(const ExpandArgs& a, int b) {
+  const int64_t last = (int64_t)a.q_len - 1 + (a.rule.q_offset ? __ldg(a.rule.q_offset + (a.mask.Bm > 1 ? b : 0)) : 0);
+  int64_t end = 0;
+  for (int t = 0; t < a.rule.n_terms; ++t) {
+    int64_t hi = a.kv_len;
+    if (a.rule.t[t].causal) hi = min(hi, last + 1);
+    if (a.rule.t[t].pre != INT64_MAX) hi = min(hi, a.rule.t[t].pre);
+    end = max(end, hi);
+  }
+  return end;
+}
+
+// CTA: one 32-token block of one (batch row, KV head), K and V
+template <int D>
+__global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ ExpandArgs a) {
+  constexpr int LPR = D / 16;                       // lanes a row: 16 bytes in, 32 bytes out
+  constexpr int kRows = kThreads / 2 / LPR;         // rows a pass, K by the first half of the threads, V by the second
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int64_t j0 = (int64_t)blockIdx.x * kScaleTokens;
+  const DevMask& M = a.mask;
+  const int c = (int)(j0 / M.bk), g = a.Hq / a.Hkv;
+  bool listed = false;
+  for (int h = 0; h < (M.Hm > 1 ? g : 1); ++h) {
+    const size_t col = ((size_t)(M.Bm > 1 ? b : 0) * M.Hm + (M.Hm > 1 ? hk * g + h : 0)) * M.nk + c;
+    listed = listed || __ldg(M.q_num + col) + __ldg(M.full_q_num + col) > 0;
+  }
+  if (!listed) return;  // the forward reads nothing of it
+  const int64_t end = min(key_end(a, b), (int64_t)a.kv_len);
+  const int pid = __ldg(a.page_table + (size_t)b * a.max_pages + j0 / a.page);
+  const bool have = pid >= 0 && pid < a.n_pages_total && j0 < end;
+  if (!have && j0 < end) report(a.status, FA_ERR_DEVICE_CHECK);
+  const int which = threadIdx.x / (kThreads / 2), tid = threadIdx.x % (kThreads / 2);
+  const int lane = tid % LPR;
+  float sc = 1.f;
+  const uint8_t* src = nullptr;
+  if (have) {
+    const int64_t ph = (int64_t)pid * a.Hkv + hk, place = j0 % a.page;
+    sc = clamp_scale(__ldg((which ? a.v_scale : a.k_scale) + ph * (a.page / kScaleTokens) + place / kScaleTokens));
+    src = static_cast<const uint8_t*>(which ? a.v_pages : a.k_pages) + (ph * a.page + place) * D + lane * 16;
+  }
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(which ? a.v_out : a.k_out) +
+                       (((size_t)b * a.Hkv + hk) * a.kv_len + j0) * D + lane * 16;
+#pragma unroll
+  for (int r = tid / LPR; r < kScaleTokens; r += kRows) {
+    if (j0 + r >= a.kv_len) break;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (have && j0 + r < end) v = __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * D));
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t lo, hi;
+      e4m3x4_to_f16(in[i], lo, hi);
+      const float2 x = f16x2_to_f32(lo), y = f16x2_to_f32(hi);
+      out[2 * i] = pack_bf16x2(x.x * sc, x.y * sc);      // exact where the scale is a power of two
+      out[2 * i + 1] = pack_bf16x2(y.x * sc, y.y * sc);
+    }
+    uint4* o = reinterpret_cast<uint4*>(dst + (size_t)r * D);
+    o[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    o[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_expand_fp8(const ExpandArgs& a, cudaStream_t st) {
+  const dim3 grid((a.kv_len + kScaleTokens - 1) / kScaleTokens, a.Hkv, a.B);
+  if (a.d == 64)
+    expand_kernel<64><<<grid, kThreads, 0, st>>>(a);
+  else
+    expand_kernel<128><<<grid, kThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

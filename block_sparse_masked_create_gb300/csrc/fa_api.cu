@@ -190,7 +190,8 @@ static PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
 }
 
 static int encode_tmap(CUtensorMapDataType dt, CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
-                       const uint64_t* strides_bytes, const uint32_t* box) {
+                       const uint64_t* strides_bytes, const uint32_t* box,
+                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = get_encode();
   if (!enc) return -1;
   cuuint64_t gd[5], gs[4];
@@ -202,7 +203,7 @@ static int encode_tmap(CUtensorMapDataType dt, CUtensorMap* m, const void* base,
   }
   for (int i = 0; i < rank - 1; ++i) gs[i] = strides_bytes[i];
   CUresult r = enc(m, dt, (cuuint32_t)rank, const_cast<void*>(base), gd, gs, bx, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : -1;
 }
@@ -215,6 +216,12 @@ int encode_tmap_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t*
 int encode_tmap_f32(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                     const uint64_t* strides_bytes, const uint32_t* box) {
   return encode_tmap(CU_TENSOR_MAP_DATA_TYPE_FLOAT32, m, base, rank, dims, strides_bytes, box);
+}
+
+int encode_tmap_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides_bytes, const uint32_t* box) {
+  return encode_tmap(CU_TENSOR_MAP_DATA_TYPE_UINT8, m, base, rank, dims, strides_bytes, box,
+                     box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -912,6 +919,366 @@ fa_status fa_flex_forward_split(const void* q, const void* k, const void* v, con
                               lse, st) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------------------------------------
+// The attention's inputs: norms, rotation, paged-cache append
+// ------------------------------------------------------------------------------------------------
+static int check_sizes(int32_t B, int32_t Hq, int32_t Hkv, int32_t N, int32_t d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || N < 1 || Hq % Hkv) return FA_ERR_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if ((int64_t)B * N > INT_MAX || (int64_t)Hq + 2 * (int64_t)Hkv > INT_MAX) return FA_ERR_SHAPE;
+  return FA_OK;
+}
+
+// rows with their strides checked; a dimension of one element has no stride
+static int take_rows(const fa_rows* r, int32_t B, int32_t N, int32_t H, Rows* out) {
+  *out = Rows{nullptr, 0, 0, 0};
+  if (!r || !r->ptr) return FA_OK;
+  Rows t{r->ptr, B > 1 ? r->stride_b : 0, N > 1 ? r->stride_n : 0, H > 1 ? r->stride_h : 0};
+  if (!aligned16(t.p) || (t.sb & 7) || (t.sn & 7) || (t.sh & 7)) return FA_ERR_INVALID_ARG;
+  *out = t;
+  return FA_OK;
+}
+
+static int take_rule(const fa_qk_rule* r, int32_t d, const float** wq, const float** wk, float* eps, const float** freq,
+                     int32_t* rot, int32_t* interleaved) {
+  *wq = *wk = *freq = nullptr;
+  *eps = 0.f;
+  *rot = *interleaved = 0;
+  if (!r) return FA_OK;
+  if (!(r->eps >= 0.f) || std::isinf(r->eps) || (r->interleaved != 0 && r->interleaved != 1)) return FA_ERR_INVALID_ARG;
+  const uintptr_t all = reinterpret_cast<uintptr_t>(r->q_weight) | reinterpret_cast<uintptr_t>(r->k_weight) |
+                        reinterpret_cast<uintptr_t>(r->inv_freq);
+  if (all & 3u) return FA_ERR_INVALID_ARG;
+  if (r->inv_freq) {
+    if (r->rot_dim < 16 || r->rot_dim > d || (r->rot_dim & 15)) return FA_ERR_UNSUPPORTED;
+    *freq = r->inv_freq;
+    *rot = r->rot_dim;
+    *interleaved = r->interleaved;
+  }
+  *wq = r->q_weight;
+  *wk = r->k_weight;
+  *eps = r->eps;
+  return FA_OK;
+}
+
+static int fill_qkv(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_qk_rule* rule, const int32_t* q_offset,
+                    int32_t B, int32_t Hq, int32_t Hkv, int32_t N, int32_t d, QkvArgs* a) {
+  std::memset(a, 0, sizeof(*a));
+  int s = check_sizes(B, Hq, Hkv, N, d);
+  if (s == FA_OK) s = take_rule(rule, d, &a->wq, &a->wk, &a->eps, &a->inv_freq, &a->rot, &a->interleaved);
+  if (s == FA_OK) s = take_rows(q, B, N, Hq, &a->q);
+  if (s == FA_OK) s = take_rows(k, B, N, Hkv, &a->k);
+  if (s == FA_OK) s = take_rows(v, B, N, Hkv, &a->v);
+  if (s == FA_OK && (reinterpret_cast<uintptr_t>(q_offset) & 3u)) s = FA_ERR_INVALID_ARG;
+  a->q_offset = q_offset;
+  a->B = B;
+  a->N = N;
+  a->Hq = Hq;
+  a->Hkv = Hkv;
+  a->d = d;
+  return s;
+}
+
+fa_status fa_qk_norm_rope(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_qk_rule* rule,
+                          const int32_t* q_offset, void* q_out, void* k_out, void* v_out, int32_t B, int32_t Hq,
+                          int32_t Hkv, int32_t N, int32_t d, fa_stream_t stream) {
+  if (!rule) return FA_ERR_INVALID_ARG;
+  QkvArgs a;
+  const int s = fill_qkv(q, k, v, rule, q_offset, B, Hq, Hkv, N, d, &a);
+  if (s != FA_OK) return (fa_status)s;
+  if (!a.q.p && !a.k.p && !a.v.p) return FA_ERR_INVALID_ARG;
+  if ((a.q.p && !q_out) || (a.k.p && !k_out) || (a.v.p && !v_out)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q_out) || !aligned16(k_out) || !aligned16(v_out)) return FA_ERR_INVALID_ARG;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  return launch_qk_norm_rope(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_qk_norm_rope_backward_workspace_bytes(int32_t B, int32_t N, int32_t d) {
+  if (B < 1 || N < 1 || d < 1 || (int64_t)B * N > INT_MAX) return 0;
+  return (size_t)qk_bwd_ctas((int64_t)B * N) * 2 * d * sizeof(float);
+}
+
+fa_status fa_qk_norm_rope_backward(const fa_rows* q, const fa_rows* k, const float* dq, const float* dk, const float* dv,
+                                   const fa_qk_rule* rule, const int32_t* q_offset, const fa_rows* dq_in,
+                                   const fa_rows* dk_in, const fa_rows* dv_in, int32_t grad_dtype, float* dq_weight,
+                                   float* dk_weight, int32_t B, int32_t Hq, int32_t Hkv, int32_t N, int32_t d,
+                                   void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+  if (!rule || (!dq && !dk && !dv)) return FA_ERR_INVALID_ARG;
+  if (grad_dtype != FA_OUT_BF16 && grad_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
+  QkvBwdArgs a;
+  std::memset(&a, 0, sizeof(a));
+  int s = check_sizes(B, Hq, Hkv, N, d);
+  if (s == FA_OK) s = take_rule(rule, d, &a.wq, &a.wk, &a.eps, &a.inv_freq, &a.rot, &a.interleaved);
+  if (s == FA_OK) s = take_rows(q, B, N, Hq, &a.q);
+  if (s == FA_OK) s = take_rows(k, B, N, Hkv, &a.k);
+  if (s == FA_OK) s = take_rows(dq_in, B, N, Hq, &a.dq_in);
+  if (s == FA_OK) s = take_rows(dk_in, B, N, Hkv, &a.dk_in);
+  if (s == FA_OK) s = take_rows(dv_in, B, N, Hkv, &a.dv_in);
+  if (s != FA_OK) return (fa_status)s;
+  if (!dq) a.wq = nullptr;  // a gradient that is left out has no weight gradient either
+  if (!dk) a.wk = nullptr;
+  if ((dq && !a.dq_in.p) || (dk && !a.dk_in.p) || (dv && !a.dv_in.p)) return FA_ERR_INVALID_ARG;
+  if ((a.wq && (!a.q.p || !dq_weight)) || (a.wk && (!a.k.p || !dk_weight))) return FA_ERR_INVALID_ARG;
+  if (!aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+  const uintptr_t words = reinterpret_cast<uintptr_t>(q_offset) | reinterpret_cast<uintptr_t>(dq_weight) |
+                          reinterpret_cast<uintptr_t>(dk_weight);
+  if (words & 3u) return FA_ERR_INVALID_ARG;
+  if (a.wq || a.wk) {
+    if (!workspace) return FA_ERR_INVALID_ARG;
+    if (workspace_bytes < fa_qk_norm_rope_backward_workspace_bytes(B, N, d)) return FA_ERR_BUFFER_TOO_SMALL;
+  }
+  a.q_offset = q_offset;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.grad_f32 = grad_dtype == FA_OUT_F32;
+  a.dwq = a.wq ? dq_weight : nullptr;
+  a.dwk = a.wk ? dk_weight : nullptr;
+  a.partial = static_cast<float*>(workspace);
+  a.B = B;
+  a.N = N;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  return launch_qk_norm_rope_backward(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+static int append_impl(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_qk_rule* rule,
+                       const int32_t* q_offset, const int32_t* n_new, void* q_out, void* k_pages, void* v_pages,
+                       float* k_scale, float* v_scale, const int32_t* page_table, int32_t n_pages_total, int32_t page,
+                       int32_t max_pages, int32_t B, int32_t Hq, int32_t Hkv, int32_t N, int32_t d, int32_t* dev_status,
+                       fa_stream_t stream) {
+  if (!k_pages || !v_pages || !page_table) return FA_ERR_INVALID_ARG;
+  QkvArgs a;
+  const int s = fill_qkv(q, k, v, rule, q_offset, B, Hq, Hkv, N, d, &a);
+  if (s != FA_OK) return s;
+  if (!a.k.p || !a.v.p || (a.q.p && !q_out)) return FA_ERR_INVALID_ARG;
+  if (n_pages_total < 1 || max_pages < 1) return FA_ERR_SHAPE;
+  if (!aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_INVALID_ARG;
+  const uintptr_t words = reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(n_new) |
+                          reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale);
+  if (words & 3u) return FA_ERR_INVALID_ARG;
+  a.n_new = n_new;
+  a.q_out = q_out;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.page_table = page_table;
+  a.n_pages_total = n_pages_total;
+  a.page = page;
+  a.max_pages = max_pages;
+  a.status = dev_status;
+  return launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_kv_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_qk_rule* rule,
+                       const int32_t* q_offset, const int32_t* n_new, void* q_out, void* k_pages, void* v_pages,
+                       const int32_t* page_table, int32_t n_pages_total, int32_t page, int32_t max_pages, int32_t B,
+                       int32_t Hq, int32_t Hkv, int32_t N, int32_t d, int32_t* dev_status, fa_stream_t stream) {
+  if (page != 16 && page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
+  return (fa_status)append_impl(q, k, v, rule, q_offset, n_new, q_out, k_pages, v_pages, nullptr, nullptr, page_table,
+                                n_pages_total, page, max_pages, B, Hq, Hkv, N, d, dev_status, stream);
+}
+
+fa_status fa_kv_append_fp8(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_qk_rule* rule,
+                           const int32_t* q_offset, const int32_t* n_new, void* q_out, void* k_pages, void* v_pages,
+                           float* k_scale, float* v_scale, const int32_t* page_table, int32_t n_pages_total, int32_t page,
+                           int32_t max_pages, int32_t B, int32_t Hq, int32_t Hkv, int32_t N, int32_t d,
+                           int32_t* dev_status, fa_stream_t stream) {
+  if (page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
+  if (!k_scale || !v_scale) return FA_ERR_INVALID_ARG;
+  return (fa_status)append_impl(q, k, v, rule, q_offset, n_new, q_out, k_pages, v_pages, k_scale, v_scale, page_table,
+                                n_pages_total, page, max_pages, B, Hq, Hkv, N, d, dev_status, stream);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Attention over an 8-bit paged cache
+// ------------------------------------------------------------------------------------------------
+// Pages of one span of the 8-bit decode: enough spans for four rounds of two CTAs an SM by the table's capacity (the
+// lengths are on the device), at least 256 tokens each and at most 4096 (32 sub-tiles for each of a CTA's 4 warps).
+static int decode_fp8_pages_per_split(int32_t Bz, int32_t Hkv, int32_t max_pages, int32_t page) {
+  const int64_t tokens = (int64_t)Bz * Hkv * max_pages * page / (152 * 2 * 4);
+  const int64_t span = std::min<int64_t>(4096, std::max<int64_t>(256, tokens));
+  return (int)std::min<int64_t>(std::max<int64_t>(1, span / page), max_pages);
+}
+
+struct DecodeFp8Plan {
+  int32_t pages_per_split, n_splits;
+  size_t slots, off_l, off_u, total;
+};
+
+static bool decode_fp8_plan(int32_t Bz, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_pages, int32_t page,
+                            DecodeFp8Plan* P) {
+  if (Bz < 1 || Hq < 1 || Hkv < 1 || d < 1 || max_pages < 1 || (page != 32 && page != 64 && page != 128)) return false;
+  P->pages_per_split = decode_fp8_pages_per_split(Bz, Hkv, max_pages, page);
+  P->n_splits = (max_pages + P->pages_per_split - 1) / P->pages_per_split;
+  P->slots = (size_t)Bz * Hq * P->n_splits;
+  P->off_l = align256(P->slots * 4);
+  P->off_u = 2 * P->off_l;
+  P->total = P->off_u + align256(P->slots * (size_t)d * 4);
+  return true;
+}
+
+size_t fa_decode_fp8_workspace_bytes(int32_t Bz, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_pages, int32_t page) {
+  DecodeFp8Plan P;
+  return decode_fp8_plan(Bz, Hq, Hkv, d, max_pages, page, &P) ? P.total : 0;
+}
+
+fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                             const float* v_scale, const int32_t* page_table, int32_t n_pages_total,
+                             const fa_block_mask* bm, const fa_score_rule* score_rule, float scale, void* out,
+                             int32_t out_dtype, float* lse, int32_t Bz, int32_t Hq, int32_t Hkv, int32_t d, int32_t page,
+                             int32_t max_pages, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                             int64_t* dev_counters, fa_stream_t stream) {
+  if (!q || !k_pages || !v_pages || !k_scale || !v_scale || !page_table || !bm || !out || !lse || !workspace)
+    return FA_ERR_INVALID_ARG;
+  if (Bz < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || n_pages_total < 1 || max_pages < 1) return FA_ERR_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
+  if (out_dtype != FA_OUT_BF16 && out_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
+  if (Hq / Hkv > 16 || Hkv > 65535 || Bz > 65535) return FA_ERR_UNSUPPORTED;
+  if (bm->bq != 1 || bm->bk != page || bm->q_len != 1 || (int64_t)bm->kv_len != (int64_t)max_pages * page ||
+      bm->Hm != 1 || !(bm->Bm == 1 || bm->Bm == Bz) || bm->nk != max_pages || bm->nq != 1)
+    return FA_ERR_SHAPE;
+  if (!bm->kv_num || !bm->kv_idx || !bm->full_kv_num || !bm->full_kv_idx) return FA_ERR_INVALID_ARG;
+  if ((int64_t)n_pages_total * Hkv * page > INT_MAX) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(workspace))
+    return FA_ERR_INVALID_ARG;
+  DecodeFp8Plan P;
+  if (!decode_fp8_plan(Bz, Hq, Hkv, d, max_pages, page, &P)) return FA_ERR_SHAPE;
+  if (workspace_bytes < P.total) return FA_ERR_BUFFER_TOO_SMALL;
+  DecFp8Args A;
+  std::memset(&A, 0, sizeof(A));
+  DecArgs& a = A.d;
+  const int s = compile_rule(&bm->rule, &a.rule);
+  if (s != FA_OK) return (fa_status)s;
+  a.rule.doc_run = bm->doc_run;
+  a.rule.doc_sorted = bm->doc_sorted;
+  a.q = q;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.page_table = page_table;
+  a.n_pages_total = n_pages_total;
+  a.out = out;
+  a.out_f32 = out_dtype == FA_OUT_F32;
+  a.lse = lse;
+  a.Bz = Bz;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.d = d;
+  a.page = page;
+  a.max_pages = max_pages;
+  a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
+  a.score = make_score(score_rule, bm->kv_len);
+  a.mask = dev_mask(bm);
+  a.pages_per_split = P.pages_per_split;
+  a.n_splits = P.n_splits;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.ws_m = reinterpret_cast<float*>(w);
+  a.ws_l = reinterpret_cast<float*>(w + P.off_l);
+  a.ws_u = reinterpret_cast<float*>(w + P.off_u);
+  a.status = dev_status;
+  a.counters = dev_counters;
+  a.timeout_ns = g_timeout_ns.load();
+  A.k_scale = k_scale;
+  A.v_scale = v_scale;
+  return (fa_status)launch_decode_fp8(A, reinterpret_cast<cudaStream_t>(stream));
+}
+
+struct PagedFp8Plan {
+  int32_t chunk;  // 0: rows are not cut
+  size_t kv_bytes, off_split, total;
+};
+
+static int paged_fp8_plan(const fa_block_mask* bm, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t chunk_blocks,
+                          PagedFp8Plan* P) {
+  if (!bm || chunk_blocks < -1) return FA_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || bm->kv_len < 1 || bm->nq < 1 || bm->nk < 1) return FA_ERR_SHAPE;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  P->kv_bytes = align256((size_t)B * Hkv * bm->kv_len * d * 2);
+  P->off_split = 2 * P->kv_bytes;
+  P->total = P->off_split;
+  P->chunk = 0;
+  if (chunk_blocks > 0) {
+    if (bm->bq != 128 || bm->bk != 128) return FA_ERR_UNSUPPORTED;
+    P->chunk = chunk_blocks;
+  } else if (chunk_blocks == 0 && bm->bq == 128 && bm->bk == 128) {
+    // a CTA takes two query blocks; cut rows only where there are fewer CTAs than SMs, into as many chunks as fill them
+    const int64_t ctas = std::max<int64_t>(1, (int64_t)B * Hq * bm->nq / 2);
+    if (ctas < 152 && bm->nk >= 32) {
+      const int64_t parts = std::min<int64_t>(152 / ctas, bm->nk / 16);
+      if (parts > 1) P->chunk = (int32_t)((bm->nk + parts - 1) / parts);
+    }
+  }
+  if (P->chunk) {
+    const size_t n = fa_forward_split_workspace_bytes(bm, B, Hq, d, P->chunk);
+    if (!n) return FA_ERR_SHAPE;
+    P->total += n;
+  }
+  return FA_OK;
+}
+
+size_t fa_forward_paged_fp8_workspace_bytes(const fa_block_mask* bm, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
+                                            int32_t chunk_blocks) {
+  PagedFp8Plan P;
+  return paged_fp8_plan(bm, B, Hq, Hkv, d, chunk_blocks, &P) == FA_OK ? P.total : 0;
+}
+
+fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                                    const float* v_scale, const int32_t* page_table, int32_t n_pages_total, int32_t page,
+                                    int32_t max_pages, const fa_block_mask* bm, const fa_score_rule* score_rule,
+                                    float scale, void* out, int32_t out_dtype, float* lse, int32_t B, int32_t Hq,
+                                    int32_t Hkv, int32_t Q_LEN, int32_t KV_LEN, int32_t d, int32_t chunk_blocks,
+                                    void* workspace, size_t workspace_bytes, int32_t* dev_status, fa_stream_t stream) {
+  if (!k_scale || !v_scale || !page_table || !workspace) return FA_ERR_INVALID_ARG;
+  int s = check_forward(q, k_pages, v_pages, bm, out, lse, B, Hq, Hkv, Q_LEN, KV_LEN, d);
+  if (s != FA_OK) return (fa_status)s;
+  if (out_dtype != FA_OUT_BF16 && out_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
+  if (page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
+  if (n_pages_total < 1 || (int64_t)max_pages * page < KV_LEN) return FA_ERR_SHAPE;
+  if (Hkv > 65535 || B > 65535) return FA_ERR_UNSUPPORTED;
+  if (!bm->q_num || !bm->full_q_num) return FA_ERR_INVALID_ARG;
+  if (bm->bk < FA_KV_SCALE_TOKENS) return FA_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(page_table) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return FA_ERR_INVALID_ARG;
+  PagedFp8Plan P;
+  s = paged_fp8_plan(bm, B, Hq, Hkv, d, chunk_blocks, &P);
+  if (s != FA_OK) return (fa_status)s;
+  if (workspace_bytes < P.total) return FA_ERR_BUFFER_TOO_SMALL;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  ExpandArgs a;
+  std::memset(&a, 0, sizeof(a));
+  s = compile_rule(&bm->rule, &a.rule);
+  if (s != FA_OK) return (fa_status)s;
+  a.k_pages = k_pages;
+  a.v_pages = v_pages;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.page_table = page_table;
+  a.n_pages_total = n_pages_total;
+  a.page = page;
+  a.max_pages = max_pages;
+  a.k_out = w;
+  a.v_out = w + P.kv_bytes;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.q_len = Q_LEN;
+  a.kv_len = KV_LEN;
+  a.d = d;
+  a.mask = dev_mask(bm);
+  a.status = dev_status;
+  if (launch_expand_fp8(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
+  if (P.chunk)
+    return fa_flex_forward_split(q, a.k_out, a.v_out, bm, score_rule, scale, out, out_dtype, lse, B, Hq, Hkv, Q_LEN,
+                                 KV_LEN, d, P.chunk, w + P.off_split, P.total - P.off_split, dev_status, stream);
+  return fa_flex_forward(q, a.k_out, a.v_out, bm, score_rule, scale, out, out_dtype, lse, B, Hq, Hkv, Q_LEN, KV_LEN, d,
+                         dev_status, nullptr, stream);
 }
 
 fa_status fa_block_mask_stats(const fa_block_mask* bm, int64_t* dev_out, fa_stream_t stream) {

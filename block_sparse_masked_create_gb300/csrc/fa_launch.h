@@ -138,10 +138,90 @@ cudaError_t launch_mask_split(const MaskOut& S, int C, int ncm, const MaskOut& D
 cudaError_t launch_split_combine(const float* o_part, const float* lse_part, int B, int Hq, int q_len, int nq,
                                  int ncm, int d, void* out, int out_f32, float* lse, cudaStream_t st);
 
+// ---- the attention's inputs: norms, rotation, paged-cache append (qkv.cu)
+struct Rows {  // element (b, n, h, 0 .. d-1) at p + b * sb + n * sn + h * sh (elements); p NULL: absent
+  void* p;
+  int64_t sb, sn, sh;
+};
+
+struct QkvArgs {
+  Rows q, k, v;              // bf16
+  const float* wq;           // [d] or NULL: no norm
+  const float* wk;
+  float eps;
+  const float* inv_freq;     // [rot / 2] or NULL: no rotation
+  int32_t rot, interleaved;
+  const int32_t* q_offset;   // [B] or NULL
+  const int32_t* n_new;      // [B] or NULL (append only)
+  void* q_out;               // bf16 [B, Hq, N, d]
+  void* k_out;               // bf16 [B, Hkv, N, d] (not for the append)
+  void* v_out;
+  void* k_pages;             // append: bf16 or e4m3 [n_pages_total, Hkv, page, d]
+  void* v_pages;
+  float* k_scale;            // append to e4m3 pages: [n_pages_total, Hkv, page / 32]; NULL: bf16 pages
+  float* v_scale;
+  const int32_t* page_table; // [B, max_pages]
+  int32_t n_pages_total, page, max_pages;
+  int32_t B, N, Hq, Hkv, d;
+  int32_t* status;
+};
+
+cudaError_t launch_qk_norm_rope(const QkvArgs& a, cudaStream_t st);
+cudaError_t launch_kv_append(const QkvArgs& a, cudaStream_t st);
+
+struct QkvBwdArgs {
+  Rows q, k;                 // bf16, the forward's inputs
+  const float* wq;
+  const float* wk;
+  float eps;
+  const float* inv_freq;
+  int32_t rot, interleaved;
+  const int32_t* q_offset;
+  const float* dq;           // fp32 [B, Hq, N, d] or NULL
+  const float* dk;           // fp32 [B, Hkv, N, d] or NULL
+  const float* dv;           // fp32 [B, Hkv, N, d] or NULL
+  Rows dq_in, dk_in, dv_in;  // bf16 or fp32
+  int32_t grad_f32;
+  float* dwq;                // [d] or NULL
+  float* dwk;
+  float* partial;            // [qk_bwd_ctas(B * N)][2][d]
+  int32_t B, N, Hq, Hkv, d;
+};
+
+int qk_bwd_ctas(int64_t tokens);
+cudaError_t launch_qk_norm_rope_backward(const QkvBwdArgs& a, cudaStream_t st);
+
+// ---- attention over e4m3 pages (decode_fp8.cu, expand_fp8.cu)
+struct DecFp8Args {
+  DecArgs d;                 // ws_le unused: one sum of the unrounded P
+  const float* k_scale;      // [n_pages_total, Hkv, page / 32]
+  const float* v_scale;
+};
+int launch_decode_fp8(const DecFp8Args& a, cudaStream_t st);
+
+struct ExpandArgs {
+  const void* k_pages;       // e4m3 [n_pages_total, Hkv, page, d]
+  const void* v_pages;
+  const float* k_scale;      // [n_pages_total, Hkv, page / 32]
+  const float* v_scale;
+  const int32_t* page_table; // [B, max_pages]
+  int32_t n_pages_total, page, max_pages;
+  void* k_out;               // bf16 [B, Hkv, kv_len, d]
+  void* v_out;
+  int32_t B, Hq, Hkv, q_len, kv_len, d;
+  DevRule rule;
+  DevMask mask;
+  int32_t* status;
+};
+cudaError_t launch_expand_fp8(const ExpandArgs& a, cudaStream_t st);
+
 // Host helpers: encode a bf16 / fp32 tensor map (dims innermost first) with 128-byte swizzle.
 int encode_tmap_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                      const uint64_t* strides_bytes /* rank-1 entries */, const uint32_t* box);
 int encode_tmap_f32(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
                     const uint64_t* strides_bytes, const uint32_t* box);
+// 8-bit elements; rows of 128 bytes with the 128-byte swizzle, rows of 64 bytes with the 64-byte one
+int encode_tmap_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,
+                   const uint64_t* strides_bytes, const uint32_t* box);
 
 }  // namespace fa

@@ -41,6 +41,16 @@ class ScoreRule(ctypes.Structure):
     _fields_ = [("alibi_slopes", ctypes.c_void_p), ("rel_bias", ctypes.c_void_p), ("softcap", ctypes.c_float)]
 
 
+class RowsC(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_n", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class QkRule(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 class BlockMaskC(ctypes.Structure):
     _fields_ = [("Bm", ctypes.c_int32), ("Hm", ctypes.c_int32), ("q_len", ctypes.c_int32),
                 ("kv_len", ctypes.c_int32), ("bq", ctypes.c_int32), ("bk", ctypes.c_int32),
@@ -112,6 +122,29 @@ def load() -> ctypes.CDLL:
                                            i32, i32, i32, i32, i32, vp, vp, vp]
     lib.fa_decode_noalloc_scratch_bytes.restype = sz
     lib.fa_decode_noalloc_scratch_bytes.argtypes = []
+    R, K = P(RowsC), P(QkRule)
+    lib.fa_qk_norm_rope.restype = ctypes.c_int
+    lib.fa_qk_norm_rope.argtypes = [R, R, R, K, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp]
+    lib.fa_qk_norm_rope_backward_workspace_bytes.restype = sz
+    lib.fa_qk_norm_rope_backward_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.fa_qk_norm_rope_backward.restype = ctypes.c_int
+    lib.fa_qk_norm_rope_backward.argtypes = [R, R, vp, vp, vp, K, vp, R, R, R, i32, vp, vp, i32, i32, i32, i32, i32, vp,
+                                             sz, vp]
+    lib.fa_kv_append.restype = ctypes.c_int
+    lib.fa_kv_append.argtypes = [R, R, R, K, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.fa_kv_append_fp8.restype = ctypes.c_int
+    lib.fa_kv_append_fp8.argtypes = [R, R, R, K, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32,
+                                     vp, vp]
+    lib.fa_decode_fp8_workspace_bytes.restype = sz
+    lib.fa_decode_fp8_workspace_bytes.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.fa_flex_decode_fp8.restype = ctypes.c_int
+    lib.fa_flex_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, P(BlockMaskC), P(ScoreRule), f32, vp, i32, vp, i32,
+                                       i32, i32, i32, i32, i32, vp, sz, vp, vp, vp]
+    lib.fa_forward_paged_fp8_workspace_bytes.restype = sz
+    lib.fa_forward_paged_fp8_workspace_bytes.argtypes = [P(BlockMaskC), i32, i32, i32, i32, i32]
+    lib.fa_flex_forward_paged_fp8.restype = ctypes.c_int
+    lib.fa_flex_forward_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, P(BlockMaskC), P(ScoreRule), f32, vp,
+                                              i32, vp, i32, i32, i32, i32, i32, i32, i32, vp, sz, vp, vp]
     lib.fa_block_mask_stats.restype = ctypes.c_int
     lib.fa_block_mask_stats.argtypes = [P(BlockMaskC), vp, vp]
     lib.fa_check_status.restype = ctypes.c_int
@@ -482,6 +515,290 @@ def flex_decode_noalloc(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.T
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), P, ctypes.byref(block_mask.c),
         ctypes.byref(score) if score else None, float(scale) if scale else 0.0, _ptr(out), _out_code(out), _ptr(lse),
         Bz, Hq, Hkv, d, page, page_table.shape[1], _ptr(status), _ptr(counters), _stream(q.device)))
+
+
+# ----------------------------------------------------------------------------------------------
+# the attention's inputs: norms, rotation, paged-cache append
+# ----------------------------------------------------------------------------------------------
+KV_SCALE_TOKENS = 32  # tokens of a page that share a scale in the 8-bit cache
+
+
+def make_qk_rule(q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False) -> QkRule:
+    """fa_qk_rule: norm weights fp32 [d] (None: no norm), rotation frequencies fp32 [rot_dim / 2] (None: no rotation;
+    the first rot_dim = 2 * len(inv_freq) elements of a row are rotated), pairs (i, i + rot_dim / 2) or, interleaved,
+    (2 i, 2 i + 1)."""
+    r = QkRule()
+    for t in (q_weight, k_weight, inv_freq):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or not t.is_contiguous()):
+            raise ValueError("norm weights and inv_freq must be contiguous 1-D fp32 device tensors")
+    r.q_weight = None if q_weight is None else q_weight.data_ptr()
+    r.k_weight = None if k_weight is None else k_weight.data_ptr()
+    r.eps = float(eps)
+    r.inv_freq = None if inv_freq is None else inv_freq.data_ptr()
+    r.rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    r.interleaved = int(bool(interleaved))
+    r._tensors = (q_weight, k_weight, inv_freq)  # the raw pointers above stay valid while the rule lives
+    return r
+
+
+def _rows(t: Optional[torch.Tensor], shape, dtype, device, what: str, written: bool = False):
+    """fa_rows of a [B, N, H, d] tensor of any b / n / h strides."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or t.stride(3) != 1:
+        raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on {device} with contiguous rows")
+    sb, sn, sh, _ = t.stride()
+    if written and any(st == 0 and n > 1 for st, n in zip((sb, sn, sh), shape)):
+        raise ValueError(f"{what} is written: its elements must not share memory")
+    return RowsC(t.data_ptr(), sb, sn, sh)
+
+
+def _same(t: Optional[torch.Tensor], shape, dtype, device, what: str):
+    if t is not None and (t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape)
+                          or not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _check_qk_rule(rule: Optional[QkRule], d: int, device):
+    for t, n in zip(rule._tensors if rule is not None else (), (d, d, None)):
+        if t is not None and (t.device != device or (n is not None and t.numel() != n)):
+            raise ValueError(f"the rule's tensors must be on {device}, its weights of {d} elements")
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def _call(device, fn, *args) -> int:
+    """fn(*args, stream) on `device`'s current stream, with that device current."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(device))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(device))
+
+
+def _qkv_shape(q, k, v):
+    """(B, Hq, Hkv, N, d, device) of the rows that are there; without query (key) rows Hq = Hkv."""
+    any_ = q if q is not None else k if k is not None else v
+    if any_ is None or any_.dim() != 4 or not any_.is_cuda:
+        raise ValueError("q, k, v must be CUDA tensors [B, N, H, d]")
+    B, N, H, d = any_.shape
+    kv = k if k is not None else v
+    Hq = q.shape[2] if q is not None else H
+    return B, Hq, kv.shape[2] if kv is not None else Hq, N, d, any_.device
+
+
+def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Optional[torch.Tensor], rule: QkRule,
+                 q_offset: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None):
+    """fa_qk_norm_rope: rows q [B,N,Hq,d], k, v [B,N,Hkv,d] bf16 (views of a packed projection are fine; None: left out)
+    -> (q_out [B,Hq,N,d], k_out, v_out [B,Hkv,N,d]), normalised and rotated, as fa_flex_forward reads them."""
+    B, Hq, Hkv, N, d, dev = _qkv_shape(q, k, v)
+    bf = torch.bfloat16
+    rows = [_rows(t, (B, N, h, d), bf, dev, n) for t, h, n in ((q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v"))]
+    outs = []
+    for t, o, h, n in ((q, q_out, Hq, "q_out"), (k, k_out, Hkv, "k_out"), (v, v_out, Hkv, "v_out")):
+        if t is None:
+            o = None
+        elif o is None:
+            o = torch.empty((B, h, N, d), dtype=bf, device=dev)
+        outs.append(_same(o, (B, h, N, d), bf, dev, n))
+    _check_qk_rule(rule, d, dev)
+    _same(q_offset, (B,), torch.int32, dev, "q_offset")
+    _check(_call(dev, load().fa_qk_norm_rope, *map(_ref, rows), ctypes.byref(rule), _ptr(q_offset), *map(_ptr, outs), B, Hq,
+                 Hkv, N, d), "fa_qk_norm_rope")
+    return tuple(outs)
+
+
+def qk_norm_rope_backward_workspace_bytes(B: int, N: int, d: int) -> int:
+    return int(load().fa_qk_norm_rope_backward_workspace_bytes(B, N, d))
+
+
+def qk_norm_rope_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], dq: Optional[torch.Tensor],
+                          dk: Optional[torch.Tensor], dv: Optional[torch.Tensor], rule: QkRule,
+                          q_offset: Optional[torch.Tensor] = None, grad_dtype=torch.bfloat16,
+                          dq_in: Optional[torch.Tensor] = None, dk_in: Optional[torch.Tensor] = None,
+                          dv_in: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """fa_qk_norm_rope_backward: gradients dq [B,Hq,N,d], dk, dv [B,Hkv,N,d] fp32 (as flex_backward returns them; None:
+    left out) -> (dq_in [B,N,Hq,d], dk_in, dv_in [B,N,Hkv,d] in the type of the tensors given, else grad_dtype; dq_weight,
+    dk_weight fp32 [d] or None). q, k are the forward's rows."""
+    given = dq if dq is not None else dk if dk is not None else dv
+    if given is None or given.dim() != 4 or not given.is_cuda:
+        raise ValueError("dq, dk, dv must be CUDA tensors [B, H, N, d]")
+    B, H, N, d = given.shape
+    dev = given.device
+    kv = dk if dk is not None else dv
+    Hq = dq.shape[1] if dq is not None else kv.shape[1]
+    Hkv = kv.shape[1] if kv is not None else Hq
+    f32, bf = torch.float32, torch.bfloat16
+    for t, h, n in ((dq, Hq, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv")):
+        _same(t, (B, h, N, d), f32, dev, n)
+    kinds = {t.dtype for t in (dq_in, dk_in, dv_in) if t is not None}
+    if len(kinds) > 1:
+        raise ValueError("dq_in, dk_in, dv_in must have one type")
+    kind = kinds.pop() if kinds else grad_dtype
+    if kind not in (bf, f32):
+        raise ValueError("gradients are bf16 or fp32")
+    rq = _rows(q, (B, N, Hq, d), bf, dev, "q") if dq is not None else None
+    rk = _rows(k, (B, N, Hkv, d), bf, dev, "k") if dk is not None else None
+    outs, rows = [], []
+    for t, o, h, n in ((dq, dq_in, Hq, "dq_in"), (dk, dk_in, Hkv, "dk_in"), (dv, dv_in, Hkv, "dv_in")):
+        if t is None:
+            o = None
+        elif o is None:
+            o = torch.empty((B, N, h, d), dtype=kind, device=dev)
+        outs.append(o)
+        rows.append(_rows(o, (B, N, h, d), kind, dev, n, written=True))
+    _check_qk_rule(rule, d, dev)
+    _same(q_offset, (B,), torch.int32, dev, "q_offset")
+    dwq = torch.empty(d, dtype=f32, device=dev) if rule.q_weight and dq is not None else None
+    dwk = torch.empty(d, dtype=f32, device=dev) if rule.k_weight and dk is not None else None
+    if workspace is None and (dwq is not None or dwk is not None):
+        workspace = torch.empty(qk_norm_rope_backward_workspace_bytes(B, N, d), dtype=torch.uint8, device=dev)
+    _check(_call(dev, load().fa_qk_norm_rope_backward, _ref(rq), _ref(rk), _ptr(dq), _ptr(dk), _ptr(dv),
+                 ctypes.byref(rule), _ptr(q_offset), *map(_ref, rows), 1 if kind == f32 else 0, _ptr(dwq), _ptr(dwk), B, Hq,
+                 Hkv, N, d, _ptr(workspace), 0 if workspace is None else workspace.numel()), "fa_qk_norm_rope_backward")
+    return (*outs, dwq, dwk)
+
+
+def _append(q, k, v, k_pages, v_pages, k_scale, v_scale, page_table, rule, q_offset, n_new, q_out, status):
+    if k is None or v is None:
+        raise ValueError("k and v are required")
+    B, Hq, Hkv, N, d, dev = _qkv_shape(q, k, v)
+    bf, i32 = torch.bfloat16, torch.int32
+    fp8 = k_scale is not None
+    rows = [_rows(t, (B, N, h, d), bf, dev, n) for t, h, n in ((q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v"))]
+    if k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("pages must be [P, Hkv, page, d] and page_table [B, max_pages]")
+    P, _, page, _ = k_pages.shape
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _same(t, (P, Hkv, page, d), torch.float8_e4m3fn if fp8 else bf, dev, n)
+    if fp8:
+        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            _same(t, (P, Hkv, page // KV_SCALE_TOKENS), torch.float32, dev, n)
+    _same(page_table, (B, page_table.shape[1]), i32, dev, "page_table")
+    _same(q_offset, (B,), i32, dev, "q_offset")
+    _same(n_new, (B,), i32, dev, "n_new")
+    _same(status, (1,), i32, dev, "status")
+    if q is not None and q_out is None:
+        q_out = torch.empty((B, Hq, N, d), dtype=bf, device=dev)
+    _same(q_out, (B, Hq, N, d), bf, dev, "q_out")
+    _check_qk_rule(rule, d, dev)
+    lib = load()
+    scales = (_ptr(k_scale), _ptr(v_scale)) if fp8 else ()
+    _check(_call(dev, lib.fa_kv_append_fp8 if fp8 else lib.fa_kv_append, *map(_ref, rows), _ref(rule), _ptr(q_offset),
+                 _ptr(n_new), _ptr(q_out if q is not None else None), _ptr(k_pages), _ptr(v_pages), *scales,
+                 _ptr(page_table), P, page, page_table.shape[1], B, Hq, Hkv, N, d, _ptr(status)),
+           "fa_kv_append_fp8" if fp8 else "fa_kv_append")
+    return q_out
+
+
+def kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              page_table: torch.Tensor, rule: Optional[QkRule] = None, q_offset: Optional[torch.Tensor] = None,
+              n_new: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """fa_kv_append: normalise and rotate the rows q [B,N,Hq,d] (or None), k, v [B,N,Hkv,d] and put the first n_new[b] keys
+    and values of request b at positions q_offset[b] .. of its pages [P,Hkv,page,d] bf16. Returns q_out [B,Hq,N,d] (for
+    N = 1, q_out[:, :, 0] is flex_decode's q); rows past n_new[b] are left as they were."""
+    return _append(q, k, v, k_pages, v_pages, None, None, page_table, rule, q_offset, n_new, q_out, status)
+
+
+def kv_append_fp8(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor,
+                  v_pages: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor, page_table: torch.Tensor,
+                  rule: Optional[QkRule] = None, q_offset: Optional[torch.Tensor] = None,
+                  n_new: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """fa_kv_append_fp8: kv_append into float8_e4m3fn pages with a power-of-two fp32 scale for each 32 tokens of a page and
+    head (k_scale, v_scale [P, Hkv, page / 32]); the cached value is scale * page value."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale are required")
+    return _append(q, k, v, k_pages, v_pages, k_scale, v_scale, page_table, rule, q_offset, n_new, q_out, status)
+
+
+# ----------------------------------------------------------------------------------------------
+# attention over an 8-bit paged cache
+# ----------------------------------------------------------------------------------------------
+def _check_fp8_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, B, d):
+    if q.dtype != torch.bfloat16 or not q.is_contiguous() or not q.is_cuda:
+        raise ValueError("q must be a contiguous bf16 CUDA tensor")
+    if k_pages.dim() != 4 or page_table.dim() != 2:
+        raise ValueError("pages must be [P, Hkv, page, d] and page_table [B, max_pages]")
+    P, Hkv, page, _ = k_pages.shape
+    dev = q.device
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _same(t, (P, Hkv, page, d), torch.float8_e4m3fn, dev, n)
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _same(t, (P, Hkv, page // KV_SCALE_TOKENS), torch.float32, dev, n)
+    _same(page_table, (B, page_table.shape[1]), torch.int32, dev, "page_table")
+    return P, Hkv, page, page_table.shape[1], dev
+
+
+def _outputs(shape, dev, out, lse, out_dtype):
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    if lse is None:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    _same(out, shape, out.dtype, dev, "out")
+    _same(lse, shape[:-1], torch.float32, dev, "lse")
+    return out, lse
+
+
+def decode_fp8_workspace_bytes(Bz: int, Hq: int, Hkv: int, d: int, max_pages: int, page: int) -> int:
+    return int(load().fa_decode_fp8_workspace_bytes(Bz, Hq, Hkv, d, max_pages, page))
+
+
+def flex_decode_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                    v_scale: torch.Tensor, page_table: torch.Tensor, block_mask: BlockMask,
+                    score: Optional[ScoreRule] = None, scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, counters: Optional[torch.Tensor] = None,
+                    out_dtype=torch.bfloat16):
+    """fa_flex_decode_fp8: flex_decode over float8_e4m3fn pages [P,Hkv,page,d] with scales fp32 [P,Hkv,page/32]."""
+    if q.dim() != 3:
+        raise ValueError("q must be [Bz, Hq, d]")
+    Bz, Hq, d = q.shape
+    q = q.contiguous()
+    P, Hkv, page, max_pages, dev = _check_fp8_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, Bz, d)
+    out, lse = _outputs((Bz, Hq, d), dev, out, lse, out_dtype)
+    if workspace is None:
+        workspace = torch.empty(max(decode_fp8_workspace_bytes(Bz, Hq, Hkv, d, max_pages, page), 16), dtype=torch.uint8,
+                                device=dev)
+    _check(_call(dev, load().fa_flex_decode_fp8, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+                 _ptr(page_table), P, ctypes.byref(block_mask.c), _ref(score), float(scale) if scale else 0.0, _ptr(out),
+                 _out_code(out), _ptr(lse), Bz, Hq, Hkv, d, page, max_pages, _ptr(workspace), workspace.numel(),
+                 _ptr(status), _ptr(counters)), "fa_flex_decode_fp8")
+    return out, lse
+
+
+def forward_paged_fp8_workspace_bytes(block_mask: BlockMask, B: int, Hq: int, Hkv: int, d: int,
+                                      chunk_blocks: int = 0) -> int:
+    return int(load().fa_forward_paged_fp8_workspace_bytes(ctypes.byref(block_mask.c), B, Hq, Hkv, d, chunk_blocks))
+
+
+def flex_forward_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                           v_scale: torch.Tensor, page_table: torch.Tensor, block_mask: BlockMask, KV_LEN: int,
+                           score: Optional[ScoreRule] = None, scale: Optional[float] = None, chunk_blocks: int = 0,
+                           out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                           out_dtype=torch.bfloat16):
+    """fa_flex_forward_paged_fp8: q [B,Hq,Q_LEN,d] over float8_e4m3fn pages [P,Hkv,page,d] with scales fp32 [P,Hkv,page/32];
+    the page size is independent of the mask's Bk. chunk_blocks: key blocks per chunk of a long row (0: chosen, -1: rows
+    are not cut)."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, Hq, Q_LEN, d]")
+    B, Hq, Q_LEN, d = q.shape
+    P, Hkv, page, max_pages, dev = _check_fp8_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, B, d)
+    out, lse = _outputs((B, Hq, Q_LEN, d), dev, out, lse, out_dtype)
+    if workspace is None:
+        n = forward_paged_fp8_workspace_bytes(block_mask, B, Hq, Hkv, d, chunk_blocks)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    _check(_call(dev, load().fa_flex_forward_paged_fp8, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
+                 _ptr(v_scale), _ptr(page_table), P, page, max_pages, ctypes.byref(block_mask.c), _ref(score),
+                 float(scale) if scale else 0.0, _ptr(out), _out_code(out), _ptr(lse), B, Hq, Hkv, Q_LEN, KV_LEN, d,
+                 chunk_blocks, _ptr(workspace), workspace.numel(), _ptr(status)), "fa_flex_forward_paged_fp8")
+    return out, lse
 
 
 def check_status(status: torch.Tensor) -> int:

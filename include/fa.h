@@ -359,6 +359,131 @@ FA_API fa_status fa_flex_decode_noalloc(const void* q, const void* k_pages, cons
                                         int32_t* dev_status, int64_t* dev_counters, fa_stream_t stream);
 FA_API size_t fa_decode_noalloc_scratch_bytes(void);
 
+/* ------------------------------------------------------------------------------------------------
+ * The attention's inputs. A projection leaves rows x[b, n, h, 0 .. d-1]; the attention wants query and key rows that
+ * are normalised and rotated by their position, head-major (fa_flex_forward) or in the pages of a cache
+ * (fa_flex_decode, fa_flex_forward_paged).
+ * ---------------------------------------------------------------------------------------------- */
+
+/* Strided bf16 rows: element (b, n, h, e) at ptr + b * stride_b + n * stride_n + h * stride_h + e (in elements), so that
+ * Q, K and V of one packed projection, or tensors of any other order, are read and written in place. ptr 16-byte
+ * aligned, strides multiples of 8 (a stride of a dimension of size 1 is not read). ptr NULL: these rows are left out. */
+typedef struct {
+  void* ptr;
+  int64_t stride_b, stride_n, stride_h;
+} fa_rows;
+
+/* What happens to a query or key row x at position p = n + q_offset[b]:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight                              (weight NULL: y = x)
+ *   (z_a, z_b) = (y_a cos t - y_b sin t, y_a sin t + y_b cos t),  t = p * inv_freq[i],  for the pairs i of the first
+ *   rot_dim elements: (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved  (inv_freq NULL: z = y)
+ * in fp32, rounded once at the end. The angle is reduced modulo 2 pi in 64-bit integers and is as exact at position
+ * 2^31 as at 1; inv_freq is finite. Value rows are moved as they are. */
+typedef struct {
+  const float* q_weight; /* device fp32 [d] or NULL */
+  const float* k_weight; /* device fp32 [d] or NULL */
+  float eps;             /* >= 0 */
+  const float* inv_freq; /* device fp32 [rot_dim / 2] or NULL */
+  int32_t rot_dim;       /* 16 .. d, a multiple of 16 (read only with inv_freq) */
+  int32_t interleaved;   /* 0 or 1 */
+} fa_qk_rule;
+
+/* Norm, rotation and transposition of a projection's rows into the tensors of fa_flex_forward, in one pass.
+ *   q [B, N, Hq, d], k, v [B, N, Hkv, d]   host pointers to fa_rows, or NULL (with the output) where not wanted
+ *   rule       host pointer
+ *   q_offset   device int32 [B] or NULL (zero), as in fa_mask_rule
+ *   q_out, k_out, v_out   device bf16 [B, Hq, N, d], [B, Hkv, N, d], [B, Hkv, N, d], contiguous, 16-byte aligned;
+ *              they overlap no input
+ * Supported: d in {64, 128}; Hq % Hkv == 0; B * N <= 2^31 - 1. Returns FA_ERR_INVALID_ARG (no rows at all, rows without
+ * their output, alignment, strides, eps), FA_ERR_SHAPE (sizes), FA_ERR_UNSUPPORTED (d, rot_dim). */
+FA_API fa_status fa_qk_norm_rope(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_qk_rule* rule,
+                                 const int32_t* q_offset, void* q_out, void* k_out, void* v_out, int32_t B, int32_t Hq,
+                                 int32_t Hkv, int32_t N, int32_t d, fa_stream_t stream);
+
+/* Its gradient: from the gradients of q_out, k_out, v_out (fp32, as fa_flex_backward writes them) to those of the rows
+ * and of the norm weights. With g the gradient rotated back, r = rsqrt(mean(x^2) + eps) and xhat = x r:
+ *   d weight = sum over rows of g xhat,   d x = r (w g - xhat mean(w g xhat))       (weight NULL: d x = g)
+ *   q, k         the forward's rows (read only for rows with a norm; may be NULL otherwise)
+ *   dq, dk, dv   device fp32 [B, Hq, N, d], [B, Hkv, N, d], [B, Hkv, N, d] or NULL: that gradient is left out
+ *   dq_in, dk_in, dv_in   host pointers to fa_rows for the results, of type grad_dtype (fa_out_dtype; strides multiples
+ *                of 8 elements); required where the gradient is given; they overlap no input
+ *   dq_weight, dk_weight  device fp32 [d]: overwritten; required where the rule has the weight and the gradient is given
+ *   workspace    device, >= fa_qk_norm_rope_backward_workspace_bytes(B, N, d) bytes, 16-byte aligned (may be NULL where
+ *                the rule has no weights). The weights' sums run in a fixed order: the same result each time.
+ * Errors as fa_qk_norm_rope, and FA_ERR_BUFFER_TOO_SMALL. */
+FA_API size_t fa_qk_norm_rope_backward_workspace_bytes(int32_t B, int32_t N, int32_t d);
+FA_API fa_status fa_qk_norm_rope_backward(const fa_rows* q, const fa_rows* k, const float* dq, const float* dk,
+                                          const float* dv, const fa_qk_rule* rule, const int32_t* q_offset,
+                                          const fa_rows* dq_in, const fa_rows* dk_in, const fa_rows* dv_in,
+                                          int32_t grad_dtype, float* dq_weight, float* dk_weight, int32_t B, int32_t Hq,
+                                          int32_t Hkv, int32_t N, int32_t d, void* workspace, size_t workspace_bytes,
+                                          fa_stream_t stream);
+
+/* Append to a paged cache: the same rows, with K and V going to slot p % page of page page_table[b][p / page] and the
+ * queries head-major. Request b appends its first n_new[b] tokens at positions q_offset[b] ..; q_out rows, pages and
+ * slots of other tokens stay as they are.
+ *   q            [B, N, Hq, d] or NULL;  q_out  device bf16 [B, Hq, N, d] (for N = 1 the [Bz, Hq, d] of fa_flex_decode)
+ *   k, v         [B, N, Hkv, d], both required
+ *   rule         host pointer or NULL (rows are moved as they are)
+ *   q_offset     device int32 [B] or NULL;  n_new  device int32 [B], 0 .. N, or NULL (N)
+ *   k_pages, v_pages  device bf16 [n_pages_total, Hkv, page, d], 16-byte aligned
+ *   page_table   device int32 [B, max_pages]; a slot that is written belongs to one request only
+ *   dev_status   a token whose position lies outside [0, max_pages * page) or whose page id lies outside
+ *                [0, n_pages_total) is left out and sets FA_ERR_DEVICE_CHECK; an n_new outside 0 .. N is clamped and sets it
+ * Supported: d in {64, 128}; page in {16, 32, 64, 128}; Hq % Hkv == 0. Errors as fa_qk_norm_rope. */
+FA_API fa_status fa_kv_append(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_qk_rule* rule,
+                              const int32_t* q_offset, const int32_t* n_new, void* q_out, void* k_pages, void* v_pages,
+                              const int32_t* page_table, int32_t n_pages_total, int32_t page, int32_t max_pages, int32_t B,
+                              int32_t Hq, int32_t Hkv, int32_t N, int32_t d, int32_t* dev_status, fa_stream_t stream);
+
+/* The same into an 8-bit cache: e4m3 values with one fp32 scale for each block of FA_KV_SCALE_TOKENS tokens of a page
+ * and KV head; the cached value is scale * e4m3. The scale of a block is the smallest power of two s with
+ * max|value| <= 448 s, within [2^-40, 2^40]; values are rounded to nearest even and saturate at 448. A token that
+ * continues a block keeps the block's earlier tokens: the scale becomes the larger of theirs and its own, and where it
+ * grows their bytes are rescaled (exact in e4m3 except where a value becomes subnormal, since the factor is a power of
+ * two). A block's first slot starts it afresh, so tokens are appended in order, and a sequence may be cut back and
+ * continued.
+ *   k_pages, v_pages  device e4m3 [n_pages_total, Hkv, page, d];  k_scale, v_scale  device fp32
+ *                     [n_pages_total, Hkv, page / FA_KV_SCALE_TOKENS];  page in {32, 64, 128}
+ *   a block that is written belongs to one request only; other arguments and errors as fa_kv_append. */
+#define FA_KV_SCALE_TOKENS 32
+FA_API fa_status fa_kv_append_fp8(const fa_rows* q, const fa_rows* k, const fa_rows* v, const fa_qk_rule* rule,
+                                  const int32_t* q_offset, const int32_t* n_new, void* q_out, void* k_pages,
+                                  void* v_pages, float* k_scale, float* v_scale, const int32_t* page_table,
+                                  int32_t n_pages_total, int32_t page, int32_t max_pages, int32_t B, int32_t Hq,
+                                  int32_t Hkv, int32_t N, int32_t d, int32_t* dev_status, fa_stream_t stream);
+
+/* fa_flex_decode over an 8-bit cache (layouts of fa_kv_append_fp8; scales are positive, not only powers of two, and read
+ * as clamped to [2^-40, 2^40]). Slots that the mask rule hides may hold anything. workspace: >=
+ * fa_decode_fp8_workspace_bytes(...) bytes, 16-byte aligned. Other arguments, limits and errors as fa_flex_decode. */
+FA_API size_t fa_decode_fp8_workspace_bytes(int32_t Bz, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_pages, int32_t page);
+FA_API fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                                    const float* v_scale, const int32_t* page_table, int32_t n_pages_total,
+                                    const fa_block_mask* block_mask, const fa_score_rule* score_rule, float scale, void* out,
+                                    int32_t out_dtype, float* lse, int32_t Bz, int32_t Hq, int32_t Hkv, int32_t d,
+                                    int32_t page, int32_t max_pages, void* workspace, size_t workspace_bytes,
+                                    int32_t* dev_status, int64_t* dev_counters, fa_stream_t stream);
+
+/* fa_flex_forward_paged over an 8-bit cache, for chunks of queries: the key blocks that the mask lists are expanded to
+ * bf16 in the workspace (exact for power-of-two scales, else rounded) and the forward runs on them. The page size is
+ * independent of the mask's Bk: page in {32, 64, 128}, max_pages * page >= KV_LEN, 16-byte aligned pages. Pages of a
+ * listed block that hold a position some causal or prefix term lets the batch row see are looked up; positions behind
+ * those may hold anything.
+ *   chunk_blocks   with Bq == Bk == 128, cut long rows into chunks of that many key blocks (fa_flex_forward_split); 0: the
+ *                  library chooses, cutting only where the uncut rows would leave SMs idle; -1: never cut
+ *   workspace      device, >= fa_forward_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned
+ * A bad id among the looked-up pages sets FA_ERR_DEVICE_CHECK (zeros are read in its place). Other arguments and errors
+ * as fa_flex_forward_paged; block_mask needs its query-side transpose. */
+FA_API size_t fa_forward_paged_fp8_workspace_bytes(const fa_block_mask* block_mask, int32_t B, int32_t Hq, int32_t Hkv,
+                                                   int32_t d, int32_t chunk_blocks);
+FA_API fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
+                                           const float* v_scale, const int32_t* page_table, int32_t n_pages_total,
+                                           int32_t page, int32_t max_pages, const fa_block_mask* block_mask,
+                                           const fa_score_rule* score_rule, float scale, void* out, int32_t out_dtype,
+                                           float* lse, int32_t B, int32_t Hq, int32_t Hkv, int32_t Q_LEN, int32_t KV_LEN,
+                                           int32_t d, int32_t chunk_blocks, void* workspace, size_t workspace_bytes,
+                                           int32_t* dev_status, fa_stream_t stream);
+
 /* Block statistics of a BlockMask ("5.1.2 FlexAttention ...", sections 2.2 and 6.3: full/partial/empty
  * counts and row lengths). dev_out: device int64[6] = {full, partial, empty, max row length (full +
  * partial), sum of row lengths, rows}. Enqueued on stream, no synchronisation. */
