@@ -8,9 +8,16 @@
 // around exactly where whole turns do, and the top 32 bits go to sincospif. The error is under 2^-24 turns at any
 // position (an fp32 product would be off by position * 2^-24).
 //
-// Bound: HBM. A row of d values is held by d / 8 lanes, 8 values (16 bytes) a lane: the norm is a few shuffles, and
-// the other element of a pair is either in the same lane (neighbouring pairs) or in the same place of one other lane
-// (halves: rot is a multiple of 16). cos and sin are computed once a token and shared by all of its heads.
+// Bound: HBM, if the instructions are few: with a thread block to a few tokens and the pair's other element fetched by
+// shuffles, a step of two rows took 265 instructions and the issue slots were 72 % busy at 37 % of the DRAM rate. So:
+//  - a warp takes a token (or, where tokens are few, a share of its heads) and walks its heads, 32 / (d / 8) rows a step:
+//    what depends on the token alone is computed once for all of them, the norm's weight is folded into cos and sin;
+//  - a lane of a row holds 8 elements as two groups of 4, placed so that both elements of each pair are its own;
+//  - arithmetic is on packed pairs of fp32;
+//  - loads run ahead through a ring of asynchronous copies in shared memory that only the thread itself reads and
+//    writes: many rows in flight without registers to hold them, and no barrier.
+#include <algorithm>
+
 #include "fa_launch.h"
 #include "fp8.cuh"
 
@@ -19,9 +26,7 @@ namespace {
 
 typedef __nv_bfloat16 bf16;
 
-constexpr int kThreads = 256;
-constexpr int kTok = 4;          // tokens of a CTA of the row kernels
-constexpr int kBatch = 4;        // rows a thread loads before it uses the first
+constexpr int kSms = 152;
 
 // Fraction of a turn per position, in units of 2^-64 (modulo one turn): inv_freq = m 2^(x-23) times
 // floor(2^64 / 2 pi).
@@ -48,68 +53,139 @@ __device__ __forceinline__ float2 cos_sin(uint64_t f, int64_t pos) {
   return make_float2(c, s);
 }
 
-// What a lane of a row does for the rotation: element e of the lane's 8 becomes y_e c[e] + p_e s[e], with p_e the
-// other element of the pair (s carries the sign).
-struct LaneRot {
-  int partner;      // lane of the row that holds the other elements (halves)
-  int i0;           // first pair index of the lane
-  float sign;       // halves: -1 in the first half, +1 in the second; 0: not rotated
-  bool inter;
+// Which elements of a row a lane holds: groups of four at ea and eb. Halves: (ea + k, eb + k) is pair i0 + k; neighbours:
+// the 8 elements from ea on are pairs i0 .. i0 + 3. Lanes behind the rotated part hold 8 neighbouring elements.
+struct LaneMap {
+  int ea, eb, i0;
+  bool rot, inter;
 };
 
 template <int D>
-__device__ __forceinline__ LaneRot lane_rot(int lane, int rot, int interleaved) {
-  LaneRot r;
-  const int e0 = lane * 8, half = rot / 2;
-  r.inter = interleaved != 0;
-  r.partner = lane;
-  r.i0 = 0;
-  r.sign = 0.f;
-  if (e0 < rot) {
-    if (r.inter) {
-      r.sign = 1.f;
-      r.i0 = e0 / 2;
-    } else {
-      const bool first = e0 < half;
-      r.sign = first ? -1.f : 1.f;
-      r.i0 = first ? e0 : e0 - half;
-      r.partner = first ? lane + half / 8 : lane - half / 8;
-    }
+__device__ __forceinline__ LaneMap lane_map(int lane, int rot, int interleaved) {
+  LaneMap m;
+  const int half = rot / 2;
+  m.inter = interleaved != 0;
+  if (!m.inter && lane * 4 < half) {
+    m.ea = lane * 4;
+    m.eb = half + lane * 4;
+    m.i0 = lane * 4;
+    m.rot = true;
+  } else {
+    m.ea = m.inter ? lane * 8 : rot + (lane - half / 4) * 8;
+    m.eb = m.ea + 4;
+    m.i0 = lane * 4;
+    m.rot = m.inter && lane * 8 < rot;
+  }
+  return m;
+}
+
+// A lane's 8 elements as fp32 pairs: a = the first elements of its four pairs, b = the second ones.
+struct Eight {
+  uint64_t a[2], b[2];
+};
+
+__device__ __forceinline__ uint64_t widen(uint32_t w) {
+  return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+__device__ __forceinline__ Eight unpack(const uint2& va, const uint2& vb, bool inter) {
+  Eight r;
+  if (inter) {
+    r.a[0] = f2_pack(__uint_as_float(va.x << 16), __uint_as_float(va.y << 16));
+    r.a[1] = f2_pack(__uint_as_float(vb.x << 16), __uint_as_float(vb.y << 16));
+    r.b[0] = f2_pack(__uint_as_float(va.x & 0xFFFF0000u), __uint_as_float(va.y & 0xFFFF0000u));
+    r.b[1] = f2_pack(__uint_as_float(vb.x & 0xFFFF0000u), __uint_as_float(vb.y & 0xFFFF0000u));
+  } else {
+    r.a[0] = widen(va.x);
+    r.a[1] = widen(va.y);
+    r.b[0] = widen(vb.x);
+    r.b[1] = widen(vb.y);
   }
   return r;
 }
 
-// c[e], s[e] of the lane from a token's table (inverse: the transposed rotation)
-template <bool INVERSE>
-__device__ __forceinline__ void lane_cos_sin(const float2* table, const LaneRot& r, float (&c)[8], float (&s)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    c[e] = 1.f;
-    s[e] = 0.f;
+// fp32 values at ea .. ea + 3 and eb .. eb + 3
+__device__ __forceinline__ Eight unpack_f32(const float4& va, const float4& vb, bool inter) {
+  Eight r;
+  if (inter) {
+    r.a[0] = f2_pack(va.x, va.z);
+    r.a[1] = f2_pack(vb.x, vb.z);
+    r.b[0] = f2_pack(va.y, va.w);
+    r.b[1] = f2_pack(vb.y, vb.w);
+  } else {
+    r.a[0] = f2_pack(va.x, va.y);
+    r.a[1] = f2_pack(va.z, va.w);
+    r.b[0] = f2_pack(vb.x, vb.y);
+    r.b[1] = f2_pack(vb.z, vb.w);
   }
-  if (r.sign == 0.f) return;
+  return r;
+}
+
+// the values in the order of their elements: ea .. ea + 3, eb .. eb + 3
+__device__ __forceinline__ void in_order(const Eight& v, bool inter, float (&y)[8]) {
+  float a[4], b[4];
+  f2_unpack(v.a[0], a[0], a[1]);
+  f2_unpack(v.a[1], a[2], a[3]);
+  f2_unpack(v.b[0], b[0], b[1]);
+  f2_unpack(v.b[1], b[2], b[3]);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float2 t = table[r.inter ? r.i0 + e / 2 : r.i0 + e];
-    c[e] = t.x;
-    const float g = r.inter ? ((e & 1) ? 1.f : -1.f) : r.sign;
-    s[e] = INVERSE ? -g * t.y : g * t.y;
+  for (int k = 0; k < 4; ++k) {
+    y[k] = inter ? ((k & 1) ? b[k >> 1] : a[k >> 1]) : a[k];
+    y[4 + k] = inter ? ((k & 1) ? b[2 + (k >> 1)] : a[2 + (k >> 1)]) : b[k];
   }
 }
 
-// Every lane of the warp calls this (rows that are not there compute on zeros).
-template <int LPR>
-__device__ __forceinline__ void rotate(float (&y)[8], const LaneRot& r, const float (&c)[8], const float (&s)[8]) {
-  float p[8];
-  if (r.inter) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = y[e ^ 1];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xFFFFFFFFu, y[e], r.partner, LPR);
+__device__ __forceinline__ Eight load_weight(const float* w, const LaneMap& m) {
+  float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
+  if (w) {
+    a = make_float4(__ldg(w + m.ea), __ldg(w + m.ea + 1), __ldg(w + m.ea + 2), __ldg(w + m.ea + 3));
+    b = make_float4(__ldg(w + m.eb), __ldg(w + m.eb + 1), __ldg(w + m.eb + 2), __ldg(w + m.eb + 3));
   }
+  return unpack_f32(a, b, m.inter);
+}
+
+// cos and sin of the lane's four pairs at a position
+struct Turn {
+  uint64_t c[2], s[2];
+};
+
+__device__ __forceinline__ Turn turn_at(const uint64_t (&f)[4], const LaneMap& m, int64_t pos) {
+  Turn t;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = fmaf(p[e], s[e], y[e] * c[e]);
+  for (int j = 0; j < 2; ++j) {
+    float2 u = make_float2(1.f, 0.f), v = u;
+    if (m.rot) {
+      u = cos_sin(f[2 * j], pos);
+      v = cos_sin(f[2 * j + 1], pos);
+    }
+    t.c[j] = f2_pack(u.x, v.x);
+    t.s[j] = f2_pack(u.y, v.y);
+  }
+  return t;
+}
+
+__device__ __forceinline__ void lane_frequencies(const float* inv_freq, const LaneMap& m, uint64_t (&f)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[k] = m.rot ? turns_per_position(__ldg(inv_freq + m.i0 + k)) : 0ull;
+}
+
+// norm and rotation with the weight folded in: z_a = r (x_a aa + x_b ab), z_b = r (x_a ba + x_b bb)
+struct Map2 {
+  uint64_t aa[2], ab[2], ba[2], bb[2];
+};
+
+__device__ __forceinline__ uint64_t f2_neg(uint64_t v) { return v ^ 0x8000000080000000ull; }
+
+__device__ __forceinline__ Map2 fold(const Turn& t, const Eight& w) {
+  Map2 m;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    m.aa[j] = f2_mul(w.a[j], t.c[j]);
+    m.ab[j] = f2_neg(f2_mul(w.b[j], t.s[j]));
+    m.ba[j] = f2_mul(w.a[j], t.s[j]);
+    m.bb[j] = f2_mul(w.b[j], t.c[j]);
+  }
+  return m;
 }
 
 template <int LPR>
@@ -125,39 +201,77 @@ __device__ __forceinline__ float row_max(float v) {
   return v;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(u[i] << 16);
-    x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ float add_up(const Eight& p) {  // sum of the 8 values
+  float x, y;
+  f2_unpack(f2_add(f2_add(p.a[0], p.a[1]), f2_add(p.b[0], p.b[1])), x, y);
+  return x + y;
 }
 
-__device__ __forceinline__ void load_w(const float* w, int e0, float (&r)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = w ? __ldg(w + e0 + e) : 1.f;
+// r of a row; every lane of the warp calls it
+template <int D>
+__device__ __forceinline__ float row_rsqrt(const Eight& x, float eps) {
+  const uint64_t q = f2_fma(x.b[1], x.b[1], f2_fma(x.b[0], x.b[0], f2_fma(x.a[1], x.a[1], f2_mul(x.a[0], x.a[0]))));
+  float u, v;
+  f2_unpack(q, u, v);
+  return rsqrtf(fmaf(row_sum<D / 8>(u + v), 1.f / D, eps));
 }
 
 template <int D>
-__device__ __forceinline__ void norm_rope(float (&x)[8], bool norm, float eps, const float (&w)[8], bool rope,
-                                          const LaneRot& r, const float (&c)[8], const float (&s)[8]) {
-  if (norm) {
-    float q = 0.f;
+__device__ __forceinline__ Eight norm_rope(const Eight& x, bool norm, float eps, const Map2& m, bool rot) {
+  Eight z;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q = fmaf(x[e], x[e], q);
-    q = row_sum<D / 8>(q);
-    const float rs = rsqrtf(q * (1.f / D) + eps);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = x[e] * rs * w[e];
+  for (int j = 0; j < 2; ++j) {
+    z.a[j] = f2_mul(x.a[j], m.aa[j]);
+    z.b[j] = f2_mul(x.b[j], m.bb[j]);
+    if (rot) {  // elsewhere an infinity must not meet its neighbour through a factor of zero
+      z.a[j] = f2_fma(x.b[j], m.ab[j], z.a[j]);
+      z.b[j] = f2_fma(x.a[j], m.ba[j], z.b[j]);
+    }
   }
-  if (rope) rotate<D / 8>(x, r, c, s);
+  if (norm) {
+    const float r = row_rsqrt<D>(x, eps);
+    const uint64_t rr = f2_pack(r, r);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      z.a[j] = f2_mul(z.a[j], rr);
+      z.b[j] = f2_mul(z.b[j], rr);
+    }
+  }
+  return z;
 }
 
-// e4m3 block of one head: rows old tokens keep their place; from scale `was` to scale `now`
+__device__ __forceinline__ void store_bf16(bf16* row, const LaneMap& m, const Eight& z) {
+  float y[8];
+  in_order(z, m.inter, y);
+  *reinterpret_cast<uint2*>(row + m.ea) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+  *reinterpret_cast<uint2*>(row + m.eb) = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+}
+
+__device__ __forceinline__ void store_e4m3(uint8_t* row, const LaneMap& m, const Eight& z, float inv) {
+  float y[8];
+  in_order(z, m.inter, y);
+  *reinterpret_cast<uint32_t*>(row + m.ea) = pack_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+  *reinterpret_cast<uint32_t*>(row + m.eb) = pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+}
+
+__device__ __forceinline__ float largest(const Eight& z) {  // NaN is passed over
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float u, v;
+    f2_unpack(z.a[j], u, v);
+    m = fmaxf(m, fmaxf(fabsf(u), fabsf(v)));
+    f2_unpack(z.b[j], u, v);
+    m = fmaxf(m, fmaxf(fabsf(u), fabsf(v)));
+  }
+  return m;
+}
+
+__device__ __forceinline__ void cp_async_8(uint32_t saddr, const void* g) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(saddr), "l"(g) : "memory");
+}
+
+// e4m3 block of one head: a row that the block held before goes from one scale to another (ratio of the two)
 template <int D>
 __device__ __forceinline__ void rescale_row(uint8_t* row, int e0, float ratio) {
   uint2* p = reinterpret_cast<uint2*>(row + e0);
@@ -174,15 +288,7 @@ __device__ __forceinline__ void rescale_row(uint8_t* row, int e0, float ratio) {
   *p = o;
 }
 
-__device__ __forceinline__ uint2 quantise8(const float (&y)[8], float inv) {
-  return make_uint2(pack_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
-                    pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-}
 
-// ------------------------------------------------------------------------------------------------
-// Rows of tokens [first, first + kTok) of the call (token = b * N + n), heads [h0, h1) of the row of heads
-// (query heads, then key heads, then value heads, absent ones left out).
-// ------------------------------------------------------------------------------------------------
 enum { kToHeads = 0, kToPages = 1, kToPagesFp8 = 2 };
 
 __device__ __forceinline__ int new_tokens(const QkvArgs& a, int b) {
@@ -195,375 +301,476 @@ __device__ __forceinline__ int new_tokens(const QkvArgs& a, int b) {
   return n;
 }
 
-// slot of position pos of request b: page id * page + place, or -1 (reported)
-__device__ __forceinline__ int64_t page_slot(const QkvArgs& a, int b, int64_t pos) {
-  int64_t at = -1;
-  if (pos >= 0 && pos < (int64_t)a.max_pages * a.page) {
-    const int c = (int)(pos / a.page);
+// where position pos of request b lives; pid -1: nowhere (reported)
+struct Place {
+  int pid, slot;
+};
+__device__ __forceinline__ Place place_of(const QkvArgs& a, int b, int64_t pos) {
+  Place r{-1, 0};
+  if (pos >= 0 && pos < (int64_t)a.max_pages * a.page) {  // pos < 2^31 + N: 32 bits without a sign
+    const uint32_t c = (uint32_t)pos / (uint32_t)a.page;
     const int pid = __ldg(a.page_table + (int64_t)b * a.max_pages + c);
-    if (pid >= 0 && pid < a.n_pages_total) at = (int64_t)pid * a.page + (pos - (int64_t)c * a.page);
+    if (pid >= 0 && pid < a.n_pages_total) r.pid = pid;
+    r.slot = (int)((uint32_t)pos - c * (uint32_t)a.page);
   }
-  if (at < 0) report(a.status, FA_ERR_DEVICE_CHECK);
-  return at;
-}
-
-template <int D, int DST>
-__device__ __forceinline__ void rows_of_tokens(const QkvArgs& a, int64_t first, int h0, int h1, int nq, int nk,
-                                               float2 (*s_cs)[D / 2]) {
-  constexpr int LPR = D / 8, SLOTS = kThreads / LPR;
-  const int tid = threadIdx.x, lane = tid % LPR, slot = tid / LPR, e0 = lane * 8;
-  const int64_t tokens = (int64_t)a.B * a.N;
-  const bool rope = a.inv_freq != nullptr && h0 < nq + nk;
-  const int half = a.rot / 2;
-  if (rope) {
-    for (int x = tid; x < kTok * half; x += kThreads) {
-      const int t = x / half, i = x - t * half;
-      const int64_t T = first + t;
-      if (T < tokens) {
-        const int b = (int)(T / a.N), n = (int)(T - (int64_t)b * a.N);
-        s_cs[t][i] = cos_sin(turns_per_position(__ldg(a.inv_freq + i)), (int64_t)n + (a.q_offset ? __ldg(a.q_offset + b) : 0));
-      }
-    }
-    __syncthreads();
-  }
-  const LaneRot lr = lane_rot<D>(lane, a.inv_freq ? a.rot : 0, a.interleaved);
-  float wq[8], wk[8];
-  load_w(a.wq, e0, wq);
-  load_w(a.wk, e0, wk);
-  for (int t = 0; t < kTok; ++t) {
-    const int64_t T = first + t;
-    if (T >= tokens) break;
-    const int b = (int)(T / a.N), n = (int)(T - (int64_t)b * a.N);
-    if (DST != kToHeads && n >= new_tokens(a, b)) continue;
-    const int64_t pos = (int64_t)n + (a.q_offset ? __ldg(a.q_offset + b) : 0);
-    const int64_t at = DST != kToHeads && h1 > nq ? page_slot(a, b, pos) : 0;
-    float c[8], s[8];
-    if (rope) lane_cos_sin<false>(s_cs[t], lr, c, s);
-    // every warp takes the same number of steps: the shuffles want all lanes
-    for (int hb = h0; hb < h1; hb += SLOTS * kBatch) {
-      uint4 raw[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int h = hb + u * SLOTS + slot;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (h < h1) {
-          const bool isq = h < nq, isk = !isq && h < nq + nk;
-          const Rows& R = isq ? a.q : isk ? a.k : a.v;
-          const int hh = isq ? h : isk ? h - nq : h - nq - nk;
-          raw[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(R.p) + b * R.sb + n * R.sn + hh * R.sh + e0));
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        if (hb + u * SLOTS >= h1) break;  // the same for all threads
-        const int h = hb + u * SLOTS + slot;
-        const bool live = h < h1, isq = h < nq, isk = !isq && h < nq + nk, isv = !isq && !isk;
-        const int hh = isq ? h : isk ? h - nq : h - nq - nk;
-        float y[8];
-        unpack8(raw[u], y);
-        const bool any_qk = __any_sync(0xFFFFFFFFu, live && !isv);
-        if (any_qk) {
-          float z[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) z[e] = y[e];
-          const bool norm_row = isq ? a.wq != nullptr : a.wk != nullptr;
-          if (a.wq || a.wk) {
-            float q2 = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q2 = fmaf(z[e], z[e], q2);
-            q2 = row_sum<LPR>(q2);
-            if (norm_row) {
-              const float rs = rsqrtf(q2 * (1.f / D) + a.eps);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) z[e] = z[e] * rs * (isq ? wq[e] : wk[e]);
-            }
-          }
-          if (rope) rotate<LPR>(z, lr, c, s);
-          if (!isv) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = z[e];
-          }
-        }
-        if (DST == kToPagesFp8) {
-          // one new token a request: its 32-token block holds the tokens before it under the scale they have, which
-          // one lane reads and writes
-          float m = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
-          m = row_max<LPR>(m);
-          const bool mine = live && !isq && at >= 0;
-          const int64_t pid = mine ? at / a.page : 0, place = mine ? at - pid * a.page : 0;
-          const int before = (int)(place % kScaleTokens);
-          float* sc = (isk ? a.k_scale : a.v_scale) + (pid * a.Hkv + hh) * (a.page / kScaleTokens) + place / kScaleTokens;
-          float was = 0.f;
-          if (mine && before && lane == 0) was = clamp_scale(*sc);
-          was = __shfl_sync(0xFFFFFFFFu, was, 0, LPR);
-          if (mine) {
-            uint8_t* base = static_cast<uint8_t*>(isk ? a.k_pages : a.v_pages) + (pid * a.Hkv + hh) * a.page * D;
-            const float now = fmaxf(need_scale(m), was);
-            if (before && now != was)
-              for (int64_t i = place - before; i < place; ++i) rescale_row<D>(base + i * D, e0, was / now);
-            *reinterpret_cast<uint2*>(base + place * D + e0) = quantise8(y, 1.f / now);
-            if (lane == 0) *sc = now;
-          }
-        }
-        if (live && (DST != kToPagesFp8 || isq)) {
-          bf16* dst;
-          if (DST == kToHeads || isq) {
-            bf16* o = static_cast<bf16*>(isq ? a.q_out : isk ? a.k_out : a.v_out);
-            dst = o + (((int64_t)b * (isq ? a.Hq : a.Hkv) + hh) * a.N + n) * D;
-          } else {
-            const int64_t pid = at / a.page;
-            dst = at < 0 ? nullptr
-                         : static_cast<bf16*>(isk ? a.k_pages : a.v_pages) + ((pid * a.Hkv + hh) * a.page + (at - pid * a.page)) * D;
-          }
-          if (dst) *reinterpret_cast<uint4*>(dst + e0) = isv ? raw[u] : pack8(y);
-        }
-      }
-    }
-  }
-}
-
-template <int D, int DST>
-__global__ void __launch_bounds__(kThreads) qkv_rows_kernel(const __grid_constant__ QkvArgs a, int heads_per_cta) {
-  __shared__ float2 s_cs[kTok][D / 2];
-  const int nq = a.q.p ? a.Hq : 0, nk = a.k.p ? a.Hkv : 0, nv = a.v.p ? a.Hkv : 0;
-  const int h0 = blockIdx.y * heads_per_cta, h1 = min(nq + nk + nv, h0 + heads_per_cta);
-  rows_of_tokens<D, DST>(a, (int64_t)blockIdx.x * kTok, h0, h1, nq, nk, s_cs);
+  if (r.pid < 0) report(a.status, FA_ERR_DEVICE_CHECK);
+  return r;
 }
 
 // ------------------------------------------------------------------------------------------------
-// Append to e4m3 pages, several tokens a request. A CTA takes one 32-token block of one request and a group of its
+// Rows. An item is one token (b, n) and one of `groups` shares of its heads: shares of the query heads, then of the key
+// heads, then of the value heads. The warps of the grid deal the items out in turn, so that neighbouring warps hold
+// neighbouring tokens, which lie side by side in the head-major tensors.
+// ------------------------------------------------------------------------------------------------
+struct Shares {
+  int groups, q, k;     // heads of a share
+};
+
+// The order of an item's steps: one kind's heads after the other's, R rows a step.
+struct Cursor {
+  int64_t item;
+  int b, n, kind, h, hend;   // h: the step's first head
+};
+
+template <int R, class Sizes>
+__device__ __forceinline__ bool next_kind(Cursor& c, int64_t items, int64_t step, int N, const Shares& sh, const Sizes& heads) {
+  for (;;) {  // the next kind, or the next item, that has heads in this share
+    if (++c.kind == 3) {
+      c.kind = 0;
+      c.item += step;
+    }
+    if (c.item >= items) return false;
+    const int64_t T = c.item / sh.groups;
+    const int g = (int)(c.item - T * sh.groups);
+    if (c.kind == 0) {
+      c.b = (int)(T / N);
+      c.n = (int)(T - (int64_t)c.b * N);
+    }
+    const int per = c.kind == 0 ? sh.q : sh.k;
+    c.h = g * per;
+    c.hend = min(heads(c.kind), c.h + per);
+    if (c.h < c.hend) return true;
+  }
+}
+
+constexpr int kRing = 8;         // rows in flight a lane
+constexpr int kRowThreads = 128;
+
+template <int D, int DST, int THREADS>
+__device__ __forceinline__ void rows_of_items(const QkvArgs& a, int64_t warp, int64_t warps, const Shares& sh, uint2* ring) {
+  constexpr int LPR = D / 8, R = 32 / LPR;
+  const int tid = threadIdx.x, lane = tid % LPR, row = (tid % 32) / LPR;
+  const int64_t items = (int64_t)a.B * a.N * sh.groups;
+  const bool append_rows = DST != kToHeads;
+  auto heads = [&](int kind) { return kind == 0 ? (a.q.p ? a.Hq : 0) : kind == 1 ? (a.k.p ? a.Hkv : 0) : (a.v.p ? a.Hkv : 0); };
+  const LaneMap lm = lane_map<D>(lane, a.inv_freq ? a.rot : 0, a.inv_freq ? a.interleaved : 0);
+  // ---- loads, kRing steps ahead
+  Cursor ld{warp, 0, 0, -1, 0, 0};
+  const bf16* src = nullptr;
+  int64_t hop = 0;
+  bool more = true;
+  int slot_in = 0;
+  const uint32_t my = smem_u32(ring + tid);
+  auto load = [&]() {
+    if (more) {
+      if (ld.h >= ld.hend) {
+        more = next_kind<R>(ld, items, warps, a.N, sh, heads);
+        if (more) {
+          const Rows& S = ld.kind == 0 ? a.q : ld.kind == 1 ? a.k : a.v;
+          src = static_cast<const bf16*>(S.p) + ld.b * S.sb + ld.n * S.sn + (ld.h + row) * S.sh;
+          hop = R * S.sh;
+        }
+      }
+      if (more) {
+        if (ld.h + row < ld.hend) {
+          cp_async_8(my + slot_in * (2 * THREADS * 8), src + lm.ea);
+          cp_async_8(my + slot_in * (2 * THREADS * 8) + THREADS * 8, src + lm.eb);
+        }
+        src += hop;
+        ld.h += R;
+      }
+    }
+    slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kRing; ++i) load();
+  // ---- work
+  uint64_t f[4] = {0, 0, 0, 0};
+  if (a.inv_freq) lane_frequencies(a.inv_freq, lm, f);
+  Cursor at{warp, 0, 0, -1, 0, 0};
+  int slot_out = 0;
+  Turn turn;
+  Place place{-1, 0};
+  bool take = true;
+  int64_t item_of_turn = -1;
+  while (next_kind<R>(at, items, warps, a.N, sh, heads)) {
+    const bool isq = at.kind == 0, isv = at.kind == 2;
+    const int H = isq ? a.Hq : a.Hkv;
+    if (item_of_turn != at.item) {
+      item_of_turn = at.item;
+      const int64_t pos = (int64_t)at.n + (a.q_offset ? __ldg(a.q_offset + at.b) : 0);
+      turn = turn_at(f, lm, pos);
+      if (append_rows) {
+        take = at.n < new_tokens(a, at.b);
+        if (take && (a.k.p || a.v.p)) place = place_of(a, at.b, pos);
+      }
+    }
+    const float* w = isq ? a.wq : isv ? nullptr : a.wk;
+    Map2 m;
+    if (!isv) m = fold(turn, load_weight(w, lm));
+    bf16* dst = nullptr;           // rows of head h at dst + h * dst_hop
+    int64_t dst_hop = 0;
+    if (isq || !append_rows) {
+      bf16* o = static_cast<bf16*>(isq ? a.q_out : isv ? a.v_out : a.k_out);
+      dst_hop = (int64_t)a.N * D;
+      dst = o + ((int64_t)at.b * H * a.N + at.n) * D;
+    } else if (DST == kToPages && place.pid >= 0) {
+      dst_hop = (int64_t)a.page * D;
+      dst = static_cast<bf16*>(isv ? a.v_pages : a.k_pages) + ((int64_t)place.pid * a.Hkv * a.page + place.slot) * D;
+    }
+    for (; at.h < at.hend; at.h += R) {
+      cp_async_wait<kRing - 1>();
+      const int h = at.h + row;
+      const bool live = h < at.hend && take;
+      const uint2* in = ring + slot_out * (2 * THREADS) + tid;
+      uint2 va = make_uint2(0, 0), vb = va;
+      if (live) {
+        va = in[0];
+        vb = in[THREADS];
+      }
+      slot_out = slot_out + 1 == kRing ? 0 : slot_out + 1;
+      load();
+      if (isv && DST != kToPagesFp8) {  // as it is
+        if (live && dst) {
+          bf16* o = dst + h * dst_hop;
+          *reinterpret_cast<uint2*>(o + lm.ea) = va;
+          *reinterpret_cast<uint2*>(o + lm.eb) = vb;
+        }
+        continue;
+      }
+      const Eight x = unpack(va, vb, lm.inter);
+      Eight z = x;
+      if (!isv) z = norm_rope<D>(x, w != nullptr, a.eps, m, lm.rot);
+      if (DST == kToPagesFp8 && !isq) {
+        // one new token a request: its 32-token block holds the tokens before it under the scale they have, which one
+        // lane reads and writes
+        const float need = need_scale(row_max<LPR>(largest(z)));
+        const bool mine = live && place.pid >= 0;
+        const int before = place.slot % kScaleTokens;
+        const int64_t head = (int64_t)place.pid * a.Hkv + h;
+        float* sc = (isv ? a.v_scale : a.k_scale) + head * (a.page / kScaleTokens) + place.slot / kScaleTokens;
+        float was = 0.f;
+        if (mine && before && lane == 0) was = clamp_scale(*sc);
+        was = __shfl_sync(0xFFFFFFFFu, was, 0, LPR);
+        if (mine) {
+          uint8_t* base = static_cast<uint8_t*>(isv ? a.v_pages : a.k_pages) + head * a.page * D;
+          const float now = fmaxf(need, was);
+          if (before && now != was)
+            for (int r = place.slot - before; r < place.slot; ++r) rescale_row<D>(base + r * D, lane * 8, was / now);
+          store_e4m3(base + place.slot * D, lm, z, 1.f / now);
+          if (lane == 0) *sc = now;
+        }
+      } else if (live && dst) {
+        store_bf16(dst + h * dst_hop, lm, z);
+      }
+    }
+  }
+  cp_async_wait<0>();
+}
+
+template <int D, int DST>
+__global__ void __launch_bounds__(kRowThreads) qkv_rows_kernel(const __grid_constant__ QkvArgs a, const Shares sh) {
+  __shared__ uint2 ring[kRing * 2 * kRowThreads];
+  rows_of_items<D, DST, kRowThreads>(a, (int64_t)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32,
+                                     (int64_t)gridDim.x * (kRowThreads / 32), sh, ring);
+}
+
+// ------------------------------------------------------------------------------------------------
+// Append to e4m3 pages, several tokens a request. A CTA takes one 32-token block of one request and a share of its
 // KV heads: for each head, K and then V, its threads hold the block's new rows, agree on the largest magnitude, and
 // write scale and values; rows that the block held before are rescaled where the scale grew. CTAs behind those take
 // the query rows.
 // ------------------------------------------------------------------------------------------------
+constexpr int kBlockThreads = 256;
+
 template <int D>
-__device__ __forceinline__ void append_block(const QkvArgs& a, int b, int j, int hk0, int hk1, float2 (*s_cs)[D / 2],
-                                             float (*s_max)[kThreads / 32]) {
-  constexpr int LPR = D / 8, SLOTS = kThreads / LPR, RPT = kScaleTokens / SLOTS > 0 ? kScaleTokens / SLOTS : 1;
-  const int tid = threadIdx.x, lane = tid % LPR, slot = tid / LPR, e0 = lane * 8;
+__device__ __forceinline__ void append_block(const QkvArgs& a, int b, int j, int hk0, int hk1, uint2* ring,
+                                             float (*s_max)[kBlockThreads / 32]) {
+  constexpr int LPR = D / 8, SLOTS = kBlockThreads / LPR, RPT = kScaleTokens / SLOTS;
+  const int tid = threadIdx.x, lane = tid % LPR, slot = tid / LPR;
   const int cnt = new_tokens(a, b);
   const int64_t first = a.q_offset ? __ldg(a.q_offset + b) : 0, last = first + cnt;
   const int64_t p0 = ((first >> 5) + j) * kScaleTokens;
   const int64_t lo = max(p0, first), hi = min(p0 + kScaleTokens, last);
   if (lo >= hi) return;
-  const int64_t at0 = page_slot(a, b, p0);
-  if (at0 < 0) return;
-  const int64_t pid = at0 / a.page, place0 = at0 - pid * a.page;
-  const bool rope = a.inv_freq != nullptr;
-  const int half = a.rot / 2;
-  if (rope) {
-    for (int x = tid; x < kScaleTokens * half; x += kThreads) {
-      const int t = x / half, i = x - t * half;
-      s_cs[t][i] = cos_sin(turns_per_position(__ldg(a.inv_freq + i)), p0 + t);
-    }
-  }
-  __syncthreads();
-  const LaneRot lr = lane_rot<D>(lane, rope ? a.rot : 0, a.interleaved);
-  float wk[8];
-  load_w(a.wk, e0, wk);
-  float c[RPT][8], s[RPT][8];
-  if (rope) {
+  const Place at0 = place_of(a, b, p0);
+  if (at0.pid < 0) return;
+  const LaneMap lm = lane_map<D>(lane, a.inv_freq ? a.rot : 0, a.inv_freq ? a.interleaved : 0);
+  const int before = (int)(lo - p0), units = 2 * (hk1 - hk0);  // K and V of each head
+  constexpr int kAhead = kRing / RPT;
+  const uint32_t my = smem_u32(ring + tid);
+  bool in[RPT];
+  int64_t n[RPT];
 #pragma unroll
-    for (int u = 0; u < RPT; ++u) lane_cos_sin<false>(s_cs[slot + u * SLOTS], lr, c[u], s[u]);
+  for (int u = 0; u < RPT; ++u) {
+    const int64_t pos = p0 + slot + u * SLOTS;
+    in[u] = pos >= lo && pos < hi;
+    n[u] = in[u] ? pos - first : 0;
   }
-  const int before = (int)(lo - p0);
-  const int units = 2 * (hk1 - hk0);  // K and V of each head
-  auto load = [&](int x, uint4 (&raw)[RPT]) {
-    const Rows& R = (x & 1) ? a.v : a.k;
-    const bf16* base = static_cast<const bf16*>(R.p) + b * R.sb + (hk0 + (x >> 1)) * R.sh + e0;
+  auto load = [&](int x) {
+    if (x < units) {
+      const Rows& S = (x & 1) ? a.v : a.k;
+      const bf16* base = static_cast<const bf16*>(S.p) + b * S.sb + (hk0 + (x >> 1)) * S.sh;
 #pragma unroll
-    for (int u = 0; u < RPT; ++u) {
-      const int64_t pos = p0 + slot + u * SLOTS;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (pos >= lo && pos < hi) raw[u] = __ldg(reinterpret_cast<const uint4*>(base + (pos - first) * R.sn));
+      for (int u = 0; u < RPT; ++u) {
+        const uint32_t to = my + ((x % kAhead) * RPT + u) * (2 * kBlockThreads * 8);
+        if (in[u]) {
+          cp_async_8(to, base + n[u] * S.sn + lm.ea);
+          cp_async_8(to + kBlockThreads * 8, base + n[u] * S.sn + lm.eb);
+        }
+      }
     }
+    cp_async_commit();
   };
-  uint4 nxt[RPT];
-  load(0, nxt);
+#pragma unroll 1
+  for (int x = 0; x < kAhead; ++x) load(x);
+  Map2 m[RPT];
+  {
+    uint64_t f[4] = {0, 0, 0, 0};
+    if (a.inv_freq) lane_frequencies(a.inv_freq, lm, f);
+    const Eight w = load_weight(a.wk, lm);
+#pragma unroll
+    for (int u = 0; u < RPT; ++u) m[u] = fold(turn_at(f, lm, p0 + slot + u * SLOTS), w);
+  }
   for (int x = 0; x < units; ++x) {
-    float y[RPT][8];
-#pragma unroll
-    for (int u = 0; u < RPT; ++u) unpack8(nxt[u], y[u]);
-    if (x + 1 < units) load(x + 1, nxt);
-    float m = 0.f;
-#pragma unroll
-    for (int u = 0; u < RPT; ++u) {
-      if (!(x & 1)) norm_rope<D>(y[u], a.wk != nullptr, a.eps, wk, rope, lr, c[u], s[u]);
-      const int64_t pos = p0 + slot + u * SLOTS;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = pos >= lo && pos < hi ? fmaxf(m, fabsf(y[u][e])) : m;
-    }
-    m = row_max<32>(m);
-    if ((tid & 31) == 0) s_max[x & 1][tid >> 5] = m;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, s_max[x & 1][w]);
+    cp_async_wait<kAhead - 1>();
     const int hk = hk0 + (x >> 1);
-    float* sc = ((x & 1) ? a.v_scale : a.k_scale) + (pid * a.Hkv + hk) * (a.page / kScaleTokens) + place0 / kScaleTokens;
-    uint8_t* base = static_cast<uint8_t*>((x & 1) ? a.v_pages : a.k_pages) + ((pid * a.Hkv + hk) * a.page + place0) * D;
-    float now = need_scale(m);
-    if (before) {
-      const float was = clamp_scale(*sc);
-      now = fmaxf(now, was);
-      if (now != was)
-        for (int i = slot; i < before; i += SLOTS) rescale_row<D>(base + (int64_t)i * D, e0, was / now);
-      __syncthreads();  // every thread has read the old scale
-    }
-    const float inv = 1.f / now;
+    const int64_t head = (int64_t)at0.pid * a.Hkv + hk;
+    float* sc = ((x & 1) ? a.v_scale : a.k_scale) + head * (a.page / kScaleTokens) + at0.slot / kScaleTokens;
+    float was = 0.f;
+    if (before) was = clamp_scale(*sc);
+    Eight z[RPT];
+    float big = 0.f;
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
-      const int r = slot + u * SLOTS;
-      if (p0 + r >= lo && p0 + r < hi) *reinterpret_cast<uint2*>(base + (int64_t)r * D + e0) = quantise8(y[u], inv);
+      uint2 va = make_uint2(0, 0), vb = va;
+      if (in[u]) {
+        const uint2* r = ring + ((x % kAhead) * RPT + u) * (2 * kBlockThreads) + tid;
+        va = r[0];
+        vb = r[kBlockThreads];
+      }
+      z[u] = unpack(va, vb, lm.inter);
+      if (!(x & 1)) z[u] = norm_rope<D>(z[u], a.wk != nullptr, a.eps, m[u], lm.rot);
+      if (in[u]) big = fmaxf(big, largest(z[u]));  // rows of zeros may be NaN without an eps
     }
+    load(x + kAhead);
+    big = row_max<32>(big);
+    if ((tid & 31) == 0) s_max[x & 1][tid >> 5] = big;
+    __syncthreads();  // the old scale is read, too
+#pragma unroll
+    for (int w = 0; w < kBlockThreads / 32; ++w) big = fmaxf(big, s_max[x & 1][w]);
+    uint8_t* base = static_cast<uint8_t*>((x & 1) ? a.v_pages : a.k_pages) + (head * a.page + at0.slot) * D;
+    const float now = fmaxf(need_scale(big), was), inv = 1.f / now;
+    if (before && now != was)
+      for (int i = slot; i < before; i += SLOTS) rescale_row<D>(base + i * D, lane * 8, was / now);
+#pragma unroll
+    for (int u = 0; u < RPT; ++u)
+      if (in[u]) store_e4m3(base + (slot + u * SLOTS) * D, lm, z[u], inv);
     if (tid == 0) *sc = now;
   }
+  cp_async_wait<0>();
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kBlockThreads)
     append_fp8_kernel(const __grid_constant__ QkvArgs a, int blocks, int heads_per_cta, int groups) {
-  __shared__ float2 s_cs[kScaleTokens][D / 2];
-  __shared__ float s_max[2][kThreads / 32];
+  __shared__ uint2 ring[kRing * 2 * kBlockThreads];
+  __shared__ float s_max[2][kBlockThreads / 32];
   const int64_t kv_ctas = (int64_t)a.B * blocks * groups;
   if ((int64_t)blockIdx.x < kv_ctas) {
     const int x = blockIdx.x, gi = x % groups, bj = x / groups;
     const int hk0 = gi * heads_per_cta;
-    append_block<D>(a, bj / blocks, bj % blocks, hk0, min(a.Hkv, hk0 + heads_per_cta), s_cs, s_max);
+    append_block<D>(a, bj / blocks, bj % blocks, hk0, min(a.Hkv, hk0 + heads_per_cta), ring, s_max);
   } else {
-    rows_of_tokens<D, kToPages>(a, ((int64_t)blockIdx.x - kv_ctas) * kTok, 0, a.Hq, a.Hq, 0, s_cs);
+    QkvArgs q = a;
+    q.k.p = q.v.p = nullptr;
+    rows_of_items<D, kToPages, kBlockThreads>(q, ((int64_t)blockIdx.x - kv_ctas) * (kBlockThreads / 32) + threadIdx.x / 32,
+                                              ((int64_t)gridDim.x - kv_ctas) * (kBlockThreads / 32), Shares{1, a.Hq, a.Hkv}, ring);
   }
 }
 
 // ------------------------------------------------------------------------------------------------
 // Backward of the rows: with g = R^T dz (the transposed rotation) and xhat = x r,
 //   dw += g xhat,   dx = r (w g - xhat mean(w g xhat))     (no weight: dx = g)
-// r is recomputed from x. A CTA walks tokens and keeps its sums of dw in registers (a lane always holds the same 8
-// places); they are joined in shared memory, written one row a CTA, and added up by a second kernel in a fixed order:
-// no atomics, the same result each time.
+// r is recomputed from x. A warp walks items as in the forward and keeps its sums of dw in registers (a lane always
+// holds the same 8 places); they are joined in shared memory, written one row a CTA, and added up by a second kernel in
+// a fixed order: no atomics, the same result each time.
 // ------------------------------------------------------------------------------------------------
-template <int D, bool F32>
-__device__ __forceinline__ void store_grad(void* p, int64_t at, const float (&g)[8]) {
+constexpr int kBwdThreads = 256;
+constexpr int kBwdRing = 6;
+constexpr int kBwdRingBytes = kBwdRing * kBwdThreads * 48;  // a row's 48 bytes a lane: 32 of dz, 16 of x
+
+template <bool F32>
+__device__ __forceinline__ void store_grad(void* p, int64_t at, const LaneMap& m, const Eight& g) {
   if (F32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
-    o[0] = make_float4(g[0], g[1], g[2], g[3]);
-    o[1] = make_float4(g[4], g[5], g[6], g[7]);
+    float y[8];
+    in_order(g, m.inter, y);
+    float* o = static_cast<float*>(p) + at;
+    *reinterpret_cast<float4*>(o + m.ea) = make_float4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<float4*>(o + m.eb) = make_float4(y[4], y[5], y[6], y[7]);
   } else {
-    *reinterpret_cast<uint4*>(static_cast<bf16*>(p) + at) = pack8(g);
+    store_bf16(static_cast<bf16*>(p) + at, m, g);
   }
 }
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(kThreads) qkv_bwd_kernel(const __grid_constant__ QkvBwdArgs a) {
-  constexpr int LPR = D / 8, SLOTS = kThreads / LPR, U = 2;
-  __shared__ float2 s_cs[kTok][D / 2];
-  __shared__ float s_dw[SLOTS][D];
-  const int tid = threadIdx.x, lane = tid % LPR, slot = tid / LPR, e0 = lane * 8;
-  const int nq = a.dq ? a.Hq : 0, nk = a.dk ? a.Hkv : 0, nv = a.dv ? a.Hkv : 0, H = nq + nk + nv;
-  const int64_t tokens = (int64_t)a.B * a.N;
-  const bool rope = a.inv_freq != nullptr;
-  const int half = a.rot / 2;
-  const LaneRot lr = lane_rot<D>(lane, rope ? a.rot : 0, a.interleaved);
-  float wq[8], wk[8], dwq[8], dwk[8];
-  load_w(a.wq, e0, wq);
-  load_w(a.wk, e0, wk);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
-  for (int64_t first = (int64_t)blockIdx.x * kTok; first < tokens; first += (int64_t)gridDim.x * kTok) {
-    if (rope) {
-      __syncthreads();  // the table of the last tokens is read
-      for (int x = tid; x < kTok * half; x += kThreads) {
-        const int t = x / half, i = x - t * half;
-        const int64_t T = first + t;
-        if (T < tokens) {
-          const int b = (int)(T / a.N), n = (int)(T - (int64_t)b * a.N);
-          s_cs[t][i] = cos_sin(turns_per_position(__ldg(a.inv_freq + i)), (int64_t)n + (a.q_offset ? __ldg(a.q_offset + b) : 0));
+__global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_constant__ QkvBwdArgs a, const Shares sh) {
+  constexpr int LPR = D / 8, R = 32 / LPR, SLOTS = kBwdThreads / LPR;
+  extern __shared__ uint4 ring[];
+  const int tid = threadIdx.x, lane = tid % LPR, row = (tid % 32) / LPR;
+  const int64_t items = (int64_t)a.B * a.N * sh.groups;
+  const int64_t warp = (int64_t)blockIdx.x * (kBwdThreads / 32) + tid / 32, warps = (int64_t)gridDim.x * (kBwdThreads / 32);
+  auto heads = [&](int kind) { return kind == 0 ? (a.dq ? a.Hq : 0) : kind == 1 ? (a.dk ? a.Hkv : 0) : (a.dv ? a.Hkv : 0); };
+  const LaneMap lm = lane_map<D>(lane, a.inv_freq ? a.rot : 0, a.inv_freq ? a.interleaved : 0);
+  Cursor ld{warp, 0, 0, -1, 0, 0};
+  const float* dy = nullptr;
+  const bf16* src = nullptr;
+  int64_t hop = 0;
+  bool more = true;
+  int slot_in = 0;
+  const uint32_t my = smem_u32(ring) + tid * 16;
+  auto load = [&]() {
+    if (more) {
+      if (ld.h >= ld.hend) {
+        more = next_kind<R>(ld, items, warps, a.N, sh, heads);
+        if (more) {
+          const int H = ld.kind == 0 ? a.Hq : a.Hkv;
+          dy = (ld.kind == 0 ? a.dq : ld.kind == 1 ? a.dk : a.dv) + (((int64_t)ld.b * H + ld.h + row) * a.N + ld.n) * D;
+          const Rows& S = ld.kind == 0 ? a.q : a.k;
+          const bool with_x = ld.kind == 0 ? a.wq != nullptr : ld.kind == 1 && a.wk != nullptr;
+          src = with_x ? static_cast<const bf16*>(S.p) + ld.b * S.sb + ld.n * S.sn + (ld.h + row) * S.sh : nullptr;
+          hop = R * S.sh;
         }
       }
-      __syncthreads();
-    }
-    for (int t = 0; t < kTok; ++t) {
-      const int64_t T = first + t;
-      if (T >= tokens) break;
-      const int b = (int)(T / a.N), n = (int)(T - (int64_t)b * a.N);
-      float c[8], s[8];
-      if (rope) lane_cos_sin<true>(s_cs[t], lr, c, s);
-      for (int hb = 0; hb < H; hb += SLOTS * U) {
-        uint4 raw[U];
-        float4 g0[U], g1[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int h = hb + u * SLOTS + slot;
-          raw[u] = make_uint4(0, 0, 0, 0);
-          g0[u] = g1[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (h < H) {
-            const bool isq = h < nq, isk = !isq && h < nq + nk;
-            const int hh = isq ? h : isk ? h - nq : h - nq - nk;
-            const float* dy = (isq ? a.dq : isk ? a.dk : a.dv) + (((int64_t)b * (isq ? a.Hq : a.Hkv) + hh) * a.N + n) * D + e0;
-            g0[u] = __ldg(reinterpret_cast<const float4*>(dy));
-            g1[u] = __ldg(reinterpret_cast<const float4*>(dy) + 1);
-            const Rows& R = isq ? a.q : a.k;
-            if ((isq && a.wq) || (isk && a.wk))
-              raw[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const bf16*>(R.p) + b * R.sb + n * R.sn + hh * R.sh + e0));
+      if (more) {
+        if (ld.h + row < ld.hend) {
+          const uint32_t to = my + slot_in * (kBwdThreads * 48);
+          cp_async_16(to, dy + lm.ea, true);
+          cp_async_16(to + kBwdThreads * 16, dy + lm.eb, true);
+          if (src) {
+            cp_async_8(to + kBwdThreads * 32, src + lm.ea);
+            cp_async_8(to + kBwdThreads * 32 + 8, src + lm.eb);
           }
         }
+        dy += (int64_t)R * a.N * D;
+        if (src) src += hop;
+        ld.h += R;
+      }
+    }
+    slot_in = slot_in + 1 == kBwdRing ? 0 : slot_in + 1;
+    cp_async_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < kBwdRing; ++i) load();
+  uint64_t f[4] = {0, 0, 0, 0};
+  if (a.inv_freq) lane_frequencies(a.inv_freq, lm, f);
+  Eight dw[2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (hb + u * SLOTS >= H) break;
-          const int h = hb + u * SLOTS + slot;
-          const bool live = h < H, isq = h < nq, isk = !isq && h < nq + nk, isv = !isq && !isk;
-          const int hh = isq ? h : isk ? h - nq : h - nq - nk;
-          float g[8] = {g0[u].x, g0[u].y, g0[u].z, g0[u].w, g1[u].x, g1[u].y, g1[u].z, g1[u].w};
-          if (__any_sync(0xFFFFFFFFu, live && !isv)) {
-            float z[8], x[8];
+  for (int j = 0; j < 2; ++j) dw[0].a[j] = dw[0].b[j] = dw[1].a[j] = dw[1].b[j] = 0ull;
+  Cursor at{warp, 0, 0, -1, 0, 0};
+  int slot_out = 0;
+  Turn turn;
+  int64_t item_of_turn = -1;
+  while (next_kind<R>(at, items, warps, a.N, sh, heads)) {
+    const bool isq = at.kind == 0, isv = at.kind == 2;
+    if (item_of_turn != at.item) {
+      item_of_turn = at.item;
+      turn = turn_at(f, lm, (int64_t)at.n + (a.q_offset ? __ldg(a.q_offset + at.b) : 0));
+    }
+    const float* wp = isq ? a.wq : isv ? nullptr : a.wk;
+    const Eight w = load_weight(wp, lm);
+    const Rows& S = isq ? a.dq_in : isv ? a.dv_in : a.dk_in;
+    const int64_t base = at.b * S.sb + at.n * S.sn;
+    Eight sum;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) z[e] = g[e];
-            if (rope) rotate<LPR>(z, lr, c, s);
-            if (a.wq || a.wk) {
-              unpack8(raw[u], x);
-              const bool norm_row = isq ? a.wq != nullptr : a.wk != nullptr;
-              float q2 = 0.f;
+    for (int j = 0; j < 2; ++j) sum.a[j] = sum.b[j] = 0ull;
+    for (; at.h < at.hend; at.h += R) {
+      cp_async_wait<kBwdRing - 1>();
+      const int h = at.h + row;
+      const bool live = h < at.hend;
+      const uint4* in = ring + slot_out * (kBwdThreads * 3) + tid;
+      float4 ga = make_float4(0.f, 0.f, 0.f, 0.f), gb = ga;
+      uint4 xr = make_uint4(0, 0, 0, 0);
+      if (live) {
+        ga = *reinterpret_cast<const float4*>(in);
+        gb = *reinterpret_cast<const float4*>(in + kBwdThreads);
+        if (wp) xr = in[2 * kBwdThreads];
+      }
+      slot_out = slot_out + 1 == kBwdRing ? 0 : slot_out + 1;
+      load();
+      Eight g = unpack_f32(ga, gb, lm.inter);
+      if (!isv) {
+        const Eight d = g;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) q2 = fmaf(x[e], x[e], q2);
-              q2 = row_sum<LPR>(q2);
-              const float r = rsqrtf(q2 * (1.f / D) + a.eps);
-              float dot = 0.f;
+        for (int j = 0; j < 2 && lm.rot; ++j) {
+          g.a[j] = f2_fma(d.a[j], turn.c[j], f2_mul(d.b[j], turn.s[j]));
+          g.b[j] = f2_fma(d.b[j], turn.c[j], f2_neg(f2_mul(d.a[j], turn.s[j])));
+        }
+        if (wp) {  // the same for the whole warp
+          const Eight x = unpack(make_uint2(xr.x, xr.y), make_uint2(xr.z, xr.w), lm.inter);
+          const float r = row_rsqrt<D>(x, a.eps);
+          Eight gx, wgx;
+          const uint64_t rr = live ? f2_pack(r, r) : 0ull;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                x[e] *= r;
-                const float gx = z[e] * x[e], w = isq ? wq[e] : wk[e];
-                if (live && norm_row) {
-                  if (isq) dwq[e] += gx;
-                  if (isk) dwk[e] += gx;
-                }
-                dot = fmaf(w, gx, dot);
-              }
-              dot = row_sum<LPR>(dot) * (1.f / D);
-              if (norm_row) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = r * ((isq ? wq[e] : wk[e]) * z[e] - x[e] * dot);
-              }
-            }
-            if (!isv) {
-#pragma unroll
-              for (int e = 0; e < 8; ++e) g[e] = z[e];
+          for (int j = 0; j < 2; ++j) {
+            gx.a[j] = f2_mul(g.a[j], x.a[j]);
+            gx.b[j] = f2_mul(g.b[j], x.b[j]);
+            wgx.a[j] = f2_mul(w.a[j], gx.a[j]);
+            wgx.b[j] = f2_mul(w.b[j], gx.b[j]);
+            if (live) {  // a row that is not there may have r = inf
+              sum.a[j] = f2_fma(gx.a[j], rr, sum.a[j]);
+              sum.b[j] = f2_fma(gx.b[j], rr, sum.b[j]);
             }
           }
-          if (live) {
-            const Rows& R = isq ? a.dq_in : isk ? a.dk_in : a.dv_in;
-            store_grad<D, F32>(R.p, b * R.sb + n * R.sn + hh * R.sh + e0, g);
+          const float dot = row_sum<LPR>(add_up(wgx)) * r;        // sum of w g xhat
+          const float k = -dot * (1.f / D) * r * r;
+          const uint64_t kk = f2_pack(k, k);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            g.a[j] = f2_fma(f2_mul(w.a[j], g.a[j]), rr, f2_mul(x.a[j], kk));
+            g.b[j] = f2_fma(f2_mul(w.b[j], g.b[j]), rr, f2_mul(x.b[j], kk));
           }
+        }
+      }
+      if (live) store_grad<F32>(S.p, base + h * S.sh, lm, g);
+    }
+    if (wp) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        if (isq) {
+          dw[0].a[j] = f2_add(dw[0].a[j], sum.a[j]);
+          dw[0].b[j] = f2_add(dw[0].b[j], sum.b[j]);
+        } else {
+          dw[1].a[j] = f2_add(dw[1].a[j], sum.a[j]);
+          dw[1].b[j] = f2_add(dw[1].b[j], sum.b[j]);
         }
       }
     }
   }
+  cp_async_wait<0>();
   if (!a.wq && !a.wk) return;
+  float (*s_dw)[D] = reinterpret_cast<float (*)[D]>(ring);  // the rings are read: [SLOTS][D]
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
+    float y[8];
+    in_order(dw[which], lm.inter, y);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s_dw[slot][e0 + e] = which ? dwk[e] : dwq[e];
+    for (int e = 0; e < 4; ++e) {
+      s_dw[tid / LPR][lm.ea + e] = y[e];
+      s_dw[tid / LPR][lm.eb + e] = y[4 + e];
+    }
     __syncthreads();
     if (tid < D) {
       float v = 0.f;
@@ -595,22 +802,22 @@ __global__ void __launch_bounds__(1024) dw_reduce_kernel(const float* partial, i
   }
 }
 
-constexpr int kSms = 152;
-
-// Groups of heads for the row kernels: one CTA a token group where that fills the GPU twice over, else the heads are
-// dealt out so that a decode step's few tokens still reach every SM.
-int heads_per_cta(int64_t token_ctas, int H, int slots) {
+// Shares of the heads: a token's heads stay together where that gives every warp that fits the GPU an item, else they
+// are dealt out so that a decode step's few tokens still reach every SM.
+Shares shares(int64_t tokens, int64_t warps, int Hq, int Hkv, int rows_a_step) {
   int groups = 1;
-  while (token_ctas * groups < 2 * kSms && (H + groups - 1) / groups > slots) ++groups;
-  return (H + groups - 1) / groups;
+  const int most = (std::max(Hq, Hkv) + rows_a_step - 1) / rows_a_step;
+  while (groups < most && tokens * groups < warps) groups *= 2;
+  return Shares{groups, (Hq + groups - 1) / groups, (Hkv + groups - 1) / groups};
 }
 
 template <int D, int DST>
 cudaError_t run_rows(const QkvArgs& a, cudaStream_t st) {
-  const int H = (a.q.p ? a.Hq : 0) + (a.k.p ? a.Hkv : 0) + (a.v.p ? a.Hkv : 0);
-  const int64_t ctas = ((int64_t)a.B * a.N + kTok - 1) / kTok;
-  const int hpc = heads_per_cta(ctas, H, kThreads / (D / 8));
-  qkv_rows_kernel<D, DST><<<dim3((unsigned)ctas, (H + hpc - 1) / hpc), kThreads, 0, st>>>(a, hpc);
+  constexpr int kWarps = kRowThreads / 32;
+  const int64_t tokens = (int64_t)a.B * a.N;
+  const Shares sh = shares(tokens, kSms * 8 * kWarps, a.Hq, a.Hkv, 32 / (D / 8));
+  const int64_t ctas = std::min<int64_t>((tokens * sh.groups + kWarps - 1) / kWarps, kSms * 8);
+  qkv_rows_kernel<D, DST><<<(unsigned)ctas, kRowThreads, 0, st>>>(a, sh);
   return cudaGetLastError();
 }
 
@@ -619,21 +826,26 @@ cudaError_t run_append(const QkvArgs& a, cudaStream_t st) {
   if (!a.k_scale) return run_rows<D, kToPages>(a, st);
   if (a.N == 1) return run_rows<D, kToPagesFp8>(a, st);
   const int blocks = (a.N + 2 * kScaleTokens - 2) / kScaleTokens;
-  const int hpc = heads_per_cta((int64_t)a.B * blocks, a.Hkv, 1);
-  const int groups = (a.Hkv + hpc - 1) / hpc;
-  const int64_t ctas = (int64_t)a.B * blocks * groups + (a.q.p ? ((int64_t)a.B * a.N + kTok - 1) / kTok : 0);
-  append_fp8_kernel<D><<<(unsigned)ctas, kThreads, 0, st>>>(a, blocks, hpc, groups);
+  int groups = 1;
+  while (groups < a.Hkv && (int64_t)a.B * blocks * groups < 4 * kSms) ++groups;
+  const int hpc = (a.Hkv + groups - 1) / groups;
+  groups = (a.Hkv + hpc - 1) / hpc;
+  const int64_t q_items = a.q.p ? (int64_t)a.B * a.N : 0, per = kBlockThreads / 32;
+  const int64_t ctas = (int64_t)a.B * blocks * groups + std::min<int64_t>((q_items + per - 1) / per, kSms * 4);
+  append_fp8_kernel<D><<<(unsigned)ctas, kBlockThreads, 0, st>>>(a, blocks, hpc, groups);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t run_bwd(const QkvBwdArgs& a, cudaStream_t st) {
-  const int ctas = qk_bwd_ctas((int64_t)a.B * a.N);
-  if (a.grad_f32)
-    qkv_bwd_kernel<D, true><<<ctas, kThreads, 0, st>>>(a);
-  else
-    qkv_bwd_kernel<D, false><<<ctas, kThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const int64_t tokens = (int64_t)a.B * a.N;
+  const int ctas = qk_bwd_ctas(tokens);
+  const Shares sh = shares(tokens, (int64_t)ctas * (kBwdThreads / 32), a.Hq, a.Hkv, 32 / (D / 8));
+  auto kern = a.grad_f32 ? qkv_bwd_kernel<D, true> : qkv_bwd_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdRingBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, kBwdThreads, kBwdRingBytes, st>>>(a, sh);
+  e = cudaGetLastError();
   if (e != cudaSuccess || (!a.wq && !a.wk)) return e;
   dw_reduce_kernel<<<2 * D / 32, dim3(32, 32), 0, st>>>(a.partial, ctas, D, a.dwq, a.dwk);
   return cudaGetLastError();
@@ -641,9 +853,10 @@ cudaError_t run_bwd(const QkvBwdArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+// CTAs of the backward's persistent grid, two an SM; fewer where there are not four tokens' worth of work for each
 int qk_bwd_ctas(int64_t tokens) {
-  const int64_t n = (tokens + kTok - 1) / kTok;
-  return (int)(n < 4 * kSms ? n : 4 * kSms);
+  const int64_t n = (tokens + 3) / 4;
+  return (int)(n < 2 * kSms ? n : 2 * kSms);
 }
 
 cudaError_t launch_qk_norm_rope(const QkvArgs& a, cudaStream_t st) {

@@ -546,17 +546,16 @@ def _rows(t: Optional[torch.Tensor], shape, dtype, device, what: str, written: b
     """fa_rows of a [B, N, H, d] tensor of any b / n / h strides."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape) or t.stride(3) != 1:
+    sb, sn, sh, sd = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
+    if sd != 1 or t.dtype != dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on {device} with contiguous rows")
-    sb, sn, sh, _ = t.stride()
     if written and any(st == 0 and n > 1 for st, n in zip((sb, sn, sh), shape)):
         raise ValueError(f"{what} is written: its elements must not share memory")
     return RowsC(t.data_ptr(), sb, sn, sh)
 
 
 def _same(t: Optional[torch.Tensor], shape, dtype, device, what: str):
-    if t is not None and (t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape)
-                          or not t.is_contiguous()):
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
 
@@ -569,6 +568,11 @@ def _check_qk_rule(rule: Optional[QkRule], d: int, device):
 
 def _ref(s):
     return None if s is None else ctypes.byref(s)
+
+
+def _at(t: Optional[torch.Tensor]):
+    """Address for an argument declared as a pointer."""
+    return None if t is None else t.data_ptr()
 
 
 def _call(device, fn, *args) -> int:
@@ -607,7 +611,7 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Option
         outs.append(_same(o, (B, h, N, d), bf, dev, n))
     _check_qk_rule(rule, d, dev)
     _same(q_offset, (B,), torch.int32, dev, "q_offset")
-    _check(_call(dev, load().fa_qk_norm_rope, *map(_ref, rows), ctypes.byref(rule), _ptr(q_offset), *map(_ptr, outs), B, Hq,
+    _check(_call(dev, load().fa_qk_norm_rope, *map(_ref, rows), ctypes.byref(rule), _at(q_offset), *map(_at, outs), B, Hq,
                  Hkv, N, d), "fa_qk_norm_rope")
     return tuple(outs)
 
@@ -657,9 +661,9 @@ def qk_norm_rope_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
     dwk = torch.empty(d, dtype=f32, device=dev) if rule.k_weight and dk is not None else None
     if workspace is None and (dwq is not None or dwk is not None):
         workspace = torch.empty(qk_norm_rope_backward_workspace_bytes(B, N, d), dtype=torch.uint8, device=dev)
-    _check(_call(dev, load().fa_qk_norm_rope_backward, _ref(rq), _ref(rk), _ptr(dq), _ptr(dk), _ptr(dv),
-                 ctypes.byref(rule), _ptr(q_offset), *map(_ref, rows), 1 if kind == f32 else 0, _ptr(dwq), _ptr(dwk), B, Hq,
-                 Hkv, N, d, _ptr(workspace), 0 if workspace is None else workspace.numel()), "fa_qk_norm_rope_backward")
+    _check(_call(dev, load().fa_qk_norm_rope_backward, _ref(rq), _ref(rk), _at(dq), _at(dk), _at(dv),
+                 ctypes.byref(rule), _at(q_offset), *map(_ref, rows), 1 if kind == f32 else 0, _at(dwq), _at(dwk), B, Hq,
+                 Hkv, N, d, _at(workspace), 0 if workspace is None else workspace.numel()), "fa_qk_norm_rope_backward")
     return (*outs, dwq, dwk)
 
 
@@ -687,10 +691,10 @@ def _append(q, k, v, k_pages, v_pages, k_scale, v_scale, page_table, rule, q_off
     _same(q_out, (B, Hq, N, d), bf, dev, "q_out")
     _check_qk_rule(rule, d, dev)
     lib = load()
-    scales = (_ptr(k_scale), _ptr(v_scale)) if fp8 else ()
-    _check(_call(dev, lib.fa_kv_append_fp8 if fp8 else lib.fa_kv_append, *map(_ref, rows), _ref(rule), _ptr(q_offset),
-                 _ptr(n_new), _ptr(q_out if q is not None else None), _ptr(k_pages), _ptr(v_pages), *scales,
-                 _ptr(page_table), P, page, page_table.shape[1], B, Hq, Hkv, N, d, _ptr(status)),
+    scales = (_at(k_scale), _at(v_scale)) if fp8 else ()
+    _check(_call(dev, lib.fa_kv_append_fp8 if fp8 else lib.fa_kv_append, *map(_ref, rows), _ref(rule), _at(q_offset),
+                 _at(n_new), _at(q_out if q is not None else None), _at(k_pages), _at(v_pages), *scales,
+                 _at(page_table), P, page, page_table.shape[1], B, Hq, Hkv, N, d, _at(status)),
            "fa_kv_append_fp8" if fp8 else "fa_kv_append")
     return q_out
 
@@ -765,10 +769,10 @@ def flex_decode_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     if workspace is None:
         workspace = torch.empty(max(decode_fp8_workspace_bytes(Bz, Hq, Hkv, d, max_pages, page), 16), dtype=torch.uint8,
                                 device=dev)
-    _check(_call(dev, load().fa_flex_decode_fp8, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-                 _ptr(page_table), P, ctypes.byref(block_mask.c), _ref(score), float(scale) if scale else 0.0, _ptr(out),
-                 _out_code(out), _ptr(lse), Bz, Hq, Hkv, d, page, max_pages, _ptr(workspace), workspace.numel(),
-                 _ptr(status), _ptr(counters)), "fa_flex_decode_fp8")
+    _check(_call(dev, load().fa_flex_decode_fp8, _at(q), _at(k_pages), _at(v_pages), _at(k_scale), _at(v_scale),
+                 _at(page_table), P, ctypes.byref(block_mask.c), _ref(score), float(scale) if scale else 0.0, _at(out),
+                 _out_code(out), _at(lse), Bz, Hq, Hkv, d, page, max_pages, _at(workspace), workspace.numel(),
+                 _at(status), _at(counters)), "fa_flex_decode_fp8")
     return out, lse
 
 
@@ -794,10 +798,10 @@ def flex_forward_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     if workspace is None:
         n = forward_paged_fp8_workspace_bytes(block_mask, B, Hq, Hkv, d, chunk_blocks)
         workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
-    _check(_call(dev, load().fa_flex_forward_paged_fp8, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale),
-                 _ptr(v_scale), _ptr(page_table), P, page, max_pages, ctypes.byref(block_mask.c), _ref(score),
-                 float(scale) if scale else 0.0, _ptr(out), _out_code(out), _ptr(lse), B, Hq, Hkv, Q_LEN, KV_LEN, d,
-                 chunk_blocks, _ptr(workspace), workspace.numel(), _ptr(status)), "fa_flex_forward_paged_fp8")
+    _check(_call(dev, load().fa_flex_forward_paged_fp8, _at(q), _at(k_pages), _at(v_pages), _at(k_scale),
+                 _at(v_scale), _at(page_table), P, page, max_pages, ctypes.byref(block_mask.c), _ref(score),
+                 float(scale) if scale else 0.0, _at(out), _out_code(out), _at(lse), B, Hq, Hkv, Q_LEN, KV_LEN, d,
+                 chunk_blocks, _at(workspace), workspace.numel(), _at(status)), "fa_flex_forward_paged_fp8")
     return out, lse
 
 

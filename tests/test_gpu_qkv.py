@@ -111,6 +111,23 @@ def test_rows_of_zeros_infinities_and_nan_keep_to_themselves():
     assert torch.equal(q[0, 1, 3], clean[0][0, 1, 3])
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_an_infinity_stays_in_its_pair(inter):
+    # no norm, a row rotated in part: an infinity reaches the other element of its own pair and nothing else
+    c = make(31, 1, 4, 1, 1, 128, 32, False, inter, offset=3)
+    clean = fa.qk_norm_rope(*split(c), c["rule"], q_offset=c["cu"]["off"])[0]
+    for e, hit in ((77, {77}), (127, {127}), (34, {34}), (5, {4, 5} if inter else {5, 21})):
+        x = c["cu"]["x"].clone()
+        x[0, 2, 0, e] = float("inf")
+        q = fa.qk_norm_rope(*split(c, x), c["rule"], q_offset=c["cu"]["off"])[0]
+        other = [i for i in range(128) if i not in hit]
+        assert torch.equal(q[..., other], clean[..., other]) and not torch.isfinite(q[0, 0, 2, e])
+        g = torch.ones(1, 1, 4, 128, device="cuda")
+        g[0, 0, 2, e] = float("inf")
+        d = fa.qk_norm_rope_backward(None, None, g, None, None, c["rule"], q_offset=c["cu"]["off"])[0]
+        assert torch.isfinite(d[..., other]).all() and not torch.isfinite(d[0, 2, 0, e])
+
+
 # ------------------------------------------------------------------------------------------ gradient
 @pytest.mark.parametrize("case", CASES)
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
