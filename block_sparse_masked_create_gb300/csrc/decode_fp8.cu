@@ -375,10 +375,13 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 // Joins the spans of one query head: m = max m_s, l = sum 2^(m_s - m) l_s, O = sum 2^(m_s - m) u_s / l. Requests of
-// one span are done already.
+// one span are done already. Four groups of threads take every fourth span.
+constexpr int kJoin = 4;
+
 template <int D>
-__global__ void __launch_bounds__(D) decode_fp8_join_kernel(const __grid_constant__ DecArgs a) {
-  const int hq = blockIdx.x, b = blockIdx.y;
+__global__ void __launch_bounds__(kJoin * D) decode_fp8_join_kernel(const __grid_constant__ DecArgs a) {
+  __shared__ float s_u[kJoin][D], s_red[kJoin * D / 32], s_l[kJoin];
+  const int hq = blockIdx.x, b = blockIdx.y, col = threadIdx.x % D, part = threadIdx.x / D;
   const DevMask& M = a.mask;
   const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm * M.nq;
   const int n_vis = __ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow);
@@ -386,19 +389,36 @@ __global__ void __launch_bounds__(D) decode_fp8_join_kernel(const __grid_constan
   const int ns = (n_vis + a.pages_per_split - 1) / a.pages_per_split;
   const size_t base = ((size_t)b * a.Hq + hq) * (size_t)a.n_splits, obase = ((size_t)b * a.Hq + hq) * D;
   float mm = -INFINITY;
-  for (int s = 0; s < ns; ++s) mm = fmaxf(mm, a.ws_m[base + s]);
+  for (int s = threadIdx.x; s < ns; s += kJoin * D) mm = fmaxf(mm, a.ws_m[base + s]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xFFFFFFFFu, mm, o));
+  if (threadIdx.x % 32 == 0) s_red[threadIdx.x / 32] = mm;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoin * D / 32; ++w) mm = fmaxf(mm, s_red[w]);
   const float ref = mm == -INFINITY ? 0.f : mm;
   float l = 0.f, u = 0.f;
-#pragma unroll 4
-  for (int s = 0; s < ns; ++s) {
+#pragma unroll 8
+  for (int s = part; s < ns; s += kJoin) {
     const float wt = ex2_approx(a.ws_m[base + s] - ref);
     l += wt * a.ws_l[base + s];
-    u += wt * a.ws_u[(base + s) * D + threadIdx.x];
+    u += wt * a.ws_u[(base + s) * D + col];
+  }
+  s_u[part][col] = u;
+  if (col == 0) s_l[part] = l;
+  __syncthreads();
+  if (part) return;
+  l = 0.f;
+  u = 0.f;
+#pragma unroll
+  for (int p = 0; p < kJoin; ++p) {
+    l += s_l[p];
+    u += s_u[p][col];
   }
   const float r = mm == -INFINITY ? 0.f : u / l;
-  if (a.out_f32) reinterpret_cast<float*>(a.out)[obase + threadIdx.x] = r;
-  else reinterpret_cast<__nv_bfloat16*>(a.out)[obase + threadIdx.x] = __float2bfloat16_rn(r);
-  if (threadIdx.x == 0) a.lse[(size_t)b * a.Hq + hq] = mm == -INFINITY ? -INFINITY : (mm + log2f(l)) * kLn2;
+  if (a.out_f32) reinterpret_cast<float*>(a.out)[obase + col] = r;
+  else reinterpret_cast<__nv_bfloat16*>(a.out)[obase + col] = __float2bfloat16_rn(r);
+  if (col == 0) a.lse[(size_t)b * a.Hq + hq] = mm == -INFINITY ? -INFINITY : (mm + log2f(l)) * kLn2;
 }
 
 template <int D>
@@ -417,7 +437,7 @@ int launch_d(const DecFp8Args& A, cudaStream_t st) {
   kern<<<dim3(a.n_splits, a.Hkv, a.Bz), kWarps * 32, C::kSmem, st>>>(A, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   if (a.n_splits > 1) {
-    decode_fp8_join_kernel<D><<<dim3(a.Hq, a.Bz), D, 0, st>>>(a);
+    decode_fp8_join_kernel<D><<<dim3(a.Hq, a.Bz), kJoin * D, 0, st>>>(a);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;

@@ -1099,12 +1099,17 @@ fa_status fa_kv_append_fp8(const fa_rows* q, const fa_rows* k, const fa_rows* v,
 // ------------------------------------------------------------------------------------------------
 // Attention over an 8-bit paged cache
 // ------------------------------------------------------------------------------------------------
-// Pages of one span of the 8-bit decode: enough spans for four rounds of two CTAs an SM by the table's capacity (the
-// lengths are on the device), at least 256 tokens each and at most 4096 (32 sub-tiles for each of a CTA's 4 warps).
+// Pages of one span of the 8-bit decode, by the table's capacity (the lengths are on the device): 304 CTAs run at a time
+// (two an SM), so the spans are cut for whole rounds of them, as many rounds as keep a span within 4096 tokens (32 sub-tiles
+// for each of a CTA's 4 warps), and no shorter than 256 tokens.
 static int decode_fp8_pages_per_split(int32_t Bz, int32_t Hkv, int32_t max_pages, int32_t page) {
-  const int64_t tokens = (int64_t)Bz * Hkv * max_pages * page / (152 * 2 * 4);
-  const int64_t span = std::min<int64_t>(4096, std::max<int64_t>(256, tokens));
-  return (int)std::min<int64_t>(std::max<int64_t>(1, span / page), max_pages);
+  const int64_t rows = (int64_t)Bz * Hkv, most = 4096 / page, least = std::max(1, 256 / page);
+  for (int rounds = 2; rounds <= 16; ++rounds) {
+    const int64_t spans = std::max<int64_t>(1, (int64_t)rounds * 304 / rows);       // a row of the table
+    const int64_t pages = (max_pages + spans - 1) / spans;
+    if (pages <= most) return (int)std::min<int64_t>(std::max<int64_t>(pages, least), max_pages);
+  }
+  return (int)std::min<int64_t>(most, max_pages);
 }
 
 struct DecodeFp8Plan {

@@ -57,24 +57,23 @@ __device__ __forceinline__ float2 cos_sin(uint64_t f, int64_t pos) {
 // the 8 elements from ea on are pairs i0 .. i0 + 3. Lanes behind the rotated part hold 8 neighbouring elements.
 struct LaneMap {
   int ea, eb, i0;
-  bool rot, inter;
+  bool rot;
 };
 
-template <int D>
-__device__ __forceinline__ LaneMap lane_map(int lane, int rot, int interleaved) {
+template <int D, bool INTER>
+__device__ __forceinline__ LaneMap lane_map(int lane, int rot) {
   LaneMap m;
   const int half = rot / 2;
-  m.inter = interleaved != 0;
-  if (!m.inter && lane * 4 < half) {
+  if (!INTER && lane * 4 < half) {
     m.ea = lane * 4;
     m.eb = half + lane * 4;
     m.i0 = lane * 4;
     m.rot = true;
   } else {
-    m.ea = m.inter ? lane * 8 : rot + (lane - half / 4) * 8;
+    m.ea = INTER ? lane * 8 : rot + (lane - half / 4) * 8;
     m.eb = m.ea + 4;
     m.i0 = lane * 4;
-    m.rot = m.inter && lane * 8 < rot;
+    m.rot = INTER && lane * 8 < rot;
   }
   return m;
 }
@@ -88,9 +87,10 @@ __device__ __forceinline__ uint64_t widen(uint32_t w) {
   return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ Eight unpack(const uint2& va, const uint2& vb, bool inter) {
+template <bool INTER>
+__device__ __forceinline__ Eight unpack(const uint2& va, const uint2& vb) {
   Eight r;
-  if (inter) {
+  if (INTER) {
     r.a[0] = f2_pack(__uint_as_float(va.x << 16), __uint_as_float(va.y << 16));
     r.a[1] = f2_pack(__uint_as_float(vb.x << 16), __uint_as_float(vb.y << 16));
     r.b[0] = f2_pack(__uint_as_float(va.x & 0xFFFF0000u), __uint_as_float(va.y & 0xFFFF0000u));
@@ -105,9 +105,10 @@ __device__ __forceinline__ Eight unpack(const uint2& va, const uint2& vb, bool i
 }
 
 // fp32 values at ea .. ea + 3 and eb .. eb + 3
-__device__ __forceinline__ Eight unpack_f32(const float4& va, const float4& vb, bool inter) {
+template <bool INTER>
+__device__ __forceinline__ Eight unpack_f32(const float4& va, const float4& vb) {
   Eight r;
-  if (inter) {
+  if (INTER) {
     r.a[0] = f2_pack(va.x, va.z);
     r.a[1] = f2_pack(vb.x, vb.z);
     r.b[0] = f2_pack(va.y, va.w);
@@ -122,7 +123,8 @@ __device__ __forceinline__ Eight unpack_f32(const float4& va, const float4& vb, 
 }
 
 // the values in the order of their elements: ea .. ea + 3, eb .. eb + 3
-__device__ __forceinline__ void in_order(const Eight& v, bool inter, float (&y)[8]) {
+template <bool INTER>
+__device__ __forceinline__ void in_order(const Eight& v, float (&y)[8]) {
   float a[4], b[4];
   f2_unpack(v.a[0], a[0], a[1]);
   f2_unpack(v.a[1], a[2], a[3]);
@@ -130,18 +132,19 @@ __device__ __forceinline__ void in_order(const Eight& v, bool inter, float (&y)[
   f2_unpack(v.b[1], b[2], b[3]);
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    y[k] = inter ? ((k & 1) ? b[k >> 1] : a[k >> 1]) : a[k];
-    y[4 + k] = inter ? ((k & 1) ? b[2 + (k >> 1)] : a[2 + (k >> 1)]) : b[k];
+    y[k] = INTER ? ((k & 1) ? b[k >> 1] : a[k >> 1]) : a[k];
+    y[4 + k] = INTER ? ((k & 1) ? b[2 + (k >> 1)] : a[2 + (k >> 1)]) : b[k];
   }
 }
 
+template <bool INTER>
 __device__ __forceinline__ Eight load_weight(const float* w, const LaneMap& m) {
   float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = a;
   if (w) {
     a = make_float4(__ldg(w + m.ea), __ldg(w + m.ea + 1), __ldg(w + m.ea + 2), __ldg(w + m.ea + 3));
     b = make_float4(__ldg(w + m.eb), __ldg(w + m.eb + 1), __ldg(w + m.eb + 2), __ldg(w + m.eb + 3));
   }
-  return unpack_f32(a, b, m.inter);
+  return unpack_f32<INTER>(a, b);
 }
 
 // cos and sin of the lane's four pairs at a position
@@ -240,16 +243,18 @@ __device__ __forceinline__ Eight norm_rope(const Eight& x, bool norm, float eps,
   return z;
 }
 
+template <bool INTER>
 __device__ __forceinline__ void store_bf16(bf16* row, const LaneMap& m, const Eight& z) {
   float y[8];
-  in_order(z, m.inter, y);
+  in_order<INTER>(z, y);
   *reinterpret_cast<uint2*>(row + m.ea) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
   *reinterpret_cast<uint2*>(row + m.eb) = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
 }
 
+template <bool INTER>
 __device__ __forceinline__ void store_e4m3(uint8_t* row, const LaneMap& m, const Eight& z, float inv) {
   float y[8];
-  in_order(z, m.inter, y);
+  in_order<INTER>(z, y);
   *reinterpret_cast<uint32_t*>(row + m.ea) = pack_e4m3x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
   *reinterpret_cast<uint32_t*>(row + m.eb) = pack_e4m3x4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
 }
@@ -319,284 +324,359 @@ __device__ __forceinline__ Place place_of(const QkvArgs& a, int b, int64_t pos) 
 
 // ------------------------------------------------------------------------------------------------
 // Rows. An item is one token (b, n) and one of `groups` shares of its heads: shares of the query heads, then of the key
-// heads, then of the value heads. The warps of the grid deal the items out in turn, so that neighbouring warps hold
-// neighbouring tokens, which lie side by side in the head-major tensors.
+// heads, then of the value heads, 32 / (d / 8) heads a step. The warps of the grid deal the items out in turn, so that
+// neighbouring warps hold neighbouring tokens, which lie side by side in the head-major tensors.
 // ------------------------------------------------------------------------------------------------
 struct Shares {
   int groups, q, k;     // heads of a share
 };
 
-// The order of an item's steps: one kind's heads after the other's, R rows a step.
+// Walks the loads: the heads [h, hend) of one kind of one item, then the next kind's or item's. A kind that is left out
+// has no heads.
 struct Cursor {
   int64_t item;
-  int b, n, kind, h, hend;   // h: the step's first head
+  int b, n, kind, h, hend;
 };
 
-template <int R, class Sizes>
-__device__ __forceinline__ bool next_kind(Cursor& c, int64_t items, int64_t step, int N, const Shares& sh, const Sizes& heads) {
-  for (;;) {  // the next kind, or the next item, that has heads in this share
+__device__ __forceinline__ bool next_kind(Cursor& c, int64_t items, int64_t step, int N, const Shares& sh, int hq, int hk, int hv,
+                                          const int32_t* n_new = nullptr) {
+  for (;;) {
     if (++c.kind == 3) {
       c.kind = 0;
       c.item += step;
     }
     if (c.item >= items) return false;
-    const int64_t T = c.item / sh.groups;
-    const int g = (int)(c.item - T * sh.groups);
+    const int64_t T = sh.groups == 1 ? c.item : c.item / sh.groups;
+    const int g = sh.groups == 1 ? 0 : (int)(c.item - T * sh.groups);
     if (c.kind == 0) {
-      c.b = (int)(T / N);
-      c.n = (int)(T - (int64_t)c.b * N);
+      c.b = (int)((uint32_t)T / (uint32_t)N);  // tokens fit 31 bits
+      c.n = (int)((uint32_t)T - (uint32_t)c.b * (uint32_t)N);
+      if (n_new && c.n >= __ldg(n_new + c.b)) {  // a token that is not there
+        c.kind = 2;
+        continue;
+      }
     }
     const int per = c.kind == 0 ? sh.q : sh.k;
     c.h = g * per;
-    c.hend = min(heads(c.kind), c.h + per);
+    c.hend = min(c.kind == 0 ? hq : c.kind == 1 ? hk : hv, c.h + per);
     if (c.h < c.hend) return true;
   }
 }
 
-constexpr int kRing = 8;         // rows in flight a lane
+constexpr int kRing = 8;         // rows in flight a lane (a power of two)
 constexpr int kRowThreads = 128;
+constexpr int kRowCtas = 5;      // of an SM, by registers; the grid is exactly those: with 8 an SM 75 us where 5 take 67
 
-template <int D, int DST, int THREADS>
-__device__ __forceinline__ void rows_of_items(const QkvArgs& a, int64_t warp, int64_t warps, const Shares& sh, uint2* ring) {
-  constexpr int LPR = D / 8, R = 32 / LPR;
-  const int tid = threadIdx.x, lane = tid % LPR, row = (tid % 32) / LPR;
-  const int64_t items = (int64_t)a.B * a.N * sh.groups;
-  const bool append_rows = DST != kToHeads;
-  auto heads = [&](int kind) { return kind == 0 ? (a.q.p ? a.Hq : 0) : kind == 1 ? (a.k.p ? a.Hkv : 0) : (a.v.p ? a.Hkv : 0); };
-  const LaneMap lm = lane_map<D>(lane, a.inv_freq ? a.rot : 0, a.inv_freq ? a.interleaved : 0);
-  // ---- loads, kRing steps ahead
-  Cursor ld{warp, 0, 0, -1, 0, 0};
-  const bf16* src = nullptr;
-  int64_t hop = 0;
-  bool more = true;
-  int slot_in = 0;
-  const uint32_t my = smem_u32(ring + tid);
-  auto load = [&]() {
+// One item at a time, with the loads ahead of it.
+template <int D, int DST, bool INTER, int THREADS>
+struct RowWarp {
+  static constexpr int LPR = D / 8, R = 32 / LPR;
+  static constexpr int kStep = 2 * THREADS * 8;    // bytes of a ring step: each lane's two groups
+  const QkvArgs& a;
+  const Shares& sh;
+  int lane, row, hq, hk, hv;
+  int64_t items, warps;
+  LaneMap lm;
+  Cursor ld;
+  const bf16* src;
+  int64_t hop;
+  bool more;
+  uint32_t ring, in, out;
+  Turn turn;
+  Place place;
+  int b, n;
+
+  __device__ __forceinline__ RowWarp(const QkvArgs& args, const Shares& shares, int64_t warp, int64_t n_warps, uint2* ring_mem)
+      : a(args), sh(shares), lane(threadIdx.x % LPR), row((threadIdx.x % 32) / LPR), hq(args.q.p ? args.Hq : 0),
+        hk(args.k.p ? args.Hkv : 0), hv(args.v.p ? args.Hkv : 0), items((int64_t)args.B * args.N * shares.groups),
+        warps(n_warps), lm(lane_map<D, INTER>(lane, args.inv_freq ? args.rot : 0)), ld{warp, 0, 0, -1, 0, 0}, src(nullptr),
+        hop(0), more(true), ring(smem_u32(ring_mem) + threadIdx.x * 8), in(0), out(0), place{-1, 0}, b(0), n(0) {
+#pragma unroll 1
+    for (int i = 0; i < kRing; ++i) load();
+  }
+
+  __device__ __forceinline__ void load() {
     if (more) {
       if (ld.h >= ld.hend) {
-        more = next_kind<R>(ld, items, warps, a.N, sh, heads);
+        more = next_kind(ld, items, warps, a.N, sh, hq, hk, hv, DST == kToHeads ? nullptr : a.n_new);
         if (more) {
           const Rows& S = ld.kind == 0 ? a.q : ld.kind == 1 ? a.k : a.v;
-          src = static_cast<const bf16*>(S.p) + ld.b * S.sb + ld.n * S.sn + (ld.h + row) * S.sh;
+          src = static_cast<const bf16*>(S.p) + ld.b * S.sb + ld.n * S.sn + (ld.h + row) * S.sh + lm.ea;
           hop = R * S.sh;
         }
       }
       if (more) {
         if (ld.h + row < ld.hend) {
-          cp_async_8(my + slot_in * (2 * THREADS * 8), src + lm.ea);
-          cp_async_8(my + slot_in * (2 * THREADS * 8) + THREADS * 8, src + lm.eb);
+          cp_async_8(ring + in, src);
+          cp_async_8(ring + in + THREADS * 8, src + (lm.eb - lm.ea));
         }
         src += hop;
         ld.h += R;
       }
     }
-    slot_in = slot_in + 1 == kRing ? 0 : slot_in + 1;
+    in = (in + kStep) & (kRing * kStep - 1);
     cp_async_commit();
-  };
-#pragma unroll 1
-  for (int i = 0; i < kRing; ++i) load();
-  // ---- work
-  uint64_t f[4] = {0, 0, 0, 0};
-  if (a.inv_freq) lane_frequencies(a.inv_freq, lm, f);
-  Cursor at{warp, 0, 0, -1, 0, 0};
-  int slot_out = 0;
-  Turn turn;
-  Place place{-1, 0};
-  bool take = true;
-  int64_t item_of_turn = -1;
-  while (next_kind<R>(at, items, warps, a.N, sh, heads)) {
-    const bool isq = at.kind == 0, isv = at.kind == 2;
-    const int H = isq ? a.Hq : a.Hkv;
-    if (item_of_turn != at.item) {
-      item_of_turn = at.item;
-      const int64_t pos = (int64_t)at.n + (a.q_offset ? __ldg(a.q_offset + at.b) : 0);
-      turn = turn_at(f, lm, pos);
-      if (append_rows) {
-        take = at.n < new_tokens(a, at.b);
-        if (take && (a.k.p || a.v.p)) place = place_of(a, at.b, pos);
-      }
-    }
-    const float* w = isq ? a.wq : isv ? nullptr : a.wk;
+  }
+
+  // KIND 0: query rows, 1: key rows, 2: value rows
+  template <int KIND>
+  __device__ __forceinline__ void heads_of(int g) {
+    const int per = KIND == 0 ? sh.q : sh.k, H = KIND == 0 ? hq : KIND == 1 ? hk : hv;
+    int h = g * per + row;
+    const int hend = min(H, g * per + per);
+    int left = (hend - g * per + R - 1) / R;
+    if (left <= 0) return;
+    constexpr bool kToCache = DST != kToHeads && KIND != 0;
+    const float* w = KIND == 0 ? a.wq : KIND == 1 ? a.wk : nullptr;
     Map2 m;
-    if (!isv) m = fold(turn, load_weight(w, lm));
-    bf16* dst = nullptr;           // rows of head h at dst + h * dst_hop
-    int64_t dst_hop = 0;
-    if (isq || !append_rows) {
-      bf16* o = static_cast<bf16*>(isq ? a.q_out : isv ? a.v_out : a.k_out);
-      dst_hop = (int64_t)a.N * D;
-      dst = o + ((int64_t)at.b * H * a.N + at.n) * D;
+    if (KIND != 2) m = fold(turn, load_weight<INTER>(w, lm));
+    bf16* dst = nullptr;
+    int64_t step = 0;
+    if (!kToCache) {
+      step = (int64_t)R * a.N * D;
+      dst = static_cast<bf16*>(KIND == 0 ? a.q_out : KIND == 1 ? a.k_out : a.v_out) +
+            (((int64_t)b * (KIND == 0 ? a.Hq : a.Hkv) + h) * a.N + n) * D + lm.ea;
     } else if (DST == kToPages && place.pid >= 0) {
-      dst_hop = (int64_t)a.page * D;
-      dst = static_cast<bf16*>(isv ? a.v_pages : a.k_pages) + ((int64_t)place.pid * a.Hkv * a.page + place.slot) * D;
+      step = (int64_t)R * a.page * D;
+      dst = static_cast<bf16*>(KIND == 1 ? a.k_pages : a.v_pages) +
+            (((int64_t)place.pid * a.Hkv + h) * a.page + place.slot) * D + lm.ea;
     }
-    for (; at.h < at.hend; at.h += R) {
+    const bool writes = dst != nullptr;
+    for (; left > 0; --left) {
       cp_async_wait<kRing - 1>();
-      const int h = at.h + row;
-      const bool live = h < at.hend && take;
-      const uint2* in = ring + slot_out * (2 * THREADS) + tid;
+      const bool live = h < hend;
       uint2 va = make_uint2(0, 0), vb = va;
       if (live) {
-        va = in[0];
-        vb = in[THREADS];
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(va.x), "=r"(va.y) : "r"(ring + out) : "memory");
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(vb.x), "=r"(vb.y) : "r"(ring + out + THREADS * 8) : "memory");
       }
-      slot_out = slot_out + 1 == kRing ? 0 : slot_out + 1;
+      out = (out + kStep) & (kRing * kStep - 1);
       load();
-      if (isv && DST != kToPagesFp8) {  // as it is
-        if (live && dst) {
-          bf16* o = dst + h * dst_hop;
-          *reinterpret_cast<uint2*>(o + lm.ea) = va;
-          *reinterpret_cast<uint2*>(o + lm.eb) = vb;
+      if (KIND == 2 && DST != kToPagesFp8) {  // as it is
+        if (live && writes) {
+          *reinterpret_cast<uint2*>(dst) = va;
+          *reinterpret_cast<uint2*>(dst + (lm.eb - lm.ea)) = vb;
         }
-        continue;
-      }
-      const Eight x = unpack(va, vb, lm.inter);
-      Eight z = x;
-      if (!isv) z = norm_rope<D>(x, w != nullptr, a.eps, m, lm.rot);
-      if (DST == kToPagesFp8 && !isq) {
-        // one new token a request: its 32-token block holds the tokens before it under the scale they have, which one
-        // lane reads and writes
-        const float need = need_scale(row_max<LPR>(largest(z)));
-        const bool mine = live && place.pid >= 0;
-        const int before = place.slot % kScaleTokens;
-        const int64_t head = (int64_t)place.pid * a.Hkv + h;
-        float* sc = (isv ? a.v_scale : a.k_scale) + head * (a.page / kScaleTokens) + place.slot / kScaleTokens;
-        float was = 0.f;
-        if (mine && before && lane == 0) was = clamp_scale(*sc);
-        was = __shfl_sync(0xFFFFFFFFu, was, 0, LPR);
-        if (mine) {
-          uint8_t* base = static_cast<uint8_t*>(isv ? a.v_pages : a.k_pages) + head * a.page * D;
-          const float now = fmaxf(need, was);
-          if (before && now != was)
-            for (int r = place.slot - before; r < place.slot; ++r) rescale_row<D>(base + r * D, lane * 8, was / now);
-          store_e4m3(base + place.slot * D, lm, z, 1.f / now);
-          if (lane == 0) *sc = now;
+      } else {
+        Eight z = unpack<INTER>(va, vb);
+        if (KIND != 2) z = norm_rope<D>(z, w != nullptr, a.eps, m, lm.rot);
+        if (kToCache && DST == kToPagesFp8) {
+          quantise(z, KIND == 1 ? a.k_pages : a.v_pages, KIND == 1 ? a.k_scale : a.v_scale, h, live);
+        } else if (live && writes) {
+          float y[8];
+          in_order<INTER>(z, y);
+          *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
+          *reinterpret_cast<uint2*>(dst + (lm.eb - lm.ea)) = make_uint2(pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
         }
-      } else if (live && dst) {
-        store_bf16(dst + h * dst_hop, lm, z);
       }
+      dst += step;
+      h += R;
     }
   }
-  cp_async_wait<0>();
-}
 
-template <int D, int DST>
-__global__ void __launch_bounds__(kRowThreads) qkv_rows_kernel(const __grid_constant__ QkvArgs a, const Shares sh) {
-  __shared__ uint2 ring[kRing * 2 * kRowThreads];
-  rows_of_items<D, DST, kRowThreads>(a, (int64_t)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32,
-                                     (int64_t)gridDim.x * (kRowThreads / 32), sh, ring);
+  // One new token a request: its 32-token block holds the tokens before it under the scale they have, which one lane
+  // reads and writes. The whole warp calls it.
+  __device__ __forceinline__ void quantise(const Eight& z, void* pages, float* scales, int h, bool live) {
+    const float need = need_scale(row_max<LPR>(largest(z)));
+    const bool mine = live && place.pid >= 0;
+    const int before = place.slot % kScaleTokens;
+    const int64_t head = (int64_t)place.pid * a.Hkv + h;
+    float* sc = scales + head * (a.page / kScaleTokens) + place.slot / kScaleTokens;
+    float was = 0.f;
+    if (mine && before && lane == 0) was = clamp_scale(*sc);
+    was = __shfl_sync(0xFFFFFFFFu, was, 0, LPR);
+    if (mine) {
+      uint8_t* base = static_cast<uint8_t*>(pages) + head * a.page * D;
+      const float now = fmaxf(need, was);
+      if (before && now != was)
+        for (int r = place.slot - before; r < place.slot; ++r) rescale_row<D>(base + r * D, lane * 8, was / now);
+      store_e4m3<INTER>(base + place.slot * D, lm, z, 1.f / now);
+      if (lane == 0) *sc = now;
+    }
+  }
+
+  __device__ __forceinline__ void run(int64_t warp) {
+    uint64_t f[4] = {0, 0, 0, 0};
+    if (a.inv_freq) lane_frequencies(a.inv_freq, lm, f);
+    for (int64_t item = warp; item < items; item += warps) {
+      const int64_t T = sh.groups == 1 ? item : item / sh.groups;
+      const int g = sh.groups == 1 ? 0 : (int)(item - T * sh.groups);
+      b = (int)((uint32_t)T / (uint32_t)a.N);
+      n = (int)((uint32_t)T - (uint32_t)b * (uint32_t)a.N);
+      if (DST != kToHeads && n >= new_tokens(a, b)) continue;  // no loads are under way for it either
+      const int64_t pos = (int64_t)n + (a.q_offset ? __ldg(a.q_offset + b) : 0);
+      turn = turn_at(f, lm, pos);
+      if (DST != kToHeads && hk) place = place_of(a, b, pos);
+      heads_of<0>(g);
+      heads_of<1>(g);
+      heads_of<2>(g);
+    }
+    cp_async_wait<0>();
+  }
+};
+
+template <int D, int DST, bool INTER>
+__global__ void __launch_bounds__(kRowThreads, kRowCtas) qkv_rows_kernel(const __grid_constant__ QkvArgs a, const __grid_constant__ Shares sh) {
+  __shared__ __align__(16) uint2 ring[kRing * 2 * kRowThreads];
+  const int64_t warp = (int64_t)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32;
+  RowWarp<D, DST, INTER, kRowThreads> w(a, sh, warp, (int64_t)gridDim.x * (kRowThreads / 32), ring);
+  w.run(warp);
 }
 
 // ------------------------------------------------------------------------------------------------
 // Append to e4m3 pages, several tokens a request. A CTA takes one 32-token block of one request and a share of its
-// KV heads: for each head, K and then V, its threads hold the block's new rows, agree on the largest magnitude, and
-// write scale and values; rows that the block held before are rescaled where the scale grew. CTAs behind those take
-// the query rows.
+// KV heads: for each head its threads hold the block's new K and V rows, agree on the two largest magnitudes (one
+// barrier), and write scales and values; rows that the block held before are rescaled where the scale grew. CTAs
+// behind those take the query rows.
 // ------------------------------------------------------------------------------------------------
 constexpr int kBlockThreads = 256;
 
-template <int D>
-__device__ __forceinline__ void append_block(const QkvArgs& a, int b, int j, int hk0, int hk1, uint2* ring,
-                                             float (*s_max)[kBlockThreads / 32]) {
-  constexpr int LPR = D / 8, SLOTS = kBlockThreads / LPR, RPT = kScaleTokens / SLOTS;
+// A head's rows of one block: the lane's values to e4m3 under the block's scale.
+template <int D, bool INTER, int RPT, int SLOTS>
+__device__ __forceinline__ void write_block(uint8_t* base, float* sc, float big, float was, int before, int slot,
+                                            const LaneMap& lm, const Eight (&z)[RPT], const bool (&in)[RPT], int lane) {
+  const float now = fmaxf(need_scale(big), was), inv = 1.f / now;
+  if (now != was)  // was = 0 where the block has no tokens yet: nothing to rescale
+    for (int i = slot; i < before; i += SLOTS) rescale_row<D>(base + i * D, lane * 8, was / now);
+#pragma unroll
+  for (int u = 0; u < RPT; ++u)
+    if (in[u]) store_e4m3<INTER>(base + (slot + u * SLOTS) * D, lm, z[u], inv);
+  if (threadIdx.x == 0) *sc = now;
+}
+
+template <int D, bool INTER>
+__device__ __forceinline__ void append_block(const QkvArgs& a, int b, int j, int hk0, int hk1, uint2* ring_mem,
+                                             uint32_t (*s_max)[2][kBlockThreads / 32]) {
+  constexpr int LPR = D / 8, SLOTS = kBlockThreads / LPR, RPT = kScaleTokens / SLOTS, kWarps = kBlockThreads / 32;
+  constexpr int kAhead = kRing / (2 * RPT), kStep = 2 * kBlockThreads * 8;
   const int tid = threadIdx.x, lane = tid % LPR, slot = tid / LPR;
+  const int64_t first = a.q_offset ? __ldg(a.q_offset + b) : 0;
   const int cnt = new_tokens(a, b);
-  const int64_t first = a.q_offset ? __ldg(a.q_offset + b) : 0, last = first + cnt;
   const int64_t p0 = ((first >> 5) + j) * kScaleTokens;
-  const int64_t lo = max(p0, first), hi = min(p0 + kScaleTokens, last);
+  const int64_t lo = max(p0, first), hi = min(p0 + kScaleTokens, first + cnt);
   if (lo >= hi) return;
-  const Place at0 = place_of(a, b, p0);
-  if (at0.pid < 0) return;
-  const LaneMap lm = lane_map<D>(lane, a.inv_freq ? a.rot : 0, a.inv_freq ? a.interleaved : 0);
-  const int before = (int)(lo - p0), units = 2 * (hk1 - hk0);  // K and V of each head
-  constexpr int kAhead = kRing / RPT;
-  const uint32_t my = smem_u32(ring + tid);
+  const LaneMap lm = lane_map<D, INTER>(lane, a.inv_freq ? a.rot : 0);
   bool in[RPT];
-  int64_t n[RPT];
+  const bf16 *kp[RPT], *vp[RPT];
 #pragma unroll
   for (int u = 0; u < RPT; ++u) {
     const int64_t pos = p0 + slot + u * SLOTS;
     in[u] = pos >= lo && pos < hi;
-    n[u] = in[u] ? pos - first : 0;
+    const int64_t n = in[u] ? pos - first : 0;
+    kp[u] = static_cast<const bf16*>(a.k.p) + b * a.k.sb + hk0 * a.k.sh + n * a.k.sn + lm.ea;
+    vp[u] = static_cast<const bf16*>(a.v.p) + b * a.v.sb + hk0 * a.v.sh + n * a.v.sn + lm.ea;
   }
-  auto load = [&](int x) {
-    if (x < units) {
-      const Rows& S = (x & 1) ? a.v : a.k;
-      const bf16* base = static_cast<const bf16*>(S.p) + b * S.sb + (hk0 + (x >> 1)) * S.sh;
+  const uint32_t ring = smem_u32(ring_mem) + tid * 8;
+  const int far = lm.eb - lm.ea, heads = hk1 - hk0;
+  uint32_t at_in = 0, at_out = 0;
+  int loaded = 0;
+  auto load = [&]() {  // K and V rows of the next head
+    if (loaded < heads) {
 #pragma unroll
       for (int u = 0; u < RPT; ++u) {
-        const uint32_t to = my + ((x % kAhead) * RPT + u) * (2 * kBlockThreads * 8);
         if (in[u]) {
-          cp_async_8(to, base + n[u] * S.sn + lm.ea);
-          cp_async_8(to + kBlockThreads * 8, base + n[u] * S.sn + lm.eb);
+          const uint32_t to = ring + at_in + u * kStep;
+          cp_async_8(to, kp[u]);
+          cp_async_8(to + kBlockThreads * 8, kp[u] + far);
+          cp_async_8(to + RPT * kStep, vp[u]);
+          cp_async_8(to + RPT * kStep + kBlockThreads * 8, vp[u] + far);
         }
+        kp[u] += a.k.sh;
+        vp[u] += a.v.sh;
       }
+      ++loaded;
     }
+    at_in = (at_in + 2 * RPT * kStep) & (kRing * kStep - 1);
     cp_async_commit();
   };
-#pragma unroll 1
-  for (int x = 0; x < kAhead; ++x) load(x);
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x) load();
+  const Place place = place_of(a, b, p0);
   Map2 m[RPT];
   {
     uint64_t f[4] = {0, 0, 0, 0};
     if (a.inv_freq) lane_frequencies(a.inv_freq, lm, f);
-    const Eight w = load_weight(a.wk, lm);
+    const Eight w = load_weight<INTER>(a.wk, lm);
 #pragma unroll
     for (int u = 0; u < RPT; ++u) m[u] = fold(turn_at(f, lm, p0 + slot + u * SLOTS), w);
   }
-  for (int x = 0; x < units; ++x) {
+  const int before = (int)(lo - p0), spp = a.page / kScaleTokens;
+  const int64_t head0 = (int64_t)place.pid * a.Hkv + hk0;
+  float* ks = a.k_scale + head0 * spp + place.slot / kScaleTokens;
+  float* vs = a.v_scale + head0 * spp + place.slot / kScaleTokens;
+  const int64_t at0 = (head0 * a.page + place.slot) * D;
+  uint8_t *kd = static_cast<uint8_t*>(a.k_pages) + at0, *vd = static_cast<uint8_t*>(a.v_pages) + at0;
+  for (int x = 0; x < (place.pid < 0 ? 0 : heads); ++x) {
     cp_async_wait<kAhead - 1>();
-    const int hk = hk0 + (x >> 1);
-    const int64_t head = (int64_t)at0.pid * a.Hkv + hk;
-    float* sc = ((x & 1) ? a.v_scale : a.k_scale) + head * (a.page / kScaleTokens) + at0.slot / kScaleTokens;
-    float was = 0.f;
-    if (before) was = clamp_scale(*sc);
-    Eight z[RPT];
-    float big = 0.f;
+    float k_was = 0.f, v_was = 0.f;
+    if (before) {
+      k_was = clamp_scale(*ks);
+      v_was = clamp_scale(*vs);
+    }
+    Eight zk[RPT], zv[RPT];
+    float k_big = 0.f, v_big = 0.f;
 #pragma unroll
     for (int u = 0; u < RPT; ++u) {
-      uint2 va = make_uint2(0, 0), vb = va;
+      uint2 ka = make_uint2(0, 0), kb = ka, va = ka, vb = ka;
       if (in[u]) {
-        const uint2* r = ring + ((x % kAhead) * RPT + u) * (2 * kBlockThreads) + tid;
-        va = r[0];
-        vb = r[kBlockThreads];
+        const uint32_t from = ring + at_out + u * kStep;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(ka.x), "=r"(ka.y) : "r"(from) : "memory");
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(kb.x), "=r"(kb.y) : "r"(from + kBlockThreads * 8) : "memory");
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(va.x), "=r"(va.y) : "r"(from + RPT * kStep) : "memory");
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(vb.x), "=r"(vb.y)
+                     : "r"(from + RPT * kStep + kBlockThreads * 8)
+                     : "memory");
       }
-      z[u] = unpack(va, vb, lm.inter);
-      if (!(x & 1)) z[u] = norm_rope<D>(z[u], a.wk != nullptr, a.eps, m[u], lm.rot);
-      if (in[u]) big = fmaxf(big, largest(z[u]));  // rows of zeros may be NaN without an eps
+      zk[u] = norm_rope<D>(unpack<INTER>(ka, kb), a.wk != nullptr, a.eps, m[u], lm.rot);
+      zv[u] = unpack<INTER>(va, vb);
+      if (in[u]) {  // rows of zeros may be NaN without an eps
+        k_big = fmaxf(k_big, largest(zk[u]));
+        v_big = fmaxf(v_big, largest(zv[u]));
+      }
     }
-    load(x + kAhead);
-    big = row_max<32>(big);
-    if ((tid & 31) == 0) s_max[x & 1][tid >> 5] = big;
-    __syncthreads();  // the old scale is read, too
+    at_out = (at_out + 2 * RPT * kStep) & (kRing * kStep - 1);
+    load();
+    // magnitudes order as their bits do
+    const uint32_t kw = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(k_big));
+    const uint32_t vw = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v_big));
+    if ((tid & 31) == 0) {
+      s_max[x & 1][0][tid >> 5] = kw;
+      s_max[x & 1][1][tid >> 5] = vw;
+    }
+    __syncthreads();  // the old scales are read, too
+    uint32_t km = 0, vm = 0;
 #pragma unroll
-    for (int w = 0; w < kBlockThreads / 32; ++w) big = fmaxf(big, s_max[x & 1][w]);
-    uint8_t* base = static_cast<uint8_t*>((x & 1) ? a.v_pages : a.k_pages) + (head * a.page + at0.slot) * D;
-    const float now = fmaxf(need_scale(big), was), inv = 1.f / now;
-    if (before && now != was)
-      for (int i = slot; i < before; i += SLOTS) rescale_row<D>(base + i * D, lane * 8, was / now);
-#pragma unroll
-    for (int u = 0; u < RPT; ++u)
-      if (in[u]) store_e4m3(base + (slot + u * SLOTS) * D, lm, z[u], inv);
-    if (tid == 0) *sc = now;
+    for (int w = 0; w < kWarps; ++w) {
+      km = max(km, s_max[x & 1][0][w]);
+      vm = max(vm, s_max[x & 1][1][w]);
+    }
+    write_block<D, INTER, RPT, SLOTS>(kd, ks, __uint_as_float(km), k_was, before, slot, lm, zk, in, lane);
+    write_block<D, INTER, RPT, SLOTS>(vd, vs, __uint_as_float(vm), v_was, before, slot, lm, zv, in, lane);
+    ks += spp;
+    vs += spp;
+    kd += (int64_t)a.page * D;
+    vd += (int64_t)a.page * D;
   }
   cp_async_wait<0>();
 }
 
-template <int D>
-__global__ void __launch_bounds__(kBlockThreads)
+template <int D, bool INTER>
+__global__ void __launch_bounds__(kBlockThreads, 3)
     append_fp8_kernel(const __grid_constant__ QkvArgs a, int blocks, int heads_per_cta, int groups) {
-  __shared__ uint2 ring[kRing * 2 * kBlockThreads];
-  __shared__ float s_max[2][kBlockThreads / 32];
+  __shared__ __align__(16) uint2 ring[kRing * 2 * kBlockThreads];
+  __shared__ __align__(16) uint32_t s_max[2][2][kBlockThreads / 32];
   const int64_t kv_ctas = (int64_t)a.B * blocks * groups;
   if ((int64_t)blockIdx.x < kv_ctas) {
     const int x = blockIdx.x, gi = x % groups, bj = x / groups;
     const int hk0 = gi * heads_per_cta;
-    append_block<D>(a, bj / blocks, bj % blocks, hk0, min(a.Hkv, hk0 + heads_per_cta), ring, s_max);
+    append_block<D, INTER>(a, bj / blocks, bj % blocks, hk0, min(a.Hkv, hk0 + heads_per_cta), ring, s_max);
   } else {
-    QkvArgs q = a;
-    q.k.p = q.v.p = nullptr;
-    rows_of_items<D, kToPages, kBlockThreads>(q, ((int64_t)blockIdx.x - kv_ctas) * (kBlockThreads / 32) + threadIdx.x / 32,
-                                              ((int64_t)gridDim.x - kv_ctas) * (kBlockThreads / 32), Shares{1, a.Hq, a.Hkv}, ring);
+    constexpr int kWarps = kBlockThreads / 32;
+    const int64_t warp = ((int64_t)blockIdx.x - kv_ctas) * kWarps + threadIdx.x / 32;
+    const Shares all{1, a.Hq, 0};  // the query rows alone
+    RowWarp<D, kToPages, INTER, kBlockThreads> w(a, all, warp, ((int64_t)gridDim.x - kv_ctas) * kWarps, ring);
+    w.run(warp);
   }
 }
 
@@ -611,28 +691,29 @@ constexpr int kBwdThreads = 256;
 constexpr int kBwdRing = 6;
 constexpr int kBwdRingBytes = kBwdRing * kBwdThreads * 48;  // a row's 48 bytes a lane: 32 of dz, 16 of x
 
-template <bool F32>
+template <bool F32, bool INTER>
 __device__ __forceinline__ void store_grad(void* p, int64_t at, const LaneMap& m, const Eight& g) {
   if (F32) {
     float y[8];
-    in_order(g, m.inter, y);
+    in_order<INTER>(g, y);
     float* o = static_cast<float*>(p) + at;
     *reinterpret_cast<float4*>(o + m.ea) = make_float4(y[0], y[1], y[2], y[3]);
     *reinterpret_cast<float4*>(o + m.eb) = make_float4(y[4], y[5], y[6], y[7]);
   } else {
-    store_bf16(static_cast<bf16*>(p) + at, m, g);
+    store_bf16<INTER>(static_cast<bf16*>(p) + at, m, g);
   }
 }
 
-template <int D, bool F32>
-__global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_constant__ QkvBwdArgs a, const Shares sh) {
+template <int D, bool F32, bool INTER>
+__global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_constant__ QkvBwdArgs a,
+                                                                 const __grid_constant__ Shares sh) {
   constexpr int LPR = D / 8, R = 32 / LPR, SLOTS = kBwdThreads / LPR;
   extern __shared__ uint4 ring[];
   const int tid = threadIdx.x, lane = tid % LPR, row = (tid % 32) / LPR;
   const int64_t items = (int64_t)a.B * a.N * sh.groups;
   const int64_t warp = (int64_t)blockIdx.x * (kBwdThreads / 32) + tid / 32, warps = (int64_t)gridDim.x * (kBwdThreads / 32);
-  auto heads = [&](int kind) { return kind == 0 ? (a.dq ? a.Hq : 0) : kind == 1 ? (a.dk ? a.Hkv : 0) : (a.dv ? a.Hkv : 0); };
-  const LaneMap lm = lane_map<D>(lane, a.inv_freq ? a.rot : 0, a.inv_freq ? a.interleaved : 0);
+  const int hq = a.dq ? a.Hq : 0, hk = a.dk ? a.Hkv : 0, hv = a.dv ? a.Hkv : 0;
+  const LaneMap lm = lane_map<D, INTER>(lane, a.inv_freq ? a.rot : 0);
   Cursor ld{warp, 0, 0, -1, 0, 0};
   const float* dy = nullptr;
   const bf16* src = nullptr;
@@ -643,7 +724,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_co
   auto load = [&]() {
     if (more) {
       if (ld.h >= ld.hend) {
-        more = next_kind<R>(ld, items, warps, a.N, sh, heads);
+        more = next_kind(ld, items, warps, a.N, sh, hq, hk, hv);
         if (more) {
           const int H = ld.kind == 0 ? a.Hq : a.Hkv;
           dy = (ld.kind == 0 ? a.dq : ld.kind == 1 ? a.dk : a.dv) + (((int64_t)ld.b * H + ld.h + row) * a.N + ld.n) * D;
@@ -682,14 +763,14 @@ __global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_co
   int slot_out = 0;
   Turn turn;
   int64_t item_of_turn = -1;
-  while (next_kind<R>(at, items, warps, a.N, sh, heads)) {
+  while (next_kind(at, items, warps, a.N, sh, hq, hk, hv)) {
     const bool isq = at.kind == 0, isv = at.kind == 2;
     if (item_of_turn != at.item) {
       item_of_turn = at.item;
       turn = turn_at(f, lm, (int64_t)at.n + (a.q_offset ? __ldg(a.q_offset + at.b) : 0));
     }
     const float* wp = isq ? a.wq : isv ? nullptr : a.wk;
-    const Eight w = load_weight(wp, lm);
+    const Eight w = load_weight<INTER>(wp, lm);
     const Rows& S = isq ? a.dq_in : isv ? a.dv_in : a.dk_in;
     const int64_t base = at.b * S.sb + at.n * S.sn;
     Eight sum;
@@ -709,7 +790,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_co
       }
       slot_out = slot_out + 1 == kBwdRing ? 0 : slot_out + 1;
       load();
-      Eight g = unpack_f32(ga, gb, lm.inter);
+      Eight g = unpack_f32<INTER>(ga, gb);
       if (!isv) {
         const Eight d = g;
 #pragma unroll
@@ -718,7 +799,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_co
           g.b[j] = f2_fma(d.b[j], turn.c[j], f2_neg(f2_mul(d.a[j], turn.s[j])));
         }
         if (wp) {  // the same for the whole warp
-          const Eight x = unpack(make_uint2(xr.x, xr.y), make_uint2(xr.z, xr.w), lm.inter);
+          const Eight x = unpack<INTER>(make_uint2(xr.x, xr.y), make_uint2(xr.z, xr.w));
           const float r = row_rsqrt<D>(x, a.eps);
           Eight gx, wgx;
           const uint64_t rr = live ? f2_pack(r, r) : 0ull;
@@ -743,7 +824,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_co
           }
         }
       }
-      if (live) store_grad<F32>(S.p, base + h * S.sh, lm, g);
+      if (live) store_grad<F32, INTER>(S.p, base + h * S.sh, lm, g);
     }
     if (wp) {
 #pragma unroll
@@ -765,7 +846,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_co
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
     float y[8];
-    in_order(dw[which], lm.inter, y);
+    in_order<INTER>(dw[which], y);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       s_dw[tid / LPR][lm.ea + e] = y[e];
@@ -815,9 +896,10 @@ template <int D, int DST>
 cudaError_t run_rows(const QkvArgs& a, cudaStream_t st) {
   constexpr int kWarps = kRowThreads / 32;
   const int64_t tokens = (int64_t)a.B * a.N;
-  const Shares sh = shares(tokens, kSms * 8 * kWarps, a.Hq, a.Hkv, 32 / (D / 8));
-  const int64_t ctas = std::min<int64_t>((tokens * sh.groups + kWarps - 1) / kWarps, kSms * 8);
-  qkv_rows_kernel<D, DST><<<(unsigned)ctas, kRowThreads, 0, st>>>(a, sh);
+  const Shares sh = shares(tokens, kSms * kRowCtas * kWarps, a.Hq, a.Hkv, 32 / (D / 8));
+  const int64_t ctas = std::min<int64_t>((tokens * sh.groups + kWarps - 1) / kWarps, kSms * kRowCtas);
+  auto kern = a.interleaved ? qkv_rows_kernel<D, DST, true> : qkv_rows_kernel<D, DST, false>;
+  kern<<<(unsigned)ctas, kRowThreads, 0, st>>>(a, sh);
   return cudaGetLastError();
 }
 
@@ -827,12 +909,13 @@ cudaError_t run_append(const QkvArgs& a, cudaStream_t st) {
   if (a.N == 1) return run_rows<D, kToPagesFp8>(a, st);
   const int blocks = (a.N + 2 * kScaleTokens - 2) / kScaleTokens;
   int groups = 1;
-  while (groups < a.Hkv && (int64_t)a.B * blocks * groups < 4 * kSms) ++groups;
+  while (groups < a.Hkv && (int64_t)a.B * blocks * groups < 2 * kSms) ++groups;
   const int hpc = (a.Hkv + groups - 1) / groups;
   groups = (a.Hkv + hpc - 1) / hpc;
   const int64_t q_items = a.q.p ? (int64_t)a.B * a.N : 0, per = kBlockThreads / 32;
-  const int64_t ctas = (int64_t)a.B * blocks * groups + std::min<int64_t>((q_items + per - 1) / per, kSms * 4);
-  append_fp8_kernel<D><<<(unsigned)ctas, kBlockThreads, 0, st>>>(a, blocks, hpc, groups);
+  const int64_t ctas = (int64_t)a.B * blocks * groups + std::min<int64_t>((q_items + per - 1) / per, kSms * 16);
+  auto kern = a.interleaved ? append_fp8_kernel<D, true> : append_fp8_kernel<D, false>;
+  kern<<<(unsigned)ctas, kBlockThreads, 0, st>>>(a, blocks, hpc, groups);
   return cudaGetLastError();
 }
 
@@ -841,7 +924,8 @@ cudaError_t run_bwd(const QkvBwdArgs& a, cudaStream_t st) {
   const int64_t tokens = (int64_t)a.B * a.N;
   const int ctas = qk_bwd_ctas(tokens);
   const Shares sh = shares(tokens, (int64_t)ctas * (kBwdThreads / 32), a.Hq, a.Hkv, 32 / (D / 8));
-  auto kern = a.grad_f32 ? qkv_bwd_kernel<D, true> : qkv_bwd_kernel<D, false>;
+  auto kern = a.grad_f32 ? (a.interleaved ? qkv_bwd_kernel<D, true, true> : qkv_bwd_kernel<D, true, false>)
+                         : (a.interleaved ? qkv_bwd_kernel<D, false, true> : qkv_bwd_kernel<D, false, false>);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdRingBytes);
   if (e != cudaSuccess) return e;
   kern<<<ctas, kBwdThreads, kBwdRingBytes, st>>>(a, sh);

@@ -561,9 +561,12 @@ def _same(t: Optional[torch.Tensor], shape, dtype, device, what: str):
 
 
 def _check_qk_rule(rule: Optional[QkRule], d: int, device):
-    for t, n in zip(rule._tensors if rule is not None else (), (d, d, None)):
-        if t is not None and (t.device != device or (n is not None and t.numel() != n)):
-            raise ValueError(f"the rule's tensors must be on {device}, its weights of {d} elements")
+    if rule is None:
+        return
+    wq, wk, f = rule._tensors
+    if ((wq is not None and (wq.device != device or wq.shape != (d,))) or
+            (wk is not None and (wk.device != device or wk.shape != (d,))) or (f is not None and f.device != device)):
+        raise ValueError(f"the rule's tensors must be on {device}, its weights of {d} elements")
 
 
 def _ref(s):
@@ -576,11 +579,13 @@ def _at(t: Optional[torch.Tensor]):
 
 
 def _call(device, fn, *args) -> int:
-    """fn(*args, stream) on `device`'s current stream, with that device current."""
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(device))
+    """fn(*args, stream) on `device`'s current stream, with that device current. (The stream's handle is taken without the
+    torch.cuda.Stream object around it, which costs as much as half the launch.)"""
+    i = device.index
+    if i == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(i))
     with torch.cuda.device(device):
-        return fn(*args, _stream(device))
+        return fn(*args, torch._C._cuda_getCurrentRawStream(i))
 
 
 def _qkv_shape(q, k, v):
@@ -601,19 +606,22 @@ def qk_norm_rope(q: Optional[torch.Tensor], k: Optional[torch.Tensor], v: Option
     -> (q_out [B,Hq,N,d], k_out, v_out [B,Hkv,N,d]), normalised and rotated, as fa_flex_forward reads them."""
     B, Hq, Hkv, N, d, dev = _qkv_shape(q, k, v)
     bf = torch.bfloat16
-    rows = [_rows(t, (B, N, h, d), bf, dev, n) for t, h, n in ((q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v"))]
-    outs = []
-    for t, o, h, n in ((q, q_out, Hq, "q_out"), (k, k_out, Hkv, "k_out"), (v, v_out, Hkv, "v_out")):
+    rq, rk, rv = (_rows(q, (B, N, Hq, d), bf, dev, "q"), _rows(k, (B, N, Hkv, d), bf, dev, "k"),
+                  _rows(v, (B, N, Hkv, d), bf, dev, "v"))
+
+    def out(t, o, h, name):
         if t is None:
-            o = None
-        elif o is None:
-            o = torch.empty((B, h, N, d), dtype=bf, device=dev)
-        outs.append(_same(o, (B, h, N, d), bf, dev, n))
+            return None
+        if o is None:
+            return torch.empty((B, h, N, d), dtype=bf, device=dev)
+        return _same(o, (B, h, N, d), bf, dev, name)
+
+    q_out, k_out, v_out = out(q, q_out, Hq, "q_out"), out(k, k_out, Hkv, "k_out"), out(v, v_out, Hkv, "v_out")
     _check_qk_rule(rule, d, dev)
     _same(q_offset, (B,), torch.int32, dev, "q_offset")
-    _check(_call(dev, load().fa_qk_norm_rope, *map(_ref, rows), ctypes.byref(rule), _at(q_offset), *map(_at, outs), B, Hq,
-                 Hkv, N, d), "fa_qk_norm_rope")
-    return tuple(outs)
+    _check(_call(dev, load().fa_qk_norm_rope, _ref(rq), _ref(rk), _ref(rv), ctypes.byref(rule), _at(q_offset), _at(q_out),
+                 _at(k_out), _at(v_out), B, Hq, Hkv, N, d), "fa_qk_norm_rope")
+    return q_out, k_out, v_out
 
 
 def qk_norm_rope_backward_workspace_bytes(B: int, N: int, d: int) -> int:
@@ -673,29 +681,38 @@ def _append(q, k, v, k_pages, v_pages, k_scale, v_scale, page_table, rule, q_off
     B, Hq, Hkv, N, d, dev = _qkv_shape(q, k, v)
     bf, i32 = torch.bfloat16, torch.int32
     fp8 = k_scale is not None
-    rows = [_rows(t, (B, N, h, d), bf, dev, n) for t, h, n in ((q, Hq, "q"), (k, Hkv, "k"), (v, Hkv, "v"))]
+    rq, rk, rv = (_rows(q, (B, N, Hq, d), bf, dev, "q"), _rows(k, (B, N, Hkv, d), bf, dev, "k"),
+                  _rows(v, (B, N, Hkv, d), bf, dev, "v"))
     if k_pages.dim() != 4 or page_table.dim() != 2:
         raise ValueError("pages must be [P, Hkv, page, d] and page_table [B, max_pages]")
     P, _, page, _ = k_pages.shape
-    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _same(t, (P, Hkv, page, d), torch.float8_e4m3fn if fp8 else bf, dev, n)
+    max_pages, pages, kind = page_table.shape[1], (P, Hkv, page, d), torch.float8_e4m3fn if fp8 else bf
+    _same(k_pages, pages, kind, dev, "k_pages")
+    _same(v_pages, pages, kind, dev, "v_pages")
     if fp8:
-        for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            _same(t, (P, Hkv, page // KV_SCALE_TOKENS), torch.float32, dev, n)
-    _same(page_table, (B, page_table.shape[1]), i32, dev, "page_table")
+        scales = (P, Hkv, page // KV_SCALE_TOKENS)
+        _same(k_scale, scales, torch.float32, dev, "k_scale")
+        _same(v_scale, scales, torch.float32, dev, "v_scale")
+    _same(page_table, (B, max_pages), i32, dev, "page_table")
     _same(q_offset, (B,), i32, dev, "q_offset")
     _same(n_new, (B,), i32, dev, "n_new")
     _same(status, (1,), i32, dev, "status")
-    if q is not None and q_out is None:
+    if q is None:
+        q_out = None
+    elif q_out is None:
         q_out = torch.empty((B, Hq, N, d), dtype=bf, device=dev)
-    _same(q_out, (B, Hq, N, d), bf, dev, "q_out")
+    else:
+        _same(q_out, (B, Hq, N, d), bf, dev, "q_out")
     _check_qk_rule(rule, d, dev)
     lib = load()
-    scales = (_at(k_scale), _at(v_scale)) if fp8 else ()
-    _check(_call(dev, lib.fa_kv_append_fp8 if fp8 else lib.fa_kv_append, *map(_ref, rows), _ref(rule), _at(q_offset),
-                 _at(n_new), _at(q_out if q is not None else None), _at(k_pages), _at(v_pages), *scales,
-                 _at(page_table), P, page, page_table.shape[1], B, Hq, Hkv, N, d, _at(status)),
-           "fa_kv_append_fp8" if fp8 else "fa_kv_append")
+    if fp8:
+        _check(_call(dev, lib.fa_kv_append_fp8, _ref(rq), _ref(rk), _ref(rv), _ref(rule), _at(q_offset), _at(n_new),
+                     _at(q_out), k_pages.data_ptr(), v_pages.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                     page_table.data_ptr(), P, page, max_pages, B, Hq, Hkv, N, d, _at(status)), "fa_kv_append_fp8")
+    else:
+        _check(_call(dev, lib.fa_kv_append, _ref(rq), _ref(rk), _ref(rv), _ref(rule), _at(q_offset), _at(n_new), _at(q_out),
+                     k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), P, page, max_pages, B, Hq, Hkv, N, d,
+                     _at(status)), "fa_kv_append")
     return q_out
 
 
@@ -729,23 +746,23 @@ def _check_fp8_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, B, d):
         raise ValueError("q must be a contiguous bf16 CUDA tensor")
     if k_pages.dim() != 4 or page_table.dim() != 2:
         raise ValueError("pages must be [P, Hkv, page, d] and page_table [B, max_pages]")
-    P, Hkv, page, _ = k_pages.shape
     dev = q.device
-    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _same(t, (P, Hkv, page, d), torch.float8_e4m3fn, dev, n)
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _same(t, (P, Hkv, page // KV_SCALE_TOKENS), torch.float32, dev, n)
-    _same(page_table, (B, page_table.shape[1]), torch.int32, dev, "page_table")
-    return P, Hkv, page, page_table.shape[1], dev
+    P, Hkv, page, _ = shape = k_pages.shape
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    _same(k_pages, (P, Hkv, page, d), f8, dev, "k_pages")
+    _same(v_pages, shape, f8, dev, "v_pages")
+    scales = (P, Hkv, page // KV_SCALE_TOKENS)
+    _same(k_scale, scales, f32, dev, "k_scale")
+    _same(v_scale, scales, f32, dev, "v_scale")
+    max_pages = page_table.shape[1]
+    _same(page_table, (B, max_pages), torch.int32, dev, "page_table")
+    return P, Hkv, page, max_pages, dev
 
 
 def _outputs(shape, dev, out, lse, out_dtype):
-    if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
-    if lse is None:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    _same(out, shape, out.dtype, dev, "out")
-    _same(lse, shape[:-1], torch.float32, dev, "lse")
+    out = torch.empty(shape, dtype=out_dtype, device=dev) if out is None else _same(out, shape, out.dtype, dev, "out")
+    rows = shape[:-1]
+    lse = torch.empty(rows, dtype=torch.float32, device=dev) if lse is None else _same(lse, rows, torch.float32, dev, "lse")
     return out, lse
 
 
