@@ -841,7 +841,7 @@ def load_traffic(wl):
         with open(p) as f:
             t = json.load(f)
         h = hashlib.sha1()
-        for name in ("fwd_tc5.cu", "fa_internal.cuh"):
+        for name in ("fwd_tc5.cu", "fwd_tiles.cuh", "fa_internal.cuh"):
             with open(os.path.join(ROOT, "block_sparse_masked_create_gb300", "csrc", name), "rb") as f:
                 h.update(f.read())
         if h.hexdigest() != t.get("source_sha1"):

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kWarps * 32)
               ix = ix < 0 ? 0 : (ix > hi ? hi : ix);
               x += __ldg(a.score.rel + (size_t)(hk * g + (up ? rb : ra)) * (size_t)(hi + 1) + ix);
             }
-            if (a.score.softcap > 0.f) x = softcap_apply(x, a.score.softcap, a.score.inv_softcap);
+            if (a.score.softcap > 0.f) x = softcap_exact(x, a.score.softcap, a.score.inv_softcap);
             x *= kLog2e;
           }
           if (!((bits >> col) & 1u)) x = -INFINITY;

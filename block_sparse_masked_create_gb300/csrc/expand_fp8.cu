@@ -15,19 +15,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// first key position that no row of batch b sees, by the causal and prefix bounds of the rule's terms
-__device__ __forceinline__ int64_t key_end(const ExpandArgs& a, int b) {
-  const int64_t last = (int64_t)a.q_len - 1 + (a.rule.q_offset ? __ldg(a.rule.q_offset + (a.mask.Bm > 1 ? b : 0)) : 0);
-  int64_t end = 0;
-  for (int t = 0; t < a.rule.n_terms; ++t) {
-    int64_t hi = a.kv_len;
-    if (a.rule.t[t].causal) hi = min(hi, last + 1);
-    if (a.rule.t[t].pre != INT64_MAX) hi = min(hi, a.rule.t[t].pre);
-    end = max(end, hi);
-  }
-  return end;
-}
-
 // CTA: one 32-token block of one (batch row, KV head), K and V
 template <int D>
 __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant__ ExpandArgs a) {
@@ -43,7 +30,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
     listed = listed || __ldg(M.q_num + col) + __ldg(M.full_q_num + col) > 0;
   }
   if (!listed) return;  // the forward reads nothing of it
-  const int64_t end = min(key_end(a, b), (int64_t)a.kv_len);
+  const int64_t end = key_end(a.rule, M.Bm, b, a.q_len, a.kv_len);
   const int pid = __ldg(a.page_table + (size_t)b * a.max_pages + j0 / a.page);
   const bool have = pid >= 0 && pid < a.n_pages_total && j0 < end;
   if (!have && j0 < end) report(a.status, FA_ERR_DEVICE_CHECK);

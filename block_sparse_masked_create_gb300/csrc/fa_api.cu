@@ -849,26 +849,9 @@ static bool split_layout(const fa_block_mask* bm, int32_t B, int32_t Hq, int32_t
   return true;
 }
 
-size_t fa_forward_split_workspace_bytes(const fa_block_mask* bm, int32_t B, int32_t Hq, int32_t d,
-                                        int32_t chunk_blocks) {
-  SplitLayout L;
-  return split_layout(bm, B, Hq, d, chunk_blocks, &L) ? L.total : 0;
-}
-
-fa_status fa_flex_forward_split(const void* q, const void* k, const void* v, const fa_block_mask* bm,
-                                const fa_score_rule* score_rule, float scale, void* out, int32_t out_dtype,
-                                float* lse, int32_t B, int32_t Hq, int32_t Hkv, int32_t Q_LEN, int32_t KV_LEN,
-                                int32_t d, int32_t chunk_blocks, void* workspace, size_t workspace_bytes,
-                                int32_t* dev_status, fa_stream_t stream) {
-  int s = check_forward(q, k, v, bm, out, lse, B, Hq, Hkv, Q_LEN, KV_LEN, d);
-  if (s != FA_OK) return (fa_status)s;
-  if (out_dtype != FA_OUT_BF16 && out_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
-  if (bm->bq != 128 || bm->bk != 128) return FA_ERR_UNSUPPORTED;
-  if (chunk_blocks < 1 || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return FA_ERR_INVALID_ARG;
-  SplitLayout L;
-  if (!split_layout(bm, B, Hq, d, chunk_blocks, &L)) return FA_ERR_SHAPE;
-  if (workspace_bytes < L.total) return FA_ERR_BUFFER_TOO_SMALL;
-  uint8_t* w = static_cast<uint8_t*>(workspace);
+// Cuts the mask's rows into the workspace's tables (enqueued on `st`).
+static int build_split(const fa_block_mask* bm, int32_t Q_LEN, int32_t KV_LEN, int32_t chunk_blocks, const SplitLayout& L,
+                       uint8_t* w, cudaStream_t st, SplitPlan* out_plan) {
   MaskOut S;
   std::memset(&S, 0, sizeof(S));
   S.Bm = bm->Bm;
@@ -893,9 +876,8 @@ fa_status fa_flex_forward_split(const void* q, const void* k, const void* v, con
   D.row_order = reinterpret_cast<int32_t*>(w + L.off_order);
   D.kv_idx = reinterpret_cast<int32_t*>(w + L.off_idx);
   D.full_kv_idx = reinterpret_cast<int32_t*>(w + L.off_fidx);
-  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (launch_mask_split(S, chunk_blocks, L.ncm, D, st) != cudaSuccess) return FA_ERR_CUDA;
-  SplitPlan P;
+  SplitPlan& P = *out_plan;
   std::memset(&P, 0, sizeof(P));
   P.mask.Bm = D.Bm;
   P.mask.Hm = D.Hm;
@@ -912,6 +894,32 @@ fa_status fa_flex_forward_split(const void* q, const void* k, const void* v, con
   P.ncm = L.ncm;
   P.o_part = reinterpret_cast<float*>(w + L.off_o);
   P.lse_part = reinterpret_cast<float*>(w + L.off_lse);
+  return FA_OK;
+}
+
+size_t fa_forward_split_workspace_bytes(const fa_block_mask* bm, int32_t B, int32_t Hq, int32_t d,
+                                        int32_t chunk_blocks) {
+  SplitLayout L;
+  return split_layout(bm, B, Hq, d, chunk_blocks, &L) ? L.total : 0;
+}
+
+fa_status fa_flex_forward_split(const void* q, const void* k, const void* v, const fa_block_mask* bm,
+                                const fa_score_rule* score_rule, float scale, void* out, int32_t out_dtype,
+                                float* lse, int32_t B, int32_t Hq, int32_t Hkv, int32_t Q_LEN, int32_t KV_LEN,
+                                int32_t d, int32_t chunk_blocks, void* workspace, size_t workspace_bytes,
+                                int32_t* dev_status, fa_stream_t stream) {
+  int s = check_forward(q, k, v, bm, out, lse, B, Hq, Hkv, Q_LEN, KV_LEN, d);
+  if (s != FA_OK) return (fa_status)s;
+  if (out_dtype != FA_OUT_BF16 && out_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
+  if (bm->bq != 128 || bm->bk != 128) return FA_ERR_UNSUPPORTED;
+  if (chunk_blocks < 1 || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return FA_ERR_INVALID_ARG;
+  SplitLayout L;
+  if (!split_layout(bm, B, Hq, d, chunk_blocks, &L)) return FA_ERR_SHAPE;
+  if (workspace_bytes < L.total) return FA_ERR_BUFFER_TOO_SMALL;
+  SplitPlan P;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  s = build_split(bm, Q_LEN, KV_LEN, chunk_blocks, L, static_cast<uint8_t*>(workspace), st, &P);
+  if (s != FA_OK) return (fa_status)s;
   s = forward_impl(false, q, k, v, bm, score_rule, scale, out, out_dtype, lse, B, Hq, Hkv, Q_LEN, KV_LEN, d,
                    dev_status, nullptr, stream, PagedKV{}, &P);
   if (s != FA_OK) return (fa_status)s;
@@ -1195,25 +1203,33 @@ fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_p
   return (fa_status)launch_decode_fp8(A, reinterpret_cast<cudaStream_t>(stream));
 }
 
+constexpr int64_t kDirectTiles = 16;
 struct PagedFp8Plan {
+  bool direct;
   int32_t chunk;  // 0: rows are not cut
-  size_t kv_bytes, off_split, total;
+  SplitLayout split;
+  size_t kv_bytes, total;
 };
 
-static int paged_fp8_plan(const fa_block_mask* bm, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, int32_t chunk_blocks,
-                          PagedFp8Plan* P) {
+static int paged_fp8_plan(const fa_block_mask* bm, const fa_score_rule* score, int32_t B, int32_t Hq, int32_t Hkv,
+                          int32_t d, int32_t chunk_blocks, PagedFp8Plan* P) {
   if (!bm || chunk_blocks < -1) return FA_ERR_INVALID_ARG;
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || bm->kv_len < 1 || bm->nq < 1 || bm->nk < 1) return FA_ERR_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
-  P->kv_bytes = align256((size_t)B * Hkv * bm->kv_len * d * 2);
-  P->off_split = 2 * P->kv_bytes;
-  P->total = P->off_split;
+  const bool big = bm->bq == 128 && bm->bk == 128;
+  P->direct = big && ((int64_t)bm->nq * (Hq / Hkv) <= kDirectTiles || (score && score->softcap > 0.f));
   P->chunk = 0;
+  P->kv_bytes = 0;
+  P->total = 256;
+  if (!P->direct) {
+    P->kv_bytes = align256((size_t)B * Hkv * bm->kv_len * d * 2);
+    P->total = 2 * P->kv_bytes;
+  }
   if (chunk_blocks > 0) {
-    if (bm->bq != 128 || bm->bk != 128) return FA_ERR_UNSUPPORTED;
+    if (!big) return FA_ERR_UNSUPPORTED;
     P->chunk = chunk_blocks;
-  } else if (chunk_blocks == 0 && bm->bq == 128 && bm->bk == 128) {
-    // a CTA takes two query blocks; cut rows only where there are fewer CTAs than SMs, into as many chunks as fill them
+  } else if (chunk_blocks == 0 && big) {
+    // a CTA takes two query blocks; rows are cut only where there are fewer CTAs than SMs, into as many chunks as fill them
     const int64_t ctas = std::max<int64_t>(1, (int64_t)B * Hq * bm->nq / 2);
     if (ctas < 152 && bm->nk >= 32) {
       const int64_t parts = std::min<int64_t>(152 / ctas, bm->nk / 16);
@@ -1221,17 +1237,16 @@ static int paged_fp8_plan(const fa_block_mask* bm, int32_t B, int32_t Hq, int32_
     }
   }
   if (P->chunk) {
-    const size_t n = fa_forward_split_workspace_bytes(bm, B, Hq, d, P->chunk);
-    if (!n) return FA_ERR_SHAPE;
-    P->total += n;
+    if (!split_layout(bm, B, Hq, d, P->chunk, &P->split)) return FA_ERR_SHAPE;
+    P->total = 2 * P->kv_bytes + P->split.total;
   }
   return FA_OK;
 }
 
-size_t fa_forward_paged_fp8_workspace_bytes(const fa_block_mask* bm, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
-                                            int32_t chunk_blocks) {
+size_t fa_forward_paged_fp8_workspace_bytes(const fa_block_mask* bm, const fa_score_rule* score_rule, int32_t B, int32_t Hq,
+                                            int32_t Hkv, int32_t d, int32_t chunk_blocks) {
   PagedFp8Plan P;
-  return paged_fp8_plan(bm, B, Hq, Hkv, d, chunk_blocks, &P) == FA_OK ? P.total : 0;
+  return paged_fp8_plan(bm, score_rule, B, Hq, Hkv, d, chunk_blocks, &P) == FA_OK ? P.total : 0;
 }
 
 fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
@@ -1245,45 +1260,99 @@ fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const vo
   if (s != FA_OK) return (fa_status)s;
   if (out_dtype != FA_OUT_BF16 && out_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
   if (page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
-  if (n_pages_total < 1 || (int64_t)max_pages * page < KV_LEN) return FA_ERR_SHAPE;
-  if (Hkv > 65535 || B > 65535) return FA_ERR_UNSUPPORTED;
-  if (!bm->q_num || !bm->full_q_num) return FA_ERR_INVALID_ARG;
+  if (n_pages_total < 1 || max_pages < 1 || (int64_t)max_pages * page < KV_LEN) return FA_ERR_SHAPE;
+  if (Hkv > 65535 || B > 65535 || (int64_t)n_pages_total * Hkv * page > INT_MAX) return FA_ERR_UNSUPPORTED;
   if (bm->bk < FA_KV_SCALE_TOKENS) return FA_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(page_table) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FA_ERR_INVALID_ARG;
   PagedFp8Plan P;
-  s = paged_fp8_plan(bm, B, Hq, Hkv, d, chunk_blocks, &P);
+  s = paged_fp8_plan(bm, score_rule, B, Hq, Hkv, d, chunk_blocks, &P);
   if (s != FA_OK) return (fa_status)s;
+  if (!bm->q_num || !bm->full_q_num) return FA_ERR_INVALID_ARG;
   if (workspace_bytes < P.total) return FA_ERR_BUFFER_TOO_SMALL;
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  ExpandArgs a;
-  std::memset(&a, 0, sizeof(a));
-  s = compile_rule(&bm->rule, &a.rule);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  DevRule rule;
+  s = compile_rule(&bm->rule, &rule);
   if (s != FA_OK) return (fa_status)s;
-  a.k_pages = k_pages;
-  a.v_pages = v_pages;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.page_table = page_table;
-  a.n_pages_total = n_pages_total;
-  a.page = page;
-  a.max_pages = max_pages;
-  a.k_out = w;
-  a.v_out = w + P.kv_bytes;
+  rule.doc_run = bm->doc_run;
+  rule.doc_sorted = bm->doc_sorted;
+  if (!P.direct) {
+    ExpandArgs e;
+    std::memset(&e, 0, sizeof(e));
+    e.k_pages = k_pages;
+    e.v_pages = v_pages;
+    e.k_scale = k_scale;
+    e.v_scale = v_scale;
+    e.page_table = page_table;
+    e.n_pages_total = n_pages_total;
+    e.page = page;
+    e.max_pages = max_pages;
+    e.k_out = w;
+    e.v_out = w + P.kv_bytes;
+    e.B = B;
+    e.Hq = Hq;
+    e.Hkv = Hkv;
+    e.q_len = Q_LEN;
+    e.kv_len = KV_LEN;
+    e.d = d;
+    e.rule = rule;
+    e.mask = dev_mask(bm);
+    e.status = dev_status;
+    if (launch_expand_fp8(e, st) != cudaSuccess) return FA_ERR_CUDA;
+    if (P.chunk)
+      return fa_flex_forward_split(q, e.k_out, e.v_out, bm, score_rule, scale, out, out_dtype, lse, B, Hq, Hkv, Q_LEN,
+                                   KV_LEN, d, P.chunk, w + 2 * P.kv_bytes, P.split.total, dev_status, stream);
+    return fa_flex_forward(q, e.k_out, e.v_out, bm, score_rule, scale, out, out_dtype, lse, B, Hq, Hkv, Q_LEN, KV_LEN, d,
+                           dev_status, nullptr, stream);
+  }
+  FwdFp8Args f;
+  std::memset(&f, 0, sizeof(f));
+  FwdArgs& a = f.a;
+  a.q = q;
+  a.k = k_pages;
+  a.v = v_pages;
+  a.out = out;
+  a.out_f32 = out_dtype == FA_OUT_F32;
+  a.lse = lse;
   a.B = B;
   a.Hq = Hq;
   a.Hkv = Hkv;
   a.q_len = Q_LEN;
   a.kv_len = KV_LEN;
   a.d = d;
+  a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
+  a.rule = rule;
+  a.score = make_score(score_rule, KV_LEN);
   a.mask = dev_mask(bm);
   a.status = dev_status;
-  if (launch_expand_fp8(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
-  if (P.chunk)
-    return fa_flex_forward_split(q, a.k_out, a.v_out, bm, score_rule, scale, out, out_dtype, lse, B, Hq, Hkv, Q_LEN,
-                                 KV_LEN, d, P.chunk, w + P.off_split, P.total - P.off_split, dev_status, stream);
-  return fa_flex_forward(q, a.k_out, a.v_out, bm, score_rule, scale, out, out_dtype, lse, B, Hq, Hkv, Q_LEN, KV_LEN, d,
-                         dev_status, nullptr, stream);
+  a.timeout_ns = g_timeout_ns.load();
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.n_pages_total = n_pages_total;
+  a.split_ncm = 1;
+  a.out_q_len = Q_LEN;
+  f.k_scale = k_scale;
+  f.v_scale = v_scale;
+  f.page = page;
+  SplitPlan S;
+  if (P.chunk) {
+    s = build_split(bm, Q_LEN, KV_LEN, P.chunk, P.split, w, st, &S);
+    if (s != FA_OK) return (fa_status)s;
+    a.mask = S.mask;
+    a.split_ncm = S.ncm;
+    a.out_q_len = S.mask.nq * 128;
+    a.out = S.o_part;
+    a.out_f32 = 1;
+    a.lse = S.lse_part;
+  }
+  if ((int64_t)B * a.mask.nq * Hq > INT_MAX) return FA_ERR_UNSUPPORTED;  // grid size
+  s = launch_fwd_fp8(f, st);
+  if (s != FA_OK || !P.chunk) return (fa_status)s;
+  return launch_split_combine(S.o_part, S.lse_part, B, Hq, Q_LEN, bm->nq, S.ncm, d, out, out_dtype == FA_OUT_F32, lse,
+                              st) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 fa_status fa_block_mask_stats(const fa_block_mask* bm, int64_t* dev_out, fa_stream_t stream) {

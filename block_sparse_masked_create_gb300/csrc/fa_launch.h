@@ -199,6 +199,15 @@ struct DecFp8Args {
 };
 int launch_decode_fp8(const DecFp8Args& a, cudaStream_t st);
 
+// The forward over e4m3 pages, 128 x 128 blocks: a.k, a.v are the pages, a.page_table the table.
+struct FwdFp8Args {
+  FwdArgs a;
+  const float* k_scale;      // [n_pages_total, Hkv, page / 32]
+  const float* v_scale;
+  int32_t page;
+};
+int launch_fwd_fp8(const FwdFp8Args& a, cudaStream_t st);  // FA_OK / FA_ERR_CUDA
+
 struct ExpandArgs {
   const void* k_pages;       // e4m3 [n_pages_total, Hkv, page, d]
   const void* v_pages;

@@ -55,4 +55,26 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// First key position that no row of batch row b sees, by the causal and prefix bounds of the rule's terms. What the pages
+// hold from there on (slots behind a sequence) is read as zero.
+__device__ __forceinline__ int key_end(const DevRule& R, int Bm, int b, int q_len, int kv_len) {
+  const int64_t last = (int64_t)q_len - 1 + (R.q_offset ? __ldg(R.q_offset + (Bm > 1 ? b : 0)) : 0);
+  int64_t end = 0;
+  for (int t = 0; t < R.n_terms; ++t) {
+    int64_t hi = kv_len;
+    if (R.t[t].causal) hi = min(hi, last + 1);
+    if (R.t[t].pre != INT64_MAX) hi = min(hi, R.t[t].pre);
+    end = max(end, hi);
+  }
+  return (int)end;
+}
+
+// c * tanh(x / c) to about 2^-22 of c: tanh(u) = 1 - 2 / (1 + e^2u), two special-function operations where tanh.approx
+// takes one (and is off by 8e-6)
+__device__ __forceinline__ float softcap_exact(float x, float c, float inv_c) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(x * inv_c * 2.885390081777927f)));
+  return c * fmaf(-2.f, r, 1.f);
+}
+
 }  // namespace fa

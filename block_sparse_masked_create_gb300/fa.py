@@ -141,7 +141,7 @@ def load() -> ctypes.CDLL:
     lib.fa_flex_decode_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, P(BlockMaskC), P(ScoreRule), f32, vp, i32, vp, i32,
                                        i32, i32, i32, i32, i32, vp, sz, vp, vp, vp]
     lib.fa_forward_paged_fp8_workspace_bytes.restype = sz
-    lib.fa_forward_paged_fp8_workspace_bytes.argtypes = [P(BlockMaskC), i32, i32, i32, i32, i32]
+    lib.fa_forward_paged_fp8_workspace_bytes.argtypes = [P(BlockMaskC), P(ScoreRule), i32, i32, i32, i32, i32]
     lib.fa_flex_forward_paged_fp8.restype = ctypes.c_int
     lib.fa_flex_forward_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, P(BlockMaskC), P(ScoreRule), f32, vp,
                                               i32, vp, i32, i32, i32, i32, i32, i32, i32, vp, sz, vp, vp]
@@ -793,9 +793,10 @@ def flex_decode_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     return out, lse
 
 
-def forward_paged_fp8_workspace_bytes(block_mask: BlockMask, B: int, Hq: int, Hkv: int, d: int,
-                                      chunk_blocks: int = 0) -> int:
-    return int(load().fa_forward_paged_fp8_workspace_bytes(ctypes.byref(block_mask.c), B, Hq, Hkv, d, chunk_blocks))
+def forward_paged_fp8_workspace_bytes(block_mask: BlockMask, B: int, Hq: int, Hkv: int, d: int, chunk_blocks: int = 0,
+                                      score: Optional[ScoreRule] = None) -> int:
+    return int(load().fa_forward_paged_fp8_workspace_bytes(ctypes.byref(block_mask.c), _ref(score), B, Hq, Hkv, d,
+                                                           chunk_blocks))
 
 
 def flex_forward_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
@@ -813,7 +814,7 @@ def flex_forward_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     P, Hkv, page, max_pages, dev = _check_fp8_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, B, d)
     out, lse = _outputs((B, Hq, Q_LEN, d), dev, out, lse, out_dtype)
     if workspace is None:
-        n = forward_paged_fp8_workspace_bytes(block_mask, B, Hq, Hkv, d, chunk_blocks)
+        n = forward_paged_fp8_workspace_bytes(block_mask, B, Hq, Hkv, d, chunk_blocks, score)
         workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
     _check(_call(dev, load().fa_flex_forward_paged_fp8, _at(q), _at(k_pages), _at(v_pages), _at(k_scale),
                  _at(v_scale), _at(page_table), P, page, max_pages, ctypes.byref(block_mask.c), _ref(score),

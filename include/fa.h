@@ -464,18 +464,20 @@ FA_API fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const vo
                                     int32_t page, int32_t max_pages, void* workspace, size_t workspace_bytes,
                                     int32_t* dev_status, int64_t* dev_counters, fa_stream_t stream);
 
-/* fa_flex_forward_paged over an 8-bit cache, for chunks of queries: the key blocks that the mask lists are expanded to
- * bf16 in the workspace (exact for power-of-two scales, else rounded) and the forward runs on them. The page size is
- * independent of the mask's Bk: page in {32, 64, 128}, max_pages * page >= KV_LEN, 16-byte aligned pages. Pages of a
- * listed block that hold a position some causal or prefix term lets the batch row see are looked up; positions behind
- * those may hold anything.
+/* fa_flex_forward_paged over an 8-bit cache, for chunks of queries. The page size is independent of the mask's Bk: page in
+ * {32, 64, 128}, max_pages * page >= KV_LEN, Bk >= 32, 16-byte aligned pages. Pages of a listed block that hold a position some
+ * term of the rule lets the batch row see (by its causal and prefix bounds) are looked up; slots behind those may hold
+ * anything. 128 x 128 blocks read the pages themselves in the tcgen05 kernel (fp16 products; the cached values enter exactly,
+ * the V scales of one 128-token key block are best within 2^10 of each other) where few query rows share them or the scores
+ * are soft-capped; else the listed blocks are first expanded to bf16 in the workspace (exact for power-of-two scales, else
+ * rounded) and the bf16 forward runs on them.
  *   chunk_blocks   with Bq == Bk == 128, cut long rows into chunks of that many key blocks (fa_flex_forward_split); 0: the
  *                  library chooses, cutting only where the uncut rows would leave SMs idle; -1: never cut
  *   workspace      device, >= fa_forward_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned
  * A bad id among the looked-up pages sets FA_ERR_DEVICE_CHECK (zeros are read in its place). Other arguments and errors
  * as fa_flex_forward_paged; block_mask needs its query-side transpose. */
-FA_API size_t fa_forward_paged_fp8_workspace_bytes(const fa_block_mask* block_mask, int32_t B, int32_t Hq, int32_t Hkv,
-                                                   int32_t d, int32_t chunk_blocks);
+FA_API size_t fa_forward_paged_fp8_workspace_bytes(const fa_block_mask* block_mask, const fa_score_rule* score_rule, int32_t B,
+                                                   int32_t Hq, int32_t Hkv, int32_t d, int32_t chunk_blocks);
 FA_API fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                                            const float* v_scale, const int32_t* page_table, int32_t n_pages_total,
                                            int32_t page, int32_t max_pages, const fa_block_mask* block_mask,

@@ -204,7 +204,8 @@ def prefill_case(seed, lens, Q, Hq, Hkv, d, page, window=0, prefix=0, bk=128, po
 
 @pytest.mark.parametrize("page,bk,Q,Hq,Hkv,d,window,softcap,alibi", [
     (128, 128, 100, 4, 2, 128, 0, 0.0, False), (32, 128, 1, 2, 2, 64, 0, 0.0, False), (64, 128, 129, 4, 1, 128, 150, 20.0, False),
-    (128, 64, 70, 4, 4, 64, 0, 0.0, True), (64, 32, 33, 2, 1, 128, 40, 0.0, False), (32, 64, 300, 3, 1, 64, 0, 0.0, False)])
+    (128, 64, 70, 4, 4, 64, 0, 0.0, True), (64, 32, 33, 2, 1, 128, 40, 0.0, False), (32, 64, 300, 3, 1, 64, 0, 0.0, False), (64, 128, 150, 16, 1, 64, 0, 0.0, True),
+    (128, 128, 700, 3, 1, 128, 200, 0.0, False)])
 @pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 def test_prefill_matches_64_bits_and_the_bf16_forward(page, bk, Q, Hq, Hkv, d, window, softcap, alibi, dtype):
     lens = [Q, Q + 1, Q + 333]
@@ -215,23 +216,70 @@ def test_prefill_matches_64_bits_and_the_bf16_forward(page, bk, Q, Hq, Hkv, d, w
     args = [t.cuda() for t in (q, kp, vp, ks, vs, table)]
     out, lse = fa.flex_forward_paged_fp8(*args, bm, kv_len, sc, status=status, out_dtype=dtype, chunk_blocks=-1)
     assert fa.check_status(status) == fa.OK
-    # power-of-two scales: the expanded values are the cached ones, so the bf16 forward over them gives the same bits
     dk, dv = ref.dequant(kp, ks), ref.dequant(vp, vs)
-    k, v = (torch.stack([torch.cat([ref.gather(t, table[b], L), torch.zeros(Hkv, kv_len - L, d, dtype=torch.float64)], 1)
-                         for b, L in enumerate(lens)]).to(BF).cuda() for t in (dk, dv))
-    o2, l2 = fa.flex_forward(args[0], k, v, bm, sc, out_dtype=dtype)
-    assert torch.equal(out, o2) and torch.equal(lse, l2)
-    os_, ls = [], []
+    expanded = bk != 128 or -(-Q // 128) * (Hq // Hkv) > 16  # many query tiles to a key block
+    if expanded:
+        # power-of-two scales: the expanded values are the cached ones, so the bf16 forward over them gives the same bits
+        k, v = (torch.stack([torch.cat([ref.gather(t, table[b], L), torch.zeros(Hkv, kv_len - L, d, dtype=torch.float64)], 1)
+                             for b, L in enumerate(lens)]).to(BF).cuda() for t in (dk, dv))
+        o2, l2 = fa.flex_forward(args[0], k, v, bm, sc, out_dtype=dtype)
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
     for b, L in enumerate(lens):
         i, j = L - Q + torch.arange(Q)[:, None], torch.arange(L)[None]
         _, al = spec_and_mask(window, 0, i, j)
-        o, z, _, _ = ref.attention(q[b].double(), ref.gather(dk, table[b], L), ref.gather(dv, table[b], L), al, d ** -0.5, slopes,
-                                   i[:, 0], softcap)
-        os_.append(o)
-        ls.append(z)
-    # the cached values are N(0, 1) times 1 or 2: the forward's tolerance for N(0, 1), doubled
-    o, z = torch.stack(os_).numpy() / 2, torch.stack(ls).numpy()
-    gc.compare(out.float().cpu().numpy() / 2, lse.cpu().numpy(), o, z, "prefill", out_bf16=dtype == BF)
+        want = ref.attention(q[b].double(), ref.gather(dk, table[b], L), ref.gather(dv, table[b], L), al, d ** -0.5, slopes, i[:, 0], softcap)
+        # ALiBi: the bias is stepped by 8 columns, at most 16 roundings of its size a block, and a product with a distance
+        extra = 20 * ref.U32 * L if alibi else 0.0
+        if not expanded:
+            close(out[b], lse[b], want, d, softcap, dtype, extra, f"request {b}")
+        else:
+            # the cached values are N(0, 1) times 1 or 2: the forward's tolerance for N(0, 1), doubled
+            gc.compare(out[b].float().cpu().numpy() / 2, lse[b].cpu().numpy(), want[0].numpy() / 2, want[1].numpy(), "prefill",
+                       out_bf16=dtype == BF)
+
+
+@pytest.mark.parametrize("kw", [dict(prefix=70), dict(window=1), dict(softcap=100.0), dict(rel=True), dict(alibi=True, softcap=30.0), dict(doc=True),
+                                dict(spread=9), dict(power=False), dict(q_scale=1e-20), dict(dense=True)], ids=str)
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 128)])
+def test_prefill_rules_and_scales(kw, d, page):
+    # 128 x 128 blocks: every score path, document masks, V scales up to 2^9 apart in a block, a rule without a causal bound
+    Q, Hq, Hkv, lens = 150, 4, 2, [150, 390]
+    kp, vp, ks, vs, table = cache(40, lens, Hkv, page, d, kw.get("spread", 1), power=kw.get("power", True))
+    B, n = len(lens), max(lens)
+    if kw.get("dense"):
+        lens = [n, n]
+        kp, vp, ks, vs, table = cache(40, lens, Hkv, page, d)
+    g = gen(41)
+    q = (torch.randn(B, Hq, Q, d, generator=g) * kw.get("q_scale", 1.0)).to(BF)
+    off = torch.tensor([L - Q for L in lens], dtype=torch.int32).cuda()
+    slopes = 2.0 ** (-8.0 * torch.arange(1, Hq + 1) / Hq) if kw.get("alibi") else None
+    rel = torch.randn(Hq, 2 * n - 1, generator=g) if kw.get("rel") else None
+    spec, _ = spec_and_mask(kw.get("window", 0), kw.get("prefix", 0), torch.zeros(1, 1), torch.zeros(1, 1))
+    doc = (torch.arange(n) // 60 % 4).to(torch.int32)[None] if kw.get("doc") else None
+    if kw.get("doc"):
+        spec += [("doc",), ("and",)]
+    if kw.get("dense"):
+        spec = [("true",)]
+    doc_c = None if doc is None else doc.cuda()
+    bm = fa.create_block_mask(fa.make_mask_rule(spec, doc_ids=doc_c, q_offset=off), B, Hq, Q, n, 128, 128, keep=[off, doc_c])
+    cap = kw.get("softcap", 0.0)
+    sc = fa.make_score_rule(None if slopes is None else slopes.cuda(), None if rel is None else rel.cuda(), cap)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = fa.flex_forward_paged_fp8(*[t.cuda() for t in (q, kp, vp, ks, vs, table)], bm, n, sc, status=status, out_dtype=F32)
+    assert fa.check_status(status) == fa.OK
+    dk, dv = ref.dequant(kp, ks), ref.dequant(vp, vs)
+    for b, L in enumerate(lens):
+        i, j = L - Q + torch.arange(Q)[:, None], torch.arange(L)[None]
+        _, al = spec_and_mask(kw.get("window", 0), kw.get("prefix", 0), i, j)
+        if doc is not None:
+            al = al & (doc[0, :L][None] == doc[0, i[:, 0]][:, None])
+        if kw.get("dense"):
+            al = torch.ones_like(al)
+        want = ref.attention(q[b].double(), ref.gather(dk, table[b], L), ref.gather(dv, table[b], L), al, d ** -0.5, slopes, i[:, 0], cap, rel, n)
+        # P in fp16 relative to a block's largest V scale: 2^-25 of 448 such scales for a key whose P is subnormal there
+        floor = 2.0 ** -25 * 448 * float(vs[table[b, :-(-L // page)].long()].nan_to_num(0).max()) * L if kw.get("spread") else 0.0
+        want = (want[0], want[1], want[2] + floor * 2.0 ** 11, want[3])
+        close(out[b], lse[b], want, d, cap, F32, 20 * ref.U32 * (L + 8), f"request {b} {kw}")
 
 
 def test_prefill_cut_rows():
@@ -241,15 +289,25 @@ def test_prefill_cut_rows():
     args = [t.cuda() for t in (q, kp, vp, ks, vs, table)]
     whole = fa.flex_forward_paged_fp8(*args, bm, kv_len, chunk_blocks=-1, out_dtype=F32)
     assert fa.forward_paged_fp8_workspace_bytes(bm, 2, 4, 2, 128, 0) > fa.forward_paged_fp8_workspace_bytes(bm, 2, 4, 2, 128, -1)
-    for chunk in (0, 1, 7):
+    for chunk in (0, 1, 7):  # (cut rows over expanded blocks: below)
         o, l = fa.flex_forward_paged_fp8(*args, bm, kv_len, chunk_blocks=chunk, out_dtype=F32)
-        # each side has its own rounding of P to bf16 (2^-8 of a weighted mean of |v| below 2)
-        assert (o - whole[0]).abs().max() <= 2 * 2.0 ** -8 * 2 and (l - whole[1]).abs().max() <= 2e-3
+        # each side has its own rounding of P to fp16 (2^-11 of a weighted mean of |v| below 2), and the merge's fp32
+        assert (o - whole[0]).abs().max() <= 2 * 2.0 ** -11 * 2 + 1e-5 and (l - whole[1]).abs().max() <= 2e-5
 
 
-def test_prefill_scales_that_are_no_powers_of_two():
+def test_prefill_cut_rows_over_expanded_blocks():
+    lens = [1500]
+    q, kp, vp, ks, vs, table, bm, off, kv_len = prefill_case(23, lens, 400, 8, 1, 64, 128)  # 32 query tiles to a key block
+    args = [t.cuda() for t in (q, kp, vp, ks, vs, table)]
+    whole = fa.flex_forward_paged_fp8(*args, bm, kv_len, chunk_blocks=-1, out_dtype=F32)
+    o, l = fa.flex_forward_paged_fp8(*args, bm, kv_len, chunk_blocks=3, out_dtype=F32)
+    # each side has its own rounding of P to bf16 (2^-8 of a weighted mean of |v| below 2)
+    assert (o - whole[0]).abs().max() <= 2 * 2.0 ** -8 * 2 and (l - whole[1]).abs().max() <= 2e-3
+
+
+def test_prefill_scales_that_are_no_powers_of_two_in_small_blocks():
     lens, Q = [200, 260], 130
-    q, kp, vp, ks, vs, table, bm, off, kv_len = prefill_case(24, lens, Q, 2, 2, 64, 32, power=False)
+    q, kp, vp, ks, vs, table, bm, off, kv_len = prefill_case(24, lens, Q, 2, 2, 64, 32, bk=64, power=False)
     out, lse = fa.flex_forward_paged_fp8(*[t.cuda() for t in (q, kp, vp, ks, vs, table)], bm, kv_len, out_dtype=F32)
     dk, dv = (ref.dequant(p, s).float().to(BF).double() for p, s in ((kp, ks), (vp, vs)))  # the values rounded to bf16
     for b, L in enumerate(lens):

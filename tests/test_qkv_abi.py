@@ -141,8 +141,8 @@ def test_decode_refusals(fa):
 def test_prefill_refusals(fa):
     lib = fa.load()
     c = mask(fa, 64, 256, 128, 128)
-    n = lib.fa_forward_paged_fp8_workspace_bytes(ref(c), 1, 4, 2, 64, 0)
-    assert n > 0 and lib.fa_forward_paged_fp8_workspace_bytes(ref(c), 1, 4, 2, 64, -2) == 0
+    n = lib.fa_forward_paged_fp8_workspace_bytes(ref(c), None, 1, 4, 2, 64, 0)
+    assert n > 0 and lib.fa_forward_paged_fp8_workspace_bytes(ref(c), None, 1, 4, 2, 64, -2) == 0
 
     def call(s=P, table=P, page=64, max_pages=4, total=9, Q=64, KV=256, chunk=0, ws=P, nbytes=n, m=c, d=64, kind=0):
         return lib.fa_flex_forward_paged_fp8(P, P, P, s, s, table, total, page, max_pages, ref(m), None, 0.0, P, kind, P, 1, 4, 2, Q, KV, d,
@@ -157,9 +157,9 @@ def test_prefill_refusals(fa):
     small = mask(fa, 64, 256, 64, 64)
     assert call(m=small, chunk=4, nbytes=1 << 40) == fa.ERR_UNSUPPORTED      # cut rows want 128 x 128 blocks
     assert call(m=mask(fa, 64, 256, 16, 16), nbytes=1 << 40) == fa.ERR_UNSUPPORTED
-    c2 = mask(fa, 64, 256, 128, 128)
-    c2.q_num = None
-    assert call(m=c2) == fa.ERR_INVALID_ARG                                  # no query-side transpose
+    small.q_num = None
+    assert call(m=small, nbytes=1 << 40) == fa.ERR_INVALID_ARG               # no query-side transpose
+    assert call(total=1 << 26) == fa.ERR_UNSUPPORTED                         # more rows than a copy's coordinate
 
 
 def test_binding_checks_types_shapes_and_devices(fa):
