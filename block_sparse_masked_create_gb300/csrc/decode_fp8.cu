@@ -25,10 +25,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;
 constexpr int kSub = kScaleTokens;   // tokens per sub-tile: one K scale and one V scale
-constexpr int kStages = 3;
 
 template <int D>
 struct Cfg {
+  static constexpr int kStages = 3;
+  static constexpr int kCtas = fp8_decode_ctas(D);       // resident an SM
   static constexpr int kTile = kSub * D;                 // bytes of a K or V sub-tile
   static constexpr int kStage = 2 * kTile;
   static constexpr int kWarpBytes = kStages * kStage;
@@ -42,11 +43,12 @@ __device__ __forceinline__ uint32_t tile_at(int row, int c) {
   return D == 128 ? (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
 }
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32)
+template <int D, bool HALF>
+__global__ void __launch_bounds__(kWarps * 32, Cfg<D>::kCtas)
     decode_fp8_kernel(const __grid_constant__ DecFp8Args A, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV) {
   using C = Cfg<D>;
+  constexpr int kStages = C::kStages;
   const DecArgs& a = A.d;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -154,6 +156,11 @@ __global__ void __launch_bounds__(kWarps * 32)
   float sr_a = 0.f, sr_b = 0.f;  // scale * log2(e) * the row's power of two
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
+    if (HALF && half) {
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) qf[c][1] = qf[c][3] = 0u;
+      break;
+    }
     const int row = half ? rb : ra;
     uint2 v[D / 16];
     float m = 0.f;
@@ -220,7 +227,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < (HALF ? 2 : 4); ++e) {
           const int col = i * 8 + t4 * 2 + (e & 1);
           const bool up = e >= 2;
           float x = sc[i][e] * (up ? sl_b : sl_a);
@@ -244,14 +251,16 @@ __global__ void __launch_bounds__(kWarps * 32)
       }
       mx_a = fmaxf(mx_a, __shfl_xor_sync(0xFFFFFFFFu, mx_a, 1));
       mx_a = fmaxf(mx_a, __shfl_xor_sync(0xFFFFFFFFu, mx_a, 2));
-      mx_b = fmaxf(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 1));
-      mx_b = fmaxf(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 2));
+      if (!HALF) {
+        mx_b = fmaxf(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 1));
+        mx_b = fmaxf(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 2));
+      }
       const float mn_a = mx_a > m_a + 8.f ? mx_a : m_a, mn_b = mx_b > m_b + 8.f ? mx_b : m_b;
       const float ref_a = mn_a == -INFINITY ? 0.f : mn_a, ref_b = mn_b == -INFINITY ? 0.f : mn_b;
       if (__any_sync(0xFFFFFFFFu, mn_a != m_a || mn_b != m_b || vs != vref)) {
-        const float al_a = ex2_approx(m_a - ref_a), al_b = ex2_approx(m_b - ref_b), w = vref / vs;
+        const float al_a = ex2_approx(m_a - ref_a), al_b = HALF ? 0.f : ex2_approx(m_b - ref_b), w = vref / vs;
         l_a *= al_a;
-        l_b *= al_b;
+        if (!HALF) l_b *= al_b;
         const float f_a = al_a * w, f_b = al_b * w;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
@@ -259,8 +268,10 @@ __global__ void __launch_bounds__(kWarps * 32)
           for (int h = 0; h < 2; ++h) {
             o[c][h][0] *= f_a;
             o[c][h][1] *= f_a;
-            o[c][h][2] *= f_b;
-            o[c][h][3] *= f_b;
+            if (!HALF) {
+              o[c][h][2] *= f_b;
+              o[c][h][3] *= f_b;
+            }
           }
         m_a = mn_a;
         m_b = mn_b;
@@ -270,11 +281,14 @@ __global__ void __launch_bounds__(kWarps * 32)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float p0 = ex2_approx(sc[i][0] - ref_a), p1 = ex2_approx(sc[i][1] - ref_a);
-        const float p2 = ex2_approx(sc[i][2] - ref_b), p3 = ex2_approx(sc[i][3] - ref_b);
         l_a += p0 + p1;
-        l_b += p2 + p3;
         pf[i >> 1][(i & 1) * 2 + 0] = pack_f16x2(p0, p1);
-        pf[i >> 1][(i & 1) * 2 + 1] = pack_f16x2(p2, p3);
+        pf[i >> 1][(i & 1) * 2 + 1] = 0u;
+        if (!HALF) {
+          const float p2 = ex2_approx(sc[i][2] - ref_b), p3 = ex2_approx(sc[i][3] - ref_b);
+          l_b += p2 + p3;
+          pf[i >> 1][(i & 1) * 2 + 1] = pack_f16x2(p2, p3);
+        }
       }
       auto pv = [&](auto kind) {
         constexpr bool masked = decltype(kind)::value;
@@ -326,22 +340,27 @@ __global__ void __launch_bounds__(kWarps * 32)
   // ---- join the 4 warps' states (the rings are free: every copy has landed)
   l_a += __shfl_xor_sync(0xFFFFFFFFu, l_a, 1);
   l_a += __shfl_xor_sync(0xFFFFFFFFu, l_a, 2);
-  l_b += __shfl_xor_sync(0xFFFFFFFFu, l_b, 1);
-  l_b += __shfl_xor_sync(0xFFFFFFFFu, l_b, 2);
+  if (!HALF) {
+    l_b += __shfl_xor_sync(0xFFFFFFFFu, l_b, 1);
+    l_b += __shfl_xor_sync(0xFFFFFFFFu, l_b, 2);
+  }
   float* sO = reinterpret_cast<float*>(smem);  // [4][16][D]
 #pragma unroll
   for (int c = 0; c < D / 16; ++c) {
     const int col = c * 16 + t4 * 4;
     *reinterpret_cast<float4*>(sO + (warp * 16 + ra) * D + col) =
         make_float4(o[c][0][0] * vref, o[c][1][0] * vref, o[c][0][1] * vref, o[c][1][1] * vref);
-    *reinterpret_cast<float4*>(sO + (warp * 16 + rb) * D + col) =
-        make_float4(o[c][0][2] * vref, o[c][1][2] * vref, o[c][0][3] * vref, o[c][1][3] * vref);
+    if (!HALF)
+      *reinterpret_cast<float4*>(sO + (warp * 16 + rb) * D + col) =
+          make_float4(o[c][0][2] * vref, o[c][1][2] * vref, o[c][0][3] * vref, o[c][1][3] * vref);
   }
   if (t4 == 0) {
     sM[warp][ra] = m_a;
-    sM[warp][rb] = m_b;
     sL[warp][ra] = l_a;
-    sL[warp][rb] = l_b;
+    if (!HALF) {
+      sM[warp][rb] = m_b;
+      sL[warp][rb] = l_b;
+    }
   }
   __syncthreads();
   const bool only = n_vis <= a.pages_per_split;  // the request's one span: the result itself
@@ -431,7 +450,7 @@ int launch_d(const DecFp8Args& A, cudaStream_t st) {
   const uint32_t box[2] = {D, kSub};
   if (encode_tmap_u8(&tk, a.k_pages, 2, dims, strides, box) != 0) return FA_ERR_CUDA;
   if (encode_tmap_u8(&tv, a.v_pages, 2, dims, strides, box) != 0) return FA_ERR_CUDA;
-  auto kern = decode_fp8_kernel<D>;
+  auto kern = a.Hq / a.Hkv <= 8 ? decode_fp8_kernel<D, true> : decode_fp8_kernel<D, false>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return FA_ERR_CUDA;
   kern<<<dim3(a.n_splits, a.Hkv, a.Bz), kWarps * 32, C::kSmem, st>>>(A, tk, tv);

@@ -198,6 +198,10 @@ struct DecFp8Args {
   const float* v_scale;
 };
 int launch_decode_fp8(const DecFp8Args& a, cudaStream_t st);
+// CTAs of the decode kernel that an SM holds. d = 128: two, by shared memory (three stages of 8 KiB a warp) and registers;
+// three with two stages took 113 us where two take 92 (two requests of 131,072 tokens). d = 64: a sub-tile is half the bytes
+// for the same work, so more warps are wanted: four took 58 us where two took 78 (three requests of 100,000 tokens).
+constexpr int fp8_decode_ctas(int d) { return d == 128 ? 2 : 4; }
 
 // The forward over e4m3 pages, 128 x 128 blocks: a.k, a.v are the pages, a.page_table the table.
 struct FwdFp8Args {

@@ -506,7 +506,7 @@ struct RowWarp {
       if (DST != kToHeads && n >= new_tokens(a, b)) continue;  // no loads are under way for it either
       const int64_t pos = (int64_t)n + (a.q_offset ? __ldg(a.q_offset + b) : 0);
       turn = turn_at(f, lm, pos);
-      if (DST != kToHeads && hk) place = place_of(a, b, pos);
+      if (DST != kToHeads && hk && sh.k) place = place_of(a, b, pos);
       heads_of<0>(g);
       heads_of<1>(g);
       heads_of<2>(g);

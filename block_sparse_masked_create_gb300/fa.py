@@ -549,7 +549,7 @@ def _rows(t: Optional[torch.Tensor], shape, dtype, device, what: str, written: b
     sb, sn, sh, sd = t.stride() if t.dim() == 4 else (0, 0, 0, 0)
     if sd != 1 or t.dtype != dtype or t.shape != shape or t.device != device:
         raise ValueError(f"{what} must be a {dtype} tensor of shape {tuple(shape)} on {device} with contiguous rows")
-    if written and any(st == 0 and n > 1 for st, n in zip((sb, sn, sh), shape)):
+    if written and not (sb and sn and sh) and any(st == 0 and n > 1 for st, n in zip((sb, sn, sh), shape)):
         raise ValueError(f"{what} is written: its elements must not share memory")
     return RowsC(t.data_ptr(), sb, sn, sh)
 
@@ -645,34 +645,38 @@ def qk_norm_rope_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
     Hq = dq.shape[1] if dq is not None else kv.shape[1]
     Hkv = kv.shape[1] if kv is not None else Hq
     f32, bf = torch.float32, torch.bfloat16
-    for t, h, n in ((dq, Hq, "dq"), (dk, Hkv, "dk"), (dv, Hkv, "dv")):
-        _same(t, (B, h, N, d), f32, dev, n)
-    kinds = {t.dtype for t in (dq_in, dk_in, dv_in) if t is not None}
-    if len(kinds) > 1:
-        raise ValueError("dq_in, dk_in, dv_in must have one type")
-    kind = kinds.pop() if kinds else grad_dtype
-    if kind not in (bf, f32):
+    _same(dq, (B, Hq, N, d), f32, dev, "dq")
+    _same(dk, (B, Hkv, N, d), f32, dev, "dk")
+    _same(dv, (B, Hkv, N, d), f32, dev, "dv")
+    first = dq_in if dq_in is not None else dk_in if dk_in is not None else dv_in
+    kind = first.dtype if first is not None else grad_dtype
+    if kind != bf and kind != f32:
         raise ValueError("gradients are bf16 or fp32")
-    rq = _rows(q, (B, N, Hq, d), bf, dev, "q") if dq is not None else None
-    rk = _rows(k, (B, N, Hkv, d), bf, dev, "k") if dk is not None else None
-    outs, rows = [], []
-    for t, o, h, n in ((dq, dq_in, Hq, "dq_in"), (dk, dk_in, Hkv, "dk_in"), (dv, dv_in, Hkv, "dv_in")):
-        if t is None:
-            o = None
-        elif o is None:
-            o = torch.empty((B, N, h, d), dtype=kind, device=dev)
-        outs.append(o)
-        rows.append(_rows(o, (B, N, h, d), kind, dev, n, written=True))
+    rows_q, rows_kv = (B, N, Hq, d), (B, N, Hkv, d)
+    rq = _rows(q, rows_q, bf, dev, "q") if dq is not None else None
+    rk = _rows(k, rows_kv, bf, dev, "k") if dk is not None else None
+
+    def out(t, o, shape):
+        return None if t is None else torch.empty(shape, dtype=kind, device=dev) if o is None else o
+
+    dq_in, dk_in, dv_in = out(dq, dq_in, rows_q), out(dk, dk_in, rows_kv), out(dv, dv_in, rows_kv)
+    gq = _rows(dq_in, rows_q, kind, dev, "dq_in", written=True)
+    gk = _rows(dk_in, rows_kv, kind, dev, "dk_in", written=True)
+    gv = _rows(dv_in, rows_kv, kind, dev, "dv_in", written=True)
     _check_qk_rule(rule, d, dev)
     _same(q_offset, (B,), torch.int32, dev, "q_offset")
     dwq = torch.empty(d, dtype=f32, device=dev) if rule.q_weight and dq is not None else None
     dwk = torch.empty(d, dtype=f32, device=dev) if rule.k_weight and dk is not None else None
-    if workspace is None and (dwq is not None or dwk is not None):
-        workspace = torch.empty(qk_norm_rope_backward_workspace_bytes(B, N, d), dtype=torch.uint8, device=dev)
-    _check(_call(dev, load().fa_qk_norm_rope_backward, _ref(rq), _ref(rk), _at(dq), _at(dk), _at(dv),
-                 ctypes.byref(rule), _at(q_offset), *map(_ref, rows), 1 if kind == f32 else 0, _at(dwq), _at(dwk), B, Hq,
-                 Hkv, N, d, _at(workspace), 0 if workspace is None else workspace.numel()), "fa_qk_norm_rope_backward")
-    return (*outs, dwq, dwk)
+    lib = load()
+    size = 0
+    if dwq is not None or dwk is not None:
+        if workspace is None:
+            workspace = torch.empty(lib.fa_qk_norm_rope_backward_workspace_bytes(B, N, d), dtype=torch.uint8, device=dev)
+        size = workspace.numel()
+    _check(_call(dev, lib.fa_qk_norm_rope_backward, _ref(rq), _ref(rk), _at(dq), _at(dk), _at(dv), ctypes.byref(rule),
+                 _at(q_offset), _ref(gq), _ref(gk), _ref(gv), 1 if kind == f32 else 0, _at(dwq), _at(dwk), B, Hq, Hkv, N, d,
+                 _at(workspace), size), "fa_qk_norm_rope_backward")
+    return dq_in, dk_in, dv_in, dwq, dwk
 
 
 def _append(q, k, v, k_pages, v_pages, k_scale, v_scale, page_table, rule, q_offset, n_new, q_out, status):

@@ -126,6 +126,17 @@ def test_decode_spans_and_long_table():
     assert st == fa.OK
 
 
+@pytest.mark.parametrize("kw", [dict(window=1), dict(window=64), dict(window=65), dict(window=700), dict(prefix=64), dict(prefix=65, window=129),
+                                dict(window=10 ** 9)], ids=str)
+def test_decode_bounded_rules_over_a_long_table(kw):
+    # the spans are cut for what the rule can see, which starts anywhere in a page (a prefix is a part of every sequence:
+    # the rule shows its keys to all rows)
+    short = max(1, kw.get("prefix", 1))
+    for shift in (0, 1, 63):
+        _, _, st, _, _, _ = run_decode(14 + shift, [3000 + shift, short + 64 + shift, short], 4, 1, 64, 64, max_pages=900, **kw)
+        assert st == fa.OK
+
+
 def test_decode_empty_rows():
     out, lse, st, _, _, _ = run_decode(6, [50, 50], 4, 2, 64, 32, offset=[-1, 49])
     assert st == fa.OK and not out[0].any() and lse[0].isneginf().all()

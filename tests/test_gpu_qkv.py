@@ -365,6 +365,29 @@ def test_append_reports_bad_pages_positions_and_counts(fp8, N):
     assert fa.check_status(status) == fa.ERR_DEVICE_CHECK
 
 
+@pytest.mark.parametrize("N", [1, 2])
+def test_append_fp8_many_requests_in_one_pool(N):
+    # more requests than CTAs at a time, every one in a block of its own; the same values as one request at a time gives
+    B, H, d, page = 3001, 1, 64, 32
+    g = gen(22)
+    x = torch.randn(B, N, 3 * H, d, generator=g).to(BF).cuda()
+    q, k, v = x.split([H, H, H], dim=2)
+    table = torch.randperm(B, generator=g).to(torch.int32)[:, None].contiguous().cuda()
+    off = torch.randint(0, 31, (B,), generator=g).to(torch.int32).cuda()
+    rule = fa.make_qk_rule(None, None, 0.0, inv_freq(64).cuda())
+    kp, vp = (torch.zeros(B, H, page, d, device="cuda").to(F8) for _ in range(2))
+    ks, vs = (torch.full((B, H, 1), 2.0 ** -40, device="cuda") for _ in range(2))
+    fa.kv_append_fp8(q, k, v, kp, vp, ks, vs, table, rule, off)
+    rows = fa.qk_norm_rope(None, k, None, rule, off)[1].transpose(1, 2).float()  # bf16 of the same rows
+    pid = table[:, 0].long()
+    b = torch.arange(B, device="cuda")
+    for n in range(N):
+        got_k = kp.float()[pid, 0, off.long() + n] * ks[pid, 0]
+        got_v = vp.float()[pid, 0, off.long() + n] * vs[pid, 0]
+        for got, want, s in ((got_k, rows[b, n, 0], ks[pid, 0]), (got_v, v[:, n, 0].float(), vs[pid, 0])):
+            assert ((got - want).abs() <= (2.0 ** -4 + 2.0 ** -7) * want.abs() + 2.0 ** -9 * s).all()
+
+
 def test_own_stream_and_captured_graph():
     c = make(19, 2, 1, 4, 2, 128, 128, True)
     page, d = 64, 128
