@@ -526,8 +526,8 @@ __global__ void __launch_bounds__(kRowThreads, kRowCtas) qkv_rows_kernel(const _
 // ------------------------------------------------------------------------------------------------
 // Append to e4m3 pages, several tokens a request. A CTA takes one 32-token block of one request and a share of its
 // KV heads: for each head its threads hold the block's new K and V rows, agree on the two largest magnitudes (one
-// barrier), and write scales and values; rows that the block held before are rescaled where the scale grew. CTAs
-// behind those take the query rows.
+// barrier), and write scales and values; rows that the block held before are rescaled where the scale grew. Other CTAs
+// take the query rows.
 // ------------------------------------------------------------------------------------------------
 constexpr int kBlockThreads = 256;
 
@@ -666,16 +666,19 @@ __global__ void __launch_bounds__(kBlockThreads, 3)
     append_fp8_kernel(const __grid_constant__ QkvArgs a, int blocks, int heads_per_cta, int groups) {
   __shared__ __align__(16) uint2 ring[kRing * 2 * kBlockThreads];
   __shared__ __align__(16) uint32_t s_max[2][2][kBlockThreads / 32];
-  const int64_t kv_ctas = (int64_t)a.B * blocks * groups;
-  if ((int64_t)blockIdx.x < kv_ctas) {
-    const int x = blockIdx.x, gi = x % groups, bj = x / groups;
+  // the two kinds of CTAs take turns: the blocks are bound by their instructions, the query rows by HBM
+  const int kv_ctas = a.B * blocks * groups, q_ctas = (int)gridDim.x - kv_ctas, both = min(kv_ctas, q_ctas);
+  const int x = (int)blockIdx.x;
+  const bool turn = x < 2 * both;
+  if (turn ? (x & 1) == 0 : kv_ctas > q_ctas) {
+    const int i = turn ? x >> 1 : x - both, gi = i % groups, bj = i / groups;
     const int hk0 = gi * heads_per_cta;
     append_block<D, INTER>(a, bj / blocks, bj % blocks, hk0, min(a.Hkv, hk0 + heads_per_cta), ring, s_max);
   } else {
     constexpr int kWarps = kBlockThreads / 32;
-    const int64_t warp = ((int64_t)blockIdx.x - kv_ctas) * kWarps + threadIdx.x / 32;
+    const int64_t warp = (int64_t)(turn ? x >> 1 : x - both) * kWarps + threadIdx.x / 32;
     const Shares all{1, a.Hq, 0};  // the query rows alone
-    RowWarp<D, kToPages, INTER, kBlockThreads> w(a, all, warp, ((int64_t)gridDim.x - kv_ctas) * kWarps, ring);
+    RowWarp<D, kToPages, INTER, kBlockThreads> w(a, all, warp, (int64_t)q_ctas * kWarps, ring);
     w.run(warp);
   }
 }
@@ -914,6 +917,7 @@ cudaError_t run_append(const QkvArgs& a, cudaStream_t st) {
   groups = (a.Hkv + hpc - 1) / hpc;
   const int64_t q_items = a.q.p ? (int64_t)a.B * a.N : 0, per = kBlockThreads / 32;
   const int64_t ctas = (int64_t)a.B * blocks * groups + std::min<int64_t>((q_items + per - 1) / per, kSms * 16);
+  if (ctas > 0x3FFFFFFF) return cudaErrorInvalidConfiguration;
   auto kern = a.interleaved ? append_fp8_kernel<D, true> : append_fp8_kernel<D, false>;
   kern<<<(unsigned)ctas, kBlockThreads, 0, st>>>(a, blocks, hpc, groups);
   return cudaGetLastError();

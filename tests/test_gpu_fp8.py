@@ -396,3 +396,31 @@ def test_prompt_then_decode_steps(fp8):
                 close(o[b][:, None], l[b][:, None], want, d, 0.0, F32, 0.0, f"step {step} request {b}")
             else:
                 assert ((o[b][:, None].double().cpu() - want[0]).abs() <= 2.0 ** -7 * want[2] + 1e-4).all()
+
+
+def test_pool_past_32_bit_offsets():
+    # pages that lie behind 4 GiB of a pool: append, decode and prefill give what they give in a small pool
+    Hq, Hkv, d, page, far = 8, 8, 128, 128, 2 ** 32 // (8 * 128 * 128)
+    g = gen(50)
+    x = torch.randn(1, 300, Hq + 2 * Hkv, d, generator=g).to(BF).cuda()
+    q, k, v = x.split([Hq, Hkv, Hkv], dim=2)
+    f = (10000.0 ** (-2 * torch.arange(d // 2, dtype=torch.float64) / d)).float().cuda()
+    rule = fa.make_qk_rule(None, None, 1e-6, f)
+    off = torch.tensor([299], dtype=torch.int32).cuda()
+    mask = fa.create_block_mask(fa.make_mask_rule([("causal",)], q_offset=off), 1, Hq, 1, 3 * page, 1, page, keep=[off])
+    chunk = fa.create_block_mask(fa.make_mask_rule([("causal",)]), 1, Hq, 299, 299, 128, 128)
+    small = fa.create_block_mask(fa.make_mask_rule([("causal",)]), 1, Hq, 299, 299, 64, 64)
+    got = []
+    for first in (0, far):
+        kp, vp = (torch.zeros(first + 3, Hkv, page, d, dtype=torch.uint8, device="cuda").view(F8) for _ in range(2))
+        ks, vs = (torch.zeros(first + 3, Hkv, page // 32, device="cuda") for _ in range(2))
+        table = torch.tensor([[first + 2, first, first + 1]], dtype=torch.int32).cuda()
+        cache_ = (kp, vp, ks, vs, table)
+        qp = fa.kv_append_fp8(q[:, :299], k[:, :299], v[:, :299], *cache_, rule)
+        qd = fa.kv_append_fp8(q[:, 299:], k[:, 299:], v[:, 299:], *cache_, rule, off)
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got.append((*fa.flex_decode_fp8(qd[:, :, 0], *cache_, mask, status=status), *fa.flex_forward_paged_fp8(qp, *cache_, chunk, 299, status=status),
+                    *fa.flex_forward_paged_fp8(qp, *cache_, small, 299, status=status), kp[first:].view(torch.uint8).clone(), ks[first:].clone()))
+        assert fa.check_status(status) == fa.OK and kp[first:].float().any()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)

@@ -442,3 +442,32 @@ def test_training_run_through_the_attention():
     # (at most the weight times r sqrt(2), within the largest value's scale), plus q and k rounded once to bf16
     for g, w in zip((torch.cat(got[:3], 2), got[3], got[4]), (x.grad, wq.grad, wk.grad)):
         assert (g.double().cpu() - w).abs().max() <= 4e-2 * w.abs().max()
+
+
+def test_rows_past_32_bit_offsets():
+    # a projection of more than 2^31 elements: its last tokens come out as those of a short one at the same positions
+    N, n, Hq, Hkv, d = 350001, 5, 32, 8, 128
+    c = make(60, 1, n, Hq, Hkv, d, 128, True)
+    x = torch.zeros(1, N, Hq + 2 * Hkv, d, dtype=BF, device="cuda")
+    assert x.numel() > 2 ** 31
+    x[:, N - n:] = c["cu"]["x"]
+    shift = torch.tensor([N - n], dtype=torch.int32, device="cuda")
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    long = fa.qk_norm_rope(*split(c, x), c["rule"], q_offset=zero)
+    short = fa.qk_norm_rope(*split(c), c["rule"], q_offset=shift)
+    for a, b in zip(long, short):
+        assert torch.equal(a[:, :, N - n:], b) and not a[:, :, :8].any()
+    g = gen(61)
+    dy = [torch.randn(1, h, n, d, generator=g).cuda() for h in (Hq, Hkv, Hkv)]
+    far = [torch.zeros(1, h, N, d, device="cuda") for h in (Hq, Hkv, Hkv)]
+    for a, b in zip(far, dy):
+        a[:, :, N - n:] = b
+    q, k, _ = split(c, x)
+    grad = torch.empty_like(x)
+    got = fa.qk_norm_rope_backward(q, k, *far, c["rule"], q_offset=zero, **dict(zip(("dq_in", "dk_in", "dv_in"), split(c, grad))))
+    q, k, _ = split(c)
+    want = fa.qk_norm_rope_backward(q, k, *dy, c["rule"], q_offset=shift)
+    for a, b in zip(got[:3], want[:3]):
+        assert torch.equal(a[:, N - n:], b) and not a[:, :8].any()
+    for a, b in zip(got[3:], want[3:]):  # other CTAs hold the rows: the same terms in another order
+        assert ((a - b).abs() <= 1e-5 * b.abs().max()).all()
