@@ -204,12 +204,6 @@ __device__ __forceinline__ float row_max(float v) {
   return v;
 }
 
-__device__ __forceinline__ float add_up(const Eight& p) {  // sum of the 8 values
-  float x, y;
-  f2_unpack(f2_add(f2_add(p.a[0], p.a[1]), f2_add(p.b[0], p.b[1])), x, y);
-  return x + y;
-}
-
 // r of a row; every lane of the warp calls it
 template <int D>
 __device__ __forceinline__ float row_rsqrt(const Eight& x, float eps) {
@@ -691,8 +685,10 @@ __global__ void __launch_bounds__(kBlockThreads, 3)
 // a fixed order: no atomics, the same result each time.
 // ------------------------------------------------------------------------------------------------
 constexpr int kBwdThreads = 256;
-constexpr int kBwdRing = 6;
-constexpr int kBwdRingBytes = kBwdRing * kBwdThreads * 48;  // a row's 48 bytes a lane: 32 of dz, 16 of x
+constexpr int kBwdCtas = 2;                                 // of an SM, the grid is exactly those
+constexpr int kBwdRing = 4;
+constexpr int kBwdStep = kBwdThreads * 48;                  // a row's 48 bytes a lane: 32 of dz, 16 of x
+constexpr int kBwdRingBytes = kBwdRing * kBwdStep;
 
 template <bool F32, bool INTER>
 __device__ __forceinline__ void store_grad(void* p, int64_t at, const LaneMap& m, const Eight& g) {
@@ -708,152 +704,187 @@ __device__ __forceinline__ void store_grad(void* p, int64_t at, const LaneMap& m
 }
 
 template <int D, bool F32, bool INTER>
-__global__ void __launch_bounds__(kBwdThreads, 2) qkv_bwd_kernel(const __grid_constant__ QkvBwdArgs a,
-                                                                 const __grid_constant__ Shares sh) {
-  constexpr int LPR = D / 8, R = 32 / LPR, SLOTS = kBwdThreads / LPR;
-  extern __shared__ uint4 ring[];
-  const int tid = threadIdx.x, lane = tid % LPR, row = (tid % 32) / LPR;
-  const int64_t items = (int64_t)a.B * a.N * sh.groups;
-  const int64_t warp = (int64_t)blockIdx.x * (kBwdThreads / 32) + tid / 32, warps = (int64_t)gridDim.x * (kBwdThreads / 32);
-  const int hq = a.dq ? a.Hq : 0, hk = a.dk ? a.Hkv : 0, hv = a.dv ? a.Hkv : 0;
-  const LaneMap lm = lane_map<D, INTER>(lane, a.inv_freq ? a.rot : 0);
-  Cursor ld{warp, 0, 0, -1, 0, 0};
-  const float* dy = nullptr;
-  const bf16* src = nullptr;
-  int64_t hop = 0;
-  bool more = true;
-  int slot_in = 0;
-  const uint32_t my = smem_u32(ring) + tid * 16;
-  auto load = [&]() {
+struct BwdWarp {
+  static constexpr int LPR = D / 8, R = 32 / LPR;
+  const QkvBwdArgs& a;
+  const Shares& sh;
+  int lane, row, hq, hk, hv;
+  int64_t items, warps;
+  LaneMap lm;
+  Cursor ld;
+  const float* dy;
+  const bf16* src;
+  int64_t dy_hop, hop;
+  bool more;
+  uint32_t ring, in, out;
+  Turn turn;
+  Eight dwq, dwk;
+  int b, n;
+
+  __device__ __forceinline__ BwdWarp(const QkvBwdArgs& args, const Shares& shares, int64_t warp, int64_t n_warps, void* ring_mem)
+      : a(args), sh(shares), lane(threadIdx.x % LPR), row((threadIdx.x % 32) / LPR), hq(args.dq ? args.Hq : 0),
+        hk(args.dk ? args.Hkv : 0), hv(args.dv ? args.Hkv : 0), items((int64_t)args.B * args.N * shares.groups),
+        warps(n_warps), lm(lane_map<D, INTER>(lane, args.inv_freq ? args.rot : 0)), ld{warp, 0, 0, -1, 0, 0}, dy(nullptr),
+        src(nullptr), dy_hop((int64_t)R * args.N * D), hop(0), more(true), ring(smem_u32(ring_mem) + threadIdx.x * 16), in(0),
+        out(0), b(0), n(0) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) dwq.a[j] = dwq.b[j] = dwk.a[j] = dwk.b[j] = 0ull;
+#pragma unroll 1
+    for (int i = 0; i < kBwdRing; ++i) load();
+  }
+
+  __device__ __forceinline__ void load() {
     if (more) {
       if (ld.h >= ld.hend) {
         more = next_kind(ld, items, warps, a.N, sh, hq, hk, hv);
         if (more) {
           const int H = ld.kind == 0 ? a.Hq : a.Hkv;
-          dy = (ld.kind == 0 ? a.dq : ld.kind == 1 ? a.dk : a.dv) + (((int64_t)ld.b * H + ld.h + row) * a.N + ld.n) * D;
+          dy = (ld.kind == 0 ? a.dq : ld.kind == 1 ? a.dk : a.dv) + (((int64_t)ld.b * H + ld.h + row) * a.N + ld.n) * D + lm.ea;
           const Rows& S = ld.kind == 0 ? a.q : a.k;
           const bool with_x = ld.kind == 0 ? a.wq != nullptr : ld.kind == 1 && a.wk != nullptr;
-          src = with_x ? static_cast<const bf16*>(S.p) + ld.b * S.sb + ld.n * S.sn + (ld.h + row) * S.sh : nullptr;
-          hop = R * S.sh;
+          src = with_x ? static_cast<const bf16*>(S.p) + ld.b * S.sb + ld.n * S.sn + (ld.h + row) * S.sh + lm.ea : nullptr;
+          hop = with_x ? R * S.sh : 0;
         }
       }
       if (more) {
         if (ld.h + row < ld.hend) {
-          const uint32_t to = my + slot_in * (kBwdThreads * 48);
-          cp_async_16(to, dy + lm.ea, true);
-          cp_async_16(to + kBwdThreads * 16, dy + lm.eb, true);
+          cp_async_16(ring + in, dy, true);
+          cp_async_16(ring + in + kBwdThreads * 16, dy + (lm.eb - lm.ea), true);
           if (src) {
-            cp_async_8(to + kBwdThreads * 32, src + lm.ea);
-            cp_async_8(to + kBwdThreads * 32 + 8, src + lm.eb);
+            cp_async_8(ring + in + kBwdThreads * 32, src);
+            cp_async_8(ring + in + kBwdThreads * 32 + 8, src + (lm.eb - lm.ea));
           }
         }
-        dy += (int64_t)R * a.N * D;
-        if (src) src += hop;
+        dy += dy_hop;
+        src += hop;
         ld.h += R;
       }
     }
-    slot_in = slot_in + 1 == kBwdRing ? 0 : slot_in + 1;
+    in = in + kBwdStep == kBwdRingBytes ? 0 : in + kBwdStep;
     cp_async_commit();
-  };
-#pragma unroll 1
-  for (int i = 0; i < kBwdRing; ++i) load();
-  uint64_t f[4] = {0, 0, 0, 0};
-  if (a.inv_freq) lane_frequencies(a.inv_freq, lm, f);
-  Eight dw[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) dw[0].a[j] = dw[0].b[j] = dw[1].a[j] = dw[1].b[j] = 0ull;
-  Cursor at{warp, 0, 0, -1, 0, 0};
-  int slot_out = 0;
-  Turn turn;
-  int64_t item_of_turn = -1;
-  while (next_kind(at, items, warps, a.N, sh, hq, hk, hv)) {
-    const bool isq = at.kind == 0, isv = at.kind == 2;
-    if (item_of_turn != at.item) {
-      item_of_turn = at.item;
-      turn = turn_at(f, lm, (int64_t)at.n + (a.q_offset ? __ldg(a.q_offset + at.b) : 0));
-    }
-    const float* wp = isq ? a.wq : isv ? nullptr : a.wk;
-    const Eight w = load_weight<INTER>(wp, lm);
-    const Rows& S = isq ? a.dq_in : isv ? a.dv_in : a.dk_in;
-    const int64_t base = at.b * S.sb + at.n * S.sn;
-    Eight sum;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) sum.a[j] = sum.b[j] = 0ull;
-    for (; at.h < at.hend; at.h += R) {
+  }
+
+  // KIND 0: query rows, 1: key rows, 2: value rows; NORM: with a weight
+  template <int KIND, bool NORM>
+  __device__ __forceinline__ void heads_of(int g) {
+    const int per = KIND == 0 ? sh.q : sh.k, H = KIND == 0 ? hq : KIND == 1 ? hk : hv;
+    int h = g * per + row;
+    const int hend = min(H, g * per + per);
+    int left = (hend - g * per + R - 1) / R;
+    if (left <= 0) return;
+    Eight w;
+    if (NORM) w = load_weight<INTER>(KIND == 0 ? a.wq : a.wk, lm);
+    const Rows& S = KIND == 0 ? a.dq_in : KIND == 1 ? a.dk_in : a.dv_in;
+    int64_t to = b * S.sb + n * S.sn + h * S.sh;
+    const int64_t step = R * S.sh;
+    Eight& dw = KIND == 0 ? dwq : dwk;
+    for (; left > 0; --left) {
       cp_async_wait<kBwdRing - 1>();
-      const int h = at.h + row;
-      const bool live = h < at.hend;
-      const uint4* in = ring + slot_out * (kBwdThreads * 3) + tid;
+      const bool live = h < hend;
       float4 ga = make_float4(0.f, 0.f, 0.f, 0.f), gb = ga;
       uint4 xr = make_uint4(0, 0, 0, 0);
       if (live) {
-        ga = *reinterpret_cast<const float4*>(in);
-        gb = *reinterpret_cast<const float4*>(in + kBwdThreads);
-        if (wp) xr = in[2 * kBwdThreads];
+        const uint32_t at = ring + out;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(ga.x), "=f"(ga.y), "=f"(ga.z), "=f"(ga.w) : "r"(at) : "memory");
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(gb.x), "=f"(gb.y), "=f"(gb.z), "=f"(gb.w)
+                     : "r"(at + kBwdThreads * 16)
+                     : "memory");
+        if (NORM)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(xr.x), "=r"(xr.y), "=r"(xr.z), "=r"(xr.w)
+                       : "r"(at + kBwdThreads * 32)
+                       : "memory");
       }
-      slot_out = slot_out + 1 == kBwdRing ? 0 : slot_out + 1;
+      out = out + kBwdStep == kBwdRingBytes ? 0 : out + kBwdStep;
       load();
-      Eight g = unpack_f32<INTER>(ga, gb);
-      if (!isv) {
-        const Eight d = g;
-#pragma unroll
-        for (int j = 0; j < 2 && lm.rot; ++j) {
-          g.a[j] = f2_fma(d.a[j], turn.c[j], f2_mul(d.b[j], turn.s[j]));
-          g.b[j] = f2_fma(d.b[j], turn.c[j], f2_neg(f2_mul(d.a[j], turn.s[j])));
-        }
-        if (wp) {  // the same for the whole warp
-          const Eight x = unpack<INTER>(make_uint2(xr.x, xr.y), make_uint2(xr.z, xr.w));
-          const float r = row_rsqrt<D>(x, a.eps);
-          Eight gx, wgx;
-          const uint64_t rr = live ? f2_pack(r, r) : 0ull;
+      Eight g8 = unpack_f32<INTER>(ga, gb);
+      if (KIND != 2) {
+        if (lm.rot) {
+          const Eight d = g8;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            gx.a[j] = f2_mul(g.a[j], x.a[j]);
-            gx.b[j] = f2_mul(g.b[j], x.b[j]);
-            wgx.a[j] = f2_mul(w.a[j], gx.a[j]);
-            wgx.b[j] = f2_mul(w.b[j], gx.b[j]);
-            if (live) {  // a row that is not there may have r = inf
-              sum.a[j] = f2_fma(gx.a[j], rr, sum.a[j]);
-              sum.b[j] = f2_fma(gx.b[j], rr, sum.b[j]);
+            g8.a[j] = f2_fma(d.a[j], turn.c[j], f2_mul(d.b[j], turn.s[j]));
+            g8.b[j] = f2_fma(d.b[j], turn.c[j], f2_neg(f2_mul(d.a[j], turn.s[j])));
+          }
+        }
+        if (NORM) {
+          const Eight x = unpack<INTER>(make_uint2(xr.x, xr.y), make_uint2(xr.z, xr.w));
+          const float r = row_rsqrt<D>(x, a.eps);
+          const uint64_t rr = f2_pack(r, r);
+          Eight gx, wg;
+          uint64_t acc = 0ull;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            gx.a[j] = f2_mul(g8.a[j], x.a[j]);
+            gx.b[j] = f2_mul(g8.b[j], x.b[j]);
+            acc = f2_fma(w.a[j], gx.a[j], acc);
+            acc = f2_fma(w.b[j], gx.b[j], acc);
+            wg.a[j] = f2_mul(w.a[j], g8.a[j]);
+            wg.b[j] = f2_mul(w.b[j], g8.b[j]);
+          }
+          if (live) {  // a row that is not there may have r = inf
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              dw.a[j] = f2_fma(gx.a[j], rr, dw.a[j]);
+              dw.b[j] = f2_fma(gx.b[j], rr, dw.b[j]);
             }
           }
-          const float dot = row_sum<LPR>(add_up(wgx)) * r;        // sum of w g xhat
+          float u, v;
+          f2_unpack(acc, u, v);
+          const float dot = row_sum<LPR>(u + v) * r;              // sum of w g xhat
           const float k = -dot * (1.f / D) * r * r;
           const uint64_t kk = f2_pack(k, k);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            g.a[j] = f2_fma(f2_mul(w.a[j], g.a[j]), rr, f2_mul(x.a[j], kk));
-            g.b[j] = f2_fma(f2_mul(w.b[j], g.b[j]), rr, f2_mul(x.b[j], kk));
+            g8.a[j] = f2_fma(wg.a[j], rr, f2_mul(x.a[j], kk));
+            g8.b[j] = f2_fma(wg.b[j], rr, f2_mul(x.b[j], kk));
           }
         }
       }
-      if (live) store_grad<F32, INTER>(S.p, base + h * S.sh, lm, g);
-    }
-    if (wp) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (isq) {
-          dw[0].a[j] = f2_add(dw[0].a[j], sum.a[j]);
-          dw[0].b[j] = f2_add(dw[0].b[j], sum.b[j]);
-        } else {
-          dw[1].a[j] = f2_add(dw[1].a[j], sum.a[j]);
-          dw[1].b[j] = f2_add(dw[1].b[j], sum.b[j]);
-        }
-      }
+      if (live) store_grad<F32, INTER>(S.p, to, lm, g8);
+      to += step;
+      h += R;
     }
   }
-  cp_async_wait<0>();
+
+  __device__ __forceinline__ void run(int64_t warp) {
+    uint64_t f[4] = {0, 0, 0, 0};
+    if (a.inv_freq) lane_frequencies(a.inv_freq, lm, f);
+    for (int64_t item = warp; item < items; item += warps) {
+      const int64_t T = sh.groups == 1 ? item : item / sh.groups;
+      const int g = sh.groups == 1 ? 0 : (int)(item - T * sh.groups);
+      b = (int)((uint32_t)T / (uint32_t)a.N);
+      n = (int)((uint32_t)T - (uint32_t)b * (uint32_t)a.N);
+      turn = turn_at(f, lm, (int64_t)n + (a.q_offset ? __ldg(a.q_offset + b) : 0));
+      if (a.wq) heads_of<0, true>(g); else heads_of<0, false>(g);
+      if (a.wk) heads_of<1, true>(g); else heads_of<1, false>(g);
+      heads_of<2, false>(g);
+    }
+    cp_async_wait<0>();
+  }
+};
+
+template <int D, bool F32, bool INTER>
+__global__ void __launch_bounds__(kBwdThreads, kBwdCtas) qkv_bwd_kernel(const __grid_constant__ QkvBwdArgs a,
+                                                                        const __grid_constant__ Shares sh) {
+  constexpr int LPR = D / 8, SLOTS = kBwdThreads / LPR;
+  extern __shared__ uint4 ring[];
+  const int tid = threadIdx.x;
+  const int64_t warp = (int64_t)blockIdx.x * (kBwdThreads / 32) + tid / 32;
+  BwdWarp<D, F32, INTER> w(a, sh, warp, (int64_t)gridDim.x * (kBwdThreads / 32), ring);
+  w.run(warp);
   if (!a.wq && !a.wk) return;
   float (*s_dw)[D] = reinterpret_cast<float (*)[D]>(ring);  // the rings are read: [SLOTS][D]
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
     float y[8];
-    in_order<INTER>(dw[which], y);
+    in_order<INTER>(which ? w.dwk : w.dwq, y);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      s_dw[tid / LPR][lm.ea + e] = y[e];
-      s_dw[tid / LPR][lm.eb + e] = y[4 + e];
+      s_dw[tid / LPR][w.lm.ea + e] = y[e];
+      s_dw[tid / LPR][w.lm.eb + e] = y[4 + e];
     }
     __syncthreads();
     if (tid < D) {
@@ -944,7 +975,7 @@ cudaError_t run_bwd(const QkvBwdArgs& a, cudaStream_t st) {
 // CTAs of the backward's persistent grid, two an SM; fewer where there are not four tokens' worth of work for each
 int qk_bwd_ctas(int64_t tokens) {
   const int64_t n = (tokens + 3) / 4;
-  return (int)(n < 2 * kSms ? n : 2 * kSms);
+  return (int)(n < kBwdCtas * kSms ? n : kBwdCtas * kSms);
 }
 
 cudaError_t launch_qk_norm_rope(const QkvArgs& a, cudaStream_t st) {
