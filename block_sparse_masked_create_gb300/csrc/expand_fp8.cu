@@ -1,9 +1,10 @@
 // e4m3 pages -> bf16 K and V in token order, for the key blocks that a BlockMask lists: the first step of the
 // forward over an 8-bit paged cache. The tcgen05 forward then reads bf16 tiles as it always does.
 //
-// Bound: HBM, 1 byte read and 2 written a value (and read again by the forward, mostly from L2 for short contexts).
-// Against the forward's 4 Q_LEN Hq / Hkv operations a value this is small once Q_LEN * Hq / Hkv is in the hundreds,
-// which is what a prompt chunk has; single tokens go through the decode kernel, which reads the bytes themselves.
+// Bound: HBM, 1 byte read and 2 written a value (and read again by the forward, mostly from L2 for short contexts): about
+// 25 us of 182 for 4 x 1024 queries over 4096 keys, 32 / 8 heads. It is taken where more than 16 query tiles share a key
+// block, or the blocks are smaller than 128; few tiles go through the kernel that reads the pages, single tokens through the
+// decode.
 //
 // Positions that no query row may see (past the last key of a causal or prefix term) become zero, so what a page
 // holds behind its sequence does not matter.

@@ -1241,6 +1241,10 @@ fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_p
   return (fa_status)launch_decode_fp8(A, reinterpret_cast<cudaStream_t>(stream));
 }
 
+// 128 x 128 blocks run on the pages themselves where at most this many query tiles (nq * Hq / Hkv) share a key block, else the
+// listed blocks are expanded to bf16 first: each CTA converts what it reads, the expansion converts once. 8192 keys, 32 / 8
+// heads, pages / expanded: 4 tiles 131 / 179 us, 8 tiles 259 / 283, 16 tiles 255 / 249, 32 tiles 250 / 229. Soft-capped scores
+// always read the pages (the cap is exact there). Other block sizes are expanded.
 constexpr int64_t kDirectTiles = 16;
 struct PagedFp8Plan {
   bool direct;

