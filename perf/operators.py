@@ -175,11 +175,13 @@ def _handles(s):
     if c["prefix"]:
         spec += [("prefix", c["prefix"]), ("or",)]
     rule = fa.make_mask_rule(spec, q_offset=s["offset"], batch_dependent=True)
-    capacity = s["table"].shape[1] * c["page"]
+    # a prefix is shown to every row, also where it is longer than a request: those positions name page 0, as in the plain form
+    s["pages"] = s["table"].clamp(min=0)
+    s["capacity"] = s["table"].shape[1] * c["page"]
     if c["op"] == "decode":
-        s["mask"] = fa.create_block_mask(rule, c["B"], c["Hq"], 1, capacity, 1, c["page"], keep=[s["offset"]])
+        s["mask"] = fa.create_block_mask(rule, c["B"], c["Hq"], 1, s["capacity"], 1, c["page"], keep=[s["offset"]])
     else:
-        s["mask"] = fa.create_block_mask(rule, c["B"], c["Hq"], c["Q"], c["hi"], 128, 128, keep=[s["offset"]])
+        s["mask"] = fa.create_block_mask(rule, c["B"], c["Hq"], c["Q"], s["capacity"], 128, 128, keep=[s["offset"]])
     s["score"] = fa.make_score_rule(s["slopes"], softcap=c["softcap"])
 
 
@@ -213,9 +215,9 @@ def _own(s):
         fa.kv_append_fp8(q, k, v, s["k"], s["v"], s["ks"], s["vs"], s["table"], s["rule"], q_offset=s["offset"], n_new=s["n_new"], q_out=s["q_out"])
         return s["q_out"], s["k"], s["ks"], s["v"], s["vs"]
     if op == "decode":
-        o, lse = fa.flex_decode_fp8(s["q"][:, :, 0], s["k"], s["v"], s["ks"], s["vs"], s["table"], s["mask"], s["score"])
+        o, lse = fa.flex_decode_fp8(s["q"][:, :, 0], s["k"], s["v"], s["ks"], s["vs"], s["pages"], s["mask"], s["score"])
         return o[:, :, None], lse[..., None]
-    return fa.flex_forward_paged_fp8(s["q"], s["k"], s["v"], s["ks"], s["vs"], s["table"], s["mask"], c["hi"], s["score"])
+    return fa.flex_forward_paged_fp8(s["q"], s["k"], s["v"], s["ks"], s["vs"], s["pages"], s["mask"], s["capacity"], s["score"])
 
 
 def _angles(s):
