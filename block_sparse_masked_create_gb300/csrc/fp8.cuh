@@ -69,12 +69,23 @@ __device__ __forceinline__ int key_end(const DevRule& R, int Bm, int b, int q_le
   return (int)end;
 }
 
-// c * tanh(x / c) to about 2^-22 of c: tanh(u) = 1 - 2 / (1 + e^2u), two special-function operations where tanh.approx
-// takes one (and is off by 8e-6)
-__device__ __forceinline__ float softcap_exact(float x, float c, float inv_c) {
+// tanh(u) = 1 - 2 / (1 + e^2u), good to 2^-22 absolute: two special-function operations where tanh.approx takes one (and is
+// off by 8e-6). Below kTanhSmall the difference would lose the small value's digits, and the Taylor series up to u^13 takes its
+// place (its next term, 929569 / 638512875 u^15, is under 2^-23 of u there).
+constexpr float kTanhSmall = 0.5f;
+constexpr float kTanh3 = -1.f / 3.f, kTanh5 = 2.f / 15.f, kTanh7 = -17.f / 315.f, kTanh9 = 62.f / 2835.f,
+                kTanh11 = -1382.f / 155925.f, kTanh13 = 21844.f / 6081075.f;
+
+__device__ __forceinline__ float tanh_exact(float u) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(x * inv_c * 2.885390081777927f)));
-  return c * fmaf(-2.f, r, 1.f);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2_approx(u * 2.885390081777927f /* 2 log2(e) */)));
+  const float s = u * u;
+  float p = fmaf(s, fmaf(s, kTanh13, kTanh11), kTanh9);
+  p = fmaf(s, fmaf(s, fmaf(s, p, kTanh7), kTanh5), kTanh3);
+  return fabsf(u) < kTanhSmall ? u * fmaf(s, p, 1.f) : fmaf(-2.f, r, 1.f);
 }
+
+// c * tanh(x / c)
+__device__ __forceinline__ float softcap_exact(float x, float c, float inv_c) { return c * tanh_exact(x * inv_c); }
 
 }  // namespace fa

@@ -60,9 +60,10 @@ def spec_and_mask(window, prefix, i, j):
 
 def close(out, lse, want, d, softcap, dtype, extra, what):
     """O and LSE against the 64-bit result. P is rounded to fp16 (2^-11) once, 2^x and the sums are good to 2^-20; a score
-    is a sum of d products in fp32, off by at most (d + 4) half steps of scale sum |q k|, and by 1e-5 of a soft-cap."""
+    is a sum of d products in fp32, off by at most (d + 4) half steps of scale sum |q k|, and by 2^-21 of a soft-cap
+    (1 - 2 / (1 + e^2u): rcp and 2^x good to 2^-22 each)."""
     o, z, av, qk = want
-    ds = ((d + 4) * ref.U32 * qk + softcap * 1e-5 + extra)[..., None]
+    ds = ((d + 4) * ref.U32 * qk + softcap * 2.0 ** -21 + extra)[..., None]
     bound = (2.0 ** -11 + 2.0 ** -20 + 2 * ds) * av
     bound = bound + ref.HALF[dtype] * (o.abs() + bound)
     err = (out.double().cpu() - o).abs()
