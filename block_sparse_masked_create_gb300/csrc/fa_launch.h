@@ -203,12 +203,15 @@ int launch_decode_fp8(const DecFp8Args& a, cudaStream_t st);
 // for the same work, so more warps are wanted: four took 58 us where two took 78 (three requests of 100,000 tokens).
 constexpr int fp8_decode_ctas(int d) { return d == 128 ? 2 : 4; }
 
-// The forward over e4m3 pages, 128 x 128 blocks: a.k, a.v are the pages, a.page_table the table.
+// The forward over e4m3 pages, 128 x 128 blocks: a.k, a.v are the pages, a.page_table the table. With pack > 1 the `pack` query
+// heads of a KV head are the rows of one tile: a.Hq = Hkv and a.q_len = pack * rule_q_len <= 128, which is the same memory.
 struct FwdFp8Args {
   FwdArgs a;
   const float* k_scale;      // [n_pages_total, Hkv, page / 32]
   const float* v_scale;
   int32_t page;
+  int32_t pack;              // 1, or query heads in a tile
+  int32_t rule_q_len;        // query positions
 };
 int launch_fwd_fp8(const FwdFp8Args& a, cudaStream_t st);  // FA_OK / FA_ERR_CUDA
 

@@ -13,6 +13,8 @@
 //   warp 9          MMA issuer, as in the bf16 forward.
 //   warps 12 .. 15  converters: a staging tile's bytes to fp16 (exact, no scale) in the swizzled layout that the products
 //                   read, a row a thread; rows that no query may see, and pages that are not there, become zero.
+// Few queries a request (heads of a KV head times positions at most 128): the heads share a tile, so that each page is read
+// and converted once for all of them, and the two tiles of a CTA are two chunks of the keys.
 // Bytes to fp16 is one conversion for two values: 128 a thread and tile, about a fifth of the issue slots that a block's
 // softmax leaves. The whole saves writing and reading the expanded cache, 3 + 2 bytes a value.
 // Bound: the tensor pipe and the softmax, as the bf16 forward, and the instruction cache, which the roles share (its stalls fell
@@ -78,7 +80,8 @@ __device__ __forceinline__ uint32_t raw_at(int row, int c) {
   return D == 128 ? (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
 }
 
-template <int D, int SK>
+// PACK: P.f.pack > 1. As a run-time choice the turns cost the other calls 6 % (the producer's registers and instructions).
+template <int D, int SK, bool PACK>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_fp8_kernel(const __grid_constant__ Params P, const __grid_constant__ CUtensorMap tmQ,
                    const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -117,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Tile T0 = make_tile(a, b, h0, r0);
   const Tile T1 = make_tile(a, b, h1, r1);
   const bool any = T0.n + T1.n > 0;
-  const int end = key_end(a.rule, M.Bm, b, a.q_len, a.kv_len);
+  const int end = key_end(a.rule, M.Bm, b, P.f.rule_q_len, a.kv_len);
   const int page = P.f.page, page_log = 31 - __clz(page);
 
   uint8_t* sQ0 = smem;
@@ -159,7 +162,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     ++issued;
     return true;
   };
+  // the next element: its column, and which tiles visit it (bits 0, 1) and whether it is the last (bit 2)
   Union uw;
+  auto take_next = [&](int& flags) -> int {
+    bool i0, i1;
+    int c;
+    if (!PACK) {
+      c = uw.take(T0, T1, desc, i0, i1);
+    } else {  // the two tiles are chunks of one row: in turns, so that one's softmax runs under the other's products
+      const int k0 = uw.w0.next_key(), k1 = uw.w1.next_key();
+      i0 = k1 == INT_MAX || (k0 != INT_MAX && uw.w0.f + uw.w0.p <= uw.w1.f + uw.w1.p);
+      i1 = !i0;
+      c = key_col(i0 ? k0 : k1, desc);
+      if (i0) uw.w0.advance(T0, desc); else uw.w1.advance(T1, desc);
+    }
+    flags = (int)i0 | ((int)i1 << 1) | (uw.done() ? 4 : 0);
+    return c;
+  };
   int c_first = -1;  // producer: column of the first element
   if (warp == kLoadWarp) {
     if (lane == 0) {
@@ -201,9 +220,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (any) {  // K of the first element: there is room, so nothing is waited for
       uw.init(T0, T1, desc);
-      bool i0, i1;
-      c_first = uw.take(T0, T1, desc, i0, i1);
-      load(false, c_first, (int)i0 | ((int)i1 << 1) | (uw.done() ? 4 : 0), WaitCtl{a.timeout_ns, a.status, &s_abort});
+      int fl;
+      c_first = take_next(fl);
+      load(false, c_first, fl, WaitCtl{a.timeout_ns, a.status, &s_abort});
     }
   }
   if (warp == kMmaWarp) {
@@ -239,9 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (c >= 0 && ok) {
       ok = load(true, c, 0, wc);
       if (!ok || uw.done()) break;
-      bool i0, i1;
-      c = uw.take(T0, T1, desc, i0, i1);
-      ok = load(false, c, (int)i0 | ((int)i1 << 1) | (uw.done() ? 4 : 0), wc);
+      int fl;
+      c = take_next(fl);
+      ok = load(false, c, fl, wc);
     }
     if (!ok || *wc.abort) {
       // drain: the last copies may still be landing in shared memory
@@ -360,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = (warp & 3) * 32 + lane;
     const Tile TT = t ? T1 : T0;
     uint8_t* const sQt = t ? sQ1 : sQ0;
-    const int q_row = TT.rq * 128 + row;  // query position within the sequence
+    const int q_row = TT.rq * 128 + row;  // row of the tile's head
     const int o_row = TT.r * 128 + row;   // output row (the same unless rows are split)
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_base + C::col_s(t);
@@ -378,7 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (TT.valid) {
       const int64_t off_b = a.rule.q_offset ? (int64_t)__ldg(a.rule.q_offset + (M.Bm > 1 ? b : 0)) : 0;
-      const int64_t ig = (int64_t)q_row + off_b;
+      // the row's query head and position (a packed tile holds the heads of a KV head one after the other)
+      const int sub_head = PACK ? min(q_row / P.f.rule_q_len, P.f.pack - 1) : 0;
+      const int head = PACK ? TT.h * P.f.pack + sub_head : TT.h;
+      const int64_t ig = (int64_t)(PACK ? q_row - sub_head * P.f.rule_q_len : q_row) + off_b;
       const int bm = M.Bm > 1 ? b : 0;
       bool ok = true;
       // ---- the row of Q to fp16, divided by the power of two under its largest magnitude
@@ -411,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar_qc[t]);
       }
       const float qs = a.scale * up;                    // times a K scale: the factor of a score column
-      const float slope2 = (SK == SK_ALIBI || SK == SK_GENERIC) && a.score.alibi ? __ldg(a.score.alibi + TT.h) * kLog2e : 0.f;
+      const float slope2 = (SK == SK_ALIBI || SK == SK_GENERIC) && a.score.alibi ? __ldg(a.score.alibi + head) * kLog2e : 0.f;
       const float cap2 = SK == SK_SOFTCAP ? a.score.softcap * kLog2e : 1.f;
       float m_ref = -INFINITY, le = 0.f, vref = 1.f;
       // scales of a block, looked up one block ahead: lane q holds the K scale of its tokens 32 q .. (q < 4), lane 4 + q
@@ -534,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (a.score.rel) {
                 int64_t ix = dist + a.score.kv_len - 1;
                 ix = ix < 0 ? 0 : (ix > 2 * (int64_t)a.score.kv_len - 2 ? 2 * (int64_t)a.score.kv_len - 2 : ix);
-                v += __ldg(a.score.rel + (size_t)TT.h * (2 * (size_t)a.score.kv_len - 1) + ix);
+                v += __ldg(a.score.rel + (size_t)head * (2 * (size_t)a.score.kv_len - 1) + ix);
               }
               if (a.score.softcap > 0.f) v = softcap_exact(v, a.score.softcap, a.score.inv_softcap);
               x[i] = v * kLog2e;
@@ -711,7 +733,7 @@ int launch_k(const FwdFp8Args& f, cudaStream_t st) {
   p.desc = a.score.alibi != nullptr;
   p.group = p.pair_rows && (a.mask.nq + 1) / 2 >= 128 ? 4 : 8;
   const int n_items = p.pair_rows ? a.B * a.Hq * ((a.mask.nq + 1) / 2) : a.B * ((a.Hq + 1) / 2) * a.mask.nq;
-  auto kern = fwd_fp8_kernel<D, SK>;
+  auto kern = f.pack > 1 ? fwd_fp8_kernel<D, SK, true> : fwd_fp8_kernel<D, SK, false>;
   cudaFuncAttributes at;  // the register split counts on what the launch allocates
   if (cudaFuncGetAttributes(&at, kern) != cudaSuccess || at.numRegs * kThreads < 256 * (kSoftmaxRegs + kOtherRegs))
     return FA_ERR_CUDA;

@@ -252,10 +252,11 @@ def test_prefill_matches_64_bits_and_the_bf16_forward(page, bk, Q, Hq, Hkv, d, w
 
 @pytest.mark.parametrize("kw", [dict(prefix=70), dict(window=1), dict(softcap=100.0), dict(rel=True), dict(alibi=True, softcap=30.0), dict(doc=True),
                                 dict(spread=9), dict(power=False), dict(q_scale=1e-20), dict(dense=True)], ids=str)
-@pytest.mark.parametrize("d,page", [(128, 64), (64, 128)])
-def test_prefill_rules_and_scales(kw, d, page):
-    # 128 x 128 blocks: every score path, document masks, V scales up to 2^9 apart in a block, a rule without a causal bound
-    Q, Hq, Hkv, lens = 150, 4, 2, [150, 390]
+@pytest.mark.parametrize("d,page,Q", [(128, 64, 150), (64, 128, 150), (128, 128, 30), (64, 32, 1)])
+def test_prefill_rules_and_scales(kw, d, page, Q):
+    # 128 x 128 blocks: every score path, document masks, V scales up to 2^9 apart in a block, a rule without a causal bound;
+    # few queries: the heads of a KV head share a tile
+    Hq, Hkv, lens = (4, 2, [150, 390]) if Q == 150 else (6, 2, [150, 390])
     kp, vp, ks, vs, table = cache(40, lens, Hkv, page, d, kw.get("spread", 1), power=kw.get("power", True))
     B, n = len(lens), max(lens)
     if kw.get("dense"):
@@ -277,7 +278,9 @@ def test_prefill_rules_and_scales(kw, d, page):
     cap = kw.get("softcap", 0.0)
     sc = fa.make_score_rule(None if slopes is None else slopes.cuda(), None if rel is None else rel.cuda(), cap)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out, lse = fa.flex_forward_paged_fp8(*[t.cuda() for t in (q, kp, vp, ks, vs, table)], bm, n, sc, status=status, out_dtype=F32)
+    args = [t.cuda() for t in (q, kp, vp, ks, vs, table)]
+    out, lse = fa.flex_forward_paged_fp8(*args, bm, n, sc, status=status, out_dtype=F32)
+    cut, cut_lse = fa.flex_forward_paged_fp8(*args, bm, n, sc, status=status, out_dtype=F32, chunk_blocks=1)
     assert fa.check_status(status) == fa.OK
     dk, dv = ref.dequant(kp, ks), ref.dequant(vp, vs)
     for b, L in enumerate(lens):
@@ -292,6 +295,8 @@ def test_prefill_rules_and_scales(kw, d, page):
         floor = 2.0 ** -25 * 448 * float(vs[table[b, :-(-L // page)].long()].nan_to_num(0).max()) * L if kw.get("spread") else 0.0
         want = (want[0], want[1], want[2] + floor * 2.0 ** 11, want[3])
         close(out[b], lse[b], want, d, cap, F32, 20 * ref.U32 * (L + 8), f"request {b} {kw}")
+        # cut into single key blocks and merged in fp32: 4 more roundings of the sums, and 2^x of differences of LSEs
+        close(cut[b], cut_lse[b], want, d, cap, F32, 20 * ref.U32 * (L + 8) + 2.0 ** -18, f"cut, request {b} {kw}")
 
 
 def test_prefill_cut_rows():
