@@ -22,6 +22,7 @@
 // 128: 134 us with the merge of the cut rows, 1020 TFLOP/s (expanding first: 263); long rows take 1.2 times the bf16 forward.
 // Registers: 512 threads launch with 128 each; the softmax warps go up to 192 and the others down to 64, together the
 // same 65,536 (with 168 and 88 the softmax spilled).
+#include <cfloat>
 #include <cstring>
 
 #include "fp8.cuh"
@@ -504,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 4; ++k) mult[k] = qs * __shfl_sync(0xFFFFFFFFu, sc, k);
         if (SK == SK_NONE) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mult[k] *= kLog2e;
+          for (int k = 0; k < 4; ++k)  // never 0: a masked column is -inf. (Under it every visible score rounds to 0 all the same.)
+            mult[k] = fmaxf(mult[k] * kLog2e, FLT_MIN);
         } else if (SK == SK_ALIBI) {
           // the bias is linear in the column: four chains step by 8 columns (see the bf16 forward)
           const float base = -slope2 * (float)(ig - j0);
