@@ -7,8 +7,9 @@
 // arrive as bytes and all products run in fp16:
 //   warps 0 .. 7    softmax, a thread a query row. Before the loop each thread turns its row of Q into fp16, divided by a
 //                   power of two (exact but for what is 2^-24 of the row's largest). A score column is multiplied by its
-//                   block's K scale, P carries its block's V scale relative to a reference that O is held in (a factor in
-//                   the exponent, four a row and block, from registers); the row sum is taken without it.
+//                   block's K scale, P carries its block's V scale (a factor in the exponent, four a row and block, from
+//                   registers); the row sum is taken without it. The unit that a row's O and sum are held in is a power of
+//                   two by the largest P times V scale that the row sees: scales of what it does not see play no part.
 //   warp 8          TMA producer: the pages of each key block of the union, as bytes, into a ring of staging tiles.
 //   warp 9          MMA issuer, as in the bf16 forward.
 //   warps 12 .. 15  converters: a staging tile's bytes to fp16 (exact, no scale) in the swizzled layout that the products
@@ -39,8 +40,7 @@ constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
 static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 512 * 128, "registers of the launch");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: P values stay <= 2^8
-constexpr float kScaleSpan = 16.f;         // the V reference moves where a block's largest V scale leaves it by more
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P times its V scale stays <= 2^8 in the row's unit
 
 enum ScoreKind { SK_NONE = 0, SK_ALIBI = 1, SK_SOFTCAP = 2, SK_GENERIC = 3 };
 
@@ -79,6 +79,11 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
 template <int D>
 __device__ __forceinline__ uint32_t raw_at(int row, int c) {
   return D == 128 ? (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)) : (uint32_t)(row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
+}
+
+// 2^n of a whole n; 0 below 2^-126
+__device__ __forceinline__ float pow2_whole(float n) {
+  return __uint_as_float((uint32_t)(int)(fminf(fmaxf(n, -127.f), 127.f) + 127.f) << 23);
 }
 
 // PACK: P.f.pack > 1. As a run-time choice the turns cost the other calls 6 % (the producer's registers and instructions).
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float qs = a.scale * up;                    // times a K scale: the factor of a score column
       const float slope2 = (SK == SK_ALIBI || SK == SK_GENERIC) && a.score.alibi ? __ldg(a.score.alibi + head) * kLog2e : 0.f;
       const float cap2 = SK == SK_SOFTCAP ? a.score.softcap * kLog2e : 1.f;
-      float m_ref = -INFINITY, le = 0.f, vref = 1.f;
+      float ref = -INFINITY, le = 0.f;  // O and the row sum are held in units of 2^ref
       // scales of a block, looked up one block ahead: lane q holds the K scale of its tokens 32 q .. (q < 4), lane 4 + q
       // the V scale. (A second walk two blocks ahead, so that no step of list -> page table -> scale is waited for, was 10 %
       // slower: the instructions weigh more than the waits, which lie under the products.)
@@ -474,24 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             });
           }
         }
-        // the V reference, the same for every row of the tile; then each lane's own scale becomes what the row needs of
-        // it: the factor of a score column, or log2 and inverse of the V scale relative to the reference
-        float vm = (lane & 4) ? sc : 0.f;
-        vm = fmaxf(vm, __shfl_xor_sync(0xFFFFFFFFu, vm, 1));
-        vm = fmaxf(vm, __shfl_xor_sync(0xFFFFFFFFu, vm, 2));
-        vm = __shfl_sync(0xFFFFFFFFu, vm, 4);
-        float fv = 1.f;
-        if (j == 0) {
-          vref = vm;
-        } else if (vm > vref * kScaleSpan || vm * kScaleSpan < vref) {
-          fv = vref / vm;
-          vref = vm;
-        }
-        float l_inv, l_log;  // exact for powers of two, else to 2^-22 (the row sum undoes the factor it is given)
+        // log2 and inverse of the lane's scale: the whole part exact, the rest good to 2^-22 (the row sum undoes the factor)
+        const uint32_t sb = __float_as_uint(sc);
+        float l_inv, l_log;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(l_inv) : "f"(sc));
-        l_inv *= vref;
-        asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l_log) : "f"(l_inv));
-        l_log = -l_log;
+        asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(l_log) : "f"(__uint_as_float((sb & 0x7FFFFFu) | 0x3F800000u)));
+        l_log += (float)((int)(sb >> 23) - 127);
         if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_s[t], (uint32_t)(j & 1), wc));
         if (!ok) continue;
         tc5_fence_after();
@@ -578,31 +571,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) x[k * 32 + i] = ((wd >> i) & 1u) ? x[k * 32 + i] : -INFINITY;
           }
         }
-        // ---- the row's block max, a chain for each factor
-        float mb = -INFINITY;
+        // ---- the row's largest p * vs in the block, a chain for each factor. What a row does not see has no part in it
+        float lg[4], top;
         {
           float mx[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
+            lg[k] = __shfl_sync(0xFFFFFFFFu, l_log, 4 + k);
             mx[k] = fmaxf(x[32 * k], x[32 * k + 1]);
 #pragma unroll
             for (int i = 2; i < 32; i += 2) mx[k] = fmax3(mx[k], x[32 * k + i], x[32 * k + i + 1]);
+            mx[k] = fmaf(mx[k], mult[k], lg[k]);
           }
-          mb = fmaxf(fmax3(mx[0] * mult[0], mx[1] * mult[1], mx[2] * mult[2]), mx[3] * mult[3]);
+          top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
         }
         float alpha = 1.f;
         bool rescale = false;
-        if (mb > m_ref + kRescaleThreshold || (m_ref == -INFINITY && mb > -INFINITY)) {
-          alpha = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - mb);
-          rescale = j > 0 && m_ref != -INFINITY;
-          m_ref = mb;
+        if (top > ref + kRescaleThreshold) {
+          const float to = floorf(top);  // whole: units change by powers of two
+          rescale = ref != -INFINITY;
+          if (rescale) alpha = pow2_whole(ref - to);
+          ref = to;
         }
-        const float mr = m_ref == -INFINITY ? 0.f : m_ref;
-        // ---- P vs / vref = 2^(mult x - m + log2(vs / vref)) in fp16, and the row sum of P
+        const float rf = ref == -INFINITY ? 0.f : ref;
+        // ---- P vs = 2^(mult x + log2 vs - ref) in fp16, and the row sum of P in the same unit
         float sum = 0.f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float add = __shfl_sync(0xFFFFFFFFu, l_log, 4 + k) - mr, inv_k = __shfl_sync(0xFFFFFFFFu, l_inv, 4 + k);
+          const float add = lg[k] - rf, inv_k = __shfl_sync(0xFFFFFFFFu, l_inv, 4 + k);
           const uint64_t mul2 = f2_pack(mult[k], mult[k]), add2 = f2_pack(add, add);
           uint64_t se[2] = {0, 0};
 #pragma unroll
@@ -625,15 +621,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         le = le * alpha + sum;
         // ---- O is stable here: S_t completed, and O_t's previous update was issued before it
-        if (j > 0 && __any_sync(0xFFFFFFFFu, rescale || fv != 1.f)) {
-          const float f = (rescale ? alpha : 1.f) * fv;
+        if (j > 0 && __any_sync(0xFFFFFFFFu, rescale)) {
 #pragma unroll
           for (int c0 = 0; c0 < D; c0 += 32) {
             uint32_t o[32];
             tc5_ld32(tO + c0, o);
             tc5_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
             tc5_st32(tO + c0, o);
           }
         }
@@ -646,9 +641,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xFFFFFFFFu, ok);
       if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&bar_o[t], (uint32_t)((TT.n - 1) & 1), wc));
       tc5_fence_after();
-      const bool empty = m_ref == -INFINITY;
-      const float inv = empty ? 0.f : vref / le;
-      if (ok && q_row < a.q_len) Lg[o_row] = empty ? -INFINITY : (m_ref + log2f(le)) * kLn2;
+      const bool empty = ref == -INFINITY;
+      const float inv = empty ? 0.f : 1.f / le;
+      if (ok && q_row < a.q_len) Lg[o_row] = empty ? -INFINITY : (ref + log2f(le)) * kLn2;
       constexpr int QB = D / 64;  // bf16 boxes, and fp32 boxes of a round, that the Q buffer holds
       const int rounds = a.out_f32 ? (D / 32) / QB : 1;
       for (int rd = 0; rd < rounds; ++rd) {

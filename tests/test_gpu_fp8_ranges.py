@@ -75,3 +75,60 @@ def test_prefill_queries_near_zero(q_scale, d, page, Q):
         for b, L in enumerate(lens):
             i, j = off[b] + torch.arange(Q)[:, None], torch.arange(L)[None]
             close(out[b], lse[b], request(q, cached, b, L, i, j <= i), d, 0.0, F32, 2.0 ** -18 if chunk > 0 else 0.0, f"request {b}")
+
+
+# ------------------------------------------------------------------------------------------ V scales far apart
+@pytest.mark.parametrize("factor", [2.0 ** 20, 2.0 ** 30, 2.0 ** 45])
+@pytest.mark.parametrize("d,page,Q,Hq", [(128, 64, 150, 4), (64, 32, 150, 4), (64, 128, 30, 6)])
+def test_prefill_large_v_scale_that_a_row_does_not_see(factor, d, page, Q, Hq):
+    # tokens 256 .. 287 are seen by the first rows of Q = 150 and by none of Q = 30
+    L, window = 390, 40
+    cached = cache(62, [L], 2, page, d)
+    cached[3][cached[4][0, 256 // page], :, 256 % page // 32] *= factor
+    q = torch.randn(1, Hq, Q, d, generator=gen(63)).to(BF)
+    i, j = L - Q + torch.arange(Q)[:, None], torch.arange(L)[None]
+    al = (j <= i) & (i - j < window)
+    want = request(q, cached, 0, L, i, al)
+    # a key's share in units of at most 2 times the row's largest
+    want = widened(want, subnormal_floor(q, cached, 0, L, al, d ** -0.5, 2.0, of_block=False))
+    for chunk in (-1, 1):
+        out, lse, st = forward(q, cached, [L], [L - Q], window, chunk=chunk)
+        assert st == fa.OK
+        close(out[0], lse[0], want, d, 0.0, F32, 2.0 ** -18, f"chunk {chunk}")
+
+
+@pytest.mark.parametrize("bk,Q,Hq,Hkv,d", [(128, 90, 8, 2, 64), (128, 20, 6, 2, 128), (64, 90, 8, 2, 64), (128, 150, 16, 1, 64)])
+def test_prefill_of_a_padded_batch_over_a_used_pool(bk, Q, Hq, Hkv, d):
+    # prompts of several lengths appended and attended in one call each: rows behind a prompt see what the pool held before (bytes
+    # without NaN, any scales), and the prompt's rows are right all the same
+    B, page = 3, 64
+    lens = [Q, Q // 3, Q - 7]
+    g = gen(66)
+    each = -(-Q // page)
+    table = torch.randperm(B * each + 1, generator=g)[:B * each].view(B, each).to(torch.int32)
+
+    def pool():
+        x = torch.randint(0, 256, (B * each + 1, Hkv, page, d), generator=g, dtype=torch.uint8)
+        x[(x & 0x7F) == NAN_BYTE] = 0
+        s = torch.tensor([2.0 ** 60, math.inf, math.nan, 0.0, -1.0, 2.0 ** 38])[torch.randint(0, 6, (B * each + 1, Hkv, page // 32), generator=g)]
+        return x.cuda().view(F8), s.cuda()
+
+    (kp, ks), (vp, vs) = pool(), pool()
+    x = torch.randn(B, Q, Hq + 2 * Hkv, d, generator=g).to(BF).cuda()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = fa.kv_append_fp8(*x.split([Hq, Hkv, Hkv], dim=2), kp, vp, ks, vs, table.cuda(), n_new=torch.tensor(lens, dtype=torch.int32).cuda(), status=status)
+    assert fa.check_status(status) == fa.OK
+    q = q.cpu()
+    for b, L in enumerate(lens):
+        q[b, :, L:] = 1.0  # rows that the append leaves as they are
+    cached = tuple(t.cpu() for t in (kp, vp, ks, vs)) + (table,)
+    out, lse, st = forward(q, cached, lens, [0] * B, bk=bk, n=Q)
+    assert st == fa.OK
+    for b, L in enumerate(lens):
+        i, j = torch.arange(L)[:, None], torch.arange(L)[None]
+        want = request(q[:, :, :L], cached, b, L, i, j <= i)
+        if bk == 128 and -(-Q // 128) * (Hq // Hkv) <= 16:
+            close(out[b, :, :L], lse[b, :, :L], want, d, 0.0, F32, 0.0, f"request {b}")
+        else:  # expanded: P is bf16
+            assert ((out[b, :, :L].double().cpu() - want[0]).abs() <= (2.0 ** -8 + 2.0 ** -10) * want[2] + 1e-4).all()
+            assert (lse[b, :, :L].double().cpu() - want[1]).abs().max() <= 2e-3
