@@ -40,7 +40,12 @@ constexpr int kSoftmaxRegs = 192, kOtherRegs = 64;
 static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 512 * 128, "registers of the launch");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units: P times its V scale stays <= 2^8 in the row's unit
+// The row's unit, 2^ref: P times its V scale lies in fp16, whose smallest step is 2^-24 and largest value just under 2^16. A new unit
+// is set 2^7 under a block's largest, and kept while a block's largest stays within 2^-1 .. 2^15 of it, so that a key 2^-13 of its
+// block's largest keeps all its bits and one 2^-23 of it is not lost. (A unit that only rises leaves the many small keys of a long row
+// that one key outweighs to the subnormals: 20,000 keys at e^-17 of one with V = 0 were off by 44 %.) Units are not lowered beyond
+// 2^-40 of the row's largest so far, which keeps sums below 2^127.
+constexpr float kUnitBelow = 7.f, kMost = 15.f, kLeast = -1.f, kUnitSpan = 40.f;
 
 enum ScoreKind { SK_NONE = 0, SK_ALIBI = 1, SK_SOFTCAP = 2, SK_GENERIC = 3 };
 
@@ -441,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float qs = a.scale * up;                    // times a K scale: the factor of a score column
       const float slope2 = (SK == SK_ALIBI || SK == SK_GENERIC) && a.score.alibi ? __ldg(a.score.alibi + head) * kLog2e : 0.f;
       const float cap2 = SK == SK_SOFTCAP ? a.score.softcap * kLog2e : 1.f;
-      float ref = -INFINITY, le = 0.f;  // O and the row sum are held in units of 2^ref
+      float ref = -INFINITY, largest = -INFINITY, le = 0.f;  // O and the row sum are held in units of 2^ref
       // scales of a block, looked up one block ahead: lane q holds the K scale of its tokens 32 q .. (q < 4), lane 4 + q
       // the V scale. (A second walk two blocks ahead, so that no step of list -> page table -> scale is waited for, was 10 %
       // slower: the instructions weigh more than the waits, which lie under the products.)
@@ -587,9 +592,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float alpha = 1.f;
         bool rescale = false;
-        if (top > ref + kRescaleThreshold) {
-          const float to = floorf(top);  // whole: units change by powers of two
-          rescale = ref != -INFINITY;
+        largest = fmaxf(largest, top);
+        if (top > ref + kMost || (top < ref + kLeast && top > -INFINITY)) {
+          const float to = floorf(fmaxf(top - kUnitBelow, largest - kUnitSpan));  // whole: units change by powers of two
+          rescale = ref != -INFINITY && to != ref;
           if (rescale) alpha = pow2_whole(ref - to);
           ref = to;
         }

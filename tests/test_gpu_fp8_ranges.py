@@ -132,3 +132,80 @@ def test_prefill_of_a_padded_batch_over_a_used_pool(bk, Q, Hq, Hkv, d):
         else:  # expanded: P is bf16
             assert ((out[b, :, :L].double().cpu() - want[0]).abs() <= (2.0 ** -8 + 2.0 ** -10) * want[2] + 1e-4).all()
             assert (lse[b, :, :L].double().cpu() - want[1]).abs().max() <= 2e-3
+
+
+# ------------------------------------------------------------------------------------------ one key outweighs a long row
+def sink_case(L, at, d, Hkv):
+    """Keys of zero but for token `at`, which q = (4, 0 ..) scores 128 * scale; V is 1 but for that token's, which is 0."""
+    page = 64
+    kp, vp, ks, vs, table = cache(67, [L], Hkv, page, d)
+    kp.zero_()
+    vp.copy_(torch.full_like(vp, 256.0, dtype=F32).to(F8))
+    ks.fill_(2.0 ** -40)
+    vs.fill_(2.0 ** -8)
+    kp[table[0, at // page], :, at % page, 0] = 256.0
+    ks[table[0, at // page], :, at % page // 32] = 2.0 ** -3
+    vp[table[0, at // page], :, at % page] = 0.0
+    return kp, vp, ks, vs, table
+
+
+@pytest.mark.parametrize("lead", [10.0, 14.0, 17.0, 17.4, 20.0, 26.0])
+@pytest.mark.parametrize("Q,Hq,d,at", [(130, 1, 64, 0), (130, 1, 64, 9999), (30, 4, 128, 0), (1, 2, 64, 40)])
+def test_prefill_one_key_outweighs_a_long_row(lead, Q, Hq, d, at):
+    L = 20000
+    cached = sink_case(L, at, d, 1)
+    q = torch.zeros(1, Hq, Q, d)
+    q[..., 0] = 4.0
+    q, scale = q.to(BF), lead / 128
+    i, j = L - Q + torch.arange(Q)[:, None], torch.arange(L)[None]
+    want = request(q, cached, 0, L, i, j <= i, scale)
+    # units of at most twice a block's largest share
+    want = widened(want, subnormal_floor(q, cached, 0, L, j <= i, scale, 2.0 ** -7 if at == 0 else 2.0))
+    for chunk in (-1, 0, 5):
+        out, lse, st = forward(q, cached, [L], [L - Q], chunk=chunk, scale=scale)
+        assert st == fa.OK
+        close(out[0], lse[0], want, d, 0.0, F32, 2.0 ** -18, f"chunk {chunk}")
+
+
+def test_prefill_scores_that_fall_and_rise():
+    # scores that fall by 60 and rise by 100 (base 2) over the row, V scales that go the other way: the reference follows
+    L, Q, d, page = 2000, 130, 64, 64
+    kp, vp, ks, vs, table = cache(68, [L], 1, page, d)
+    t = torch.arange(L // 32 + 2).float()
+    level = torch.where(t < 25, -2.0 * t, -50 + 2.5 * (t - 25)).round()
+    kp.zero_()
+    kp[..., 0] = torch.full(kp[..., 0].shape, 256.0).to(F8)
+    for c in range(-(-L // 32)):
+        p, s = int(table[0, c * 32 // page]), c * 32 % page // 32
+        kp[p, 0, s * 32:s * 32 + 32, 0] = torch.tensor(float(level[c])).to(F8)
+        ks[p, 0, s] = 1.0
+        vs[p, 0, s] = 2.0 ** float(-level[c] / 2).__round__()
+    q = torch.zeros(1, 2, Q, d)
+    q[..., 0] = 1.0
+    q, cached = q.to(BF), (kp, vp, ks, vs, table)
+    i, j = L - Q + torch.arange(Q)[:, None], torch.arange(L)[None]
+    want = widened(request(q, cached, 0, L, i, j <= i, 0.7), subnormal_floor(q, cached, 0, L, j <= i, 0.7, 2.0))
+    for chunk in (-1, 3):
+        out, lse, st = forward(q, cached, [L], [L - Q], chunk=chunk, scale=0.7)
+        assert st == fa.OK
+        close(out[0], lse[0], want, d, 0.0, F32, 2.0 ** -18, f"chunk {chunk}")
+
+
+@pytest.mark.parametrize("power", [True, False])
+@pytest.mark.parametrize("d,page,Q,Hq", [(128, 64, 150, 4), (64, 128, 30, 6)])
+def test_prefill_v_scales_2_to_the_30_apart(power, d, page, Q, Hq):
+    lens = [150, 390]
+    kp, _, ks, _, table = cache(64, lens, 2, page, d, power=power)
+    _, vp, _, vs, _ = cache(64, lens, 2, page, d, 30, power=power)
+    cached = kp, vp, ks, vs, table
+    q = torch.randn(2, Hq, Q, d, generator=gen(65)).to(BF)
+    off = [L - Q for L in lens]
+    for chunk in (-1, 1):
+        out, lse, st = forward(q, cached, lens, off, chunk=chunk)
+        assert st == fa.OK
+        for b, L in enumerate(lens):
+            i, j = off[b] + torch.arange(Q)[:, None], torch.arange(L)[None]
+            want = widened(request(q, cached, b, L, i, j <= i), subnormal_floor(q, cached, b, L, j <= i, d ** -0.5, 2.0))
+            # the row sum is held in the unit of p * v_scale: a logarithm of up to 2^6 is added to the LSE (2^-19), and the logarithms
+            # of scales that are no powers of two are good to 2^-19
+            close(out[b], lse[b], want, d, 0.0, F32, 2.0 ** -18, f"request {b}, chunk {chunk}")
