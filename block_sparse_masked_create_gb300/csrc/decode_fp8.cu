@@ -10,7 +10,8 @@
 //    32-bit register of four neighbouring bytes feeds one MMA step as it is; V comes through a transposing ldmatrix of
 //    16-bit pairs, one byte permute splits even and odd columns, and a lane ends up with four neighbouring columns of O.
 //  - P is fp16 (2^-12 relative, against 2^-9 for bf16), unscaled: O is held in units of the current V scale and changes
-//    units only where the scale does. The reference maximum moves only past a factor of 2^8.
+//    units only where the scale does. P's own unit lies 2^7 or more under the largest P of the warp's keys (1024 at most) and
+//    moves only past a factor of 2^8, so that a P below 2^-21 of that largest is off by at most 2^-32 of it.
 //  - what a sub-tile needs besides its bytes (page, scales, mask bits) is looked up by one lane for each sub-tile of the
 //    warp at the start, all at once, and handed round by shuffles.
 //  - groups of at most 8 query heads (HALF) leave rows 8 .. 15 of the MMA tile out of the softmax.
@@ -27,6 +28,8 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kWarps = 4;
+// P in fp16, in units of 2^m: m is set 2^7 under a sub-tile's largest and kept until one lies past 2^15 of it
+constexpr float kUnitBelow = 7.f, kMost = 15.f;
 constexpr int kSub = kScaleTokens;   // tokens per sub-tile: one K scale and one V scale
 
 template <int D>
@@ -258,7 +261,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::kCtas)
         mx_b = fmaxf(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 1));
         mx_b = fmaxf(mx_b, __shfl_xor_sync(0xFFFFFFFFu, mx_b, 2));
       }
-      const float mn_a = mx_a > m_a + 8.f ? mx_a : m_a, mn_b = mx_b > m_b + 8.f ? mx_b : m_b;
+      const float mn_a = mx_a > m_a + kMost ? mx_a - kUnitBelow : m_a, mn_b = mx_b > m_b + kMost ? mx_b - kUnitBelow : m_b;
       const float ref_a = mn_a == -INFINITY ? 0.f : mn_a, ref_b = mn_b == -INFINITY ? 0.f : mn_b;
       if (__any_sync(0xFFFFFFFFu, mn_a != m_a || mn_b != m_b || vs != vref)) {
         const float al_a = ex2_approx(m_a - ref_a), al_b = HALF ? 0.f : ex2_approx(m_b - ref_b), w = vref / vs;

@@ -209,3 +209,22 @@ def test_prefill_v_scales_2_to_the_30_apart(power, d, page, Q, Hq):
             # the row sum is held in the unit of p * v_scale: a logarithm of up to 2^6 is added to the LSE (2^-19), and the logarithms
             # of scales that are no powers of two are good to 2^-19
             close(out[b], lse[b], want, d, 0.0, F32, 2.0 ** -18, f"request {b}, chunk {chunk}")
+
+
+# ------------------------------------------------------------------------------------------ the same in the decode
+@pytest.mark.parametrize("lead", [14.0, 17.4, 20.0])
+@pytest.mark.parametrize("Hq,d,at", [(1, 64, 0), (4, 128, 5000), (16, 64, 0)])
+def test_decode_one_key_outweighs_a_long_row(lead, Hq, d, at):
+    L, page = 20000, 64
+    cached = sink_case(L, at, d, 1)
+    q = torch.zeros(1, Hq, d)
+    q[..., 0] = 4.0
+    q, scale = q.to(BF), lead / 128
+    off = torch.tensor([L - 1], dtype=torch.int32).cuda()
+    n = cached[4].shape[1] * page
+    bm = fa.create_block_mask(fa.make_mask_rule([("causal",)], q_offset=off), 1, Hq, 1, n, 1, page, keep=[off])
+    out, lse = fa.flex_decode_fp8(q.cuda(), *[t.cuda() for t in cached], bm, None, scale, out_dtype=F32)
+    i, j = torch.tensor([[L - 1]]), torch.arange(L)[None]
+    o, z, av, qk = request(q[:, :, None], cached, 0, L, i, j <= i, scale)
+    # 2^-32 of the key's weight, which is under 1, for the 1024 keys at most that share its sum (V is 1)
+    close(out[0][:, None], lse[0][:, None], (o, z, av + 1024 * 2.0 ** -32 * 2.0 ** 11, qk), d, 0.0, F32, 0.0, "decode")
