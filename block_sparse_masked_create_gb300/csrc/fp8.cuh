@@ -3,6 +3,8 @@
 
 #include <cuda_fp16.h>
 
+#include <climits>
+
 #include "fa_internal.cuh"
 
 namespace fa {
@@ -67,6 +69,15 @@ __device__ __forceinline__ int key_end(const DevRule& R, int Bm, int b, int q_le
     end = max(end, hi);
   }
   return (int)end;
+}
+
+// First key position that some row of batch row b may see, by the terms' windows (0 where a term has none): slots before it, of
+// pages that fell out of every window, are read as zero and their page ids not looked at.
+__device__ __forceinline__ int key_begin(const DevRule& R, int Bm, int b) {
+  const int64_t first = R.q_offset ? __ldg(R.q_offset + (Bm > 1 ? b : 0)) : 0;
+  int64_t begin = INT_MAX;
+  for (int t = 0; t < R.n_terms; ++t) begin = min(begin, R.t[t].win == INT64_MAX ? (int64_t)0 : max(first - R.t[t].win + 1, (int64_t)0));
+  return (int)begin;
 }
 
 // tanh(u) = 1 - 2 / (1 + e^2u), good to 2^-22 absolute: two special-function operations where tanh.approx takes one (and is

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Tile T0 = make_tile(a, b, h0, r0);
   const Tile T1 = make_tile(a, b, h1, r1);
   const bool any = T0.n + T1.n > 0;
-  const int end = key_end(a.rule, M.Bm, b, P.f.rule_q_len, a.kv_len);
+  const int begin = key_begin(a.rule, M.Bm, b), end = key_end(a.rule, M.Bm, b, P.f.rule_q_len, a.kv_len);
   const int page = P.f.page, page_log = 31 - __clz(page);
 
   uint8_t* sQ0 = smem;
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int boxes = 128 / page;
   auto load = [&](bool is_v, int c, int fl, const WaitCtl& wc) -> bool {
     const int s = issued % NRAW, j = c * 128 + lane * page;
-    const bool need = lane < boxes && j < end;
+    const bool need = lane < boxes && j < end && j + page > begin;
     if (!is_v) {  // the block's pages, one a lane (V takes the same); the look-up is under way while the warp waits
       l_pid = -1;
       if (need) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(l_pid) : "l"(a.page_table + (size_t)b * a.max_pages + (j >> page_log)));
@@ -283,13 +283,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kConvWarp) {
     // =============================== converters ===============================
     const int row = tid - kConvWarp * 32;
+    const uint32_t seen = (uint32_t)max(end - begin, 0);
     bool last = false;
     for (int i = 0; any; ++i) {
       const int sr = i % NRAW, s = i % NST;
       const bool is_v = i & 1;
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&bar_raw[sr], (uint32_t)((i / NRAW) & 1), wc))) break;
       const int c = s_raw[2 * sr], fl = s_raw[2 * sr + 1];
-      const bool zero = c * 128 + row >= end || !((fl >> (8 + (row >> page_log))) & 1);
+      const bool zero = (uint32_t)(c * 128 + row - begin) >= seen || !((fl >> (8 + (row >> page_log))) & 1);
       const uint32_t src = smem_u32(sRaw + sr * C::kRawBytes);
       uint8_t* const dst = sRing + s * C::kSlotBytes;
       if (i >= NST && !__all_sync(0xFFFFFFFFu, mbar_wait(&bar_empty[s], (uint32_t)(((i / NST) - 1) & 1), wc))) break;

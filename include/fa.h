@@ -467,8 +467,8 @@ FA_API fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const vo
 
 /* fa_flex_forward_paged over an 8-bit cache, for chunks of queries. The page size is independent of the mask's Bk: page in
  * {32, 64, 128}, max_pages * page >= KV_LEN, Bk >= 32, 16-byte aligned pages. Pages of a listed block that hold a position some
- * term of the rule lets the batch row see (by its causal and prefix bounds) are looked up; slots behind those may hold
- * anything. 128 x 128 blocks read the pages themselves in the tcgen05 kernel (fp16 products; the cached values enter exactly,
+ * term of the rule lets the batch row see (by its causal, prefix and window bounds) are looked up; slots before and behind
+ * those may hold anything, and so may the table's entries for pages of such slots alone. 128 x 128 blocks read the pages themselves in the tcgen05 kernel (fp16 products; the cached values enter exactly,
  * the V scales of one 128-token key block are best within 2^10 of each other) where few query rows share them or the scores
  * are soft-capped; else the listed blocks are first expanded to bf16 in the workspace (exact for power-of-two scales, else
  * rounded) and the bf16 forward runs on them.

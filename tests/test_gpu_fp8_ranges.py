@@ -228,3 +228,66 @@ def test_decode_one_key_outweighs_a_long_row(lead, Hq, d, at):
     o, z, av, qk = request(q[:, :, None], cached, 0, L, i, j <= i, scale)
     # 2^-32 of the key's weight, which is under 1, for the 1024 keys at most that share its sum (V is 1)
     close(out[0][:, None], lse[0][:, None], (o, z, av + 1024 * 2.0 ** -32 * 2.0 ** 11, qk), d, 0.0, F32, 0.0, "decode")
+
+
+# ------------------------------------------------------------------------------------------ hidden slots
+@pytest.mark.parametrize("bk,page,Q,Hq,Hkv,d", [(128, 32, 30, 2, 2, 64), (128, 64, 30, 8, 2, 128), (64, 32, 30, 2, 1, 64), (128, 32, 140, 2, 2, 64),
+                                                (128, 64, 140, 16, 1, 64)])
+def test_prefill_slots_before_the_window_may_hold_anything(bk, page, Q, Hq, Hkv, d):
+    # pages that fell out of every row's window are handed on: their table entries are gone, slots of the page where the window
+    # begins hold NaN, scales too
+    L, window = 390, 5
+    cached = cache(69, [L], Hkv, page, d)
+    q = torch.randn(1, Hq, Q, d, generator=gen(70)).to(BF)
+    i, j = L - Q + torch.arange(Q)[:, None], torch.arange(L)[None]
+    al = (j <= i) & (i - j < window)
+    want = request(q, cached, 0, L, i, al)
+    first = L - Q - window + 1
+    kp, vp, ks, vs, table = cached
+    for c in range(-(-L // page)):
+        pid = int(table[0, c])
+        for p, s in ((kp, ks), (vp, vs)):
+            p.view(torch.uint8)[pid, :, :max(0, min(page, first - c * page))] = NAN_BYTE
+            s[pid, :, :max(0, min(page, first - c * page)) // 32] = math.nan
+        if (c + 1) * page <= first:
+            table[0, c] = -1
+    for chunk in (-1, 1) if bk == 128 else (-1,):
+        out, lse, st = forward(q, cached, [L], [L - Q], window, bk=bk, chunk=chunk)
+        assert st == fa.OK
+        if bk == 128 and -(-Q // 128) * (Hq // Hkv) <= 16:
+            close(out[0], lse[0], want, d, 0.0, F32, 2.0 ** -18, f"chunk {chunk}")
+        else:
+            assert ((out[0].double().cpu() - want[0]).abs() <= (2.0 ** -8 + 2.0 ** -10) * want[2] + 1e-4).all()
+            assert (lse[0].double().cpu() - want[1]).abs().max() <= 2e-3
+
+
+def test_prefill_window_and_prefix_keep_the_prefix():
+    # a prefix term shows the first keys to every row: nothing is cut off before it
+    L, Q, d = 390, 30, 64
+    cached = cache(71, [L], 2, 32, d)
+    q = torch.randn(1, 4, Q, d, generator=gen(72)).to(BF)
+    i, j = L - Q + torch.arange(Q)[:, None], torch.arange(L)[None]
+    _, al = spec_and_mask(5, 3, i, j)
+    out, lse, st = forward(q, cached, [L], [L - Q], 5, prefix=3)
+    assert st == fa.OK
+    close(out[0], lse[0], request(q, cached, 0, L, i, al), d, 0.0, F32, 0.0, "prefix")
+
+
+@pytest.mark.parametrize("bk,Hq,Hkv", [(128, 4, 2), (128, 2, 2), (64, 4, 2)])
+def test_prefill_of_a_batch_padded_in_front(bk, Hq, Hkv):
+    # rows at negative positions see nothing
+    lens, Q, d = [40, 200, 1], 100, 64
+    cached = cache(73, lens, Hkv, 64, d)
+    q = torch.randn(3, Hq, Q, d, generator=gen(74)).to(BF)
+    off = [L - Q for L in lens]
+    out, lse, st = forward(q, cached, lens, off, bk=bk)
+    assert st == fa.OK
+    for b, L in enumerate(lens):
+        i, j = off[b] + torch.arange(Q)[:, None], torch.arange(L)[None]
+        want = request(q, cached, b, L, i, j <= i)
+        pad = max(0, -off[b])
+        assert not out[b, :, :pad].any() and lse[b, :, :pad].isneginf().all()
+        if bk == 128:
+            close(out[b], lse[b], want, d, 0.0, F32, 0.0, f"request {b}")
+        else:
+            assert ((out[b].double().cpu() - want[0]).abs() <= (2.0 ** -8 + 2.0 ** -10) * want[2] + 1e-4).all()
