@@ -560,6 +560,15 @@ def _same(t: Optional[torch.Tensor], shape, dtype, device, what: str):
     return t
 
 
+def _scratch(t: Optional[torch.Tensor], device) -> int:
+    """Bytes of a caller's workspace (0: none given)."""
+    if t is None:
+        return 0
+    if not t.is_contiguous() or t.device != device:
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return t.numel() * t.element_size()
+
+
 def _check_qk_rule(rule: Optional[QkRule], d: int, device):
     if rule is None:
         return
@@ -637,6 +646,8 @@ def qk_norm_rope_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
     left out) -> (dq_in [B,N,Hq,d], dk_in, dv_in [B,N,Hkv,d] in the type of the tensors given, else grad_dtype; dq_weight,
     dk_weight fp32 [d] or None). q, k are the forward's rows."""
     given = dq if dq is not None else dk if dk is not None else dv
+    if given is not None:
+        size = _scratch(workspace, given.device)
     if given is None or given.dim() != 4 or not given.is_cuda:
         raise ValueError("dq, dk, dv must be CUDA tensors [B, H, N, d]")
     B, H, N, d = given.shape
@@ -668,11 +679,9 @@ def qk_norm_rope_backward(q: Optional[torch.Tensor], k: Optional[torch.Tensor], 
     dwq = torch.empty(d, dtype=f32, device=dev) if rule.q_weight and dq is not None else None
     dwk = torch.empty(d, dtype=f32, device=dev) if rule.k_weight and dk is not None else None
     lib = load()
-    size = 0
-    if dwq is not None or dwk is not None:
-        if workspace is None:
-            workspace = torch.empty(lib.fa_qk_norm_rope_backward_workspace_bytes(B, N, d), dtype=torch.uint8, device=dev)
-        size = workspace.numel()
+    if workspace is None and (dwq is not None or dwk is not None):
+        size = lib.fa_qk_norm_rope_backward_workspace_bytes(B, N, d)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     _check(_call(dev, lib.fa_qk_norm_rope_backward, _ref(rq), _ref(rk), _at(dq), _at(dk), _at(dv), ctypes.byref(rule),
                  _at(q_offset), _ref(gq), _ref(gk), _ref(gv), 1 if kind == f32 else 0, _at(dwq), _at(dwk), B, Hq, Hkv, N, d,
                  _at(workspace), size), "fa_qk_norm_rope_backward")
@@ -785,15 +794,18 @@ def flex_decode_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
         raise ValueError("q must be [Bz, Hq, d]")
     Bz, Hq, d = q.shape
     q = q.contiguous()
+    _same(status, (1,), torch.int32, q.device, "status")
+    _same(counters, (4,), torch.int64, q.device, "counters")
+    size = _scratch(workspace, q.device)
     P, Hkv, page, max_pages, dev = _check_fp8_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, Bz, d)
     out, lse = _outputs((Bz, Hq, d), dev, out, lse, out_dtype)
     if workspace is None:
-        workspace = torch.empty(max(decode_fp8_workspace_bytes(Bz, Hq, Hkv, d, max_pages, page), 16), dtype=torch.uint8,
-                                device=dev)
+        size = max(decode_fp8_workspace_bytes(Bz, Hq, Hkv, d, max_pages, page), 16)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     _check(_call(dev, load().fa_flex_decode_fp8, _at(q), _at(k_pages), _at(v_pages), _at(k_scale), _at(v_scale),
                  _at(page_table), P, ctypes.byref(block_mask.c), _ref(score), float(scale) if scale else 0.0, _at(out),
-                 _out_code(out), _at(lse), Bz, Hq, Hkv, d, page, max_pages, _at(workspace), workspace.numel(),
-                 _at(status), _at(counters)), "fa_flex_decode_fp8")
+                 _out_code(out), _at(lse), Bz, Hq, Hkv, d, page, max_pages, _at(workspace), size, _at(status),
+                 _at(counters)), "fa_flex_decode_fp8")
     return out, lse
 
 
@@ -815,15 +827,17 @@ def flex_forward_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Q_LEN, d]")
     B, Hq, Q_LEN, d = q.shape
+    _same(status, (1,), torch.int32, q.device, "status")
+    size = _scratch(workspace, q.device)
     P, Hkv, page, max_pages, dev = _check_fp8_cache(q, k_pages, v_pages, k_scale, v_scale, page_table, B, d)
     out, lse = _outputs((B, Hq, Q_LEN, d), dev, out, lse, out_dtype)
     if workspace is None:
-        n = forward_paged_fp8_workspace_bytes(block_mask, B, Hq, Hkv, d, chunk_blocks, score)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+        size = max(forward_paged_fp8_workspace_bytes(block_mask, B, Hq, Hkv, d, chunk_blocks, score), 256)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     _check(_call(dev, load().fa_flex_forward_paged_fp8, _at(q), _at(k_pages), _at(v_pages), _at(k_scale),
                  _at(v_scale), _at(page_table), P, page, max_pages, ctypes.byref(block_mask.c), _ref(score),
                  float(scale) if scale else 0.0, _at(out), _out_code(out), _at(lse), B, Hq, Hkv, Q_LEN, KV_LEN, d,
-                 chunk_blocks, _at(workspace), workspace.numel(), _at(status)), "fa_flex_forward_paged_fp8")
+                 chunk_blocks, _at(workspace), size, _at(status)), "fa_flex_forward_paged_fp8")
     return out, lse
 
 
