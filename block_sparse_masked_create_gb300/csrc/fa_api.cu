@@ -7,6 +7,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -234,6 +235,12 @@ int encode_tmap_u8(CUtensorMap* m, const void* base, int rank, const uint64_t* d
 }
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// arrays of 32-bit words
+static bool words_aligned(std::initializer_list<const void*> ps) {
+  uintptr_t all = 0;
+  for (const void* p : ps) all |= reinterpret_cast<uintptr_t>(p);
+  return (all & 3u) == 0;
+}
 
 // Decode splits of 4096 tokens: long enough that a CTA's start-up (barriers, page-table reads, the first
 // copies in flight) is small against its 2 MiB of K/V at d = 128, short enough that the 64-request paged
@@ -1076,9 +1083,7 @@ static int append_impl(const fa_rows* q, const fa_rows* k, const fa_rows* v, con
   if (!a.k.p || !a.v.p || (a.q.p && !q_out)) return FA_ERR_INVALID_ARG;
   if (n_pages_total < 1 || max_pages < 1) return FA_ERR_SHAPE;
   if (!aligned16(q_out) || !aligned16(k_pages) || !aligned16(v_pages)) return FA_ERR_INVALID_ARG;
-  const uintptr_t words = reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(n_new) |
-                          reinterpret_cast<uintptr_t>(k_scale) | reinterpret_cast<uintptr_t>(v_scale);
-  if (words & 3u) return FA_ERR_INVALID_ARG;
+  if (!words_aligned({page_table, n_new, k_scale, v_scale, dev_status})) return FA_ERR_INVALID_ARG;
   a.n_new = n_new;
   a.q_out = q_out;
   a.k_pages = k_pages;
@@ -1190,7 +1195,9 @@ fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_p
     return FA_ERR_SHAPE;
   if (!bm->kv_num || !bm->kv_idx || !bm->full_kv_num || !bm->full_kv_idx) return FA_ERR_INVALID_ARG;
   if ((int64_t)n_pages_total * Hkv * page > INT_MAX) return FA_ERR_UNSUPPORTED;
-  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(workspace))
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(workspace) ||
+      !words_aligned({page_table, k_scale, v_scale, lse, dev_status}) || (reinterpret_cast<uintptr_t>(out) & (out_dtype == FA_OUT_F32 ? 3u : 1u)) ||
+      (reinterpret_cast<uintptr_t>(dev_counters) & 7u))
     return FA_ERR_INVALID_ARG;
   DecodeFp8Plan P;
   if (!decode_fp8_plan(Bz, Hq, Hkv, d, max_pages, page, &P)) return FA_ERR_SHAPE;
@@ -1309,7 +1316,7 @@ fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const vo
   if (n_pages_total < 1 || max_pages < 1 || (int64_t)max_pages * page < KV_LEN) return FA_ERR_SHAPE;
   if (Hkv > 65535 || B > 65535 || (int64_t)n_pages_total * Hkv * page > INT_MAX) return FA_ERR_UNSUPPORTED;
   if (bm->bk < FA_KV_SCALE_TOKENS) return FA_ERR_UNSUPPORTED;
-  if ((reinterpret_cast<uintptr_t>(page_table) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  if (!words_aligned({page_table, k_scale, v_scale, lse, dev_status}) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return FA_ERR_INVALID_ARG;
   PagedFp8Plan P;
   s = paged_fp8_plan(bm, score_rule, B, Hq, Hkv, d, chunk_blocks, &P);

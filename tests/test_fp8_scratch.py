@@ -57,6 +57,41 @@ def test_scratch_is_checked(fa):
     assert fa._scratch(torch.zeros(3, 5), torch.device("cpu")) == 60 and fa._scratch(None, torch.device("cpu")) == 0
 
 
+def test_misaligned_arrays_are_refused(fa):
+    lib, ok = fa.load(), ctypes.c_void_p(4096)
+
+    def mask(q_len, bq, bk):
+        c = fa.BlockMaskC()
+        c.Bm, c.Hm, c.q_len, c.kv_len, c.bq, c.bk = 1, 1, q_len, 256, bq, bk
+        c.nq, c.nk = -(-q_len // bq), 256 // bk
+        for name in ("kv_num", "kv_idx", "full_kv_num", "full_kv_idx", "q_num", "q_idx", "full_q_num", "full_q_idx", "block_class"):
+            setattr(c, name, 4096)
+        c.rule = fa.make_mask_rule([("causal",)])
+        return ctypes.byref(c)
+
+    one, many = mask(1, 1, 64), mask(64, 128, 128)
+
+    def decode(ks=ok, vs=ok, table=ok, out=ok, kind=1, lse=ok, status=None, counters=None):
+        return lib.fa_flex_decode_fp8(ok, ok, ok, ks, vs, table, 9, one, None, 0.0, out, kind, lse, 2, 4, 2, 64, 64, 4, ok, 1 << 30,
+                                      status, counters, None)
+
+    def prefill(ks=ok, vs=ok, table=ok, out=ok, lse=ok, status=None):
+        return lib.fa_flex_forward_paged_fp8(ok, ok, ok, ks, vs, table, 9, 64, 4, many, None, 0.0, out, 1, lse, 1, 4, 2, 64, 256, 64, 0, ok,
+                                             1 << 30, status, None)
+
+    odd = ctypes.c_void_p(4098)
+    for name in ("ks", "vs", "table", "out", "lse", "status"):
+        assert decode(**{name: odd}) == fa.ERR_INVALID_ARG, name
+        assert prefill(**{name: odd}) == fa.ERR_INVALID_ARG, name
+    assert decode(out=ctypes.c_void_p(4097), kind=0) == fa.ERR_INVALID_ARG
+    assert decode(counters=ctypes.c_void_p(4100)) == fa.ERR_INVALID_ARG
+
+    row = fa.RowsC(4096, 4096, 512, 64)
+    for fn, scales in ((lib.fa_kv_append, ()), (lib.fa_kv_append_fp8, (ok, ok))):
+        assert fn(None, ctypes.byref(row), ctypes.byref(row), None, None, None, None, ok, ok, *scales, ok, 9, 64, 4, 2, 4, 2, 8, 64, odd,
+                  None) == fa.ERR_INVALID_ARG
+
+
 @pytest.mark.gpu
 def test_scratch_of_another_device_is_refused_on_the_gpu(fa):
     bf, f8 = torch.bfloat16, torch.float8_e4m3fn
