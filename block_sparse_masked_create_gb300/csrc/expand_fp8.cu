@@ -31,9 +31,11 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
     listed = listed || __ldg(M.q_num + col) + __ldg(M.full_q_num + col) > 0;
   }
   if (!listed) return;  // the forward reads nothing of it
-  const int64_t begin = key_begin(a.rule, M.Bm, b), end = key_end(a.rule, M.Bm, b, a.q_len, a.kv_len);
-  const bool seen = j0 < end && j0 + kScaleTokens > begin;
   const int pid = __ldg(a.page_table + (size_t)b * a.max_pages + j0 / a.page);
+  const KeyRange keys = key_range(a.rule, M.Bm, b, a.q_len, a.kv_len);
+  // the block's rows that some query row sees
+  const int lo = (int)max((int64_t)0, keys.begin - j0), rows = (int)min((int64_t)kScaleTokens, keys.end - j0) - lo;
+  const bool seen = rows > 0;
   const bool have = pid >= 0 && pid < a.n_pages_total && seen;
   if (!have && seen) report(a.status, FA_ERR_DEVICE_CHECK);
   const int which = threadIdx.x / (kThreads / 2), tid = threadIdx.x % (kThreads / 2);
@@ -51,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
   for (int r = tid / LPR; r < kScaleTokens; r += kRows) {
     if (j0 + r >= a.kv_len) break;
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (have && j0 + r >= begin && j0 + r < end) v = __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * D));
+    if (have && (uint32_t)(r - lo) < (uint32_t)rows) v = __ldg(reinterpret_cast<const uint4*>(src + (size_t)r * D));
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     uint32_t out[8];
 #pragma unroll

@@ -3,8 +3,6 @@
 
 #include <cuda_fp16.h>
 
-#include <climits>
-
 #include "fa_internal.cuh"
 
 namespace fa {
@@ -57,27 +55,24 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// First key position that no row of batch row b sees, by the causal and prefix bounds of the rule's terms. What the pages
-// hold from there on (slots behind a sequence) is read as zero.
-__device__ __forceinline__ int key_end(const DevRule& R, int Bm, int b, int q_len, int kv_len) {
-  const int64_t last = (int64_t)q_len - 1 + (R.q_offset ? __ldg(R.q_offset + (Bm > 1 ? b : 0)) : 0);
-  int64_t end = 0;
+// The key positions [begin, end) that some query row of batch row b may see, by the rule's terms: their causal and prefix bounds for
+// the end, their windows for the begin. What pages hold before (they fell out of every window) and behind (slots after a
+// sequence) is read as zero, and ids of pages with nothing in between are not looked at.
+struct KeyRange {
+  int begin, end;
+};
+__device__ __forceinline__ KeyRange key_range(const DevRule& R, int Bm, int b, int q_len, int kv_len) {
+  const int64_t first = R.q_offset ? __ldg(R.q_offset + (Bm > 1 ? b : 0)) : 0, behind = first + q_len;
+  int64_t begin = kv_len, end = 0;
   for (int t = 0; t < R.n_terms; ++t) {
-    int64_t hi = kv_len;
-    if (R.t[t].causal) hi = min(hi, last + 1);
+    int64_t lo = 0, hi = kv_len;
+    if (R.t[t].win != INT64_MAX) lo = max(lo, first - R.t[t].win + 1);
+    if (R.t[t].causal) hi = min(hi, behind);
     if (R.t[t].pre != INT64_MAX) hi = min(hi, R.t[t].pre);
+    begin = min(begin, lo);
     end = max(end, hi);
   }
-  return (int)end;
-}
-
-// First key position that some row of batch row b may see, by the terms' windows (0 where a term has none): slots before it, of
-// pages that fell out of every window, are read as zero and their page ids not looked at.
-__device__ __forceinline__ int key_begin(const DevRule& R, int Bm, int b) {
-  const int64_t first = R.q_offset ? __ldg(R.q_offset + (Bm > 1 ? b : 0)) : 0;
-  int64_t begin = INT_MAX;
-  for (int t = 0; t < R.n_terms; ++t) begin = min(begin, R.t[t].win == INT64_MAX ? (int64_t)0 : max(first - R.t[t].win + 1, (int64_t)0));
-  return (int)begin;
+  return KeyRange{(int)begin, (int)end};
 }
 
 // tanh(u) = 1 - 2 / (1 + e^2u), good to 2^-22 absolute: two special-function operations where tanh.approx takes one (and is

@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Tile T0 = make_tile(a, b, h0, r0);
   const Tile T1 = make_tile(a, b, h1, r1);
   const bool any = T0.n + T1.n > 0;
-  const int begin = key_begin(a.rule, M.Bm, b), end = key_end(a.rule, M.Bm, b, P.f.rule_q_len, a.kv_len);
+  const KeyRange keys = key_range(a.rule, M.Bm, b, P.f.rule_q_len, a.kv_len);
+  const int begin = keys.begin, end = keys.end;
   const int page = P.f.page, page_log = 31 - __clz(page);
 
   uint8_t* sQ0 = smem;
