@@ -1249,9 +1249,13 @@ fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_p
 }
 
 // 128 x 128 blocks run on the pages themselves where at most this many query tiles (nq * Hq / Hkv) share a key block, else the
-// listed blocks are expanded to bf16 first: each CTA converts what it reads, the expansion converts once. 8192 keys, 32 / 8
-// heads, pages / expanded: 4 tiles 131 / 179 us, 8 tiles 259 / 283, 16 tiles 255 / 249, 32 tiles 250 / 229. Soft-capped scores
-// always read the pages (the cap is exact there). Other block sizes are expanded.
+// listed blocks are expanded to bf16 first: each CTA converts what it reads, the expansion converts once. Pages / expanded, us:
+//   32 / 8 heads, 8192 keys: 4 tiles 131 / 179, 8 tiles 258 / 284, 12 tiles 255 / 257, 16 tiles 255 / 249, 32 tiles 249 / 227
+//   the same, 2048 keys: 77 / 85 with 8, 75 / 74 with 12, 75 / 72 with 16, 70 / 63 with 32; 32,768 keys: 969 / 971, 970 / 938, 966 / 870
+//   16 / 2 heads, 8192 keys: 81 / 97 with 8, 128 / 129 with 16, 254 / 233 with 32; 8 / 8 heads: 252 / 277, 245 / 246 with 12, 240 / 235
+// They meet at 12 tiles. The border lies at 16, where the pages cost up to 5 % more, for what they keep: P in fp16 and not bf16 (2^-12
+// against 2^-9), and no workspace of the cache's size. Soft-capped scores always read the pages (the cap is exact there). Other
+// block sizes are expanded.
 constexpr int64_t kDirectTiles = 16;
 struct PagedFp8Plan {
   bool direct;

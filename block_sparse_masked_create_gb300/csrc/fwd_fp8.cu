@@ -20,7 +20,7 @@
 // softmax leaves. The whole saves writing and reading the expanded cache, 3 + 2 bytes a value.
 // Bound: the tensor pipe and the softmax, as the bf16 forward, and the instruction cache, which the roles share (its stalls fell
 // when the converters' loop was rolled: 142 -> 134 us). Measured on one GB300: 256 queries after 130,816 tokens, 8 heads, d =
-// 128: 134 us with the merge of the cut rows, 1020 TFLOP/s (expanding first: 263); long rows take 1.2 times the bf16 forward.
+// 128: 132 us with the merge of the cut rows, 1040 TFLOP/s (expanding first: 263); long rows take 1.2 times the bf16 forward.
 // Registers: 512 threads launch with 128 each; the softmax warps go up to 192 and the others down to 64, together the
 // same 65,536 (with 168 and 88 the softmax spilled).
 #include <cfloat>

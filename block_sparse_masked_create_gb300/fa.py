@@ -823,7 +823,8 @@ def flex_forward_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
                            out_dtype=torch.bfloat16):
     """fa_flex_forward_paged_fp8: q [B,Hq,Q_LEN,d] over float8_e4m3fn pages [P,Hkv,page,d] with scales fp32 [P,Hkv,page/32];
     the page size is independent of the mask's Bk. chunk_blocks: key blocks per chunk of a long row (0: chosen, -1: rows
-    are not cut)."""
+    are not cut). A batch may be padded in front (rows at negative positions see nothing) or behind (those rows see slots that
+    nobody wrote, which must hold no NaN bytes; the other rows are right)."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Q_LEN, d]")
     B, Hq, Q_LEN, d = q.shape

@@ -377,7 +377,8 @@ typedef struct {
  *   y = x * rsqrt(mean(x^2) + eps) * weight                              (weight NULL: y = x)
  *   (z_a, z_b) = (y_a cos t - y_b sin t, y_a sin t + y_b cos t),  t = p * inv_freq[i],  for the pairs i of the first
  *   rot_dim elements: (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved  (inv_freq NULL: z = y)
- * in fp32, rounded once at the end. The angle is reduced modulo 2 pi in 64-bit integers and is as exact at position
+ * in fp32, rounded once at the end (so the sum of squares, and with eps = 0 the inverse square of the root, are within fp32's
+ * range: rows of magnitudes 1e-18 .. 1e18, or of zeros with eps > 0). The angle is reduced modulo 2 pi in 64-bit integers and is as exact at position
  * 2^31 as at 1; inv_freq is finite. Value rows are moved as they are. */
 typedef struct {
   const float* q_weight; /* device fp32 [d] or NULL */
@@ -468,13 +469,24 @@ FA_API fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const vo
 /* fa_flex_forward_paged over an 8-bit cache, for chunks of queries. The page size is independent of the mask's Bk: page in
  * {32, 64, 128}, max_pages * page >= KV_LEN, Bk >= 32, 16-byte aligned pages. Pages of a listed block that hold a position some
  * term of the rule lets the batch row see (by its causal, prefix and window bounds) are looked up; slots before and behind
- * those may hold anything, and so may the table's entries for pages of such slots alone. 128 x 128 blocks read the pages themselves in the tcgen05 kernel (fp16 products; the cached values enter exactly,
- * the V scales of one 128-token key block are best within 2^10 of each other) where few query rows share them or the scores
- * are soft-capped; else the listed blocks are first expanded to bf16 in the workspace (exact for power-of-two scales, else
- * rounded) and the bf16 forward runs on them.
+ * those may hold anything, and so may the table's entries for pages of such slots alone. Every query row counts: a row that pads
+ * a request behind its end sees slots that nobody wrote. Such rows' results are what the slots give; the other rows' stay right
+ * as long as those slots hold no NaN bytes (0x7F, 0xFF; their scales may be anything) and their pages are in the table. Rows that
+ * pad in front, at negative positions, see nothing.
+ * Two ways lead to the result; the sums of scores, of P and of P V are fp32 in both:
+ *  - 128 x 128 blocks whose key blocks at most 16 query tiles share (ceil(Q_LEN / 128) * Hq / Hkv), whose scores are soft-capped,
+ *    or with at most 128 query rows a KV head (Q_LEN * Hq / Hkv, one mask for all heads) read the pages themselves in the tcgen05
+ *    kernel: fp16 products, the cached values enter exactly, whatever their scales, and P is rounded to fp16 (2^-12); a P * V scale
+ *    under 2^-13 of the largest of its row and key block is off by up to 2^-24 of that (or 2^-49 of the row's largest). Scores
+ *    times log2(e) lie within +-2^22.
+ *  - else the listed blocks are first expanded to bf16 in the workspace (exact for power-of-two scales, else rounded) and
+ *    fa_flex_forward runs on them: P is rounded to bf16 (2^-9), the soft-cap is good to 8e-6 of the cap.
  *   chunk_blocks   with Bq == Bk == 128, cut long rows into chunks of that many key blocks (fa_flex_forward_split); 0: the
- *                  library chooses, cutting only where the uncut rows would leave SMs idle; -1: never cut
- *   workspace      device, >= fa_forward_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned, for one call at a time
+ *                  library chooses, cutting where the uncut rows would leave SMs idle, and, with at most 128 query rows a KV
+ *                  head and at least 16 key blocks, always into two at least; -1: never cut
+ *   workspace      device, >= fa_forward_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned, for one call at a time: the
+ *                  chunks' tables and results, and for expanded blocks 4 * B * Hkv * KV_LEN * d bytes, of the mask's KV_LEN and
+ *                  not of the requests' lengths (64 requests of up to 131,072 tokens, 8 heads, d = 128: 34 GB)
  * A bad id among the looked-up pages sets FA_ERR_DEVICE_CHECK (zeros are read in its place). Other arguments and errors
  * as fa_flex_forward_paged; block_mask needs its query-side transpose. */
 FA_API size_t fa_forward_paged_fp8_workspace_bytes(const fa_block_mask* block_mask, const fa_score_rule* score_rule, int32_t B,
