@@ -291,3 +291,44 @@ def test_prefill_of_a_batch_padded_in_front(bk, Hq, Hkv):
             close(out[b], lse[b], want, d, 0.0, F32, 0.0, f"request {b}")
         else:
             assert ((out[b].double().cpu() - want[0]).abs() <= (2.0 ** -8 + 2.0 ** -10) * want[2] + 1e-4).all()
+
+
+# ------------------------------------------------------------------------------------------ captured calls
+@pytest.mark.parametrize("bk,Q,Hq,Hkv,d,chunk", [(128, 150, 4, 2, 128, 0), (128, 20, 6, 2, 64, 0), (128, 150, 4, 2, 64, 1), (64, 70, 4, 2, 64, -1),
+                                                 (128, 150, 16, 1, 64, 2)])
+def test_prefill_captured_twice_and_replayed_at_once(bk, Q, Hq, Hkv, d, chunk):
+    # two graphs on two streams, each with a workspace of its own, replayed on inputs written after the capture
+    L = 3000
+    kp, vp, ks, vs, table = cache(77, [L], Hkv, 64, d)
+    table = table.cuda()
+    off = torch.tensor([L - Q], dtype=torch.int32).cuda()
+    bm = fa.create_block_mask(fa.make_mask_rule([("causal",)], q_offset=off), 1, Hq, Q, L, bk, bk, keep=[off])
+    need = max(fa.forward_paged_fp8_workspace_bytes(bm, 1, Hq, Hkv, d, chunk), 256)
+    runs = []
+    for i in range(2):
+        hold = [torch.zeros_like(t, device="cuda") for t in (torch.zeros(1, Hq, Q, d, dtype=BF), kp, vp, ks, vs)]
+        out, lse = torch.empty(1, Hq, Q, d, device="cuda"), torch.empty(1, Hq, Q, device="cuda")
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            call = lambda: fa.flex_forward_paged_fp8(*hold, table, bm, L, chunk_blocks=chunk, out=out, lse=lse, workspace=ws)  # noqa: B023,E731
+            call()
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                call()
+        runs.append((s, graph, hold, out, lse, ws))
+    torch.cuda.synchronize()
+    want = []
+    for i, (_, _, hold, _, _, _) in enumerate(runs):
+        for t, x in zip(hold, (torch.randn(1, Hq, Q, d, generator=gen(79 + i)).to(BF), kp, vp, ks, vs * 2.0 ** i)):
+            t.copy_(x)
+        want.append(fa.flex_forward_paged_fp8(*hold, table, bm, L, chunk_blocks=chunk, out_dtype=F32))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, graph, _, _, _, _ in runs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for (_, _, _, out, lse, _), (o, z) in zip(runs, want):
+        assert torch.isfinite(o).all() and torch.equal(out, o) and torch.equal(lse, z)
