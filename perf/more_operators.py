@@ -73,7 +73,7 @@ def draw(rng):
     keep = first + last + _log(rng, 1, 64) - 1
     least = 1
     if op == "choose":  # blocks enough for a choice: its outputs are nothing else
-        least = (first + last + 24) * block
+        least = (first + last + 24) * max(block, 64)
         window = window and max(window, least)
         keep = first + last + rng.randint(1, 12)
     if op == "train" or op == "choose" and rng.random() < 0.5:
