@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   const int g = a.Hq / a.Hkv;
   const DevMask& M = a.mask;
   const int bm = M.Bm > 1 ? b : 0;
-  const size_t mrow = (size_t)bm * M.Hm * M.nq;  // Hm == 1, nq == 1
+  const size_t mrow = (size_t)bm * M.Hm + (M.Hm > 1 ? hk : 0);  // Hm is 1 or Hkv, nq == 1
   const int n_full = __ldg(M.full_kv_num + mrow), n_part = __ldg(M.kv_num + mrow);
   const int n_vis = n_full + n_part;
   const int e0 = s * a.pages_per_split;
@@ -337,7 +337,7 @@ template <int D>
 __global__ void __launch_bounds__(128) decode_combine_kernel(const __grid_constant__ DecArgs a) {
   const int hq = blockIdx.x, b = blockIdx.y;
   const DevMask& M = a.mask;
-  const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm * M.nq;
+  const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, hq);
   const int n_vis = __ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow);
   const int ns = (n_vis + a.pages_per_split - 1) / a.pages_per_split;
   const size_t base = ((size_t)b * a.Hq + hq) * (size_t)a.n_splits;

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::kCtas)
   const int g = a.Hq / a.Hkv, PAGE = a.page;
   const DevMask& M = a.mask;
   const int bm = M.Bm > 1 ? b : 0;
-  const size_t mrow = (size_t)bm * M.Hm * M.nq;  // Hm == 1, nq == 1
+  const size_t mrow = (size_t)bm * M.Hm + (M.Hm > 1 ? hk : 0);  // Hm is 1 or Hkv, nq == 1
   const int n_full = __ldg(M.full_kv_num + mrow), n_vis = n_full + __ldg(M.kv_num + mrow);
   const int e0 = s * a.pages_per_split;
   const size_t hq0 = (size_t)b * a.Hq + (size_t)hk * g;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kJoin * D) decode_fp8_join_kernel(const __grid
   __shared__ float s_u[kJoin][D], s_red[kJoin * D / 32], s_l[kJoin];
   const int hq = blockIdx.x, b = blockIdx.y, col = threadIdx.x % D, part = threadIdx.x / D;
   const DevMask& M = a.mask;
-  const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm * M.nq;
+  const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, hq);
   const int n_vis = __ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow);
   if (n_vis <= a.pages_per_split) return;
   const int ns = (n_vis + a.pages_per_split - 1) / a.pages_per_split;

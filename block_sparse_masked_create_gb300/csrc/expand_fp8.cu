@@ -24,10 +24,11 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const __grid_constant_
   const int hk = blockIdx.y, b = blockIdx.z;
   const int64_t j0 = (int64_t)blockIdx.x * kScaleTokens;
   const DevMask& M = a.mask;
-  const int c = (int)(j0 / M.bk), g = a.Hq / a.Hkv;
+  const int c = (int)(j0 / M.bk);
   bool listed = false;
-  for (int h = 0; h < (M.Hm > 1 ? g : 1); ++h) {
-    const size_t col = ((size_t)(M.Bm > 1 ? b : 0) * M.Hm + (M.Hm > 1 ? hk * g + h : 0)) * M.nk + c;
+  const int per = M.Hm > 1 ? M.Hm / a.Hkv : 0;      // rows of the mask for this KV head (Hm = 1: the one row of all heads)
+  for (int h = 0; h < max(per, 1); ++h) {
+    const size_t col = ((size_t)(M.Bm > 1 ? b : 0) * M.Hm + hk * per + h) * M.nk + c;
     listed = listed || __ldg(M.q_num + col) + __ldg(M.full_q_num + col) > 0;
   }
   if (!listed) return;  // the forward reads nothing of it

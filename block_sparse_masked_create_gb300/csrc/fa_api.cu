@@ -250,6 +250,14 @@ static int decode_pages_per_split(int page, int max_pages) {
   return std::min(ps, std::max(max_pages, 1));
 }
 
+// Spans of rows that list `pages` pages at most (blocks that a score chose): as few tokens as fill the SMs, a multiple of 128 for
+// the four warps' sub-tiles, in no more slots than the workspace has.
+static int decode_short_pages_per_split(int64_t rows, int pages, int page, int slots) {
+  const int64_t spans = std::max<int64_t>(1, std::min<int64_t>(slots, 152 / rows));
+  const int least = std::max(1, 128 / page);
+  return (int)std::min<int64_t>(std::max<int64_t>(least, (pages + spans - 1) / spans), pages);
+}
+
 static int check_forward(const void* q, const void* k, const void* v, const fa_block_mask* bm, void* out,
                          float* lse, int B, int Hq, int Hkv, int Q_LEN, int KV_LEN, int d) {
   if (!q || !k || !v || !bm || !out || !lse) return FA_ERR_INVALID_ARG;
@@ -257,7 +265,7 @@ static int check_forward(const void* q, const void* k, const void* v, const fa_b
   if (Hq % Hkv) return FA_ERR_SHAPE;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (bm->q_len != Q_LEN || bm->kv_len != KV_LEN) return FA_ERR_SHAPE;  // never trimmed silently
-  if (!(bm->Bm == 1 || bm->Bm == B) || !(bm->Hm == 1 || bm->Hm == Hq)) return FA_ERR_SHAPE;
+  if (!(bm->Bm == 1 || bm->Bm == B) || !(bm->Hm == 1 || bm->Hm == Hq || bm->Hm == Hkv)) return FA_ERR_SHAPE;
   if (bm->nq != (Q_LEN + bm->bq - 1) / bm->bq || bm->nk != (KV_LEN + bm->bk - 1) / bm->bk) return FA_ERR_SHAPE;
   auto okb = [](int x) { return x == 16 || x == 32 || x == 64 || x == 128; };
   if (!okb(bm->bq) || !okb(bm->bk)) return FA_ERR_UNSUPPORTED;
@@ -477,6 +485,7 @@ fa_status fa_create_block_mask(const fa_mask_rule* rule, int32_t B, int32_t H, i
   out->doc_sorted = T.doc_sorted;
   out->row_order = T.row_order;
   out->rule = *rule;
+  out->row_max = 0;
   return FA_OK;
 }
 
@@ -578,6 +587,7 @@ fa_status fa_block_mask_select_rows(const fa_block_mask* src, const int32_t* dev
   out->rule = src->rule;
   out->rule.q_offset = dev_q_pos;  // the one query row of request b sits at global position q_pos[b]
   out->rule.batch_dependent = 1;
+  out->row_max = src->row_max;
   return FA_OK;
 }
 
@@ -655,7 +665,8 @@ fa_status fa_flex_forward_host(const void* host_q, const void* host_k, const voi
   if (workspace_bytes < P.n_slots * P.slot_bytes) return FA_ERR_BUFFER_TOO_SMALL;
   if (reinterpret_cast<uintptr_t>(dev_workspace) & 255u) return FA_ERR_INVALID_ARG;
   const fa_block_mask& M = *block_mask;
-  if (M.q_len != Q_LEN || M.kv_len != KV_LEN || !(M.Bm == 1 || M.Bm == B) || !(M.Hm == 1 || M.Hm == Hq))
+  if (M.q_len != Q_LEN || M.kv_len != KV_LEN || !(M.Bm == 1 || M.Bm == B) ||
+      !(M.Hm == 1 || M.Hm == Hq || M.Hm == Hkv))
     return FA_ERR_SHAPE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   cudaStream_t s_in = nullptr, s_out = nullptr, s_c1 = nullptr;
@@ -703,9 +714,10 @@ fa_status fa_flex_forward_host(const void* host_q, const void* host_k, const voi
     fa_block_mask V = M;
     size_t row0 = 0;
     if (M.Bm > 1) row0 += (size_t)b * M.Hm * M.nq;
-    if (M.Hm > 1) row0 += (size_t)h0 * M.nq;
+    const int per = M.Hm > 1 ? M.Hm / Hkv : 0;  // rows of the head dimension for each KV head
+    row0 += (size_t)hk0 * per * M.nq;
     V.Bm = 1;
-    V.Hm = M.Hm > 1 ? nq : 1;
+    V.Hm = M.Hm > 1 ? nk * per : 1;
     V.kv_num = M.kv_num + row0;
     V.full_kv_num = M.full_kv_num + row0;
     V.kv_idx = M.kv_idx + row0 * M.nk;
@@ -795,7 +807,7 @@ fa_status fa_flex_decode(const void* q, const void* k_pages, const void* v_pages
   if (out_dtype != FA_OUT_BF16 && out_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
   if (Hq / Hkv > 16) return FA_ERR_UNSUPPORTED;
   if (bm->bq != 1 || bm->bk != page || bm->q_len != 1 || (int64_t)bm->kv_len != (int64_t)max_pages * page ||
-      bm->Hm != 1 || !(bm->Bm == 1 || bm->Bm == Bz) || bm->nk != max_pages || bm->nq != 1)
+      !(bm->Hm == 1 || bm->Hm == Hkv) || !(bm->Bm == 1 || bm->Bm == Bz) || bm->nk != max_pages || bm->nq != 1)
     return FA_ERR_SHAPE;
   if ((int64_t)n_pages_total * Hkv * page > INT_MAX) return FA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(workspace))
@@ -827,6 +839,10 @@ fa_status fa_flex_decode(const void* q, const void* k_pages, const void* v_pages
   a.mask = dev_mask(bm);
   a.pages_per_split = decode_pages_per_split(page, max_pages);
   a.n_splits = (max_pages + a.pages_per_split - 1) / a.pages_per_split;
+  if (bm->row_max > 0 && bm->row_max < max_pages) {  // rows known to be short
+    a.pages_per_split = decode_short_pages_per_split((int64_t)Bz * Hkv, bm->row_max, page, a.n_splits);
+    a.n_splits = (bm->row_max + a.pages_per_split - 1) / a.pages_per_split;
+  }
   const size_t slots = (size_t)Bz * Hq * a.n_splits;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.ws_m = reinterpret_cast<float*>(w);
@@ -1191,7 +1207,7 @@ fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_p
   if (out_dtype != FA_OUT_BF16 && out_dtype != FA_OUT_F32) return FA_ERR_INVALID_ARG;
   if (Hq / Hkv > 16 || Hkv > 65535 || Bz > 65535) return FA_ERR_UNSUPPORTED;
   if (bm->bq != 1 || bm->bk != page || bm->q_len != 1 || (int64_t)bm->kv_len != (int64_t)max_pages * page ||
-      bm->Hm != 1 || !(bm->Bm == 1 || bm->Bm == Bz) || bm->nk != max_pages || bm->nq != 1)
+      !(bm->Hm == 1 || bm->Hm == Hkv) || !(bm->Bm == 1 || bm->Bm == Bz) || bm->nk != max_pages || bm->nq != 1)
     return FA_ERR_SHAPE;
   if (!bm->kv_num || !bm->kv_idx || !bm->full_kv_num || !bm->full_kv_idx) return FA_ERR_INVALID_ARG;
   if ((int64_t)n_pages_total * Hkv * page > INT_MAX) return FA_ERR_UNSUPPORTED;
@@ -1207,7 +1223,8 @@ fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_p
   DecArgs& a = A.d;
   const int s = compile_rule_noexcept(&bm->rule, &a.rule);
   if (s != FA_OK) return (fa_status)s;
-  const int32_t seen = most_pages(a.rule, max_pages, page);
+  int32_t seen = most_pages(a.rule, max_pages, page);
+  if (bm->row_max > 0) seen = std::min(seen, bm->row_max);
   if (seen < max_pages) {  // spans for what the rule can see, in no more slots than the workspace has
     DecodeFp8Plan N = P;
     N.pages_per_split = decode_fp8_pages_per_split(Bz, Hkv, d, seen, page);
@@ -1272,7 +1289,7 @@ static int paged_fp8_plan(const fa_block_mask* bm, const fa_score_rule* score, i
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   const bool big = bm->bq == 128 && bm->bk == 128;
   const int32_t g = Hq / Hkv;
-  P->pack = big && bm->Hm == 1 && (int64_t)bm->q_len * g <= 128 ? g : 1;
+  P->pack = big && (bm->Hm == 1 || bm->Hm == Hkv) && (int64_t)bm->q_len * g <= 128 ? g : 1;
   P->direct = big && (P->pack > 1 || (int64_t)bm->nq * g <= kDirectTiles || (score && score->softcap > 0.f));
   P->chunk = 0;
   P->kv_bytes = 0;
@@ -1414,6 +1431,214 @@ fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const vo
                               st) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------------------------------------
+// Bounds of key blocks, and blocks chosen by them
+// ------------------------------------------------------------------------------------------------
+fa_status fa_key_bounds(const void* k, void* bounds, int32_t B, int32_t Hkv, int32_t KV_LEN, int32_t d, int32_t Bk,
+                        fa_stream_t stream) {
+  if (!k || !bounds) return FA_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || KV_LEN < 1 || Bk < 1 || Bk > 128) return FA_ERR_SHAPE;
+  if ((d != 64 && d != 128) || B > 65535 || Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(k) || !aligned16(bounds)) return FA_ERR_INVALID_ARG;
+  BoundsArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.k = k;
+  a.bounds = bounds;
+  a.page = Bk;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.kv_len = KV_LEN;
+  a.d = d;
+  return launch_bounds(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+static fa_status kv_bounds_impl(const void* k_pages, const float* k_scale, void* bounds, const int32_t* page_table,
+                                const int32_t* q_offset, const int32_t* n_new, int32_t n_pages_total, int32_t page,
+                                int32_t max_pages, int32_t B, int32_t Hkv, int32_t N, int32_t d, int32_t* dev_status,
+                                fa_stream_t stream) {
+  if (!k_pages || !bounds || !page_table) return FA_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || N < 1 || n_pages_total < 1 || max_pages < 1) return FA_ERR_SHAPE;
+  if ((d != 64 && d != 128) || B > 65535 || Hkv > 65535) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(k_pages) || !aligned16(bounds) || !words_aligned({k_scale, page_table, q_offset, n_new, dev_status}))
+    return FA_ERR_INVALID_ARG;
+  BoundsArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.k = k_pages;
+  a.k_scale = k_scale;
+  a.bounds = bounds;
+  a.page_table = page_table;
+  a.n_pages_total = n_pages_total;
+  a.page = page;
+  a.max_pages = max_pages;
+  a.q_offset = q_offset;
+  a.n_new = n_new;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.N = N;
+  a.d = d;
+  a.status = dev_status;
+  return launch_bounds(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_kv_bounds(const void* k_pages, void* bounds, const int32_t* page_table, const int32_t* q_offset,
+                       const int32_t* n_new, int32_t n_pages_total, int32_t page, int32_t max_pages, int32_t B, int32_t Hkv,
+                       int32_t N, int32_t d, int32_t* dev_status, fa_stream_t stream) {
+  if (page != 16 && page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
+  return kv_bounds_impl(k_pages, nullptr, bounds, page_table, q_offset, n_new, n_pages_total, page, max_pages, B, Hkv, N, d,
+                        dev_status, stream);
+}
+
+fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, void* bounds, const int32_t* page_table,
+                           const int32_t* q_offset, const int32_t* n_new, int32_t n_pages_total, int32_t page,
+                           int32_t max_pages, int32_t B, int32_t Hkv, int32_t N, int32_t d, int32_t* dev_status,
+                           fa_stream_t stream) {
+  if (page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
+  if (!k_scale) return FA_ERR_INVALID_ARG;
+  return kv_bounds_impl(k_pages, k_scale, bounds, page_table, q_offset, n_new, n_pages_total, page, max_pages, B, Hkv, N, d,
+                        dev_status, stream);
+}
+
+struct SelectPlan {
+  MaskLayout mask;
+  int32_t parts;
+  size_t off_scores, off_err, off_zone, total;
+};
+
+static int select_blocks_plan(const fa_block_mask* src, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, SelectPlan* P) {
+  if (!src) return FA_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || src->nq < 1 || src->nk < 1 || src->q_len < 1 || src->kv_len < 1) return FA_ERR_SHAPE;
+  if (src->Bm != 1 && src->Bm != B) return FA_ERR_SHAPE;
+  if (src->bq < 1 || src->bk < 1 || src->nq != (src->q_len + src->bq - 1) / src->bq ||
+      src->nk != (src->kv_len + src->bk - 1) / src->bk)
+    return FA_ERR_SHAPE;
+  if (src->Hm != 1 || (d != 64 && d != 128) || src->nk > kSelectMaxBlocks || B > 65535 || Hq > 65535) return FA_ERR_UNSUPPORTED;
+  fa_mask_rule r;
+  std::memset(&r, 0, sizeof(r));
+  r.n_ops = 1;
+  r.op[0] = FA_M_TRUE;
+  r.batch_dependent = 1;
+  r.head_dependent = 1;
+  const int s = mask_layout(&r, B, Hkv, src->q_len, src->kv_len, src->bq, src->bk, &P->mask);
+  if (s != FA_OK) return s;
+  const size_t rows = (size_t)B * Hkv * src->nq;
+  // one query block's sums are split among its heads where there are fewer (request, KV head, query block)s than two for each SM
+  P->parts = src->q_len == 1 ? 0 : rows < 2 * 152 ? Hq / Hkv : 1;
+  P->off_scores = align256(rows * P->parts * 4 * d * sizeof(float));
+  P->off_err = P->off_scores + align256(rows * src->nk * sizeof(float));
+  P->off_zone = P->off_err + align256(rows * select_err_floats(src->q_len, src->nk) * sizeof(float));
+  P->total = P->off_zone + align256(rows * src->nk * sizeof(uint64_t));
+  return FA_OK;
+}
+
+size_t fa_block_mask_select_blocks_bytes(const fa_block_mask* src, int32_t B, int32_t Hkv) {
+  SelectPlan P;
+  return select_blocks_plan(src, B, Hkv, Hkv, 128, &P) == FA_OK ? P.mask.total : 0;
+}
+
+size_t fa_block_mask_select_blocks_workspace_bytes(const fa_block_mask* src, int32_t B, int32_t Hq, int32_t Hkv, int32_t d) {
+  SelectPlan P;
+  return select_blocks_plan(src, B, Hq, Hkv, d, &P) == FA_OK ? P.total : 0;
+}
+
+fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, const void* bounds, const int32_t* page_table,
+                                      int32_t n_pages_total, int32_t max_pages, int32_t B, int32_t Hq, int32_t Hkv, int32_t d,
+                                      int32_t keep, int32_t first, int32_t last, void* dev_buf, size_t buf_bytes,
+                                      fa_block_mask* out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                      fa_stream_t stream) {
+  if (!src || !q || !bounds || !dev_buf || !out || !workspace) return FA_ERR_INVALID_ARG;
+  SelectPlan P;
+  int s = select_blocks_plan(src, B, Hq, Hkv, d, &P);
+  if (s != FA_OK) return (fa_status)s;
+  if (!src->block_class || keep < 1 || first < 0 || last < 0 || (int64_t)first + last > keep) return FA_ERR_INVALID_ARG;
+  if (page_table && (n_pages_total < 1 || max_pages < src->nk)) return FA_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(bounds) || !words_aligned({page_table, dev_status}) ||
+      ((reinterpret_cast<uintptr_t>(dev_buf) | reinterpret_cast<uintptr_t>(workspace)) & 255u))
+    return FA_ERR_INVALID_ARG;
+  if (buf_bytes < P.mask.total || workspace_bytes < P.total) return FA_ERR_BUFFER_TOO_SMALL;
+  DevRule R;
+  s = compile_rule_noexcept(&src->rule, &R);
+  if (s != FA_OK) return (fa_status)s;
+  R.doc_run = src->doc_run;
+  R.doc_sorted = src->doc_sorted;
+  SelectArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = q;
+  a.bounds = bounds;
+  a.page_table = page_table;
+  a.n_pages_total = n_pages_total;
+  a.max_pages = max_pages;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.q_len = src->q_len;
+  a.d = d;
+  a.bq = src->bq;
+  a.nq = src->nq;
+  a.nk = src->nk;
+  a.src_class = src->block_class;
+  a.src_Bm = src->Bm;
+  a.keep = keep;
+  a.first = first;
+  a.last = last;
+  uint8_t* base = static_cast<uint8_t*>(dev_buf);
+  const size_t* off = P.mask.off;
+  MaskOut& T = a.out;
+  T.Bm = B;
+  T.Hm = Hkv;
+  T.q_len = src->q_len;
+  T.kv_len = src->kv_len;
+  T.bq = src->bq;
+  T.bk = src->bk;
+  T.nq = src->nq;
+  T.nk = src->nk;
+  T.kv_num = reinterpret_cast<int32_t*>(base + off[0]);
+  T.full_kv_num = reinterpret_cast<int32_t*>(base + off[1]);
+  T.q_num = reinterpret_cast<int32_t*>(base + off[2]);
+  T.full_q_num = reinterpret_cast<int32_t*>(base + off[3]);
+  T.kv_idx = reinterpret_cast<int32_t*>(base + off[4]);
+  T.full_kv_idx = reinterpret_cast<int32_t*>(base + off[5]);
+  T.q_idx = reinterpret_cast<int32_t*>(base + off[6]);
+  T.full_q_idx = reinterpret_cast<int32_t*>(base + off[7]);
+  T.block_class = base + off[8];
+  T.row_order = src->nq > 1 ? reinterpret_cast<int32_t*>(base + off[11]) : nullptr;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.pooled = reinterpret_cast<float*>(w);
+  a.parts = P.parts;
+  a.scores = reinterpret_cast<float*>(w + P.off_scores);
+  a.err = reinterpret_cast<float*>(w + P.off_err);
+  a.zone = reinterpret_cast<uint64_t*>(w + P.off_zone);
+  a.status = dev_status;
+  fa_block_mask m;
+  std::memset(&m, 0, sizeof(m));
+  m.Bm = B;
+  m.Hm = Hkv;
+  m.q_len = T.q_len;
+  m.kv_len = T.kv_len;
+  m.bq = T.bq;
+  m.bk = T.bk;
+  m.nq = T.nq;
+  m.nk = T.nk;
+  m.kv_num = T.kv_num;
+  m.kv_idx = T.kv_idx;
+  m.full_kv_num = T.full_kv_num;
+  m.full_kv_idx = T.full_kv_idx;
+  m.q_num = T.q_num;
+  m.q_idx = T.q_idx;
+  m.full_q_num = T.full_q_num;
+  m.full_q_idx = T.full_q_idx;
+  m.block_class = T.block_class;
+  m.doc_run = src->doc_run;  // same document ids, same runs
+  m.doc_sorted = src->doc_sorted;
+  m.row_order = T.row_order;
+  m.rule = src->rule;
+  m.rule.batch_dependent = 1;
+  m.rule.head_dependent = 1;
+  m.row_max = std::min(keep, T.nk);
+  if (launch_select_blocks(a, R, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
+  *out = m;
+  return FA_OK;
 }
 
 fa_status fa_block_mask_stats(const fa_block_mask* bm, int64_t* dev_out, fa_stream_t stream) {

@@ -23,6 +23,9 @@ struct DevMask {
   const int32_t* row_order;    // [Bm,Hm,nq] rows by visited length, longest first (NULL: nq-1 .. 0)
 };
 
+// Row of the head dimension that query head h of Hq reads: Hm is 1, Hq, or the number of KV heads (a group's heads are neighbours).
+__device__ __forceinline__ int mask_head(const DevMask& M, int Hq, int h) { return M.Hm > 1 ? h / (Hq / M.Hm) : 0; }
+
 struct MaskOut {
   int32_t Bm, Hm, q_len, kv_len, bq, bk, nq, nk;
   int32_t* kv_num;
@@ -40,6 +43,8 @@ struct MaskOut {
 };
 
 cudaError_t launch_mask_build(const DevRule& R, const MaskOut& T, cudaStream_t st);
+// the query-side transpose and the row order of T, whose row tables and classes are there; R bounds what is looked at
+cudaError_t launch_mask_transpose(const DevRule& R, const MaskOut& T, cudaStream_t st);
 cudaError_t launch_mask_stats(const MaskOut& T, int64_t* dev_out, cudaStream_t st);
 // row block q_pos[b] / S.bq of S per request b, re-classified at position q_pos[b] = R.q_offset[b] -> D with
 // Bm = Bz, nq = 1 (D's buffers laid out by the caller)
@@ -230,6 +235,42 @@ struct ExpandArgs {
   int32_t* status;
 };
 cudaError_t launch_expand_fp8(const ExpandArgs& a, cudaStream_t st);
+
+// ---- bounds of key blocks, and blocks chosen by them (select.cu)
+struct BoundsArgs {
+  const void* k;             // bf16 [B, Hkv, kv_len, d], or pages bf16 / e4m3 [n_pages_total, Hkv, page, d]
+  const float* k_scale;      // e4m3 pages: [n_pages_total, Hkv, page / 32]; else NULL
+  void* bounds;              // bf16 [B, Hkv, nk, 2, d] or [n_pages_total, Hkv, 2, d]: smallest, largest
+  const int32_t* page_table; // [B, max_pages] or NULL: contiguous keys
+  int32_t n_pages_total, page, max_pages;  // page: the block's tokens
+  const int32_t* q_offset;   // [B] or NULL
+  const int32_t* n_new;      // [B] or NULL (N)
+  int32_t B, Hkv, N, kv_len, d;
+  int32_t* status;
+};
+cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t st);
+
+constexpr int kSelectMaxBlocks = 32768;  // key blocks of a row: what the choice keeps of it fits in shared memory
+struct SelectArgs {
+  const void* q;             // bf16 [B, Hq, q_len, d]
+  const void* bounds;        // bf16 [B, Hkv, nk, 2, d], or with a page table [n_pages_total, Hkv, 2, d]
+  const int32_t* page_table; // [B, max_pages] or NULL
+  int32_t n_pages_total, max_pages;
+  int32_t B, Hq, Hkv, q_len, d, bq, nq, nk;
+  const uint8_t* src_class;  // [src_Bm, nq, nk]
+  int32_t src_Bm;
+  int32_t keep, first, last;
+  MaskOut out;               // Bm = B, Hm = Hkv
+  float* pooled;             // [B, Hkv, nq, parts, 2, 2 d] (q_len > 1)
+  int32_t parts;             // divisions of a group's heads
+  float* scores;             // [B, Hkv, nq, nk]
+  float* err;                // [B, Hkv, nq, select_err_floats]
+  uint64_t* zone;            // [B, Hkv, nq, nk]
+  int32_t* status;
+};
+int select_token_ranks(int64_t rows, int32_t nk);
+size_t select_err_floats(int32_t q_len, int32_t nk);
+cudaError_t launch_select_blocks(const SelectArgs& a, const DevRule& R, cudaStream_t st);
 
 // Host helpers: encode a bf16 / fp32 tensor map (dims innermost first) with 128-byte swizzle.
 int encode_tmap_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,

@@ -685,6 +685,10 @@ cudaError_t launch_mask_build(const DevRule& R0, const MaskOut& T, cudaStream_t 
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
+  return launch_mask_transpose(R, T, st);
+}
+
+cudaError_t launch_mask_transpose(const DevRule& R, const MaskOut& T, cudaStream_t st) {
   dim3 g2(T.nk + (T.row_order ? 1 : 0), T.Hm, T.Bm);  // + one CTA per (b_m, h_m) for the row order
   mask_transpose_kernel<<<g2, kThreads, 0, st>>>(R, T);
   return cudaGetLastError();

@@ -59,7 +59,7 @@ class BlockMaskC(ctypes.Structure):
                 ("full_kv_idx", ctypes.c_void_p), ("q_num", ctypes.c_void_p), ("q_idx", ctypes.c_void_p),
                 ("full_q_num", ctypes.c_void_p), ("full_q_idx", ctypes.c_void_p),
                 ("block_class", ctypes.c_void_p), ("doc_run", ctypes.c_void_p), ("doc_sorted", ctypes.c_void_p),
-                ("row_order", ctypes.c_void_p), ("rule", MaskRule)]
+                ("row_order", ctypes.c_void_p), ("rule", MaskRule), ("row_max", ctypes.c_int32)]
 
 
 _lib = None
@@ -145,6 +145,19 @@ def load() -> ctypes.CDLL:
     lib.fa_flex_forward_paged_fp8.restype = ctypes.c_int
     lib.fa_flex_forward_paged_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, P(BlockMaskC), P(ScoreRule), f32, vp,
                                               i32, vp, i32, i32, i32, i32, i32, i32, i32, vp, sz, vp, vp]
+    lib.fa_key_bounds.restype = ctypes.c_int
+    lib.fa_key_bounds.argtypes = [vp, vp, i32, i32, i32, i32, i32, vp]
+    lib.fa_kv_bounds.restype = ctypes.c_int
+    lib.fa_kv_bounds.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.fa_kv_bounds_fp8.restype = ctypes.c_int
+    lib.fa_kv_bounds_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, vp, vp]
+    lib.fa_block_mask_select_blocks_bytes.restype = sz
+    lib.fa_block_mask_select_blocks_bytes.argtypes = [P(BlockMaskC), i32, i32]
+    lib.fa_block_mask_select_blocks_workspace_bytes.restype = sz
+    lib.fa_block_mask_select_blocks_workspace_bytes.argtypes = [P(BlockMaskC), i32, i32, i32, i32]
+    lib.fa_block_mask_select_blocks.restype = ctypes.c_int
+    lib.fa_block_mask_select_blocks.argtypes = [P(BlockMaskC), vp, vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32, vp, sz,
+                                                P(BlockMaskC), vp, sz, vp, vp]
     lib.fa_block_mask_stats.restype = ctypes.c_int
     lib.fa_block_mask_stats.argtypes = [P(BlockMaskC), vp, vp]
     lib.fa_check_status.restype = ctypes.c_int
@@ -840,6 +853,110 @@ def flex_forward_paged_fp8(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
                  float(scale) if scale else 0.0, _at(out), _out_code(out), _at(lse), B, Hq, Hkv, Q_LEN, KV_LEN, d,
                  chunk_blocks, _at(workspace), size, _at(status)), "fa_flex_forward_paged_fp8")
     return out, lse
+
+
+# ----------------------------------------------------------------------------------------------
+# key blocks chosen by a cheap score
+# ----------------------------------------------------------------------------------------------
+def key_bounds(k: torch.Tensor, Bk: int = 128, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fa_key_bounds: keys [B,Hkv,KV_LEN,d] bf16 -> bounds [B,Hkv,ceil(KV_LEN/Bk),2,d] bf16, the smallest and the largest value of each
+    channel among each block's keys."""
+    if k.dim() != 4 or not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor [B, Hkv, KV_LEN, d]")
+    B, Hkv, n, d = k.shape
+    _same(k, k.shape, torch.bfloat16, k.device, "k")
+    if not 1 <= Bk <= 128:
+        raise ValueError("Bk must be 1..128")
+    shape = (B, Hkv, (n + Bk - 1) // Bk, 2, d)
+    out = torch.empty(shape, dtype=torch.bfloat16, device=k.device) if out is None else _same(out, shape, torch.bfloat16, k.device, "out")
+    _check(_call(k.device, load().fa_key_bounds, _at(k), _at(out), B, Hkv, n, d, Bk), "fa_key_bounds")
+    return out
+
+
+def _kv_bounds(k_pages, k_scale, bounds, page_table, N, q_offset, n_new, status):
+    if k_pages.dim() != 4 or page_table.dim() != 2 or not k_pages.is_cuda:
+        raise ValueError("pages must be a CUDA tensor [P, Hkv, page, d] and page_table [B, max_pages]")
+    dev = k_pages.device
+    P, Hkv, page, d = k_pages.shape
+    B, max_pages = page_table.shape
+    _same(k_pages, k_pages.shape, torch.bfloat16 if k_scale is None else torch.float8_e4m3fn, dev, "k_pages")
+    _same(k_scale, (P, Hkv, page // KV_SCALE_TOKENS), torch.float32, dev, "k_scale")
+    _same(bounds, (P, Hkv, 2, d), torch.bfloat16, dev, "bounds")
+    i32 = torch.int32
+    _same(page_table, (B, max_pages), i32, dev, "page_table")
+    _same(q_offset, (B,), i32, dev, "q_offset")
+    _same(n_new, (B,), i32, dev, "n_new")
+    _same(status, (1,), i32, dev, "status")
+    tail = (_at(page_table), _at(q_offset), _at(n_new), P, page, max_pages, B, Hkv, N, d, _at(status))
+    if k_scale is None:
+        _check(_call(dev, load().fa_kv_bounds, _at(k_pages), _at(bounds), *tail), "fa_kv_bounds")
+    else:
+        _check(_call(dev, load().fa_kv_bounds_fp8, _at(k_pages), _at(k_scale), _at(bounds), *tail), "fa_kv_bounds_fp8")
+    return bounds
+
+
+def kv_bounds(k_pages: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tensor, N: int = 1,
+              q_offset: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fa_kv_bounds: after kv_append of up to N tokens a request at q_offset, the bounds [P,Hkv,2,d] bf16 of the pages that they
+    reach are brought up to date (in place; returned). Other pages' bounds stay as they are."""
+    return _kv_bounds(k_pages, None, bounds, page_table, N, q_offset, n_new, status)
+
+
+def kv_bounds_fp8(k_pages: torch.Tensor, k_scale: torch.Tensor, bounds: torch.Tensor, page_table: torch.Tensor, N: int = 1,
+                  q_offset: Optional[torch.Tensor] = None, n_new: Optional[torch.Tensor] = None,
+                  status: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fa_kv_bounds_fp8: kv_bounds of float8_e4m3fn pages with scales fp32 [P,Hkv,page/32]."""
+    if k_scale is None:
+        raise ValueError("k_scale is required")
+    return _kv_bounds(k_pages, k_scale, bounds, page_table, N, q_offset, n_new, status)
+
+
+def select_blocks_workspace_bytes(src: BlockMask, B: int, Hq: int, Hkv: int, d: int) -> int:
+    return int(load().fa_block_mask_select_blocks_workspace_bytes(ctypes.byref(src.c), B, Hq, Hkv, d))
+
+
+def select_blocks(src: BlockMask, q: torch.Tensor, bounds: torch.Tensor, keep: int, first: int = 1, last: int = 1,
+                  page_table: Optional[torch.Tensor] = None, out: Optional[BlockMask] = None,
+                  workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> BlockMask:
+    """fa_block_mask_select_blocks: from each row of src (Hm = 1), for each request and KV head, at most `keep` of the blocks it visits:
+    the first `first`, the last `last`, and of the others those with the largest bound on <q, k>, summed over the query block's rows
+    and the heads of the group. q [B,Hq,Q_LEN,d] bf16 (or [B,Hq,d] for one query); bounds [B,Hkv,nk,2,d] of key_bounds, or with a
+    page_table int32 [B,max_pages] (one page a block) [P,Hkv,2,d] of kv_bounds. Returns a mask with Bm = B, Hm = Hkv for flex_decode,
+    flex_decode_fp8, the forwards and flex_backward. Reuses `out`'s buffer."""
+    if q.dim() not in (3, 4) or not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor [B, Hq, Q_LEN, d] or [B, Hq, d]")
+    dev, bf, c = q.device, torch.bfloat16, src.c
+    B, Hq, d = q.shape[0], q.shape[1], q.shape[-1]
+    _same(q, (B, Hq, d) if q.dim() == 3 and c.q_len == 1 else (B, Hq, c.q_len, d), bf, dev, "q")
+    if src.buf.device != dev:
+        raise ValueError(f"src must be on {dev}")
+    if page_table is None:
+        if bounds.dim() != 5:
+            raise ValueError("bounds must be [B, Hkv, nk, 2, d]")
+        Hkv, P, max_pages = bounds.shape[1], 0, 0
+        _same(bounds, (B, Hkv, c.nk, 2, d), bf, dev, "bounds")
+    else:
+        if bounds.dim() != 4 or page_table.dim() != 2:
+            raise ValueError("bounds must be [P, Hkv, 2, d] and page_table [B, max_pages]")
+        P, Hkv, max_pages = bounds.shape[0], bounds.shape[1], page_table.shape[1]
+        _same(bounds, (P, Hkv, 2, d), bf, dev, "bounds")
+        _same(page_table, (B, max_pages), torch.int32, dev, "page_table")
+    _same(status, (1,), torch.int32, dev, "status")
+    size = _scratch(workspace, dev)
+    lib = load()
+    ref = ctypes.byref(c)
+    n = lib.fa_block_mask_select_blocks_bytes(ref, B, Hkv)
+    if workspace is None:
+        size = lib.fa_block_mask_select_blocks_workspace_bytes(ref, B, Hq, Hkv, d)
+        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
+    if out is None or out.buf.numel() < n or out.buf.device != dev or out.buf is src.buf:
+        out = BlockMask(BlockMaskC(), torch.empty(max(n, 256), dtype=torch.uint8, device=dev), [])
+    _check(_call(dev, lib.fa_block_mask_select_blocks, ref, _at(q), _at(bounds), _at(page_table), P, max_pages, B, Hq, Hkv, d, keep,
+                 first, last, _at(out.buf), out.buf.numel(), ctypes.byref(out.c), _at(workspace), size, _at(status)),
+           "fa_block_mask_select_blocks")
+    out.keep = [src]  # its rule's tensors and its document runs stay valid with it
+    return out
 
 
 def check_status(status: torch.Tensor) -> int:

@@ -139,6 +139,7 @@ typedef struct {
                                dQ kernel take their query blocks in this order. NULL (one row per table):
                                rows nq-1 .. 0. Tables of more than 2048 key blocks keep nq-1 .. 0 too. */
   fa_mask_rule rule;
+  int32_t row_max;          /* the most blocks a row lists, where the builder knows (fa_block_mask_select_blocks); 0: not known */
 } fa_block_mask;
 
 /* Bytes of device buffer fa_create_block_mask needs for these sizes (0 on invalid arguments). */
@@ -183,6 +184,65 @@ FA_API fa_status fa_block_mask_select_rows(const fa_block_mask* src, const int32
                                            void* dev_buf, size_t buf_bytes, fa_block_mask* out,
                                            int32_t* dev_status, fa_stream_t stream);
 
+/* Bounds of key blocks, for fa_block_mask_select_blocks: the smallest and the largest value that each channel takes among a block's keys,
+ * exactly (a NaN among them makes both NaN).
+ *   k        device bf16 [B, Hkv, KV_LEN, d], 16-byte aligned
+ *   bounds   device bf16 [B, Hkv, ceil(KV_LEN / Bk), 2, d] (smallest, largest), 16-byte aligned; overwritten
+ *   Bk       1..128
+ * Supported: d in {64, 128}; B, Hkv <= 65535. */
+FA_API fa_status fa_key_bounds(const void* k, void* bounds, int32_t B, int32_t Hkv, int32_t KV_LEN, int32_t d, int32_t Bk,
+                               fa_stream_t stream);
+
+/* The same for the pages of a cache, after an append (fa_kv_append, fa_kv_append_fp8; same q_offset, n_new and N): the bounds of every
+ * page that request b's tokens at positions q_offset[b] .. q_offset[b] + n_new[b] - 1 reach, over that page's slots up to the last
+ * of them. Whole pages are looked at again, so the result depends on the cache alone: a sequence may be cut back, and a page's
+ * e4m3 block rescaled. Other pages' bounds stay as they are, and so do pages of requests without new tokens; slots behind the
+ * last token may hold anything.
+ *   k_pages   device bf16 (fa_kv_bounds) or e4m3 with k_scale (fa_kv_bounds_fp8) [n_pages_total, Hkv, page, d]
+ *   bounds    device bf16 [n_pages_total, Hkv, 2, d], 16-byte aligned. A cached e4m3 value is its page value times its scale
+ *             (read as clamped to [2^-40, 2^40]); bounds of these are rounded outwards, exact for power-of-two scales
+ *   page_table  device int32 [B, max_pages]; a page that is written belongs to one request only
+ *   q_offset  device int32 [B] or NULL (zero);  n_new  device int32 [B], 0 .. N, or NULL (N)
+ *   dev_status  tokens outside [0, max_pages * page) and pages whose id lies outside [0, n_pages_total) are left out and set
+ *             FA_ERR_DEVICE_CHECK; an n_new outside 0 .. N is clamped and sets it
+ * Supported: d in {64, 128}; page in {16, 32, 64, 128} ({32, 64, 128} for e4m3); B, Hkv <= 65535. */
+FA_API fa_status fa_kv_bounds(const void* k_pages, void* bounds, const int32_t* page_table, const int32_t* q_offset,
+                              const int32_t* n_new, int32_t n_pages_total, int32_t page, int32_t max_pages, int32_t B,
+                              int32_t Hkv, int32_t N, int32_t d, int32_t* dev_status, fa_stream_t stream);
+FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, void* bounds, const int32_t* page_table,
+                                  const int32_t* q_offset, const int32_t* n_new, int32_t n_pages_total, int32_t page,
+                                  int32_t max_pages, int32_t B, int32_t Hkv, int32_t N, int32_t d, int32_t* dev_status,
+                                  fa_stream_t stream);
+
+/* Blocks of a mask chosen by a cheap score: from each row of src, for each batch row b and KV head, at most `keep` of the blocks it
+ * visits. The first `first` and the last `last` of them in column order are always kept, and of the others those with the largest
+ *   score(c) = sum over the query block's rows i < Q_LEN and the query heads h of the group, sum over e of
+ *              max(q[b,h,i,e] * smallest[c,e], q[b,h,i,e] * largest[c,e]),
+ * which bounds the sum of <q, k> over those queries for any choice of keys in the block (scale, score rule and mask rule
+ * do not enter). Scores are compared in 64 bits, ties go to the lower column; scores closer than 2^-40 of the magnitudes that they
+ * add up may rank either way. A NaN score ranks above all others (a NaN key or query cannot be hidden by the choice).
+ * The result is src's mask with the other blocks empty: classes, row lists, query-side transpose and row order as
+ * fa_create_block_mask would lay them out, with Bm = B, Hm = Hkv, for every attention entry point (fa_flex_decode and
+ * fa_flex_decode_fp8 for one query, the forwards and fa_flex_backward for query blocks). The choice itself has no gradient.
+ *   src        host pointer to a mask with Hm = 1, Bm in {1, B} and at most 32768 key blocks
+ *   q          device bf16 [B, Hq, Q_LEN, d] (the [Bz, Hq, d] of fa_flex_decode where Q_LEN = 1), 16-byte aligned
+ *   bounds     page_table NULL: device bf16 [B, Hkv, nk, 2, d] (fa_key_bounds); else device bf16 [n_pages_total, Hkv, 2, d]
+ *              (fa_kv_bounds) with key block c of batch row b in page page_table[b * max_pages + c], max_pages >= nk, one page a block
+ *   keep       >= 1;  first, last >= 0, first + last <= keep
+ *   dev_buf    device buffer of >= fa_block_mask_select_blocks_bytes(src, B, Hkv) bytes, 256-byte aligned
+ *   out        host struct, filled with pointers into dev_buf and src's document run arrays; may be src
+ *   workspace  device, >= fa_block_mask_select_blocks_workspace_bytes(src, B, Hq, Hkv, d) bytes, 256-byte aligned, for one call at a time
+ *   dev_status a page id of a visited block outside [0, n_pages_total) sets FA_ERR_DEVICE_CHECK; that block ranks lowest
+ * Returns FA_ERR_INVALID_ARG (NULL, alignment, keep / first / last), FA_ERR_SHAPE (sizes, src->Bm), FA_ERR_UNSUPPORTED (src->Hm > 1, too
+ * many blocks, d not in {64, 128}, B or Hq > 65535), FA_ERR_BUFFER_TOO_SMALL. */
+FA_API size_t fa_block_mask_select_blocks_bytes(const fa_block_mask* src, int32_t B, int32_t Hkv);
+FA_API size_t fa_block_mask_select_blocks_workspace_bytes(const fa_block_mask* src, int32_t B, int32_t Hq, int32_t Hkv, int32_t d);
+FA_API fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, const void* bounds,
+                                             const int32_t* page_table, int32_t n_pages_total, int32_t max_pages, int32_t B,
+                                             int32_t Hq, int32_t Hkv, int32_t d, int32_t keep, int32_t first, int32_t last,
+                                             void* dev_buf, size_t buf_bytes, fa_block_mask* out, void* workspace,
+                                             size_t workspace_bytes, int32_t* dev_status, fa_stream_t stream);
+
 /* Element type of O. The softmax statistics and the accumulator are fp32 in every case; FA_OUT_F32
  * stores the fp32 result as is, FA_OUT_BF16 rounds it to bf16 (round to nearest even) on the store. */
 typedef enum { FA_OUT_BF16 = 0, FA_OUT_F32 = 1 } fa_out_dtype;
@@ -194,7 +254,7 @@ typedef enum { FA_OUT_BF16 = 0, FA_OUT_F32 = 1 } fa_out_dtype;
  *   q            device bf16 [B, Hq, Q_LEN, d]
  *   k, v         device bf16 [B, Hkv, KV_LEN, d]; query head h reads KV head floor(h / (Hq/Hkv))
  *   block_mask   host pointer to a mask made by fa_create_block_mask with q_len == Q_LEN, kv_len ==
- *                KV_LEN, Bm in {1, B}, Hm in {1, Hq} (a length mismatch is an error, never trimmed)
+ *                KV_LEN, Bm in {1, B}, Hm in {1, Hkv, Hq} (a length mismatch is an error, never trimmed)
  *   score_rule   host pointer or NULL (no score rule)
  *   scale        > 0, or <= 0 for 1/sqrt(d)
  *   out          device [B, Hq, Q_LEN, d] of type out_dtype;  lse  device fp32 [B, Hq, Q_LEN] (natural log)
@@ -316,7 +376,7 @@ FA_API fa_status fa_flex_backward(const void* q, const void* k, const void* v, c
  *   v_pages      device bf16 [n_pages_total, Hkv, page, d]
  *   page_table   device int32 [Bz, max_pages]
  *   block_mask   made with Bq = 1, Bk = page, Q_LEN = 1, KV_LEN = max_pages * page, Bm in {1, Bz},
- *                Hm == 1; its rule's q_offset[b] is the query's global position (cur_pos = L_b - 1)
+ *                Hm in {1, Hkv}; its rule's q_offset[b] is the query's global position (cur_pos = L_b - 1)
  *   workspace    device buffer of >= fa_decode_workspace_bytes(...) bytes, 16-byte aligned; holds the
  *                per-split (m, l, u) between the two kernels
  *   out          device [Bz, Hq, d] of type out_dtype;  lse  device fp32 [Bz, Hq]
