@@ -1503,7 +1503,7 @@ fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, void* boun
 struct SelectPlan {
   MaskLayout mask;
   int32_t parts;
-  size_t off_scores, off_err, off_zone, total;
+  size_t off_zone, total;
 };
 
 static int select_blocks_plan(const fa_block_mask* src, int32_t B, int32_t Hq, int32_t Hkv, int32_t d, SelectPlan* P) {
@@ -1525,9 +1525,7 @@ static int select_blocks_plan(const fa_block_mask* src, int32_t B, int32_t Hq, i
   const size_t rows = (size_t)B * Hkv * src->nq;
   // one query block's sums are split among its heads where there are fewer (request, KV head, query block)s than two for each SM
   P->parts = src->q_len == 1 ? 0 : rows < 2 * 152 ? Hq / Hkv : 1;
-  P->off_scores = align256(rows * P->parts * 4 * d * sizeof(float));
-  P->off_err = P->off_scores + align256(rows * src->nk * sizeof(float));
-  P->off_zone = P->off_err + align256(rows * select_err_floats(src->q_len, src->nk) * sizeof(float));
+  P->off_zone = align256(rows * P->parts * 4 * d * sizeof(float));
   P->total = P->off_zone + align256(rows * src->nk * sizeof(uint64_t));
   return FA_OK;
 }
@@ -1606,8 +1604,6 @@ fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, c
   uint8_t* w = static_cast<uint8_t*>(workspace);
   a.pooled = reinterpret_cast<float*>(w);
   a.parts = P.parts;
-  a.scores = reinterpret_cast<float*>(w + P.off_scores);
-  a.err = reinterpret_cast<float*>(w + P.off_err);
   a.zone = reinterpret_cast<uint64_t*>(w + P.off_zone);
   a.status = dev_status;
   fa_block_mask m;

@@ -263,13 +263,10 @@ struct SelectArgs {
   MaskOut out;               // Bm = B, Hm = Hkv
   float* pooled;             // [B, Hkv, nq, parts, 2, 2 d] (q_len > 1)
   int32_t parts;             // divisions of a group's heads
-  float* scores;             // [B, Hkv, nq, nk]
-  float* err;                // [B, Hkv, nq, select_err_floats]
   uint64_t* zone;            // [B, Hkv, nq, nk]
   int32_t* status;
 };
-int select_token_ranks(int64_t rows, int32_t nk);
-size_t select_err_floats(int32_t q_len, int32_t nk);
+int select_ranks(int64_t rows, int32_t nk);
 cudaError_t launch_select_blocks(const SelectArgs& a, const DevRule& R, cudaStream_t st);
 
 // Host helpers: encode a bf16 / fp32 tensor map (dims innermost first) with 128-byte swizzle.

@@ -218,186 +218,202 @@ __global__ void __launch_bounds__(kBound8Threads) kv_bounds_fp8_kernel(const __g
 }
 
 // ------------------------------------------------------------------------------------------------ sums over queries
-// hi + lo += x, exactly up to 2^-48 of the result
-__device__ __forceinline__ void add_pair(float& hi, float& lo, float x) {
-  const float s = __fadd_rn(hi, x), t = __fsub_rn(s, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(x, t)));
-  hi = s;
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// a + b of two pairs of floats, a * b + c
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 floats_of(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
 }
 
-// Q- [0, D) and Q+ [D, 2 D) of the 8 channels that a thread has
-struct Sums {
-  float hi[2][8], lo[2][8];
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) hi[0][i] = hi[1][i] = lo[0][i] = lo[1][i] = 0.f;
-  }
-  __device__ __forceinline__ void add(uint4 v) {
-    const uint32_t t[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = (i & 1) ? bf_hi(t[i >> 1]) : bf_lo(t[i >> 1]);
-      add_pair(hi[0][i], lo[0][i], x > 0.f ? 0.f : x);   // NaN goes to Q-, and from there to every score
-      add_pair(hi[1][i], lo[1][i], x > 0.f ? x : 0.f);
-    }
-  }
-};
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 
-constexpr int kPoolThreads = 256;
+// s + rest = s + x (+ rest): what the addition rounds off goes to rest
+__device__ __forceinline__ void add_exact(float& s, float& rest, float x) {
+  const float t = __fadd_rn(s, x), u = __fsub_rn(t, s);
+  rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(x, u)));
+  s = t;
+}
+// the same for two sums at once
+__device__ __forceinline__ void add_exact2(uint64_t& s, uint64_t& rest, uint64_t x) {
+  constexpr uint64_t kMinus = 0xBF800000BF800000ull;  // (-1, -1): a - b as b * -1 + a
+  const uint64_t t = add2(s, x), u = fma2(s, kMinus, t);
+  rest = add2(rest, add2(fma2(fma2(u, kMinus, t), kMinus, s), fma2(u, kMinus, x)));
+  s = t;
+}
 
-// grid (nq, Hkv * parts, B): the sums of one query block over Hq / Hkv / parts heads -> pooled [B, Hkv, nq, parts, 2 (hi, lo), 2 D]
+// grid (nq, Hkv * parts, B): Q-, Q+ of one query block over Hq / Hkv / parts heads, in pairs of floats (2^-46 of the magnitudes), as the
+// sums of all values and of the positive ones -> pooled [B, Hkv, nq, parts, 2 (sum, rest), 2 D]
 template <int D>
-__global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constant__ SelectArgs a) {
-  constexpr int LPR = D / 8, kRows = kPoolThreads / LPR, kWarps = kPoolThreads / 32;
-  __shared__ float s_sum[kWarps][2][2 * D];  // hi, lo
+__global__ void __launch_bounds__(kThreads) pool_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int LPR = D / 8, kRows = kThreads / LPR, kPass = 128 / kRows;  // bq <= 128
+  __shared__ float s_sum[kWarps][2][2 * D];
   const int r = blockIdx.x, hk = blockIdx.y / a.parts, part = blockIdx.y % a.parts, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = tid % LPR;
   const int g = a.Hq / a.Hkv, h0 = hk * g + part * g / a.parts, h1 = hk * g + (part + 1) * g / a.parts;
   const int i0 = r * a.bq, rows = min(a.bq, a.q_len - i0);
-  Sums s;
-  s.clear();
+  uint64_t all[4], pos[4], all_r[4], pos_r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) all[i] = pos[i] = all_r[i] = pos_r[i] = 0;
   for (int h = h0; h < h1; ++h) {
     const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.Hq + h) * a.q_len + i0) * D);
-#pragma unroll 8
-    for (int i = tid / LPR; i < rows; i += kRows) s.add(__ldg(src + (size_t)i * LPR + x));
+    uint4 v[kPass];
+#pragma unroll
+    for (int k = 0; k < kPass; ++k) {
+      const int i = tid / LPR + k * kRows;
+      v[k] = i < rows ? __ldg(src + (size_t)i * LPR + x) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kPass; ++k) {
+      const uint32_t t[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float u = bf_lo(t[i]), w = bf_hi(t[i]);
+        add_exact2(all[i], all_r[i], pair_of(u, w));
+        add_exact2(pos[i], pos_r[i], pair_of(max_nan(u, 0.f), max_nan(w, 0.f)));
+      }
+    }
   }
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float oh = __shfl_xor_sync(kAll, s.hi[w][i], o), ol = __shfl_xor_sync(kAll, s.lo[w][i], o);
-        add_pair(s.hi[w][i], s.lo[w][i], oh);
-        s.lo[w][i] += ol;
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t u = __shfl_xor_sync(kAll, all[i], o), p = __shfl_xor_sync(kAll, pos[i], o);
+      all_r[i] = add2(all_r[i], __shfl_xor_sync(kAll, all_r[i], o));
+      pos_r[i] = add2(pos_r[i], __shfl_xor_sync(kAll, pos_r[i], o));
+      add_exact2(all[i], all_r[i], u);
+      add_exact2(pos[i], pos_r[i], p);
+    }
   if (lane < LPR) {
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s_sum[warp][0][w * D + x * 8 + i] = s.hi[w][i];
-        s_sum[warp][1][w * D + x * 8 + i] = s.lo[w][i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      *reinterpret_cast<uint64_t*>(&s_sum[warp][0][x * 8 + 2 * i]) = all[i];
+      *reinterpret_cast<uint64_t*>(&s_sum[warp][1][x * 8 + 2 * i]) = all_r[i];
+      *reinterpret_cast<uint64_t*>(&s_sum[warp][0][D + x * 8 + 2 * i]) = pos[i];
+      *reinterpret_cast<uint64_t*>(&s_sum[warp][1][D + x * 8 + 2 * i]) = pos_r[i];
+    }
   }
   __syncthreads();
   float* out = a.pooled + ((((size_t)b * a.Hkv + hk) * a.nq + r) * a.parts + part) * 4 * D;
-  for (int e = tid; e < 2 * D; e += kPoolThreads) {
-    float hi = s_sum[0][0][e], lo = s_sum[0][1][e];
+  if (tid < D) {
+    float sum[2], rest[2];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-      add_pair(hi, lo, s_sum[w][0][e]);
-      lo += s_sum[w][1][e];
+    for (int k = 0; k < 2; ++k) {
+      sum[k] = s_sum[0][0][k * D + tid];
+      rest[k] = s_sum[0][1][k * D + tid];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) {
+        rest[k] += s_sum[w][1][k * D + tid];
+        add_exact(sum[k], rest[k], s_sum[w][0][k * D + tid]);
+      }
     }
-    out[e] = hi;
-    out[2 * D + e] = lo;
+    rest[0] -= rest[1];  // Q- = all - positive
+    add_exact(sum[0], rest[0], -sum[1]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {  // the rest below the sum's last bit
+      const float t = sum[k] + rest[k];
+      out[2 * D + k * D + tid] = t - t == 0.f ? rest[k] - (t - sum[k]) : 0.f;
+      out[k * D + tid] = t;
+    }
   }
 }
 
 // ------------------------------------------------------------------------------------------------ scores
-// the bounds of block c, or NULL where its page does not exist
+// Where the bounds of a (request, KV head)'s blocks lie: block id at base + id * stride
 template <int D>
-__device__ __forceinline__ const __nv_bfloat16* box_of(const SelectArgs& a, int b, int hk, int c) {
-  const __nv_bfloat16* base = static_cast<const __nv_bfloat16*>(a.bounds);
-  if (!a.page_table) return base + (((size_t)b * a.Hkv + hk) * a.nk + c) * 2 * D;
-  const int pid = __ldg(a.page_table + (size_t)b * a.max_pages + c);
-  return pid < 0 || pid >= a.n_pages_total ? nullptr : base + ((size_t)pid * a.Hkv + hk) * 2 * D;
-}
-
-// 32 query blocks x 64 key blocks of one (request, KV head). Sums of products run over 32 of the 2 D terms before they are added up.
-constexpr int kTileR = 32, kTileC = 64, kTileK = 32, kTileThreads = 128;
-
-template <int D>
-__global__ void __launch_bounds__(kTileThreads) score_tile_kernel(const __grid_constant__ SelectArgs a) {
-  __shared__ __align__(16) float s_q[kTileK][kTileR + 4], s_b[kTileK][kTileC + 4];
-  __shared__ float s_most[kTileK];
-  const int nct = (a.nk + kTileC - 1) / kTileC;
-  const int ct = blockIdx.x % nct, c0 = ct * kTileC, r0 = (blockIdx.x / nct) * kTileR, hk = blockIdx.y, b = blockIdx.z;
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
-  const size_t row0 = ((size_t)b * a.Hkv + hk) * a.nq + r0;
-  const int rn = min(kTileR, a.nq - r0), cn = min(kTileC, a.nk - c0);
-  const uint8_t* cls = a.src_class + ((size_t)(a.src_Bm > 1 ? b : 0) * a.nq + r0) * a.nk + c0;
-  bool any = false;
-  for (int x = tid; x < rn * kTileC; x += kTileThreads) any = any || (x % kTileC < cn && cls[(size_t)(x / kTileC) * a.nk + x % kTileC] != 0);
-  if (!__syncthreads_or(any)) {  // no query block here sees any of the key blocks
-    if (tid < rn) a.err[(row0 + tid) * nct + ct] = 0.f;
-    return;
+struct Boxes {
+  const __nv_bfloat16* base;
+  size_t stride;
+  const int32_t* table;  // of the request, or NULL: id = column
+  int total;
+  __device__ __forceinline__ Boxes(const SelectArgs& a, int b, int hk) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.bounds);
+    table = a.page_table ? a.page_table + (size_t)b * a.max_pages : nullptr;
+    total = a.n_pages_total;
+    base = table ? p + (size_t)hk * 2 * D : p + ((size_t)b * a.Hkv + hk) * a.nk * 2 * D;
+    stride = table ? (size_t)a.Hkv * 2 * D : 2 * D;
   }
-  const int lc = c0 + tid / 2;
-  const __nv_bfloat16* box = lc < a.nk ? box_of<D>(a, b, hk, lc) : nullptr;
-  const bool missing = lc < a.nk && !box;
-  const int lr = tid / 4, lk = tid % 4 * 8;
-  float acc[4][4], err = 0.f;
+  __device__ __forceinline__ int id(int c) const {  // -1: there is none
+    if (!table) return c;
+    const int pid = __ldg(table + c);
+    return pid < 0 || pid >= total ? -1 : pid;
+  }
+  __device__ __forceinline__ const __nv_bfloat16* at(int id) const { return base + (size_t)id * stride; }
+};
+
+// A warp scores the blocks of its lanes' ids (-1: none), 16 bytes of a block a lane: 8 (d = 64: 16) blocks in flight, whose partial sums
+// meet in a butterfly that halves the blocks a lane still has with every step. q: the lane's 8 terms of Q-, Q+; most: largest magnitudes
+// of its 8 bounds so far. 4 products in a row, 6 sums.
+template <int D>
+__device__ __forceinline__ float score_lanes(const Boxes<D>& box, int id, const uint64_t (&q)[4], uint32_t (&most)[4]) {
+  constexpr int LPB = D / 4, BPW = 32 / LPB, kStep = 8 * BPW;
+  const int lane = threadIdx.x & 31, x = lane % LPB;
+  const uint32_t have = __ballot_sync(kAll, id >= 0);
+  float out = -INFINITY;
+#pragma unroll 1
+  for (int k = 0; k < 32; k += kStep) {
+    if (!((have >> k) & ((1u << kStep) - 1u))) continue;
+    uint4 v[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  for (int k0 = 0; k0 < 2 * D; k0 += kTileK) {
-    float q[8];
+    for (int j = 0; j < 8; ++j) {
+      const int w = __shfl_sync(kAll, id, k + j * BPW + lane / LPB);
+      v[j] = w >= 0 ? __ldg(reinterpret_cast<const uint4*>(box.at(w)) + x) : make_uint4(0, 0, 0, 0);
+    }
+    float s[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = 0.f;
-    if (lr < rn)
-      for (int p = 0; p < a.parts; ++p) {
-        const float4* src = reinterpret_cast<const float4*>(a.pooled + ((row0 + lr) * a.parts + p) * 4 * D + k0 + lk);
-        const float4 u = __ldg(src), v = __ldg(src + 1);
-        q[0] += u.x, q[1] += u.y, q[2] += u.z, q[3] += u.w, q[4] += v.x, q[5] += v.y, q[6] += v.z, q[7] += v.w;
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t t[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+      uint64_t p = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        p = fma2(q[i], pair_of(bf_lo(t[i]), bf_hi(t[i])), p);
+        most[i] = bits_of(__hmax2(as_bf2(most[i]), __habs2(as_bf2(t[i]))));
       }
-    uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (box) {
-      const uint4* src = reinterpret_cast<const uint4*>(box + k0 + tid % 2 * 16);
-      w[0] = __ldg(src);
-      w[1] = __ldg(src + 1);
+      const float2 f = floats_of(p);
+      s[j] = f.x + f.y;
     }
-    __syncthreads();
+    constexpr int O = LPB / 2;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_q[lk + i][lr] = q[i];
+    for (int n = 4, o = O; n > 0; n >>= 1, o >>= 1) {
+      const bool up = lane & o;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t t = i < 4 ? (&w[0].x)[i & 3] : (&w[1].x)[i & 3];
-      s_b[tid % 2 * 16 + 2 * i][tid / 2] = bf_lo(t);
-      s_b[tid % 2 * 16 + 2 * i + 1][tid / 2] = bf_hi(t);
-    }
-    __syncthreads();
-    float most = 0.f;  // the largest magnitude of a channel among the tile's blocks
-#pragma unroll
-    for (int i = 0; i < kTileC / 4; ++i) most = fmaxf(most, fabsf(s_b[tid / 4][tid % 4 + 4 * i]));
-    most = fmaxf(most, __shfl_xor_sync(kAll, most, 1));
-    most = fmaxf(most, __shfl_xor_sync(kAll, most, 2));
-    if (tid % 4 == 0) s_most[tid / 4] = most;
-    float part[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) part[i][0] = part[i][1] = part[i][2] = part[i][3] = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < kTileK; ++k) {
-      const float4 u = *reinterpret_cast<const float4*>(&s_q[k][ty * 4]), v = *reinterpret_cast<const float4*>(&s_b[k][tx * 4]);
-      const float qq[4] = {u.x, u.y, u.z, u.w}, bb[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) part[i][j] = fmaf(qq[i], bb[j], part[i][j]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] += part[i][j];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) err = fmaf(fabsf(q[i]), s_most[lk + i], err);
-  }
-  err += __shfl_xor_sync(kAll, err, 1);
-  err += __shfl_xor_sync(kAll, err, 2);
-  if (tid % 4 == 0 && lr < rn) a.err[(row0 + lr) * nct + ct] = err;
-  __shared__ uint8_t s_missing[kTileC];
-  if (tid % 2 == 0) s_missing[tid / 2] = missing;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int rr = ty * 4 + i, cc = tx * 4 + j;
-      if (rr < rn && cc < cn) {
-        if (s_missing[cc] && cls[(size_t)rr * a.nk + cc]) report(a.status, FA_ERR_DEVICE_CHECK);
-        a.scores[(row0 + rr) * a.nk + c0 + cc] = s_missing[cc] ? -INFINITY : acc[i][j];
+      for (int j = 0; j < n; ++j) {
+        const float mine = up ? s[j + n] : s[j], other = up ? s[j] : s[j + n];
+        s[j] = mine + __shfl_xor_sync(kAll, other, o);
       }
     }
+#pragma unroll
+    for (int o = O / 8; o > 0; o >>= 1) s[0] += __shfl_xor_sync(kAll, s[0], o);
+    const int t = lane - k, slot = (t / BPW) & 7;
+    const int from = (t % BPW) * LPB + ((slot >> 2) & 1) * O + ((slot >> 1) & 1) * (O / 2) + (slot & 1) * (O / 4);
+    const float mine = __shfl_sync(kAll, s[0], from & 31);
+    if (t >= 0 && t < kStep) out = mine;
+  }
+  return out;
 }
 
 // ------------------------------------------------------------------------------------------------ the choice
@@ -458,131 +474,147 @@ struct Group {
     if (W > 1) run = red[2 * W];
     return run;
   }
+  // The want-th largest of key [0, n), zeros not counted; want of them are there. Every warp goes over all keys itself; W > 1: each tries
+  // a threshold of its own. Done as soon as a threshold has exactly `want` keys above it.
+  __device__ __forceinline__ uint32_t kth(const uint32_t* key, int n, int want) {
+    const int lane = threadIdx.x & 31;
+    uint32_t lo = kAll, hi = 0;
+    for (int c = lane; c < n; c += 32) {
+      const uint32_t k = key[c];
+      if (k) lo = min(lo, k);
+      hi = max(hi, k);
+    }
+    lo = __reduce_min_sync(kAll, lo);
+    hi = __reduce_max_sync(kAll, hi);
+    while (lo < hi) {
+      const uint32_t span = hi - lo;
+      auto at = [&](int w) { return lo + max(1u, (uint32_t)(((uint64_t)span * (w + 1) + (W == 1 ? 1 : W - 1)) / (W == 1 ? 2 : W))); };
+      const uint32_t mine = at(warp());
+      int m = 0;
+      for (int c = lane; c < n; c += 32) m += key[c] >= mine;
+      m = __reduce_add_sync(kAll, m);
+      uint32_t exact = 0;
+      if (W == 1) {
+        if (m == want) exact = mine;
+        else if (m > want) lo = mine;
+        else hi = mine - 1;
+      } else {
+        if (lane == 0) red[flip * W + warp()] = m;
+        __syncthreads();
+        uint32_t nlo = lo, nhi = hi;
+#pragma unroll
+        for (int w = W - 1; w >= 0; --w) {
+          const int k = red[flip * W + w];
+          if (k == want) exact = at(w);
+          if (k < want) nhi = at(w) - 1;
+        }
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+          if (red[flip * W + w] >= want) nlo = at(w);
+        lo = nlo;
+        hi = nhi;
+        flip ^= 1;
+      }
+      if (exact) {
+        uint32_t t = kAll;
+        for (int c = lane; c < n; c += 32)
+          if (key[c] >= exact) t = min(t, key[c]);
+        return __reduce_min_sync(kAll, t);
+      }
+    }
+    return lo;
+  }
 };
 
-// shared memory of choose_row, in words
+// A row's shared memory, in words
 __host__ __device__ constexpr size_t row_words(int nk, int W) { return (size_t)5 * ((nk + 31) / 32) + nk + 2 * W + 2; }
+struct RowMem {
+  int nk, nw;
+  uint32_t *wc, *wp, *wx, *pa, *pb, *key;  // a bit a column: candidates, partial blocks, chosen; prefix sums (two); order of the scores
+  int* red;
+  __device__ __forceinline__ RowMem(uint32_t* sm, int n) {
+    nk = n;
+    nw = (n + 31) / 32;
+    wc = sm, wp = wc + nw, wx = wp + nw, pa = wx + nw, pb = pa + nw, key = pb + nw;
+    red = reinterpret_cast<int*>(key + nk);
+  }
+};
 
-// One row of the mask: query block r of (request b, KV head hk). err bounds the sum of the magnitudes that a score adds up; gamma
-// times it bounds the score's error. qd(e): term e of Q-, Q+ in 64 bits.
-template <int W, int D, class QFn>
-__device__ void choose_row(const SelectArgs& a, int b, int hk, int r, float err, float gamma, uint32_t* sm, QFn qd) {
+// Which blocks lie so near the border that 32 bits do not tell: `left` of `z` go in.
+struct Border {
+  float over, under;
+  int left, z;
+  __device__ __forceinline__ bool sure(uint32_t k) const { return k != 0u && value_of(k) > over; }
+  __device__ __forceinline__ bool near(uint32_t k) const {  // a NaN on either side: near
+    const float s = value_of(k);
+    return k != 0u && !(s > over) && !(s < under);
+  }
+};
+
+constexpr int kZone = 32;
+struct Zone {  // the blocks near a border, scored exactly
+  int n;
+  int col[kZone];
+  uint64_t key[kZone];
+};
+
+// A lane's terms of Q-, Q+ for exact scores, sum and rest
+template <int D>
+struct ExactQ {
+  static constexpr int V = 2 * D / 32;
+  float hi[V], lo[V];
+};
+
+// Exact score of a block, by a warp: products and sums in pairs of floats (2^-46 of the magnitudes), or where those could overflow or
+// underflow (`wide`) in 64 bits.
+template <int D>
+__device__ __forceinline__ double exact_score(const __nv_bfloat16* box, const ExactQ<D>& q, bool wide) {
+  constexpr int V = ExactQ<D>::V;
+  const uint32_t* src = reinterpret_cast<const uint32_t*>(box) + (threadIdx.x & 31) * (V / 2);
+  uint32_t v[V / 2];
+#pragma unroll
+  for (int j = 0; j < V / 2; ++j) v[j] = __ldg(src + j);
+  if (wide) {
+    double s = 0.0;
+#pragma unroll
+    for (int e = 0; e < V; ++e) s = fma((double)q.hi[e] + (double)q.lo[e], (double)((e & 1) ? bf_hi(v[e / 2]) : bf_lo(v[e / 2])), s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+    return s;
+  }
+  float s = 0.f, rest = 0.f;
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    const float y = (e & 1) ? bf_hi(v[e / 2]) : bf_lo(v[e / 2]), p = __fmul_rn(q.hi[e], y);
+    rest = __fadd_rn(rest, fmaf(q.lo[e], y, fmaf(q.hi[e], y, -p)));
+    add_exact(s, rest, p);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float os = __shfl_xor_sync(kAll, s, o), orest = __shfl_xor_sync(kAll, rest, o);
+    rest = __fadd_rn(rest, orest);
+    add_exact(s, rest, os);
+  }
+  return (double)s + (double)rest;
+}
+
+// The tables of one row from its chosen columns
+template <int W>
+__device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const RowMem& M, Group<W>& grp) {
   using G = Group<W>;
-  const int nk = a.nk, nw = (nk + 31) / 32, tid = G::tid(), lane = threadIdx.x & 31, warp = G::warp();
-  uint32_t *wc = sm, *wp = wc + nw, *wx = wp + nw, *pa = wx + nw, *pb = pa + nw, *key = pb + nw;
-  G grp{reinterpret_cast<int*>(key + nk), 0};
+  const int nk = M.nk, lane = threadIdx.x & 31;
   const uint32_t below = (1u << lane) - 1u;
-  const size_t row = ((size_t)b * a.Hkv + hk) * a.nq + r;
-  const uint8_t* cls = a.src_class + ((size_t)(a.src_Bm > 1 ? b : 0) * a.nq + r) * nk;
-  for (int i = warp; i < nw; i += W) {
-    const int c = i * 32 + lane, v = c < nk ? cls[c] : 0;
-    const uint32_t some = __ballot_sync(kAll, v != FA_BLOCK_EMPTY), part = __ballot_sync(kAll, v == FA_BLOCK_PARTIAL);
-    if (lane == 0) {
-      wc[i] = wx[i] = some;
-      wp[i] = part;
-    }
-  }
-  const int n = grp.prefix([&](int i) { return wc[i]; }, nw, pa);
-  if (n > a.keep) {
-    const float* score = a.scores + row * nk;
-    const int want = a.keep - a.first - a.last;
-    for (int i = warp; i < nw; i += W) {
-      const int c = i * 32 + lane, rank = (int)pa[i] + __popc(wc[i] & below);
-      const bool seen = (wc[i] >> lane) & 1u, always = seen && (rank < a.first || rank >= n - a.last);
-      const uint32_t w = __ballot_sync(kAll, always);
-      if (lane == 0) wx[i] = w;
-      if (c < nk) key[c] = seen && !always ? order_of(score[c]) : 0u;
-    }
-    G::sync();
-    if (want > 0) {
-      uint32_t at = 0;  // the want-th largest
-      for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
-        int m = 0;
-        for (int c = tid; c < nk; c += 32 * W) m += key[c] >= (at | bit);
-        if (grp.sum(m) >= want) at |= bit;
-      }
-      const float t = value_of(at), e2 = 2.f * fmaf(gamma, err, 1e-42f), over = t + e2, under = t - e2;
-      auto sure = [&](uint32_t k) { return k != 0u && value_of(k) > over; };
-      auto near = [&](uint32_t k) { const float s = value_of(k); return k != 0u && !(s > over) && !(s < under); };  // NaN: near
-      int m = 0, z = 0;
-      for (int c = tid; c < nk; c += 32 * W) {
-        m += sure(key[c]);
-        z += near(key[c]);
-      }
-      m = grp.sum(m);
-      z = grp.sum(z);
-      if (z == want - m) {
-        for (int i = warp; i < nw; i += W) {
-          const int c = i * 32 + lane;
-          const uint32_t w = __ballot_sync(kAll, c < nk && (sure(key[c]) || near(key[c])));
-          if (lane == 0) wx[i] |= w;
-        }
-      } else {
-        // more candidates than places: their scores in 64 bits, a warp each
-        constexpr int V = 2 * D / 32;
-        double q[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) q[i] = qd(lane * V + i);
-        uint64_t* zone = a.zone + row * nk;
-        for (int i = warp; i < nw; i += W) {
-          const int c = i * 32 + lane;
-          for (uint32_t w = __ballot_sync(kAll, c < nk && near(key[c])); w; w &= w - 1) {
-            const int cc = i * 32 + __ffs(w) - 1;
-            const __nv_bfloat16* box = box_of<D>(a, b, hk, cc);
-            double s = -INFINITY;
-            if (box) {
-              s = 0.0;
-              const uint32_t* src = reinterpret_cast<const uint32_t*>(box) + lane * (V / 2);
-#pragma unroll
-              for (int j = 0; j < V / 2; ++j) {
-                const uint32_t v = __ldg(src + j);
-                s = fma(q[2 * j], (double)bf_lo(v), s);
-                s = fma(q[2 * j + 1], (double)bf_hi(v), s);
-              }
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-            }
-            if (lane == 0) zone[cc] = order_of(s);
-          }
-        }
-        G::sync();
-        const int left = want - m;
-        uint64_t cut = 0;  // the left-th largest of them
-        for (uint64_t bit = 1ull << 63; bit; bit >>= 1) {
-          int k = 0;
-          for (int c = tid; c < nk; c += 32 * W) k += near(key[c]) && zone[c] >= (cut | bit);
-          if (grp.sum(k) >= left) cut |= bit;
-        }
-        int k = 0;
-        for (int c = tid; c < nk; c += 32 * W) k += near(key[c]) && zone[c] > cut;
-        const int ties = left - grp.sum(k);  // of those equal to it, the lowest columns
-        for (int i = warp; i < nw; i += W) {
-          const int c = i * 32 + lane;
-          const uint32_t w = __ballot_sync(kAll, c < nk && near(key[c]) && zone[c] == cut);
-          if (lane == 0) pb[i] = w;
-        }
-        grp.prefix([&](int i) { return pb[i]; }, nw, pa);
-        for (int i = warp; i < nw; i += W) {
-          const int c = i * 32 + lane;
-          bool in = false;
-          if (c < nk) in = sure(key[c]) || (near(key[c]) && (zone[c] > cut || (zone[c] == cut && (int)pa[i] + __popc(pb[i] & below) < ties)));
-          const uint32_t w = __ballot_sync(kAll, in);
-          if (lane == 0) wx[i] |= w;
-        }
-      }
-    }
-  }
-  const int np = grp.prefix([&](int i) { return wx[i] & wp[i]; }, nw, pa);
-  const int nf = grp.prefix([&](int i) { return wx[i] & ~wp[i]; }, nw, pb);
+  const int np = grp.prefix([&](int i) { return M.wx[i] & M.wp[i]; }, M.nw, M.pa);
+  const int nf = grp.prefix([&](int i) { return M.wx[i] & ~M.wp[i]; }, M.nw, M.pb);
   const MaskOut& T = a.out;
   int32_t *pi = T.kv_idx + row * nk, *fi = T.full_kv_idx + row * nk;
-  for (int i = warp; i < nw; i += W) {
+  for (int i = G::warp(); i < M.nw; i += W) {
     const int c = i * 32 + lane;
     if (c >= nk) continue;
-    const uint32_t p = wx[i] & wp[i], f = wx[i] & ~wp[i];
+    const uint32_t p = M.wx[i] & M.wp[i], f = M.wx[i] & ~M.wp[i];
     const bool in_p = (p >> lane) & 1u, in_f = (f >> lane) & 1u;
-    if (in_p) pi[pa[i] + __popc(p & below)] = c;
-    if (in_f) fi[pb[i] + __popc(f & below)] = c;
+    if (in_p) pi[M.pa[i] + __popc(p & below)] = c;
+    if (in_f) fi[M.pb[i] + __popc(f & below)] = c;
     T.block_class[row * nk + c] = in_p ? FA_BLOCK_PARTIAL : in_f ? FA_BLOCK_FULL : FA_BLOCK_EMPTY;
     if (a.nq == 1) {  // the transpose of one row
       T.q_num[row * nk + c] = in_p;
@@ -591,128 +623,243 @@ __device__ void choose_row(const SelectArgs& a, int b, int hk, int r, float err,
       T.full_q_idx[row * nk + c] = 0;
     }
   }
-  for (int x = np + tid; x < nk; x += 32 * W) pi[x] = 0;
-  for (int x = nf + tid; x < nk; x += 32 * W) fi[x] = 0;
-  if (tid == 0) {
+  for (int x = np + G::tid(); x < nk; x += 32 * W) pi[x] = 0;
+  for (int x = nf + G::tid(); x < nk; x += 32 * W) fi[x] = 0;
+  if (G::tid() == 0) {
     T.kv_num[row] = np;
     T.full_kv_num[row] = nf;
   }
 }
 
-constexpr int kRowWarps = 8;
-// A score that score_tile_kernel leaves: parts of Q added up (g at most), rounded; 32 products in a row, 8 sums; twice that for the bound's own
-__device__ __forceinline__ float tile_gamma(const SelectArgs& a) { return (float)(96 + 2 * a.parts) * 5.9604644775390625e-8f; }
-
-// W = 1: a warp a row, 8 rows a CTA; W = 8: a CTA a row
+// W = 1: a warp a row, 8 rows of one (request, KV head) a CTA, grid (ceil(nq / 8), Hkv, B). W = 8: a cluster of `ranks` CTAs a row, grid
+// (nq * ranks, Hkv, B): each scores its share of the blocks into the first one's shared memory, and that one chooses.
 template <int W, int D>
-__global__ void __launch_bounds__(kRowWarps * 32) choose_rows_kernel(const __grid_constant__ SelectArgs a) {
-  extern __shared__ uint32_t dyn[];
-  const int sub = W == 1 ? threadIdx.x >> 5 : 0, r = blockIdx.x * (kRowWarps / W) + sub, hk = blockIdx.y, b = blockIdx.z;
-  if (r >= a.nq) return;
-  const size_t row = ((size_t)b * a.Hkv + hk) * a.nq + r;
-  const int nct = (a.nk + kTileC - 1) / kTileC;
-  float err = 0.f;
-  for (int i = threadIdx.x & 31; i < nct; i += 32) {
-    const float e = a.err[row * nct + i];
-    err = e > err || e != e ? e : err;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float e = __shfl_xor_sync(kAll, err, o);
-    err = e > err || e != e ? e : err;
-  }
-  const float* pooled = a.pooled + row * a.parts * 4 * D;
-  choose_row<W, D>(a, b, hk, r, err, tile_gamma(a), dyn + sub * row_words(a.nk, W), [&](int e) {
-    double s = 0.0;
-    for (int p = 0; p < a.parts; ++p) s += (double)pooled[p * 4 * D + e] + (double)pooled[p * 4 * D + 2 * D + e];
-    return s;
-  });
-}
-
-// ------------------------------------------------------------------------------------------------ one query a request
-// A cluster of CTAs a (request, KV head): each sums the heads' queries for itself and scores its share of the blocks, and the first one chooses.
-constexpr int kTokenWarps = 8;
-
-template <int D>
-__global__ void __launch_bounds__(kTokenWarps * 32) choose_token_kernel(const __grid_constant__ SelectArgs a, int ranks) {
+__global__ void __launch_bounds__(kThreads, W == 1 ? 3 : 4) choose_kernel(const __grid_constant__ SelectArgs a, int ranks) {
   namespace cg = cooperative_groups;
+  using G = Group<W>;
+  constexpr int LPB = D / 4, V = ExactQ<D>::V;
   extern __shared__ uint32_t dyn[];
-  __shared__ float s_q[2][2 * D];  // hi, lo of Q-, Q+
-  constexpr int LPB = 2 * D / 8, BPW = 32 / LPB;  // lanes a block (16 bytes each), blocks a warp has at once
-  const int rank = blockIdx.x % ranks, hk = blockIdx.x / ranks, b = blockIdx.y;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int g = a.Hq / a.Hkv, nk = a.nk, nw = (nk + 31) / 32;
-  const size_t row = (size_t)b * a.Hkv + hk;
-  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * a.Hq + (size_t)hk * g) * D;
-  if (tid < 2 * D) {
-    const int e = tid % D;
-    float hi = 0.f, lo = 0.f;
-    for (int h = 0; h < g; ++h) {
-      const float x = __bfloat162float(q[(size_t)h * D + e]);
-      add_pair(hi, lo, tid < D ? (x > 0.f ? 0.f : x) : (x > 0.f ? x : 0.f));
+  __shared__ Zone s_zone[kWarps / W];
+  __shared__ float s_err[W == 1 ? 1 : 8 * kWarps];
+  __shared__ float s_q[W == 1 ? 1 : 2][W == 1 ? 1 : 2 * D];  // one query: sum and rest
+  const int lane = threadIdx.x & 31, gw = G::warp(), nk = a.nk;
+  const int rank = W == 1 ? 0 : blockIdx.x % ranks, hk = blockIdx.y, b = blockIdx.z;
+  const int r = W == 1 ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / ranks;
+  if (W == 1 && r >= a.nq) return;  // no barrier of the CTA from here on for W = 1
+  const bool token = W > 1 && a.q_len == 1;
+  const RowMem M(dyn + (W == 1 ? (threadIdx.x >> 5) * row_words(nk, 1) : 0), nk);
+  G grp{M.red, 0};
+  const uint32_t below = (1u << lane) - 1u;
+  const size_t row = ((size_t)b * a.Hkv + hk) * a.nq + r;
+  const Boxes<D> box(a, b, hk);
+  const uint8_t* cls = a.src_class + ((size_t)(a.src_Bm > 1 ? b : 0) * a.nq + r) * nk;
+  const int want = a.keep - a.first - a.last, g = a.Hq / a.Hkv;
+  if (W > 1 && ranks > 1) cg::this_cluster().barrier_arrive();  // every CTA of the cluster runs before the first one's memory is written
+
+  // the blocks' ids, the loads of all chunks in flight together (key [c] holds them until the score takes their place)
+  for (int i = rank * W + gw; i < M.nw; i += W * ranks) {
+    const int c = i * 32 + lane, v = c < nk ? cls[c] : 0;
+    const uint32_t some = __ballot_sync(kAll, v != FA_BLOCK_EMPTY), part = __ballot_sync(kAll, v == FA_BLOCK_PARTIAL);
+    const int id = v != FA_BLOCK_EMPTY ? box.id(c) : -2;
+    if (c < nk) M.key[c] = (uint32_t)id;
+    if (lane == 0) {
+      M.wc[i] = M.wx[i] = some;
+      M.wp[i] = part;
     }
-    s_q[0][tid] = hi;
-    s_q[1][tid] = lo;
   }
-  __syncthreads();
-  const uint8_t* cls = a.src_class + (size_t)(a.src_Bm > 1 ? b : 0) * nk;
-  float qf[8], most = 0.f;
-  const int x = lane % LPB;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) qf[i] = s_q[0][x * 8 + i];
-  for (int i = rank * kTokenWarps + warp; i < nw; i += ranks * kTokenWarps) {
-    const int c = i * 32 + lane;
-    const bool seen = c < nk && cls[c] != FA_BLOCK_EMPTY;
-    const __nv_bfloat16* mine = seen ? box_of<D>(a, b, hk, c) : nullptr;
-    if (seen && !mine) report(a.status, FA_ERR_DEVICE_CHECK);
-    float out = -INFINITY;
-    const uint32_t w = __ballot_sync(kAll, mine != nullptr);
+  if (W > 1 && ranks > 1 && rank == 0)  // the first CTA needs the bits of the others' blocks too
+    for (int i = gw; i < M.nw; i += W) {
+      if (i / W % ranks == 0) continue;
+      const int c = i * 32 + lane, v = c < nk ? cls[c] : 0;
+      const uint32_t some = __ballot_sync(kAll, v != FA_BLOCK_EMPTY), part = __ballot_sync(kAll, v == FA_BLOCK_PARTIAL);
+      if (lane == 0) {
+        M.wc[i] = M.wx[i] = some;
+        M.wp[i] = part;
+      }
+    }
+
+  // Q-, Q+ of the row: this lane's terms
+  uint64_t q[4];
+  const int e0 = lane % LPB * 8;
+  if (token) {
+    if (threadIdx.x < 2 * D) {
+      const int e = threadIdx.x % D;
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * a.Hq + (size_t)hk * g) * D + e;
+      float s = 0.f, rest = 0.f;
 #pragma unroll 4
-    for (int k = 0; k < 32; k += BPW) {
-      if (!((w >> k) & ((1u << BPW) - 1u))) continue;
-      const int j = k + lane / LPB;
-      const uint64_t src = __shfl_sync(kAll, reinterpret_cast<uint64_t>(mine), j);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (src) v = __ldg(reinterpret_cast<const uint4*>(src) + x);
-      const uint32_t t[4] = {v.x, v.y, v.z, v.w};
-      float s = 0.f, m = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = (e & 1) ? bf_hi(t[e >> 1]) : bf_lo(t[e >> 1]);
-        s = fmaf(qf[e], y, s);
-        m = fmaf(fabsf(qf[e]), fabsf(y), m);
+      for (int h = 0; h < g; ++h) {
+        const float x = __bfloat162float(src[(size_t)h * D]);
+        add_exact(s, rest, threadIdx.x < D ? min_nan(x, 0.f) : max_nan(x, 0.f));
       }
-      most = m > most || m != m ? m : most;
-#pragma unroll
-      for (int o = LPB / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-      if (BPW == 1) {
-        if (lane == k) out = s;
-      } else {
-        const float s0 = __shfl_sync(kAll, s, 0), s1 = __shfl_sync(kAll, s, 16);
-        if (lane == k) out = s0;
-        if (lane == k + 1) out = s1;
-      }
+      s_q[0][threadIdx.x] = s;
+      s_q[1][threadIdx.x] = rest;
     }
-    if (c < nk) a.scores[row * nk + c] = mine ? out : -INFINITY;
-  }
-  // a bound on the magnitudes of any block: the lanes' largest parts, added up
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most += __shfl_xor_sync(kAll, most, o);
-  if (lane == 0) a.err[row * (8 * kTokenWarps) + rank * kTokenWarps + warp] = most;
-  if (ranks > 1) {
-    cg::this_cluster().sync();
-    if (rank) return;
-  } else {
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint64_t*>(&s_q[0][e0 + 2 * i]);
+  } else {
+    float hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hi[i] = lo[i] = 0.f;
+    for (int p = 0; p < a.parts; ++p) {
+      const float4* src = reinterpret_cast<const float4*>(a.pooled + (row * a.parts + p) * 4 * D + e0);
+      const float4 u = __ldg(src), v = __ldg(src + 1);
+      const float t[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) add_exact(hi[i], lo[i], t[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = pair_of(hi[2 * i] + lo[2 * i], hi[2 * i + 1] + lo[2 * i + 1]);
   }
-  float err = 0.f;
-  for (int i = 0; i < ranks * kTokenWarps; ++i) {
-    const float e = __ldcg(a.err + row * (8 * kTokenWarps) + i);
+
+  // the scores
+  uint32_t* key = M.key;
+  if (W > 1 && ranks > 1) {
+    cg::this_cluster().barrier_wait();
+    key = cg::this_cluster().map_shared_rank(M.key, 0);
+  }
+  uint32_t most[4] = {0u, 0u, 0u, 0u};
+  for (int i = rank * W + gw; i < M.nw; i += W * ranks) {
+    const int c = i * 32 + lane, id = c < nk ? (int)M.key[c] : -2;
+    const uint32_t any = __ballot_sync(kAll, id >= 0);
+    if (id == -1) report(a.status, FA_ERR_DEVICE_CHECK);
+    float s = -INFINITY;
+    if (any && want > 0) s = score_lanes<D>(box, id, q, most);
+    if (c < nk) key[c] = id == -2 ? 0u : order_of(s);
+  }
+  float err = 0.f;  // a bound on the magnitudes that any of the scores adds up
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = floats_of(q[i]);
+    err = fmaf(fabsf(f.x), bf_lo(most[i]), err);
+    err = fmaf(fabsf(f.y), bf_hi(most[i]), err);
+  }
+#pragma unroll
+  for (int o = LPB / 2; o > 0; o >>= 1) err += __shfl_xor_sync(kAll, err, o);
+  if (LPB < 32) {
+    const float e = __shfl_xor_sync(kAll, err, LPB & 31);  // the other half's blocks
     err = e > err || e != e ? e : err;
   }
-  // Q rounded, 8 products in a row, 5 sums; twice that for the bound's own
-  choose_row<kTokenWarps, D>(a, b, hk, 0, err, 32.f * 5.9604644775390625e-8f, dyn,
-                             [&](int e) { return (double)s_q[0][e] + (double)s_q[1][e]; });
+  if (W > 1) {
+    if (lane == 0) (ranks > 1 ? cg::this_cluster().map_shared_rank(s_err, 0) : s_err)[rank * W + gw] = err;
+    if (ranks > 1) {
+      cg::this_cluster().sync();
+      if (rank) return;
+    } else {
+      __syncthreads();
+    }
+    err = 0.f;
+    for (int i = 0; i < ranks * W; ++i) err = s_err[i] > err || s_err[i] != s_err[i] ? s_err[i] : err;
+  }
+
+  const int n = grp.prefix([&](int i) { return M.wc[i]; }, M.nw, M.pa);
+  if (n > a.keep) {
+    for (int i = gw; i < M.nw; i += W) {  // always kept: not among the others
+      const int c = i * 32 + lane, place = (int)M.pa[i] + __popc(M.wc[i] & below);
+      const bool always = ((M.wc[i] >> lane) & 1u) && (place < a.first || place >= n - a.last);
+      if (always) M.key[c] = 0u;
+      const uint32_t w = __ballot_sync(kAll, always);
+      if (lane == 0) M.wx[i] = w;
+    }
+    G::sync();
+    if (want > 0) {
+      const float t = value_of(grp.kth(M.key, nk, want));
+      // Q rounded, a product in 10 steps; the rest is for the rounding of the bound itself
+      const float e2 = 2.f * fmaf(16.f * 5.9604644775390625e-8f, err, 1e-42f);
+      Border bd{t + e2, t - e2, 0, 0};
+      int m = 0, z = 0;
+      for (int c = lane; c < nk; c += 32) {
+        m += bd.sure(M.key[c]);
+        z += bd.near(M.key[c]);
+      }
+      bd.left = want - __reduce_add_sync(kAll, m);
+      bd.z = __reduce_add_sync(kAll, z);
+      const bool fits = bd.z == bd.left;
+      for (int i = gw; i < M.nw; i += W) {
+        const int c = i * 32 + lane;
+        const uint32_t k = c < nk ? M.key[c] : 0u, w = __ballot_sync(kAll, bd.sure(k) || (fits && bd.near(k)));
+        if (lane == 0) M.wx[i] |= w;
+      }
+      if (!fits) {  // 32 bits do not tell which of the blocks near the border are in: their scores exactly, a warp each
+        ExactQ<D> xq;
+        if (token) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            xq.hi[e] = s_q[0][lane * V + e];
+            xq.lo[e] = s_q[W == 1 ? 0 : 1][lane * V + e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < V; ++e) xq.hi[e] = xq.lo[e] = 0.f;
+          for (int p = 0; p < a.parts; ++p) {
+            const float* src = a.pooled + (row * a.parts + p) * 4 * D + lane * V;
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+              xq.lo[e] = __fadd_rn(xq.lo[e], __ldg(src + 2 * D + e));
+              add_exact(xq.hi[e], xq.lo[e], __ldg(src + e));
+            }
+          }
+        }
+        const bool wide = !(err > 8.7e-19f && err < 1e36f);  // 2^-60: what a product rounds off is a normal number still
+        const bool few = bd.z <= kZone;
+        Zone& Z = s_zone[W == 1 ? threadIdx.x >> 5 : 0];
+        uint64_t* zone = a.zone + row * nk;
+        if (G::tid() == 0) Z.n = 0;
+        G::sync();
+        for (int i = gw; i < M.nw; i += W) {
+          const int c = i * 32 + lane;
+          for (uint32_t w = __ballot_sync(kAll, c < nk && bd.near(M.key[c])); w; w &= w - 1) {
+            const int cc = i * 32 + __ffs(w) - 1, id = box.id(cc);
+            const uint64_t k = order_of(id >= 0 ? exact_score<D>(box.at(id), xq, wide) : -INFINITY);
+            if (lane == 0) {
+              if (few) {
+                const int slot = atomicAdd(&Z.n, 1);  // in any order: their columns are kept with them
+                Z.col[slot] = cc;
+                Z.key[slot] = k;
+              } else {
+                zone[cc] = k;
+              }
+            }
+          }
+        }
+        G::sync();
+        if (few) {
+          if (gw == 0) {
+            const bool mine = lane < bd.z;
+            const uint64_t k = mine ? Z.key[lane] : 0;
+            const int c = mine ? Z.col[lane] : 0;
+            int better = 0;
+            for (int j = 0; j < bd.z; ++j) better += Z.key[j] > k || (Z.key[j] == k && Z.col[j] < c);
+            if (mine && better < bd.left) atomicOr(&M.wx[c >> 5], 1u << (c & 31));
+          }
+        } else {
+          uint64_t cut = 0;  // the left-th largest of them
+          for (uint64_t bit = 1ull << 63; bit; bit >>= 1) {
+            int k = 0;
+            for (int c = G::tid(); c < nk; c += 32 * W) k += bd.near(M.key[c]) && zone[c] >= (cut | bit);
+            if (grp.sum(k) >= bd.left) cut |= bit;
+          }
+          int k = 0;
+          for (int c = G::tid(); c < nk; c += 32 * W) k += bd.near(M.key[c]) && zone[c] > cut;
+          const int ties = bd.left - grp.sum(k);  // of those equal to it, the lowest columns
+          for (int i = gw; i < M.nw; i += W) {
+            const int c = i * 32 + lane;
+            const uint32_t w = __ballot_sync(kAll, c < nk && bd.near(M.key[c]) && zone[c] == cut);
+            if (lane == 0) M.pb[i] = w;
+          }
+          grp.prefix([&](int i) { return M.pb[i]; }, M.nw, M.pa);
+          for (int i = gw; i < M.nw; i += W) {
+            const int c = i * 32 + lane;
+            bool in = false;
+            if (c < nk && bd.near(M.key[c])) in = zone[c] > cut || (zone[c] == cut && (int)M.pa[i] + __popc(M.pb[i] & below) < ties);
+            const uint32_t w = __ballot_sync(kAll, in);
+            if (lane == 0) M.wx[i] |= w;
+          }
+        }
+      }
+    }
+  }
+  write_row<W>(a, row, M, grp);
 }
 
 template <int D>
@@ -735,13 +882,24 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 template <int D>
 cudaError_t launch_select_d(const SelectArgs& a, const DevRule& R, cudaStream_t st) {
   cudaError_t e;
-  if (a.q_len == 1) {
-    const size_t smem = row_words(a.nk, kTokenWarps) * 4;
-    const int ranks = select_token_ranks(a.B * (int64_t)a.Hkv, a.nk);
-    if ((e = allow_smem(choose_token_kernel<D>, smem)) != cudaSuccess) return e;
+  if (a.q_len > 1) {
+    pool_kernel<D><<<dim3(a.nq, a.Hkv * a.parts, a.B), kThreads, 0, st>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int64_t rows = (int64_t)a.B * a.Hkv * a.nq;
+  // a warp a row keeps many rows in flight; one row, or rows of more than 1024 blocks (shared memory), take a CTA or more each
+  if (a.nq > 1 && a.nk <= 1024) {
+    const size_t smem = kWarps * row_words(a.nk, 1) * 4;
+    if ((e = allow_smem(choose_kernel<1, D>, smem)) != cudaSuccess) return e;
+    choose_kernel<1, D><<<dim3((a.nq + kWarps - 1) / kWarps, a.Hkv, a.B), kThreads, smem, st>>>(a, 1);
+    e = cudaGetLastError();
+  } else {
+    const size_t smem = row_words(a.nk, kWarps) * 4;
+    const int ranks = select_ranks(rows, a.nk);
+    if ((e = allow_smem(choose_kernel<kWarps, D>, smem)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.Hkv * ranks, a.B);
-    cfg.blockDim = dim3(kTokenWarps * 32);
+    cfg.gridDim = dim3(a.nq * ranks, a.Hkv, a.B);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -750,38 +908,19 @@ cudaError_t launch_select_d(const SelectArgs& a, const DevRule& R, cudaStream_t 
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, choose_token_kernel<D>, a, ranks);
+    e = cudaLaunchKernelEx(&cfg, choose_kernel<kWarps, D>, a, ranks);
   }
-  pool_kernel<D><<<dim3(a.nq, a.Hkv * a.parts, a.B), kPoolThreads, 0, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int nct = (a.nk + kTileC - 1) / kTileC, nrt = (a.nq + kTileR - 1) / kTileR;
-  score_tile_kernel<D><<<dim3(nct * nrt, a.Hkv, a.B), kTileThreads, 0, st>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // a warp a row keeps many rows in flight; rows of more than 1024 blocks would take too much shared memory that way
-  if (a.nk <= 1024) {
-    const size_t smem = kRowWarps * row_words(a.nk, 1) * 4;
-    if ((e = allow_smem(choose_rows_kernel<1, D>, smem)) != cudaSuccess) return e;
-    choose_rows_kernel<1, D><<<dim3((a.nq + kRowWarps - 1) / kRowWarps, a.Hkv, a.B), kRowWarps * 32, smem, st>>>(a);
-  } else {
-    const size_t smem = row_words(a.nk, kRowWarps) * 4;
-    if ((e = allow_smem(choose_rows_kernel<kRowWarps, D>, smem)) != cudaSuccess) return e;
-    choose_rows_kernel<kRowWarps, D><<<dim3(a.nq, a.Hkv, a.B), kRowWarps * 32, smem, st>>>(a);
-  }
-  if ((e = cudaGetLastError()) != cudaSuccess || a.nq == 1) return e;
+  if (e != cudaSuccess || a.nq == 1) return e;
   return launch_mask_transpose(R, a.out, st);
 }
 
 }  // namespace
 
-// CTAs that share the blocks of one (request, KV head)
-int select_token_ranks(int64_t rows, int32_t nk) {
+// CTAs that share the blocks of one row
+int select_ranks(int64_t rows, int32_t nk) {
   int n = 1;
-  while (n < 8 && rows * n < 2 * 152 && nk >= 128 * n) n *= 2;
+  while (n < 8 && 2 * n * rows <= 4 * 152 && nk >= 128 * n) n *= 2;
   return n;
-}
-
-size_t select_err_floats(int32_t q_len, int32_t nk) {
-  return q_len == 1 ? 8 * kTokenWarps : (nk + kTileC - 1) / kTileC;
 }
 
 cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t st) {

@@ -254,26 +254,22 @@ class BlockMask:
     def shape(self):
         return (self.c.Bm, self.c.Hm, self.c.nq, self.c.nk)
 
-    def _view(self, addr: int, n: int, dtype) -> torch.Tensor:
-        off = addr - self.buf.data_ptr()
-        nbytes = n * (4 if dtype == torch.int32 else 1)
-        return self.buf[off:off + nbytes].view(dtype)
-
     def tables(self) -> dict:
         """Device views of the tables: kv_num [Bm,Hm,nq], kv_idx [Bm,Hm,nq,nk], ..., block_class."""
         Bm, Hm, nq, nk = self.shape
-        c = self.c
-        out = {}
-        for name, n, shp in (("kv_num", Bm * Hm * nq, (Bm, Hm, nq)), ("full_kv_num", Bm * Hm * nq, (Bm, Hm, nq)),
-                             ("q_num", Bm * Hm * nk, (Bm, Hm, nk)), ("full_q_num", Bm * Hm * nk, (Bm, Hm, nk)),
-                             ("kv_idx", Bm * Hm * nq * nk, (Bm, Hm, nq, nk)),
-                             ("full_kv_idx", Bm * Hm * nq * nk, (Bm, Hm, nq, nk)),
-                             ("q_idx", Bm * Hm * nk * nq, (Bm, Hm, nk, nq)),
-                             ("full_q_idx", Bm * Hm * nk * nq, (Bm, Hm, nk, nq))):
-            out[name] = self._view(getattr(c, name), n, torch.int32).view(shp)
-        out["block_class"] = self._view(c.block_class, Bm * Hm * nq * nk, torch.uint8).view(Bm, Hm, nq, nk)
+        c, at = self.c, self.buf.data_ptr()
+        words = self.buf[:self.buf.numel() // 4 * 4].view(torch.int32)
+        first = words.storage_offset()
+
+        def view(name, m, n=1):  # [Bm, Hm, m] or [Bm, Hm, m, n], one call of the tensor library each
+            shape, step = ((Bm, Hm, m, n), (Hm * m * n, m * n, n, 1)) if n > 1 or name.endswith("idx") else ((Bm, Hm, m), (Hm * m, m, 1))
+            return words.as_strided(shape, step, first + (getattr(c, name) - at) // 4)
+
+        out = {name: view(name, m) for name, m in (("kv_num", nq), ("full_kv_num", nq), ("q_num", nk), ("full_q_num", nk))}
+        out |= {name: view(name, m, n) for name, m, n in (("kv_idx", nq, nk), ("full_kv_idx", nq, nk), ("q_idx", nk, nq), ("full_q_idx", nk, nq))}
+        out["block_class"] = self.buf.as_strided((Bm, Hm, nq, nk), (Hm * nq * nk, nq * nk, nk, 1), self.buf.storage_offset() + c.block_class - at)
         if c.row_order:
-            out["row_order"] = self._view(c.row_order, Bm * Hm * nq, torch.int32).view(Bm, Hm, nq)
+            out["row_order"] = view("row_order", nq)
         return out
 
 

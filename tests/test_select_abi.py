@@ -84,7 +84,7 @@ def test_select_blocks_refusals(fa):
     c = mask(fa)
     n = lib.fa_block_mask_select_blocks_bytes(ctypes.byref(c), 2, 2)
     wn = lib.fa_block_mask_select_blocks_workspace_bytes(ctypes.byref(c), 2, 4, 2, 64)
-    assert n >= 2 * 2 * 2 * 4 * 17 and wn >= 2 * 2 * 2 * 4 * 12
+    assert n >= 2 * 2 * 2 * 4 * 17 and wn >= 2 * 2 * 2 * 4 * 8
     assert call(n=n - 1) == fa.ERR_BUFFER and call(wn=wn - 1) == fa.ERR_BUFFER
     many = fa.make_mask_rule([("causal",), ("doc",), ("or",)] + [op for w in (1, 2, 3) for op in (("window", w), ("prefix", w), ("or",), ("and",))])
     c.rule = many
