@@ -13,6 +13,8 @@
 // all fit are they scored again in 64 bits.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "fa_launch.h"
 #include "fp8.cuh"
 
@@ -266,78 +268,122 @@ __device__ __forceinline__ void add_exact2(uint64_t& s, uint64_t& rest, uint64_t
   s = t;
 }
 
-// grid (nq, Hkv * parts, B): Q-, Q+ of one query block over Hq / Hkv / parts heads, in pairs of floats (2^-46 of the magnitudes), as the
-// sums of all values and of the positive ones -> pooled [B, Hkv, nq, parts, 2 (sum, rest), 2 D]
-template <int D>
-__global__ void __launch_bounds__(kThreads) pool_kernel(const __grid_constant__ SelectArgs a) {
-  constexpr int LPR = D / 8, kRows = kThreads / LPR, kPass = 128 / kRows;  // bq <= 128
-  __shared__ float s_sum[kWarps][2][2 * D];
-  const int r = blockIdx.x, hk = blockIdx.y / a.parts, part = blockIdx.y % a.parts, b = blockIdx.z;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = tid % LPR;
-  const int g = a.Hq / a.Hkv, h0 = hk * g + part * g / a.parts, h1 = hk * g + (part + 1) * g / a.parts;
-  const int i0 = r * a.bq, rows = min(a.bq, a.q_len - i0);
-  uint64_t all[4], pos[4], all_r[4], pos_r[4];
+// Sums of values that stay under a known size: s starts at a power of two C over twice their number times that size, so |s| >= |x| at every
+// step, and what s + x rounds off is x - ((s + x) - s), exactly: four additions where an unknown order of magnitudes takes seven.
+struct LargeSum {
+  float s[8], rest[8];  // of 8 channels
+  __device__ __forceinline__ void start() {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) all[i] = pos[i] = all_r[i] = pos_r[i] = 0;
-  for (int h = h0; h < h1; ++h) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.Hq + h) * a.q_len + i0) * D);
-    uint4 v[kPass];
+    for (int i = 0; i < 8; ++i) s[i] = rest[i] = 0.f;
+  }
+  __device__ __forceinline__ void add(int i, float x) {
+    const float t = __fadd_rn(s[i], x);
+    rest[i] = __fadd_rn(rest[i], __fsub_rn(x, __fsub_rn(t, s[i])));
+    s[i] = t;
+  }
+  __device__ __forceinline__ void grow(float was, float c) {  // another C
 #pragma unroll
-    for (int k = 0; k < kPass; ++k) {
-      const int i = tid / LPR + k * kRows;
-      v[k] = i < rows ? __ldg(src + (size_t)i * LPR + x) : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < 8; ++i) {
+      const float x = s[i] - was;  // exact: s lies within a factor of 2 of C
+      s[i] = c;
+      add(i, x);
     }
+  }
+};
+
+// grid (nq, Hkv * parts, B): Q-, Q+ of one query block over Hq / Hkv / parts heads, in pairs of floats, as the sums of all values and of the
+// positive ones -> pooled [B, Hkv, nq, parts, 2 (sum, rest), 2 D]. Of n values under m in a lane, a sum's error is at most n^2 m 2^-46 (the
+// rounding of the rests' sum), and next to nothing where they lie within 2^16 of each other. Two warps, half of the rows each: long enough a
+// way through memory that the joining at its end costs little.
+constexpr int kPoolThreads = 64, kAhead = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes a row, rows a load
+  __shared__ float s_sum[2][2 * D];
+  const int r = blockIdx.x, hk = blockIdx.y / a.parts, part = blockIdx.y % a.parts, b = blockIdx.z;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = lane % LPR;
+  const int g = a.Hq / a.Hkv, h0 = hk * g + part * g / a.parts, h1 = hk * g + (part + 1) * g / a.parts;
+  const int i0 = r * a.bq, rows = min(a.bq, a.q_len - i0), half = (rows + 1) / 2;
+  const int begin = warp * half + lane / LPR, end = min(rows, warp * half + half);
+  const int mine = end > begin ? (end - begin + RPL - 1) / RPL : 0;  // rows of a head that this lane reads
+  const int steps = (half + RPL - 1) / RPL;
+  const int shift = 34 - __clz((h1 - h0) * steps);                    // 2^shift >= 4 x the number of values
+  LargeSum all, pos;
+  float big = 0.f, under = 0.f;  // C, and what the values have to stay under
+  all.start();
+  pos.start();
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.Hq + h0) * a.q_len + i0 + begin) * D) + x;
+  for (int h = h0; h < h1; ++h, src += (size_t)a.q_len * LPR) {
+    for (int t = 0; t < steps; t += kAhead) {
+      uint4 v[kAhead];
 #pragma unroll
-    for (int k = 0; k < kPass; ++k) {
-      const uint32_t t[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+      for (int k = 0; k < kAhead; ++k) v[k] = t + k < mine ? __ldg(src + (t + k) * 32) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float u = bf_lo(t[i]), w = bf_hi(t[i]);
-        add_exact2(all[i], all_r[i], pair_of(u, w));
-        add_exact2(pos[i], pos_r[i], pair_of(max_nan(u, 0.f), max_nan(w, 0.f)));
+      for (int k = 0; k < kAhead; ++k) {
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        float y[8], top = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[e] = (e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
+          top = fmaxf(top, fabsf(y[e]));
+        }
+        if (top >= under) {  // the first values, and larger ones than those so far
+          const int ex = min((int)(__float_as_uint(top) >> 23), 253 - shift);  // top < 2^(ex - 126)
+          under = __uint_as_float((uint32_t)(ex + 1) << 23);
+          const float c = __uint_as_float((uint32_t)(ex + 1 + shift) << 23);
+          all.grow(big, c);
+          pos.grow(big, c);
+          big = c;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          all.add(e, y[e]);
+          pos.add(e, fmaxf(y[e], 0.f));
+        }
       }
     }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    all.s[e] -= big;
+    pos.s[e] -= big;
   }
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t u = __shfl_xor_sync(kAll, all[i], o), p = __shfl_xor_sync(kAll, pos[i], o);
-      all_r[i] = add2(all_r[i], __shfl_xor_sync(kAll, all_r[i], o));
-      pos_r[i] = add2(pos_r[i], __shfl_xor_sync(kAll, pos_r[i], o));
-      add_exact2(all[i], all_r[i], u);
-      add_exact2(pos[i], pos_r[i], p);
+    for (int e = 0; e < 8; ++e) {
+      const float u = __shfl_xor_sync(kAll, all.s[e], o), p = __shfl_xor_sync(kAll, pos.s[e], o);
+      all.rest[e] += __shfl_xor_sync(kAll, all.rest[e], o);
+      pos.rest[e] += __shfl_xor_sync(kAll, pos.rest[e], o);
+      add_exact(all.s[e], all.rest[e], u);
+      add_exact(pos.s[e], pos.rest[e], p);
     }
-  if (lane < LPR) {
+  if (warp == 1 && lane < LPR) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      *reinterpret_cast<uint64_t*>(&s_sum[warp][0][x * 8 + 2 * i]) = all[i];
-      *reinterpret_cast<uint64_t*>(&s_sum[warp][1][x * 8 + 2 * i]) = all_r[i];
-      *reinterpret_cast<uint64_t*>(&s_sum[warp][0][D + x * 8 + 2 * i]) = pos[i];
-      *reinterpret_cast<uint64_t*>(&s_sum[warp][1][D + x * 8 + 2 * i]) = pos_r[i];
+    for (int e = 0; e < 8; ++e) {
+      s_sum[0][x * 8 + e] = all.s[e];
+      s_sum[1][x * 8 + e] = all.rest[e];
+      s_sum[0][D + x * 8 + e] = pos.s[e];
+      s_sum[1][D + x * 8 + e] = pos.rest[e];
     }
   }
   __syncthreads();
-  float* out = a.pooled + ((((size_t)b * a.Hkv + hk) * a.nq + r) * a.parts + part) * 4 * D;
-  if (tid < D) {
-    float sum[2], rest[2];
+  if (warp == 1 || lane >= LPR) return;
+  float* out = a.pooled + ((((size_t)b * a.Hkv + hk) * a.nq + r) * a.parts + part) * 4 * D + x * 8;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      sum[k] = s_sum[0][0][k * D + tid];
-      rest[k] = s_sum[0][1][k * D + tid];
+  for (int e = 0; e < 8; ++e) {
+    all.rest[e] += s_sum[1][x * 8 + e];
+    add_exact(all.s[e], all.rest[e], s_sum[0][x * 8 + e]);
+    pos.rest[e] += s_sum[1][D + x * 8 + e];
+    add_exact(pos.s[e], pos.rest[e], s_sum[0][D + x * 8 + e]);
+    all.rest[e] -= pos.rest[e];  // Q- = all - positive
+    add_exact(all.s[e], all.rest[e], -pos.s[e]);
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) {
-        rest[k] += s_sum[w][1][k * D + tid];
-        add_exact(sum[k], rest[k], s_sum[w][0][k * D + tid]);
-      }
-    }
-    rest[0] -= rest[1];  // Q- = all - positive
-    add_exact(sum[0], rest[0], -sum[1]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {  // the rest below the sum's last bit
-      const float t = sum[k] + rest[k];
-      out[2 * D + k * D + tid] = t - t == 0.f ? rest[k] - (t - sum[k]) : 0.f;
-      out[k * D + tid] = t;
+    for (int w = 0; w < 2; ++w) {  // the rest below the sum's last bit
+      const float s = w ? pos.s[e] : all.s[e], rest = w ? pos.rest[e] : all.rest[e], t = s + rest;
+      out[w * D + e] = t;
+      out[2 * D + w * D + e] = t - t == 0.f ? rest - (t - s) : 0.f;
     }
   }
 }
@@ -367,21 +413,32 @@ struct Boxes {
 
 // A warp scores the blocks of its lanes' ids (-1: none), 16 bytes of a block a lane: 8 (d = 64: 16) blocks in flight, whose partial sums
 // meet in a butterfly that halves the blocks a lane still has with every step. q: the lane's 8 terms of Q-, Q+; most: largest magnitudes
-// of its 8 bounds so far. 4 products in a row, 6 sums.
-template <int D>
+// of its 8 bounds so far. 4 products in a row, 6 sums. AHEAD: the next blocks are loaded before these are summed (a warp that works alone).
+template <int D, bool AHEAD>
 __device__ __forceinline__ float score_lanes(const Boxes<D>& box, int id, const uint64_t (&q)[4], uint32_t (&most)[4]) {
   constexpr int LPB = D / 4, BPW = 32 / LPB, kStep = 8 * BPW;
   const int lane = threadIdx.x & 31, x = lane % LPB;
   const uint32_t have = __ballot_sync(kAll, id >= 0);
   float out = -INFINITY;
-#pragma unroll 1
-  for (int k = 0; k < 32; k += kStep) {
-    if (!((have >> k) & ((1u << kStep) - 1u))) continue;
-    uint4 v[8];
+  uint4 v[8], ahead[AHEAD ? 8 : 1];
+  auto load = [&](int k, uint4* to) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int w = __shfl_sync(kAll, id, k + j * BPW + lane / LPB);
-      v[j] = w >= 0 ? __ldg(reinterpret_cast<const uint4*>(box.at(w)) + x) : make_uint4(0, 0, 0, 0);
+      const int w = __shfl_sync(kAll, id, (k + j * BPW + lane / LPB) & 31);
+      to[j] = w >= 0 ? __ldg(reinterpret_cast<const uint4*>(box.at(w)) + x) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if (AHEAD) load(0, ahead);
+#pragma unroll 1
+  for (int k = 0; k < 32; k += kStep) {
+    if (!AHEAD && !((have >> k) & ((1u << kStep) - 1u))) continue;
+    if (AHEAD) {
+      if (!(have >> k)) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = ahead[AHEAD ? j : 0];
+      if (k + kStep < 32) load(k + kStep, ahead);
+    } else {
+      load(k, v);
     }
     float s[8];
 #pragma unroll
@@ -474,69 +531,58 @@ struct Group {
     if (W > 1) run = red[2 * W];
     return run;
   }
-  // The want-th largest of key [0, n), zeros not counted; want of them are there. Every warp goes over all keys itself; W > 1: each tries
-  // a threshold of its own. Done as soon as a threshold has exactly `want` keys above it.
-  __device__ __forceinline__ uint32_t kth(const uint32_t* key, int n, int want) {
-    const int lane = threadIdx.x & 31;
-    uint32_t lo = kAll, hi = 0;
-    for (int c = lane; c < n; c += 32) {
-      const uint32_t k = key[c];
+  __device__ __forceinline__ uint32_t least(uint32_t v) {
+    v = __reduce_min_sync(kAll, v);
+    if (W == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[flip * W + warp()] = (int)v;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) v = min(v, (uint32_t)red[flip * W + w]);
+    flip ^= 1;
+    return v;
+  }
+  // The want-th largest of the keys that `each` goes over (f(key) for each of this thread's), zeros not counted; want of them are there. A
+  // threshold with exactly `want` keys from it on ends the search early, after about log2 of their number steps.
+  template <class EachFn>
+  __device__ __forceinline__ uint32_t kth(EachFn each, int want) {
+    uint32_t lo = kAll, top = kAll;
+    each([&](uint32_t k) {
       if (k) lo = min(lo, k);
-      hi = max(hi, k);
-    }
-    lo = __reduce_min_sync(kAll, lo);
-    hi = __reduce_max_sync(kAll, hi);
+      top = min(top, ~k);
+    });
+    lo = least(lo);
+    uint32_t hi = ~least(top);
     while (lo < hi) {
-      const uint32_t span = hi - lo;
-      auto at = [&](int w) { return lo + max(1u, (uint32_t)(((uint64_t)span * (w + 1) + (W == 1 ? 1 : W - 1)) / (W == 1 ? 2 : W))); };
-      const uint32_t mine = at(warp());
+      const uint32_t mid = lo + (hi - lo) / 2 + 1;
       int m = 0;
-      for (int c = lane; c < n; c += 32) m += key[c] >= mine;
-      m = __reduce_add_sync(kAll, m);
-      uint32_t exact = 0;
-      if (W == 1) {
-        if (m == want) exact = mine;
-        else if (m > want) lo = mine;
-        else hi = mine - 1;
-      } else {
-        if (lane == 0) red[flip * W + warp()] = m;
-        __syncthreads();
-        uint32_t nlo = lo, nhi = hi;
-#pragma unroll
-        for (int w = W - 1; w >= 0; --w) {
-          const int k = red[flip * W + w];
-          if (k == want) exact = at(w);
-          if (k < want) nhi = at(w) - 1;
-        }
-#pragma unroll
-        for (int w = 0; w < W; ++w)
-          if (red[flip * W + w] >= want) nlo = at(w);
-        lo = nlo;
-        hi = nhi;
-        flip ^= 1;
-      }
-      if (exact) {
+      each([&](uint32_t k) { m += k >= mid; });
+      m = sum(m);
+      if (m == want) {
         uint32_t t = kAll;
-        for (int c = lane; c < n; c += 32)
-          if (key[c] >= exact) t = min(t, key[c]);
-        return __reduce_min_sync(kAll, t);
+        each([&](uint32_t k) {
+          if (k >= mid) t = min(t, k);
+        });
+        return least(t);
       }
+      if (m > want) lo = mid;
+      else hi = mid - 1;
     }
     return lo;
   }
 };
 
 // A row's shared memory, in words
-__host__ __device__ constexpr size_t row_words(int nk, int W) { return (size_t)5 * ((nk + 31) / 32) + nk + 2 * W + 2; }
+__host__ __device__ constexpr size_t row_words(int nk, int W) { return (size_t)5 * ((nk + 31) / 32) + nk + 2 * W + 3; }
 struct RowMem {
   int nk, nw;
   uint32_t *wc, *wp, *wx, *pa, *pb, *key;  // a bit a column: candidates, partial blocks, chosen; prefix sums (two); order of the scores
-  int* red;
+  int *total, *red;     // partial and full blocks chosen; what Group needs
   __device__ __forceinline__ RowMem(uint32_t* sm, int n) {
     nk = n;
     nw = (n + 31) / 32;
     wc = sm, wp = wc + nw, wx = wp + nw, pa = wx + nw, pb = pa + nw, key = pb + nw;
-    red = reinterpret_cast<int*>(key + nk);
+    total = reinterpret_cast<int*>(key + nk);
+    red = total + 2;
   }
 };
 
@@ -598,14 +644,138 @@ __device__ __forceinline__ double exact_score(const __nv_bfloat16* box, const Ex
   return (double)s + (double)rest;
 }
 
-// The tables of one row from its chosen columns
-template <int W>
-__device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const RowMem& M, Group<W>& grp) {
+// Chooses among the scored blocks of a row, by W warps: M.key -> M.wx, with the prefix sums and totals that write_row needs. err bounds the
+// magnitudes that a score adds up; exact_q gives the lane's terms of Q-, Q+.
+template <int W, int D, class QFn>
+__device__ void search_row(const SelectArgs& a, size_t row, const Boxes<D>& box, const RowMem& M, Zone& Z, float err, QFn exact_q) {
   using G = Group<W>;
-  const int nk = M.nk, lane = threadIdx.x & 31;
+  G grp{M.red, 0};
+  const int lane = threadIdx.x & 31, gw = G::warp(), nk = M.nk, want = a.keep - a.first - a.last;
   const uint32_t below = (1u << lane) - 1u;
+  const int n = grp.prefix([&](int i) { return M.wc[i]; }, M.nw, M.pa);
+  if (n > a.keep) {
+    for (int i = gw; i < M.nw; i += W) {  // always kept: not among the others
+      const int c = i * 32 + lane, place = (int)M.pa[i] + __popc(M.wc[i] & below);
+      const bool always = ((M.wc[i] >> lane) & 1u) && (place < a.first || place >= n - a.last);
+      if (always) M.key[c] = 0u;
+      const uint32_t w = __ballot_sync(kAll, always);
+      if (lane == 0) M.wx[i] = w;
+    }
+    G::sync();
+    if (want > 0) {
+      // this thread's keys in registers, or where there are too many in shared memory
+      constexpr int kHeld = 16;
+      uint32_t held[kHeld];
+      const bool small = nk <= kHeld * 32 * W;
+      if (small) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+          const int c = G::tid() + j * 32 * W;
+          held[j] = c < nk ? M.key[c] : 0u;
+        }
+      }
+      auto each = [&](auto f) {
+        if (small) {
+#pragma unroll
+          for (int j = 0; j < kHeld; ++j)
+            if (j * 32 * W < nk) f(held[j]);
+        } else {
+#pragma unroll 8
+          for (int c = G::tid(); c < nk; c += 32 * W) f(M.key[c]);
+        }
+      };
+      const float t = value_of(grp.kth(each, want));
+      // Q rounded, a product in 10 steps; the rest is for the rounding of the bound itself
+      const float e2 = 2.f * fmaf(16.f * 5.9604644775390625e-8f, err, 1e-42f);
+      Border bd{t + e2, t - e2, 0, 0};
+      int m = 0, z = 0;
+      each([&](uint32_t k) {
+        m += bd.sure(k);
+        z += bd.near(k);
+      });
+      bd.left = want - grp.sum(m);
+      bd.z = grp.sum(z);
+      const bool fits = bd.z == bd.left;
+      for (int i = gw; i < M.nw; i += W) {
+        const int c = i * 32 + lane;
+        const uint32_t k = c < nk ? M.key[c] : 0u, w = __ballot_sync(kAll, bd.sure(k) || (fits && bd.near(k)));
+        if (lane == 0) M.wx[i] |= w;
+      }
+      if (!fits) {  // 32 bits do not tell which of the blocks near the border are in: their scores exactly, a warp each
+        const ExactQ<D> xq = exact_q();
+        const bool wide = !(err > 8.7e-19f && err < 1e36f);  // 2^-60: what a product rounds off is a normal number still
+        const bool few = bd.z <= kZone;
+        uint64_t* zone = a.zone + row * nk;
+        if (G::tid() == 0) Z.n = 0;
+        G::sync();
+        for (int i = gw; i < M.nw; i += W) {
+          const int c = i * 32 + lane;
+          for (uint32_t w = __ballot_sync(kAll, c < nk && bd.near(M.key[c])); w; w &= w - 1) {
+            const int cc = i * 32 + __ffs(w) - 1, id = box.id(cc);
+            const uint64_t k = order_of(id >= 0 ? exact_score<D>(box.at(id), xq, wide) : -INFINITY);
+            if (lane == 0) {
+              if (few) {
+                const int slot = atomicAdd(&Z.n, 1);  // in any order: their columns are kept with them
+                Z.col[slot] = cc;
+                Z.key[slot] = k;
+              } else {
+                zone[cc] = k;
+              }
+            }
+          }
+        }
+        G::sync();
+        if (few) {
+          if (gw == 0) {
+            const bool mine = lane < bd.z;
+            const uint64_t k = mine ? Z.key[lane] : 0;
+            const int c = mine ? Z.col[lane] : 0;
+            int better = 0;
+            for (int j = 0; j < bd.z; ++j) better += Z.key[j] > k || (Z.key[j] == k && Z.col[j] < c);
+            if (mine && better < bd.left) atomicOr(&M.wx[c >> 5], 1u << (c & 31));
+          }
+        } else {
+          uint64_t cut = 0;  // the left-th largest of them
+          for (uint64_t bit = 1ull << 63; bit; bit >>= 1) {
+            int k = 0;
+            for (int c = G::tid(); c < nk; c += 32 * W) k += bd.near(M.key[c]) && zone[c] >= (cut | bit);
+            if (grp.sum(k) >= bd.left) cut |= bit;
+          }
+          int k = 0;
+          for (int c = G::tid(); c < nk; c += 32 * W) k += bd.near(M.key[c]) && zone[c] > cut;
+          const int ties = bd.left - grp.sum(k);  // of those equal to it, the lowest columns
+          for (int i = gw; i < M.nw; i += W) {
+            const int c = i * 32 + lane;
+            const uint32_t w = __ballot_sync(kAll, c < nk && bd.near(M.key[c]) && zone[c] == cut);
+            if (lane == 0) M.pb[i] = w;
+          }
+          grp.prefix([&](int i) { return M.pb[i]; }, M.nw, M.pa);
+          for (int i = gw; i < M.nw; i += W) {
+            const int c = i * 32 + lane;
+            bool in = false;
+            if (c < nk && bd.near(M.key[c])) in = zone[c] > cut || (zone[c] == cut && (int)M.pa[i] + __popc(M.pb[i] & below) < ties);
+            const uint32_t w = __ballot_sync(kAll, in);
+            if (lane == 0) M.wx[i] |= w;
+          }
+        }
+      }
+    }
+  }
   const int np = grp.prefix([&](int i) { return M.wx[i] & M.wp[i]; }, M.nw, M.pa);
   const int nf = grp.prefix([&](int i) { return M.wx[i] & ~M.wp[i]; }, M.nw, M.pb);
+  if (G::tid() == 0) {
+    M.total[0] = np;
+    M.total[1] = nf;
+  }
+  G::sync();
+}
+
+// The tables of one row from its chosen columns, by W warps
+template <int W>
+__device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const RowMem& M) {
+  using G = Group<W>;
+  const int nk = M.nk, lane = threadIdx.x & 31, np = M.total[0], nf = M.total[1];
+  const uint32_t below = (1u << lane) - 1u;
   const MaskOut& T = a.out;
   int32_t *pi = T.kv_idx + row * nk, *fi = T.full_kv_idx + row * nk;
   for (int i = G::warp(); i < M.nw; i += W) {
@@ -615,6 +785,8 @@ __device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const
     const bool in_p = (p >> lane) & 1u, in_f = (f >> lane) & 1u;
     if (in_p) pi[M.pa[i] + __popc(p & below)] = c;
     if (in_f) fi[M.pb[i] + __popc(f & below)] = c;
+    if (c >= np) pi[c] = 0;
+    if (c >= nf) fi[c] = 0;
     T.block_class[row * nk + c] = in_p ? FA_BLOCK_PARTIAL : in_f ? FA_BLOCK_FULL : FA_BLOCK_EMPTY;
     if (a.nq == 1) {  // the transpose of one row
       T.q_num[row * nk + c] = in_p;
@@ -623,18 +795,19 @@ __device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const
       T.full_q_idx[row * nk + c] = 0;
     }
   }
-  for (int x = np + G::tid(); x < nk; x += 32 * W) pi[x] = 0;
-  for (int x = nf + G::tid(); x < nk; x += 32 * W) fi[x] = 0;
   if (G::tid() == 0) {
     T.kv_num[row] = np;
     T.full_kv_num[row] = nf;
   }
 }
 
+// Rows of up to kAlone blocks, whose keys one warp holds in registers, are searched by it alone: the steps are too short for barriers.
+constexpr int kAlone = 512;
+
 // W = 1: a warp a row, 8 rows of one (request, KV head) a CTA, grid (ceil(nq / 8), Hkv, B). W = 8: a cluster of `ranks` CTAs a row, grid
 // (nq * ranks, Hkv, B): each scores its share of the blocks into the first one's shared memory, and that one chooses.
 template <int W, int D>
-__global__ void __launch_bounds__(kThreads, W == 1 ? 3 : 4) choose_kernel(const __grid_constant__ SelectArgs a, int ranks) {
+__global__ void __launch_bounds__(kThreads, W == 1 ? 2 : 4) choose_kernel(const __grid_constant__ SelectArgs a, int ranks) {
   namespace cg = cooperative_groups;
   using G = Group<W>;
   constexpr int LPB = D / 4, V = ExactQ<D>::V;
@@ -644,12 +817,10 @@ __global__ void __launch_bounds__(kThreads, W == 1 ? 3 : 4) choose_kernel(const 
   __shared__ float s_q[W == 1 ? 1 : 2][W == 1 ? 1 : 2 * D];  // one query: sum and rest
   const int lane = threadIdx.x & 31, gw = G::warp(), nk = a.nk;
   const int rank = W == 1 ? 0 : blockIdx.x % ranks, hk = blockIdx.y, b = blockIdx.z;
-  const int r = W == 1 ? blockIdx.x * kWarps + (threadIdx.x >> 5) : blockIdx.x / ranks;
-  if (W == 1 && r >= a.nq) return;  // no barrier of the CTA from here on for W = 1
+  const int r = a.nq - 1 - (W == 1 ? (int)blockIdx.x * kWarps + (int)(threadIdx.x >> 5) : (int)blockIdx.x / ranks);  // causal: long rows first
+  if (W == 1 && r < 0) return;  // no barrier of the CTA from here on for W = 1
   const bool token = W > 1 && a.q_len == 1;
   const RowMem M(dyn + (W == 1 ? (threadIdx.x >> 5) * row_words(nk, 1) : 0), nk);
-  G grp{M.red, 0};
-  const uint32_t below = (1u << lane) - 1u;
   const size_t row = ((size_t)b * a.Hkv + hk) * a.nq + r;
   const Boxes<D> box(a, b, hk);
   const uint8_t* cls = a.src_class + ((size_t)(a.src_Bm > 1 ? b : 0) * a.nq + r) * nk;
@@ -724,7 +895,7 @@ __global__ void __launch_bounds__(kThreads, W == 1 ? 3 : 4) choose_kernel(const 
     const uint32_t any = __ballot_sync(kAll, id >= 0);
     if (id == -1) report(a.status, FA_ERR_DEVICE_CHECK);
     float s = -INFINITY;
-    if (any && want > 0) s = score_lanes<D>(box, id, q, most);
+    if (any && want > 0) s = score_lanes<D, W == 1>(box, id, q, most);
     if (c < nk) key[c] = id == -2 ? 0u : order_of(s);
   }
   float err = 0.f;  // a bound on the magnitudes that any of the scores adds up
@@ -748,118 +919,45 @@ __global__ void __launch_bounds__(kThreads, W == 1 ? 3 : 4) choose_kernel(const 
     } else {
       __syncthreads();
     }
-    err = 0.f;
-    for (int i = 0; i < ranks * W; ++i) err = s_err[i] > err || s_err[i] != s_err[i] ? s_err[i] : err;
   }
-
-  const int n = grp.prefix([&](int i) { return M.wc[i]; }, M.nw, M.pa);
-  if (n > a.keep) {
-    for (int i = gw; i < M.nw; i += W) {  // always kept: not among the others
-      const int c = i * 32 + lane, place = (int)M.pa[i] + __popc(M.wc[i] & below);
-      const bool always = ((M.wc[i] >> lane) & 1u) && (place < a.first || place >= n - a.last);
-      if (always) M.key[c] = 0u;
-      const uint32_t w = __ballot_sync(kAll, always);
-      if (lane == 0) M.wx[i] = w;
+  auto search = [&](auto warps) {
+    float all = err;
+    if (W > 1) {
+      all = 0.f;
+      for (int i = 0; i < ranks * W; ++i) all = s_err[i] > all || s_err[i] != s_err[i] ? s_err[i] : all;
     }
-    G::sync();
-    if (want > 0) {
-      const float t = value_of(grp.kth(M.key, nk, want));
-      // Q rounded, a product in 10 steps; the rest is for the rounding of the bound itself
-      const float e2 = 2.f * fmaf(16.f * 5.9604644775390625e-8f, err, 1e-42f);
-      Border bd{t + e2, t - e2, 0, 0};
-      int m = 0, z = 0;
-      for (int c = lane; c < nk; c += 32) {
-        m += bd.sure(M.key[c]);
-        z += bd.near(M.key[c]);
-      }
-      bd.left = want - __reduce_add_sync(kAll, m);
-      bd.z = __reduce_add_sync(kAll, z);
-      const bool fits = bd.z == bd.left;
-      for (int i = gw; i < M.nw; i += W) {
-        const int c = i * 32 + lane;
-        const uint32_t k = c < nk ? M.key[c] : 0u, w = __ballot_sync(kAll, bd.sure(k) || (fits && bd.near(k)));
-        if (lane == 0) M.wx[i] |= w;
-      }
-      if (!fits) {  // 32 bits do not tell which of the blocks near the border are in: their scores exactly, a warp each
-        ExactQ<D> xq;
-        if (token) {
+    search_row<decltype(warps)::value, D>(a, row, box, M, s_zone[W == 1 ? threadIdx.x >> 5 : 0], all, [&]() {
+      ExactQ<D> x;
+      if (token) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          x.hi[e] = s_q[0][lane * V + e];
+          x.lo[e] = s_q[W == 1 ? 0 : 1][lane * V + e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x.hi[e] = x.lo[e] = 0.f;
+        for (int p = 0; p < a.parts; ++p) {
+          const float* src = a.pooled + (row * a.parts + p) * 4 * D + lane * V;
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            xq.hi[e] = s_q[0][lane * V + e];
-            xq.lo[e] = s_q[W == 1 ? 0 : 1][lane * V + e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < V; ++e) xq.hi[e] = xq.lo[e] = 0.f;
-          for (int p = 0; p < a.parts; ++p) {
-            const float* src = a.pooled + (row * a.parts + p) * 4 * D + lane * V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              xq.lo[e] = __fadd_rn(xq.lo[e], __ldg(src + 2 * D + e));
-              add_exact(xq.hi[e], xq.lo[e], __ldg(src + e));
-            }
-          }
-        }
-        const bool wide = !(err > 8.7e-19f && err < 1e36f);  // 2^-60: what a product rounds off is a normal number still
-        const bool few = bd.z <= kZone;
-        Zone& Z = s_zone[W == 1 ? threadIdx.x >> 5 : 0];
-        uint64_t* zone = a.zone + row * nk;
-        if (G::tid() == 0) Z.n = 0;
-        G::sync();
-        for (int i = gw; i < M.nw; i += W) {
-          const int c = i * 32 + lane;
-          for (uint32_t w = __ballot_sync(kAll, c < nk && bd.near(M.key[c])); w; w &= w - 1) {
-            const int cc = i * 32 + __ffs(w) - 1, id = box.id(cc);
-            const uint64_t k = order_of(id >= 0 ? exact_score<D>(box.at(id), xq, wide) : -INFINITY);
-            if (lane == 0) {
-              if (few) {
-                const int slot = atomicAdd(&Z.n, 1);  // in any order: their columns are kept with them
-                Z.col[slot] = cc;
-                Z.key[slot] = k;
-              } else {
-                zone[cc] = k;
-              }
-            }
-          }
-        }
-        G::sync();
-        if (few) {
-          if (gw == 0) {
-            const bool mine = lane < bd.z;
-            const uint64_t k = mine ? Z.key[lane] : 0;
-            const int c = mine ? Z.col[lane] : 0;
-            int better = 0;
-            for (int j = 0; j < bd.z; ++j) better += Z.key[j] > k || (Z.key[j] == k && Z.col[j] < c);
-            if (mine && better < bd.left) atomicOr(&M.wx[c >> 5], 1u << (c & 31));
-          }
-        } else {
-          uint64_t cut = 0;  // the left-th largest of them
-          for (uint64_t bit = 1ull << 63; bit; bit >>= 1) {
-            int k = 0;
-            for (int c = G::tid(); c < nk; c += 32 * W) k += bd.near(M.key[c]) && zone[c] >= (cut | bit);
-            if (grp.sum(k) >= bd.left) cut |= bit;
-          }
-          int k = 0;
-          for (int c = G::tid(); c < nk; c += 32 * W) k += bd.near(M.key[c]) && zone[c] > cut;
-          const int ties = bd.left - grp.sum(k);  // of those equal to it, the lowest columns
-          for (int i = gw; i < M.nw; i += W) {
-            const int c = i * 32 + lane;
-            const uint32_t w = __ballot_sync(kAll, c < nk && bd.near(M.key[c]) && zone[c] == cut);
-            if (lane == 0) M.pb[i] = w;
-          }
-          grp.prefix([&](int i) { return M.pb[i]; }, M.nw, M.pa);
-          for (int i = gw; i < M.nw; i += W) {
-            const int c = i * 32 + lane;
-            bool in = false;
-            if (c < nk && bd.near(M.key[c])) in = zone[c] > cut || (zone[c] == cut && (int)M.pa[i] + __popc(M.pb[i] & below) < ties);
-            const uint32_t w = __ballot_sync(kAll, in);
-            if (lane == 0) M.wx[i] |= w;
+            x.lo[e] = __fadd_rn(x.lo[e], __ldg(src + 2 * D + e));
+            add_exact(x.hi[e], x.lo[e], __ldg(src + e));
           }
         }
       }
-    }
+      return x;
+    });
+  };
+  if (W == 1) {
+    search(std::integral_constant<int, 1>{});
+  } else if (nk <= kAlone) {
+    if (gw == 0) search(std::integral_constant<int, 1>{});
+    __syncthreads();
+  } else {
+    search(std::integral_constant<int, W>{});
   }
-  write_row<W>(a, row, M, grp);
+  write_row<W>(a, row, M);
 }
 
 template <int D>
@@ -874,6 +972,8 @@ cudaError_t launch_bounds_d(const BoundsArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+constexpr int kWarpBlocks = 128;
+
 template <class K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
   return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
@@ -883,12 +983,12 @@ template <int D>
 cudaError_t launch_select_d(const SelectArgs& a, const DevRule& R, cudaStream_t st) {
   cudaError_t e;
   if (a.q_len > 1) {
-    pool_kernel<D><<<dim3(a.nq, a.Hkv * a.parts, a.B), kThreads, 0, st>>>(a);
+    pool_kernel<D><<<dim3(a.nq, a.Hkv * a.parts, a.B), kPoolThreads, 0, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const int64_t rows = (int64_t)a.B * a.Hkv * a.nq;
-  // a warp a row keeps many rows in flight; one row, or rows of more than 1024 blocks (shared memory), take a CTA or more each
-  if (a.nq > 1 && a.nk <= 1024) {
+  // short rows take a warp each; one row, and long ones, a CTA or more
+  if (a.nq > 1 && a.nk <= kWarpBlocks) {
     const size_t smem = kWarps * row_words(a.nk, 1) * 4;
     if ((e = allow_smem(choose_kernel<1, D>, smem)) != cudaSuccess) return e;
     choose_kernel<1, D><<<dim3((a.nq + kWarps - 1) / kWarps, a.Hkv, a.B), kThreads, smem, st>>>(a, 1);

@@ -249,6 +249,7 @@ class BlockMask:
     c: BlockMaskC
     buf: torch.Tensor
     keep: list = field(default_factory=list)   # tensors the rule points into
+    select: Optional[tuple] = None             # select_blocks: sizes asked for last, and the bytes that they need
 
     @property
     def shape(self):
@@ -256,20 +257,21 @@ class BlockMask:
 
     def tables(self) -> dict:
         """Device views of the tables: kv_num [Bm,Hm,nq], kv_idx [Bm,Hm,nq,nk], ..., block_class."""
-        Bm, Hm, nq, nk = self.shape
-        c, at = self.c, self.buf.data_ptr()
-        words = self.buf[:self.buf.numel() // 4 * 4].view(torch.int32)
-        first = words.storage_offset()
-
-        def view(name, m, n=1):  # [Bm, Hm, m] or [Bm, Hm, m, n], one call of the tensor library each
-            shape, step = ((Bm, Hm, m, n), (Hm * m * n, m * n, n, 1)) if n > 1 or name.endswith("idx") else ((Bm, Hm, m), (Hm * m, m, 1))
-            return words.as_strided(shape, step, first + (getattr(c, name) - at) // 4)
-
-        out = {name: view(name, m) for name, m in (("kv_num", nq), ("full_kv_num", nq), ("q_num", nk), ("full_q_num", nk))}
-        out |= {name: view(name, m, n) for name, m, n in (("kv_idx", nq, nk), ("full_kv_idx", nq, nk), ("q_idx", nk, nq), ("full_q_idx", nk, nq))}
-        out["block_class"] = self.buf.as_strided((Bm, Hm, nq, nk), (Hm * nq * nk, nq * nk, nk, 1), self.buf.storage_offset() + c.block_class - at)
+        c, buf = self.c, self.buf
+        b, h, nq, nk = c.Bm, c.Hm, c.nq, c.nk
+        words = buf.view(torch.int32) if buf.numel() % 4 == 0 else buf[:buf.numel() // 4 * 4].view(torch.int32)
+        view = words.as_strided                      # one call of the tensor library for each table
+        at = buf.data_ptr() - 4 * words.storage_offset()
+        g = h * nq * nk
+        row, col, rows, cols = (b, h, nq), (b, h, nk), (b, h, nq, nk), (b, h, nk, nq)
+        by_row, by_col, by_rows, by_cols = (h * nq, nq, 1), (h * nk, nk, 1), (g, nq * nk, nk, 1), (g, nq * nk, nq, 1)
+        out = {"kv_num": view(row, by_row, (c.kv_num - at) // 4), "full_kv_num": view(row, by_row, (c.full_kv_num - at) // 4),
+               "q_num": view(col, by_col, (c.q_num - at) // 4), "full_q_num": view(col, by_col, (c.full_q_num - at) // 4),
+               "kv_idx": view(rows, by_rows, (c.kv_idx - at) // 4), "full_kv_idx": view(rows, by_rows, (c.full_kv_idx - at) // 4),
+               "q_idx": view(cols, by_cols, (c.q_idx - at) // 4), "full_q_idx": view(cols, by_cols, (c.full_q_idx - at) // 4),
+               "block_class": buf.as_strided(rows, by_rows, buf.storage_offset() + c.block_class - buf.data_ptr())}
         if c.row_order:
-            out["row_order"] = view("row_order", nq)
+            out["row_order"] = view(row, by_row, (c.row_order - at) // 4)
         return out
 
 
@@ -920,12 +922,15 @@ def select_blocks(src: BlockMask, q: torch.Tensor, bounds: torch.Tensor, keep: i
     and the heads of the group. q [B,Hq,Q_LEN,d] bf16 (or [B,Hq,d] for one query); bounds [B,Hkv,nk,2,d] of key_bounds, or with a
     page_table int32 [B,max_pages] (one page a block) [P,Hkv,2,d] of kv_bounds. Returns a mask with Bm = B, Hm = Hkv for flex_decode,
     flex_decode_fp8, the forwards and flex_backward. Reuses `out`'s buffer."""
-    if q.dim() not in (3, 4) or not q.is_cuda:
+    shape = q.shape
+    if len(shape) not in (3, 4) or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [B, Hq, Q_LEN, d] or [B, Hq, d]")
     dev, bf, c = q.device, torch.bfloat16, src.c
-    B, Hq, d = q.shape[0], q.shape[1], q.shape[-1]
-    _same(q, (B, Hq, d) if q.dim() == 3 and c.q_len == 1 else (B, Hq, c.q_len, d), bf, dev, "q")
-    if src.buf.device != dev:
+    B, Hq, d = shape[0], shape[1], shape[-1]
+    n = c.q_len
+    _same(q, (B, Hq, d) if len(shape) == 3 and n == 1 else (B, Hq, n, d), bf, dev, "q")
+    buf = src.buf
+    if buf.device != dev:
         raise ValueError(f"src must be on {dev}")
     if page_table is None:
         if bounds.dim() != 5:
@@ -935,21 +940,27 @@ def select_blocks(src: BlockMask, q: torch.Tensor, bounds: torch.Tensor, keep: i
     else:
         if bounds.dim() != 4 or page_table.dim() != 2:
             raise ValueError("bounds must be [P, Hkv, 2, d] and page_table [B, max_pages]")
-        P, Hkv, max_pages = bounds.shape[0], bounds.shape[1], page_table.shape[1]
+        P, Hkv = bounds.shape[0], bounds.shape[1]
+        max_pages = page_table.shape[1]
         _same(bounds, (P, Hkv, 2, d), bf, dev, "bounds")
         _same(page_table, (B, max_pages), torch.int32, dev, "page_table")
-    _same(status, (1,), torch.int32, dev, "status")
+    if status is not None:
+        _same(status, (1,), torch.int32, dev, "status")
+    lib, ref = load(), ctypes.byref(c)
     size = _scratch(workspace, dev)
-    lib = load()
-    ref = ctypes.byref(c)
-    n = lib.fa_block_mask_select_blocks_bytes(ref, B, Hkv)
+    need = (B, Hq, Hkv, d, c.nq, c.nk, n)
+    if src.select is None or src.select[0] != need:  # a layer's call after another's asks for the same sizes
+        src.select = (need, lib.fa_block_mask_select_blocks_bytes(ref, B, Hkv),
+                      lib.fa_block_mask_select_blocks_workspace_bytes(ref, B, Hq, Hkv, d))
+    _, n, scratch = src.select
     if workspace is None:
-        size = lib.fa_block_mask_select_blocks_workspace_bytes(ref, B, Hq, Hkv, d)
-        workspace = torch.empty(max(size, 256), dtype=torch.uint8, device=dev)
-    if out is None or out.buf.numel() < n or out.buf.device != dev or out.buf is src.buf:
-        out = BlockMask(BlockMaskC(), torch.empty(max(n, 256), dtype=torch.uint8, device=dev), [])
-    _check(_call(dev, lib.fa_block_mask_select_blocks, ref, _at(q), _at(bounds), _at(page_table), P, max_pages, B, Hq, Hkv, d, keep,
-                 first, last, _at(out.buf), out.buf.numel(), ctypes.byref(out.c), _at(workspace), size, _at(status)),
+        size = scratch or 256
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    if out is None or out.buf is buf or out.buf.device != dev or out.buf.numel() < n:
+        out = BlockMask(BlockMaskC(), torch.empty(n or 256, dtype=torch.uint8, device=dev))
+    buf = out.buf
+    _check(_call(dev, lib.fa_block_mask_select_blocks, ref, q.data_ptr(), bounds.data_ptr(), _at(page_table), P, max_pages, B, Hq, Hkv, d,
+                 keep, first, last, buf.data_ptr(), buf.numel(), ctypes.byref(out.c), workspace.data_ptr(), size, _at(status)),
            "fa_block_mask_select_blocks")
     out.keep = [src]  # its rule's tensors and its document runs stay valid with it
     return out
