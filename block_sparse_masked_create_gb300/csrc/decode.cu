@@ -5,13 +5,13 @@
 // Kernel 1: one CTA per (split s, KV head hk, request b). The CTA takes pages [s*PS, (s+1)*PS) of the
 // request's visit list (its BlockMask row: full blocks, then partial blocks) and serves all g = Hq/Hkv
 // query heads of hk at once, so every K/V byte is read once. Logical block c is physical page
-// page_table[b][c] (the gather is fused: no KV copy). Each of the 4 warps streams 32-token sub-tiles of
+// page_table[b][c] (the gather is fused: no KV copy). Each of the 4 warps streams sub-tiles of 32 (short rows: 16) tokens of
 // those pages through its own 3-stage TMA ring (128-byte swizzle), computes S = Q K^T and O += P V with
 // mma.sync (the g query heads are rows of a 16-row tile), and keeps an online-softmax state; the warps'
 // states are merged in shared memory and written as (m_s, l_s, u_s) (u unnormalised, log2 domain).
 // Kernel 2: one CTA per (query head, request) merges its splits: m = max m_s, l = sum 2^(m_s-m) l_s,
-// O = sum 2^(m_s-m) u_s / l, LSE = (m + log2 l) ln 2. A request with no visible block writes O = 0,
-// LSE = -inf; a split with no block is never read.
+// O = sum 2^(m_s-m) u_s / l, LSE = (m + log2 l) ln 2. A request of one split is written by kernel 1. A
+// request with no visible block writes O = 0, LSE = -inf; a split with no block is never read.
 #include "fa_launch.h"
 
 namespace fa {
@@ -20,33 +20,38 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kDecWarps = 4;
-constexpr int kSub = 32;   // tokens per sub-tile
 constexpr int kStages = 3;
 
-template <int D>
+// SUB tokens a sub-tile. d = 128: 32 for long rows, one CTA an SM; 16 for short ones (blocks that a score chose), two CTAs, so that
+// one's start and end run under the other's loads (64 requests of 2048 chosen tokens, 8 KV heads: 120 us with 32, 104 us with 16, 90 us with
+// the pages looked up once and the one split's result written by its CTA: 5.95 TB/s).
+template <int D, int SUB>
 struct DecCfg {
-  static constexpr int kBoxBytes = kSub * 128;                 // one [32][64] bf16 box
-  static constexpr int kTileBytes = kSub * D * 2;              // K or V sub-tile
+  static constexpr int kBoxBytes = SUB * 128;                  // one [SUB][64] bf16 box
+  static constexpr int kTileBytes = SUB * D * 2;               // K or V sub-tile
   static constexpr int kStageBytes = 2 * kTileBytes;           // K + V
   static constexpr int kWarpBytes = kStages * kStageBytes;
   static constexpr int kSmem = kDecWarps * kWarpBytes + 1024 /* alignment slack */ + 256;
 };
 
-// byte offset of 16-byte chunk c16 (0 .. D/8-1) of row `row` in a TMA-written [32][D] sub-tile made of
-// D/64 boxes of [32][64] with the 128-byte swizzle (chunk ^= row & 7 inside each box)
+// byte offset of 16-byte chunk c16 (0 .. D/8-1) of row `row` in a TMA-written [SUB][D] sub-tile made of
+// D/64 boxes of [SUB][64] with the 128-byte swizzle (chunk ^= row & 7 inside each box)
+template <int kSub>
 __device__ __forceinline__ uint32_t dswz(int row, int c16) {
   return (uint32_t)((c16 >> 3) * (kSub * 128) + row * 128 + (((c16 & 7) ^ (row & 7)) << 4));
 }
 
-template <int D>
+template <int D, int kSub>
 __global__ void __launch_bounds__(kDecWarps * 32)
     decode_split_kernel(const __grid_constant__ DecArgs a, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, int PAGE) {
-  using C = DecCfg<D>;
+  using C = DecCfg<D, kSub>;
+  constexpr int kTiles = kSub / 8;  // MMA tiles of 8 tokens
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t bars[kDecWarps][kStages];
   __shared__ int32_t s_abort;
+  __shared__ int32_t s_block[kDecMaxSpan], s_page[kDecMaxSpan];  // logical block and page (-1: none) of the span's entries
 
   const int s = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -57,7 +62,17 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   const int n_full = __ldg(M.full_kv_num + mrow), n_part = __ldg(M.kv_num + mrow);
   const int n_vis = n_full + n_part;
   const int e0 = s * a.pages_per_split;
-  if (e0 >= n_vis) return;  // this split has no block: the combine never reads it
+  const size_t hq0 = (size_t)b * a.Hq + (size_t)hk * g;
+  if (e0 >= n_vis) {  // nothing here: the combine never reads it, and a request without any key is written by split 0
+    if (s == 0) {
+      for (int x = tid; x < g * D; x += kDecWarps * 32) {
+        if (a.out_f32) reinterpret_cast<float*>(a.out)[hq0 * D + x] = 0.f;
+        else reinterpret_cast<__nv_bfloat16*>(a.out)[hq0 * D + x] = __float2bfloat16_rn(0.f);
+      }
+      if (tid < g) a.lse[hq0 + tid] = -INFINITY;
+    }
+    return;
+  }
   const int e1 = min(n_vis, e0 + a.pages_per_split);
   const int32_t* full_idx = M.full_kv_idx + mrow * M.nk;
   const int32_t* part_idx = M.kv_idx + mrow * M.nk;
@@ -81,6 +96,12 @@ __global__ void __launch_bounds__(kDecWarps * 32)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  for (int k = tid; k < e1 - e0; k += kDecWarps * 32) {
+    const int e = e0 + k, c = e < n_full ? __ldg(full_idx + e) : __ldg(part_idx + e - n_full);
+    const int pid = __ldg(a.page_table + (size_t)b * a.max_pages + c);
+    s_block[k] = c;
+    s_page[k] = pid < 0 || pid >= a.n_pages_total ? -1 : pid;
+  }
   __syncthreads();
   WaitCtl wc{a.timeout_ns, a.status, &s_abort};
 
@@ -90,12 +111,10 @@ __global__ void __launch_bounds__(kDecWarps * 32)
 
   // resolve sub-tile -> (logical block c, token offset, physical page or -1)
   auto sub_info = [&](int k, int& c, int& t0, int& pid) {
-    const int u = warp + k * kDecWarps;
-    const int e = e0 + u / subs_per_page;
+    const int u = warp + k * kDecWarps, e = u / subs_per_page;
     t0 = (u % subs_per_page) * kSub;
-    c = e < n_full ? __ldg(full_idx + e) : __ldg(part_idx + e - n_full);
-    pid = __ldg(a.page_table + (size_t)b * a.max_pages + c);
-    if (pid < 0 || pid >= a.n_pages_total) pid = -1;
+    c = s_block[e];
+    pid = s_page[e];
   };
   auto issue = [&](int k) {  // lane 0 only
     int c, t0, pid;
@@ -120,7 +139,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
 
   // Q fragments: row = query head hk*g + row (rows >= g are zero)
   const int ra = lane >> 2, rb = ra + 8;
-  const __nv_bfloat16* Qb = reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * a.Hq + (size_t)hk * g) * D;
+  const __nv_bfloat16* Qb = reinterpret_cast<const __nv_bfloat16*>(a.q) + hq0 * D;
   uint32_t qf[D / 16][4];
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
@@ -161,16 +180,16 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       const int e = e0 + (warp + k * kDecWarps) / subs_per_page;
       const bool partial = e >= n_full;
       const int64_t j0 = (int64_t)c * PAGE + t0;
-      float sc[4][4];
+      float sc[kTiles][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+      for (int i = 0; i < kTiles; ++i) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
 #pragma unroll
-        for (int nt = 0; nt < 4; nt += 2) {
+        for (int nt = 0; nt < kTiles; nt += 2) {
           const int mi = lane >> 3, rr = nt * 8 + (mi >> 1) * 8 + (lane & 7), c16 = ks * 2 + (mi & 1);
           uint32_t b0, b1, b2, b3;
-          ldsm_x4(kb + dswz(rr, c16), b0, b1, b2, b3);
+          ldsm_x4(kb + dswz<kSub>(rr, c16), b0, b1, b2, b3);
           mma_bf16_16816(sc[nt], qf[ks], b0, b1);
           mma_bf16_16816(sc[nt + 1], qf[ks], b2, b3);
         }
@@ -185,7 +204,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       }
       float mx_a = -INFINITY, mx_b = -INFINITY;
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int nt = 0; nt < kTiles; ++nt) {
 #pragma unroll
         for (int e2 = 0; e2 < 4; ++e2) {
           const int col = nt * 8 + (lane & 3) * 2 + (e2 & 1);
@@ -222,10 +241,10 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       const float al_a = ex2_approx(m_a - ref_a), al_b = ex2_approx(m_b - ref_b);
       m_a = mn_a;
       m_b = mn_b;
-      uint32_t pf[2][4];
+      uint32_t pf[kSub / 16][4];
       float ps_a = 0.f, ps_b = 0.f, pe_a = 0.f, pe_b = 0.f;
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
+      for (int nt = 0; nt < kTiles; ++nt) {
         const float p0 = ex2_approx(sc[nt][0] - ref_a), p1 = ex2_approx(sc[nt][1] - ref_a);
         const float p2 = ex2_approx(sc[nt][2] - ref_b), p3 = ex2_approx(sc[nt][3] - ref_b);
         const uint32_t pa = pack_bf16x2(p0, p1), pb = pack_bf16x2(p2, p3);
@@ -248,12 +267,12 @@ __global__ void __launch_bounds__(kDecWarps * 32)
         o[dt][3] *= al_b;
       }
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
+      for (int kk = 0; kk < kSub / 16; ++kk) {
 #pragma unroll
         for (int dt = 0; dt < D / 8; dt += 2) {
           const int mi = lane >> 3, rr = kk * 16 + (mi & 1) * 8 + (lane & 7), c16 = dt + (mi >> 1);
           uint32_t b0, b1, b2, b3;
-          ldsm_x4_t(vb + dswz(rr, c16), b0, b1, b2, b3);
+          ldsm_x4_t(vb + dswz<kSub>(rr, c16), b0, b1, b2, b3);
           mma_bf16_16816(o[dt], pf[kk], b0, b1);
           mma_bf16_16816(o[dt + 1], pf[kk], b2, b3);
         }
@@ -308,6 +327,7 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   }
   __syncthreads();
   const size_t ns = (size_t)a.n_splits;
+  const bool only = n_vis <= a.pages_per_split;  // the request's one split: the result itself
   for (int x = tid; x < g * D; x += kDecWarps * 32) {
     const int row = x / D, col = x % D;
     float mm = -INFINITY;
@@ -322,13 +342,20 @@ __global__ void __launch_bounds__(kDecWarps * 32)
       l += wt * sL[w * 16 + row];
       le += wt * sLe[w * 16 + row];
     }
-    const size_t hq = (size_t)hk * g + row;
-    const size_t slot = ((size_t)b * a.Hq + hq) * ns + s;
-    a.ws_u[slot * D + col] = u;
-    if (col == 0) {
-      a.ws_m[slot] = mm;
-      a.ws_l[slot] = l;
-      a.ws_le[slot] = le;
+    if (only) {
+      const bool empty = mm == -INFINITY;
+      const float r = u * (empty ? 0.f : 1.f / l);
+      if (a.out_f32) reinterpret_cast<float*>(a.out)[(hq0 + row) * D + col] = r;
+      else reinterpret_cast<__nv_bfloat16*>(a.out)[(hq0 + row) * D + col] = __float2bfloat16_rn(r);
+      if (col == 0) a.lse[hq0 + row] = empty ? -INFINITY : (mm + __log2f(le)) * kLn2;
+    } else {
+      const size_t slot = (hq0 + row) * ns + s;
+      a.ws_u[slot * D + col] = u;
+      if (col == 0) {
+        a.ws_m[slot] = mm;
+        a.ws_l[slot] = l;
+        a.ws_le[slot] = le;
+      }
     }
   }
 }
@@ -339,6 +366,7 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const __grid_consta
   const DevMask& M = a.mask;
   const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, hq);
   const int n_vis = __ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow);
+  if (n_vis <= a.pages_per_split) return;  // written by its one split
   const int ns = (n_vis + a.pages_per_split - 1) / a.pages_per_split;
   const size_t base = ((size_t)b * a.Hq + hq) * (size_t)a.n_splits;
   const size_t obase = ((size_t)b * a.Hq + hq) * D;
@@ -364,9 +392,9 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const __grid_consta
   if (threadIdx.x == 0) a.lse[(size_t)b * a.Hq + hq] = empty ? -INFINITY : (mm + __log2f(le)) * kLn2;
 }
 
-template <int D>
+template <int D, int kSub>
 int launch_d(const DecArgs& a, cudaStream_t st) {
-  using C = DecCfg<D>;
+  using C = DecCfg<D, kSub>;
   CUtensorMap tk, tv;
   const uint64_t rows = (uint64_t)a.n_pages_total * a.Hkv * a.page;
   const uint64_t dims[2] = {(uint64_t)D, rows};
@@ -374,23 +402,24 @@ int launch_d(const DecArgs& a, cudaStream_t st) {
   const uint32_t box[2] = {64, kSub};
   if (encode_tmap_bf16(&tk, a.k_pages, 2, dims, strides, box) != 0) return FA_ERR_CUDA;
   if (encode_tmap_bf16(&tv, a.v_pages, 2, dims, strides, box) != 0) return FA_ERR_CUDA;
-  auto kern = decode_split_kernel<D>;
+  auto kern = decode_split_kernel<D, kSub>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
     return FA_ERR_CUDA;
   dim3 g1(a.n_splits, a.Hkv, a.Bz);
   kern<<<g1, kDecWarps * 32, C::kSmem, st>>>(a, tk, tv, a.page);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  dim3 g2(a.Hq, a.Bz);
-  decode_combine_kernel<D><<<g2, 128, 0, st>>>(a);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (a.n_splits > 1) {
+    decode_combine_kernel<D><<<dim3(a.Hq, a.Bz), 128, 0, st>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  }
   return FA_OK;
 }
 
 }  // namespace
 
 int launch_decode(const DecArgs& a, cudaStream_t st) {
-  if (a.d == 64) return launch_d<64>(a, st);
-  if (a.d == 128) return launch_d<128>(a, st);
+  if (a.d == 64) return launch_d<64, 32>(a, st);
+  if (a.d == 128) return a.short_rows ? launch_d<128, 16>(a, st) : launch_d<128, 32>(a, st);
   return FA_ERR_UNSUPPORTED;
 }
 

@@ -99,11 +99,13 @@ struct DecArgs {
   float* ws_le;     // [Bz, Hq, n_splits]  sum of the unrounded P (LSE)
   float* ws_u;      // [Bz, Hq, n_splits, d]
   int32_t pages_per_split, n_splits;
+  int32_t short_rows;  // the mask's rows are known to be short (bf16 pages)
   int32_t* status;
   int64_t* counters;
   uint64_t timeout_ns;
 };
 
+constexpr int kDecMaxSpan = 512;  // pages of a split at most (bf16 pages)
 int launch_decode(const DecArgs& a, cudaStream_t st);
 
 struct BwdArgs {
