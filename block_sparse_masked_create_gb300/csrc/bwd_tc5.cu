@@ -6,7 +6,8 @@
 //   delta kernel; dV = P^T dO; dP = dO V^T; dS = P (dP - D) g with g = ds'/ds; dQ = scale dS K;
 //   dK = scale dS^T Q; dK and dV summed over the query heads of a KV head, without atomics.
 //
-// dK/dV kernel: one CTA per (key block c, KV head, batch row). K_c and V_c stay in shared memory; the CTA
+// dK/dV kernel: one CTA (for chosen blocks, where a few columns are long, up to a cluster of four that share the
+// column and add their sums up) per (key block c, KV head, batch row). K_c and V_c stay in shared memory; the CTA
 // walks, for every query head of the group, the column of block c in the query-side transpose (full
 // blocks, then partial ones). Per query block, with the key rows in the TMEM lanes:
 //   S^T = K Q^T and dP^T = V dO^T (both operands in shared memory) -> TMEM;
@@ -17,6 +18,8 @@
 // Warp roles (both): warps 0-7 gradient math (warpgroup w owns 64 of the 128 columns, warp w % 4 its
 // 32 TMEM lanes), warp 8 TMA producer, warp 9 MMA issuer (one elected lane issues). Every wait is bounded;
 // a wait that runs out sets FA_ERR_TIMEOUT and the CTA drains its copies and MMAs before it exits.
+#include <cooperative_groups.h>
+
 #include <cstring>
 
 #include "fa_launch.h"
@@ -28,6 +31,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 320;
 constexpr int kGradThreads = 256;
+constexpr int kFewItems = 16;  // query blocks of a shared column for each of its CTAs at least
 
 template <int D>
 struct BwdTc5 {
@@ -50,6 +54,7 @@ struct BwdTc5 {
   static constexpr int kQOffBar = kQOffDoc + 2 * 128 * 4;
   static constexpr int kQSmem = kQOffBar + 256;
   static_assert(kKvSmem <= 232448 && kQSmem <= 232448, "shared memory per CTA");
+  static_assert(2 * 128 * (D + 4) * 4 <= kKvOffStat, "a CTA's sums of a shared column");
 };
 
 // K-major operand tile (TMA box {64, 128} with the 128-byte swizzle): k-step ks (16 elements) starts at
@@ -136,6 +141,7 @@ __device__ __forceinline__ Bits128 rule_key_bits(const DevRule& R, int64_t j, in
 
 struct Tc5BwdParams {
   BwdArgs a;
+  int ranks;  // dK/dV: CTAs (a cluster) that share a key block's column
 };
 
 // The (query head, query block, partial?) of item k of the dK/dV walk over key block c: the query heads
@@ -189,8 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) report(a.status, FA_ERR_DEVICE_CHECK);
     return;
   }
-  const int c = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
-  const int n = kv_items(a, b, hk, c);
+  const int c = P.ranks > 1 ? blockIdx.x / P.ranks : blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
+  // this CTA's items of the column: from k_first on, n of them. A cluster's CTAs that the column is too short for leave at once.
+  const int n_all = kv_items(a, b, hk, c);
+  const int ranks = P.ranks > 1 ? min(P.ranks, max(1, (n_all + kFewItems - 1) / kFewItems)) : 1;
+  const int rank = P.ranks > 1 ? blockIdx.x % P.ranks : 0;
+  if (rank >= ranks) return;
+  const int k_first = (int)((int64_t)n_all * rank / ranks), n = (int)((int64_t)n_all * (rank + 1) / ranks) - k_first;
   uint8_t* sK = smem + C::kKvOffK;
   uint8_t* sV = smem + C::kKvOffV;
   float* sStat = reinterpret_cast<float*>(smem + C::kKvOffStat);  // [2][3][128]
@@ -255,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (k >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(bar_free + st, (uint32_t)(((k >> 1) - 1) & 1), wc))) break;
       int h, r;
       bool partial;
-      kv_item(a, b, hk, c, k, h, r, partial);
+      kv_item(a, b, hk, c, k_first + k, h, r, partial);
       mbar_arrive_expect_tx_elect(bar_ld + st, 2 * C::kTile);
 #pragma unroll
       for (int x = 0; x < D / 64; ++x) {
@@ -336,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float v_n = 0.f;
     int doc_n = -1;
     auto fetch = [&](int kk) {
-      kv_item(a, b, hk, c, kk, h_n, r_n, p_n);
+      kv_item(a, b, hk, c, k_first + kk, h_n, r_n, p_n);
       const int64_t i = (int64_t)r_n * 128 + (tid & 127);
       const size_t qrow = ((size_t)b * a.Hq + h_n) * a.q_len + i;
       const bool in = i < a.q_len;
@@ -455,7 +466,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool done = __all_sync(0xFFFFFFFFu, n == 0 || mbar_wait_drain(bar_done, 0, a.timeout_ns));
     tc5_fence_after();
     const bool in = j < a.kv_len;
-    if (ok && done) {
+    if (ranks > 1) {
+      // this CTA's share of the sums into shared memory, where every copy has landed and every product has read: rows of D + 4 floats
+      const bool have = ok && done && n > 0;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        float* dst = reinterpret_cast<float*>(smem) + (size_t)which * 128 * (D + 4) + (size_t)row * (D + 4) + wg * (D / 2);
+#pragma unroll
+        for (int part = 0; part < D / 64; ++part) {
+          uint32_t v[32];
+          if (have) {
+            tc5_ld32(lane_addr + (which ? C::kKvColDK : C::kKvColDV) + wg * (D / 2) + 32 * part, v);
+            tc5_wait_ld();
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4*>(dst + 32 * part + e) =
+                have ? make_float4(__uint_as_float(v[e]), __uint_as_float(v[e + 1]), __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+    } else if (ok && done) {
       float* dVg = a.dv + (((size_t)b * a.Hkv + hk) * a.kv_len + (in ? j : 0)) * D + wg * (D / 2);
       float* dKg = a.dk + (((size_t)b * a.Hkv + hk) * a.kv_len + (in ? j : 0)) * D + wg * (D / 2);
 #pragma unroll
@@ -483,6 +514,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
+  }
+  if (ranks > 1) {
+    // the cluster's shares added up in the order of the ranks, a part of the key rows by each
+    namespace cg = cooperative_groups;
+    cg::cluster_group cl = cg::this_cluster();
+    __syncwarp();
+    cl.sync();
+    if (warp < kLoadWarp) {
+      const int rows = (128 + ranks - 1) / ranks;
+      for (int x = tid; x < 2 * rows * (D / 4); x += kGradThreads) {
+        const int which = x / (rows * (D / 4)), y = x % (rows * (D / 4)), row = rank * rows + y / (D / 4), col = y % (D / 4) * 4;
+        const int64_t j = (int64_t)c * 128 + row;
+        if (row >= 128 || j >= a.kv_len) continue;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int p = 0; p < ranks; ++p) {
+          const float* src = cl.map_shared_rank(reinterpret_cast<float*>(smem), p) + (size_t)which * 128 * (D + 4) + (size_t)row * (D + 4) + col;
+          const float4 v = *reinterpret_cast<const float4*>(src);
+          sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        const float f = which ? a.scale : 1.f;
+        float* out = (which ? a.dk : a.dv) + (((size_t)b * a.Hkv + hk) * a.kv_len + j) * D + col;
+        *reinterpret_cast<float4*>(out) = make_float4(sum.x * f, sum.y * f, sum.z * f, sum.w * f);
+      }
+    }
+    __syncwarp();
+    cl.sync();  // no CTA leaves while another reads its shared memory
   }
   tc5_fence_before();
   __syncthreads();
@@ -793,8 +851,24 @@ int launch_tc5(const BwdArgs& a, cudaStream_t st) {
     return FA_ERR_CUDA;
   kq<<<dim3(a.mask.nq, a.Hq, a.B), kThreads, C::kQSmem, st>>>(p, tq, tk, tv, tdo);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  kk<<<dim3(a.mask.nk, a.Hkv, a.B), kThreads, C::kKvSmem, st>>>(p, tq, tk, tv, tdo);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  // Chosen blocks make long columns (the first blocks of a row are in every row). A column is nq * Hq / Hkv items at most, all of them are
+  // about nq * Hq / Hkv * row_max * Hkv * B: where the longest would outlast an SM's share, a cluster shares each column. One sequence of
+  // 8192, 16 / 4 heads, 16 of up to 64 blocks: 595 us with one CTA a column, 445 with two, 425 with three, 380 with four, 468 with eight
+  // (a cluster waits for as many free SMs of one part of the GPU).
+  const int64_t share = (int64_t)a.row_max * a.Hkv * a.B;
+  p.ranks = a.row_max == 0 || share >= 152 ? 1 : share >= 76 ? 2 : 4;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.mask.nk * p.ranks, a.Hkv, a.B);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kKvSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = p.ranks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.ranks > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kk, p, tq, tk, tv, tdo) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace

@@ -396,6 +396,7 @@ static int backward_impl(const void* q, const void* k, const void* v, const void
   a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   a.score = make_score(score, KV_LEN);
   a.mask = dev_mask(bm);
+  a.row_max = bm->row_max;
   a.status = dev_status;
   a.timeout_ns = g_timeout_ns.load();
   if ((long long)B * Hq > 65535LL * 65535LL || Hq > 65535 || B > 65535) return FA_ERR_UNSUPPORTED;

@@ -434,6 +434,8 @@ GRAD = 2e-2  # of a gradient's largest magnitude, as for the backward over any m
     (1, 900, 6, 2, 64, 128, 2, 0, 0, 0.0, 300),      # rows may lose the block of their own position
     (1, 1, 2, 1, 64, 128, 1, 0, 1, 0.0, 0),
     (1, 1025, 16, 2, 128, 128, 4, 1, 2, 0.0, 0),
+    (2, 1500, 8, 4, 64, 128, 10, 1, 1, 0.0, 0),      # columns of a key block shared by two CTAs
+    (2, 1400, 8, 8, 64, 128, 10, 1, 1, 0.0, 0),      # and by none
 ])
 def test_forward_and_backward_over_the_choice(fa, B, N, Hq, Hkv, d, block, keep, first, last, cap, window):
     spec = [("causal",)] + ([("window", window), ("and",)] if window else [])
