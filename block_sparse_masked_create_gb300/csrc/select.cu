@@ -685,8 +685,8 @@ __device__ void search_row(const SelectArgs& a, size_t row, const Boxes<D>& box,
         }
       };
       const float t = value_of(grp.kth(each, want));
-      // Q rounded, a product in 10 steps; the rest is for the rounding of the bound itself
-      const float e2 = 2.f * fmaf(16.f * 5.9604644775390625e-8f, err, 1e-42f);
+      // Q rounded (twice), a product in 13 steps; the rest is for the rounding of the bound itself
+      const float e2 = 2.f * fmaf(17.f * 5.9604644775390625e-8f, err, 1e-42f);
       Border bd{t + e2, t - e2, 0, 0};
       int m = 0, z = 0;
       each([&](uint32_t k) {
@@ -960,6 +960,146 @@ __global__ void __launch_bounds__(kThreads, W == 1 ? 2 : 4) choose_kernel(const 
   write_row<W>(a, row, M);
 }
 
+// ------------------------------------------------------------------------------------------------ rows of many query blocks
+// Eight neighbouring rows a CTA: a block's bounds are read and unpacked once for all of them (a lane holds 8 of its 2 d terms, and those of Q for
+// the eight rows), and the partial sums of the eight meet in a butterfly that halves the rows a lane still has with every step. Then a
+// warp a row. A warp for each (row, block) took 2.2 times the instructions.
+constexpr int kRows = kWarps;
+
+__host__ __device__ constexpr size_t rows_pitch(int nk) { return row_words(nk, 1) | 1; }  // odd: the rows' keys of a column lie in different banks
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) choose_rows_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int LPB = D / 4, BPW = 32 / LPB, kLoads = 4 / BPW, V = ExactQ<D>::V, O = LPB / 2;
+  extern __shared__ uint32_t dyn[];
+  __shared__ Zone s_zone[kRows];
+  __shared__ float s_err[kWarps][kRows];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nk = a.nk;
+  const int hk = blockIdx.y, b = blockIdx.z, top = a.nq - 1 - (int)blockIdx.x * kRows, r = top - warp;  // causal: long rows first
+  const size_t head = ((size_t)b * a.Hkv + hk) * a.nq;
+  const Boxes<D> box(a, b, hk);
+  const RowMem M(dyn + warp * rows_pitch(nk), nk);
+  const uint8_t* cls = a.src_class + ((size_t)(a.src_Bm > 1 ? b : 0) * a.nq + max(r, 0)) * nk;
+#pragma unroll 4
+  for (int i = 0; i < M.nw; ++i) {
+    const int c = i * 32 + lane, v = r >= 0 && c < nk ? cls[c] : 0;
+    const uint32_t some = __ballot_sync(kAll, v != FA_BLOCK_EMPTY), part = __ballot_sync(kAll, v == FA_BLOCK_PARTIAL);
+    if (c < nk) M.key[c] = 0u;
+    if (lane == 0) {
+      M.wc[i] = M.wx[i] = some;
+      M.wp[i] = part;
+    }
+  }
+  // this lane's terms of Q-, Q+ for the eight rows
+  float q[kRows][8];
+  const int e0 = lane % LPB * 8;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    float hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hi[e] = lo[e] = 0.f;
+    for (int p = 0; p < a.parts && top >= k; ++p) {
+      const float4* src = reinterpret_cast<const float4*>(a.pooled + ((head + top - k) * a.parts + p) * 4 * D + e0);
+      const float4 u = __ldg(src), v = __ldg(src + 1);
+      const float t[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) add_exact(hi[e], lo[e], t[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[k][e] = hi[e] + lo[e];
+  }
+  const int slot = ((lane & O) ? 4 : 0) + ((lane & (O / 2)) ? 2 : 0) + ((lane & (O / 4)) ? 1 : 0);  // the row whose sum ends up here
+  const bool writer = lane % (LPB / 8) == 0;
+  auto meet = [&](float (&s)[kRows]) {
+#pragma unroll
+    for (int n = 4, o = O; n > 0; n >>= 1, o >>= 1) {
+      const bool up = lane & o;
+#pragma unroll
+      for (int j = 0; j < n; ++j) {
+        const float mine = up ? s[j + n] : s[j], other = up ? s[j] : s[j + n];
+        s[j] = mine + __shfl_xor_sync(kAll, other, o);
+      }
+    }
+#pragma unroll
+    for (int o = O / 8; o > 0; o >>= 1) s[0] += __shfl_xor_sync(kAll, s[0], o);
+    return s[0];
+  };
+  __syncthreads();
+  // the scores: four columns of each 32 a warp
+  uint32_t most[4] = {0u, 0u, 0u, 0u};
+  if (a.keep > a.first + a.last)
+    for (int i = 0; i < M.nw; ++i) {
+      const uint32_t any = __reduce_or_sync(kAll, lane < kRows ? dyn[lane * rows_pitch(nk) + i] : 0u) >> (warp * 4) & 15u;  // wc of the rows
+      if (!any) continue;
+      const int c0 = i * 32 + warp * 4;
+      int id = -2;
+      if (lane < 4 && ((any >> lane) & 1u)) {
+        id = box.id(c0 + lane);
+        if (id < 0) report(a.status, FA_ERR_DEVICE_CHECK);
+      }
+      uint4 v[kLoads];
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const int w = __shfl_sync(kAll, id, j * BPW + lane / LPB);
+        v[j] = w >= 0 ? __ldg(reinterpret_cast<const uint4*>(box.at(w)) + lane % LPB) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const uint32_t t[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        float s[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) s[k] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float y = (e & 1) ? bf_hi(t[e >> 1]) : bf_lo(t[e >> 1]);
+#pragma unroll
+          for (int k = 0; k < kRows; ++k) s[k] = fmaf(q[k][e], y, s[k]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) most[e] = bits_of(__hmax2(as_bf2(most[e]), __habs2(as_bf2(t[e]))));
+        const float x = meet(s);
+        const int n = j * BPW + lane / LPB, w = __shfl_sync(kAll, id, n);
+        uint32_t* row = dyn + slot * rows_pitch(nk);
+        if (writer && ((row[i] >> (warp * 4 + n)) & 1u)) row[5 * M.nw + c0 + n] = order_of(w >= 0 ? x : -INFINITY);  // M.key of that row
+      }
+    }
+  {
+    float s[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      s[k] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[k] = fmaf(fabsf(q[k][e]), (e & 1) ? bf_hi(most[e >> 1]) : bf_lo(most[e >> 1]), s[k]);
+    }
+    float err = meet(s);
+    if (LPB < 32) {
+      const float e = __shfl_xor_sync(kAll, err, LPB & 31);  // the other half's blocks
+      err = e > err || e != e ? e : err;
+    }
+    if (writer && lane < LPB) s_err[warp][slot] = err;
+  }
+  __syncthreads();
+  if (r < 0) return;
+  float err = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) err = s_err[w][warp] > err || s_err[w][warp] != s_err[w][warp] ? s_err[w][warp] : err;
+  search_row<1, D>(a, head + r, box, M, s_zone[warp], err, [&]() {
+    ExactQ<D> x;
+#pragma unroll
+    for (int e = 0; e < V; ++e) x.hi[e] = x.lo[e] = 0.f;
+    for (int p = 0; p < a.parts; ++p) {
+      const float* src = a.pooled + ((head + r) * a.parts + p) * 4 * D + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        x.lo[e] = __fadd_rn(x.lo[e], __ldg(src + 2 * D + e));
+        add_exact(x.hi[e], x.lo[e], __ldg(src + e));
+      }
+    }
+    return x;
+  });
+  write_row<1>(a, head + r, M);
+}
+
 template <int D>
 cudaError_t launch_bounds_d(const BoundsArgs& a, cudaStream_t st) {
   if (!a.page_table) {
@@ -972,7 +1112,8 @@ cudaError_t launch_bounds_d(const BoundsArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-constexpr int kWarpBlocks = 128;
+// Rows of many query blocks go eight to a CTA, as long as their keys fit in its shared memory; one row, and longer ones, take a CTA or more.
+constexpr int kRowsBlocks = 4096;
 
 template <class K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
@@ -987,11 +1128,10 @@ cudaError_t launch_select_d(const SelectArgs& a, const DevRule& R, cudaStream_t 
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const int64_t rows = (int64_t)a.B * a.Hkv * a.nq;
-  // short rows take a warp each; one row, and long ones, a CTA or more
-  if (a.nq > 1 && a.nk <= kWarpBlocks) {
-    const size_t smem = kWarps * row_words(a.nk, 1) * 4;
-    if ((e = allow_smem(choose_kernel<1, D>, smem)) != cudaSuccess) return e;
-    choose_kernel<1, D><<<dim3((a.nq + kWarps - 1) / kWarps, a.Hkv, a.B), kThreads, smem, st>>>(a, 1);
+  if (a.nq > 1 && a.nk <= kRowsBlocks) {
+    const size_t smem = kRows * rows_pitch(a.nk) * 4;
+    if ((e = allow_smem(choose_rows_kernel<D>, smem)) != cudaSuccess) return e;
+    choose_rows_kernel<D><<<dim3((a.nq + kRows - 1) / kRows, a.Hkv, a.B), kThreads, smem, st>>>(a);
     e = cudaGetLastError();
   } else {
     const size_t smem = row_words(a.nk, kWarps) * 4;
