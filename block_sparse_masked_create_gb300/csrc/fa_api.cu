@@ -1569,10 +1569,8 @@ fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, c
     return FA_ERR_INVALID_ARG;
   if (buf_bytes < P.mask.total || workspace_bytes < P.total) return FA_ERR_BUFFER_TOO_SMALL;
   DevRule R;
-  s = compile_rule_noexcept(&src->rule, &R);
+  s = compile_rule_noexcept(&src->rule, &R);  // the attention entries would refuse it later
   if (s != FA_OK) return (fa_status)s;
-  R.doc_run = src->doc_run;
-  R.doc_sorted = src->doc_sorted;
   SelectArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = q;
@@ -1645,7 +1643,7 @@ fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, c
   m.rule.batch_dependent = 1;
   m.rule.head_dependent = 1;
   m.row_max = std::min(keep, T.nk);
-  if (launch_select_blocks(a, R, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
+  if (launch_select_blocks(a, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_CUDA;
   *out = m;
   return FA_OK;
 }

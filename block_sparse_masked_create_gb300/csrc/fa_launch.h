@@ -43,8 +43,8 @@ struct MaskOut {
 };
 
 cudaError_t launch_mask_build(const DevRule& R, const MaskOut& T, cudaStream_t st);
-// the query-side transpose and the row order of T, whose row tables and classes are there; R bounds what is looked at
-cudaError_t launch_mask_transpose(const DevRule& R, const MaskOut& T, cudaStream_t st);
+// the query-side transpose and the row order of T (nq > 1), whose row tables and classes are there
+cudaError_t launch_mask_columns(const MaskOut& T, cudaStream_t st);
 cudaError_t launch_mask_stats(const MaskOut& T, int64_t* dev_out, cudaStream_t st);
 // row block q_pos[b] / S.bq of S per request b, re-classified at position q_pos[b] = R.q_offset[b] -> D with
 // Bm = Bz, nq = 1 (D's buffers laid out by the caller)
@@ -270,7 +270,7 @@ struct SelectArgs {
   int32_t* status;
 };
 int select_ranks(int64_t rows, int32_t nk);
-cudaError_t launch_select_blocks(const SelectArgs& a, const DevRule& R, cudaStream_t st);
+cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t st);
 
 // Host helpers: encode a bf16 / fp32 tensor map (dims innermost first) with 128-byte swizzle.
 int encode_tmap_bf16(CUtensorMap* m, const void* base, int rank, const uint64_t* dims,

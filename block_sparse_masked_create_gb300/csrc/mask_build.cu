@@ -562,6 +562,63 @@ __global__ void __launch_bounds__(kThreads) mask_transpose_kernel(DevRule R, Mas
   }
 }
 
+// Transpose and row order of a table whose rows and classes are there (blocks that a score chose: no rule bounds where they lie). A CTA takes 8 KV
+// blocks of one (b_m, h_m), and a warp lists the query blocks of two of them, 32 rows a ballot. One more CTA per (b_m, h_m) makes the row order.
+constexpr int kColumns = 8, kColumnRows = 1024;
+
+__global__ void __launch_bounds__(kThreads) mask_columns_kernel(MaskOut T) {
+  constexpr int kWarps = kThreads / 32, kMine = kColumns / kWarps;
+  __shared__ int s_tmp[8], s_cnt[kOrderBins];
+  __shared__ uint8_t s_cls[kColumnRows][kColumns + 4];  // rows 12 bytes apart
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nq = T.nq, nk = T.nk;
+  if (blockIdx.x == 0) {  // first: it takes longest
+    mask_row_order(T, blockIdx.y, blockIdx.z, s_cnt, s_tmp);
+    return;
+  }
+  const int c0 = ((int)blockIdx.x - 1) * kColumns;
+  const uint32_t below = (1u << lane) - 1u;
+  const size_t head = (size_t)blockIdx.z * T.Hm + blockIdx.y;
+  const uint8_t* cls = T.block_class + head * nq * nk;
+  int np[kMine], nf[kMine];
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) np[j] = nf[j] = 0;
+  for (int r0 = 0; r0 < nq; r0 += kColumnRows) {
+    const int rn = min(kColumnRows, nq - r0);
+    __syncthreads();
+    const int x0 = threadIdx.x % kColumns;
+#pragma unroll 8
+    for (int r = threadIdx.x / kColumns; r < rn; r += kThreads / kColumns)
+      if (c0 + x0 < nk) s_cls[r][x0] = cls[(size_t)(r0 + r) * nk + c0 + x0];
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int x = warp * kMine + j, c = c0 + x;
+      if (c >= nk) continue;
+      int32_t *pi = T.q_idx + (head * nk + c) * nq, *fi = T.full_q_idx + (head * nk + c) * nq;
+      for (int r = 0; r < rn; r += 32) {
+        const int v = r + lane < rn ? s_cls[r + lane][x] : 0;
+        const uint32_t p = __ballot_sync(0xFFFFFFFFu, v == FA_BLOCK_PARTIAL), f = __ballot_sync(0xFFFFFFFFu, v == FA_BLOCK_FULL);
+        if (v == FA_BLOCK_PARTIAL) pi[np[j] + __popc(p & below)] = r0 + r + lane;
+        if (v == FA_BLOCK_FULL) fi[nf[j] + __popc(f & below)] = r0 + r + lane;
+        np[j] += __popc(p);
+        nf[j] += __popc(f);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kMine; ++j) {
+    const int c = c0 + warp * kMine + j;
+    if (c >= nk) continue;
+    const size_t col = head * nk + c;
+    for (int x = np[j] + lane; x < nq; x += 32) T.q_idx[col * nq + x] = 0;
+    for (int x = nf[j] + lane; x < nq; x += 32) T.full_q_idx[col * nq + x] = 0;
+    if (lane == 0) {
+      T.q_num[col] = np[j];
+      T.full_q_num[col] = nf[j];
+    }
+  }
+}
+
 __global__ void __launch_bounds__(256) mask_stats_kernel(MaskOut T, unsigned long long* out) {
   const long long rows = (long long)T.Bm * T.Hm * T.nq;
   long long f = 0, p = 0, mx = 0;
@@ -685,12 +742,13 @@ cudaError_t launch_mask_build(const DevRule& R0, const MaskOut& T, cudaStream_t 
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
-  return launch_mask_transpose(R, T, st);
-}
-
-cudaError_t launch_mask_transpose(const DevRule& R, const MaskOut& T, cudaStream_t st) {
   dim3 g2(T.nk + (T.row_order ? 1 : 0), T.Hm, T.Bm);  // + one CTA per (b_m, h_m) for the row order
   mask_transpose_kernel<<<g2, kThreads, 0, st>>>(R, T);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_mask_columns(const MaskOut& T, cudaStream_t st) {
+  mask_columns_kernel<<<dim3(1 + (T.nk + kColumns - 1) / kColumns, T.Hm, T.Bm), kThreads, 0, st>>>(T);
   return cudaGetLastError();
 }
 

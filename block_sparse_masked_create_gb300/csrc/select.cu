@@ -975,7 +975,7 @@ __global__ void __launch_bounds__(kThreads, 2) choose_rows_kernel(const __grid_c
   __shared__ Zone s_zone[kRows];
   __shared__ float s_err[kWarps][kRows];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nk = a.nk;
-  const int hk = blockIdx.y, b = blockIdx.z, top = a.nq - 1 - (int)blockIdx.x * kRows, r = top - warp;  // causal: long rows first
+  const int hk = blockIdx.x, b = blockIdx.z, top = a.nq - 1 - (int)blockIdx.y * kRows, r = top - warp;  // causal: all heads' long rows first
   const size_t head = ((size_t)b * a.Hkv + hk) * a.nq;
   const Boxes<D> box(a, b, hk);
   const RowMem M(dyn + warp * rows_pitch(nk), nk);
@@ -995,18 +995,23 @@ __global__ void __launch_bounds__(kThreads, 2) choose_rows_kernel(const __grid_c
   const int e0 = lane % LPB * 8;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    float hi[8], lo[8];
+    const float4* src = reinterpret_cast<const float4*>(a.pooled + (head + max(top - k, 0)) * a.parts * 4 * D + e0);
+    const float4 u = __ldg(src), v = __ldg(src + 1);
+    q[k][0] = u.x, q[k][1] = u.y, q[k][2] = u.z, q[k][3] = u.w, q[k][4] = v.x, q[k][5] = v.y, q[k][6] = v.z, q[k][7] = v.w;
+    if (a.parts > 1) {
+      float lo[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) hi[e] = lo[e] = 0.f;
-    for (int p = 0; p < a.parts && top >= k; ++p) {
-      const float4* src = reinterpret_cast<const float4*>(a.pooled + ((head + top - k) * a.parts + p) * 4 * D + e0);
-      const float4 u = __ldg(src), v = __ldg(src + 1);
-      const float t[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+      for (int e = 0; e < 8; ++e) lo[e] = 0.f;
+      for (int p = 1; p < a.parts; ++p) {
+        src += D;
+        const float4 u = __ldg(src), v = __ldg(src + 1);
+        const float t[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) add_exact(hi[e], lo[e], t[e]);
+        for (int e = 0; e < 8; ++e) add_exact(q[k][e], lo[e], t[e]);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[k][e] += lo[e];
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[k][e] = hi[e] + lo[e];
   }
   const int slot = ((lane & O) ? 4 : 0) + ((lane & (O / 2)) ? 2 : 0) + ((lane & (O / 4)) ? 1 : 0);  // the row whose sum ends up here
   const bool writer = lane % (LPB / 8) == 0;
@@ -1025,27 +1030,38 @@ __global__ void __launch_bounds__(kThreads, 2) choose_rows_kernel(const __grid_c
     return s[0];
   };
   __syncthreads();
-  // the scores: four columns of each 32 a warp
+  // the scores: four columns of each 32 a warp, the next ones' loads under the sums
   uint32_t most[4] = {0u, 0u, 0u, 0u};
-  if (a.keep > a.first + a.last)
-    for (int i = 0; i < M.nw; ++i) {
+  int id = -2;
+  uint4 v[kLoads];
+  auto fetch = [&](int i) {  // the next 32 columns from the i-th on in which any of the rows has one of this warp's four
+    for (; i < M.nw; ++i) {
       const uint32_t any = __reduce_or_sync(kAll, lane < kRows ? dyn[lane * rows_pitch(nk) + i] : 0u) >> (warp * 4) & 15u;  // wc of the rows
       if (!any) continue;
-      const int c0 = i * 32 + warp * 4;
-      int id = -2;
+      id = -2;
       if (lane < 4 && ((any >> lane) & 1u)) {
-        id = box.id(c0 + lane);
+        id = box.id(i * 32 + warp * 4 + lane);
         if (id < 0) report(a.status, FA_ERR_DEVICE_CHECK);
       }
-      uint4 v[kLoads];
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
         const int w = __shfl_sync(kAll, id, j * BPW + lane / LPB);
         v[j] = w >= 0 ? __ldg(reinterpret_cast<const uint4*>(box.at(w)) + lane % LPB) : make_uint4(0, 0, 0, 0);
       }
+      break;
+    }
+    return i;
+  };
+  if (a.keep > a.first + a.last)
+    for (int i = fetch(0); i < M.nw;) {
+      const int at = i, c0 = i * 32 + warp * 4, now = id;
+      uint4 u[kLoads];
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) u[j] = v[j];
+      i = fetch(i + 1);
 #pragma unroll
       for (int j = 0; j < kLoads; ++j) {
-        const uint32_t t[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+        const uint32_t t[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
         float s[kRows];
 #pragma unroll
         for (int k = 0; k < kRows; ++k) s[k] = 0.f;
@@ -1058,9 +1074,9 @@ __global__ void __launch_bounds__(kThreads, 2) choose_rows_kernel(const __grid_c
 #pragma unroll
         for (int e = 0; e < 4; ++e) most[e] = bits_of(__hmax2(as_bf2(most[e]), __habs2(as_bf2(t[e]))));
         const float x = meet(s);
-        const int n = j * BPW + lane / LPB, w = __shfl_sync(kAll, id, n);
+        const int n = j * BPW + lane / LPB, w = __shfl_sync(kAll, now, n);
         uint32_t* row = dyn + slot * rows_pitch(nk);
-        if (writer && ((row[i] >> (warp * 4 + n)) & 1u)) row[5 * M.nw + c0 + n] = order_of(w >= 0 ? x : -INFINITY);  // M.key of that row
+        if (writer && ((row[at] >> (warp * 4 + n)) & 1u)) row[5 * M.nw + c0 + n] = order_of(w >= 0 ? x : -INFINITY);  // M.key of that row
       }
     }
   {
@@ -1121,7 +1137,7 @@ cudaError_t allow_smem(K kernel, size_t bytes) {
 }
 
 template <int D>
-cudaError_t launch_select_d(const SelectArgs& a, const DevRule& R, cudaStream_t st) {
+cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t st) {
   cudaError_t e;
   if (a.q_len > 1) {
     pool_kernel<D><<<dim3(a.nq, a.Hkv * a.parts, a.B), kPoolThreads, 0, st>>>(a);
@@ -1131,7 +1147,7 @@ cudaError_t launch_select_d(const SelectArgs& a, const DevRule& R, cudaStream_t 
   if (a.nq > 1 && a.nk <= kRowsBlocks) {
     const size_t smem = kRows * rows_pitch(a.nk) * 4;
     if ((e = allow_smem(choose_rows_kernel<D>, smem)) != cudaSuccess) return e;
-    choose_rows_kernel<D><<<dim3((a.nq + kRows - 1) / kRows, a.Hkv, a.B), kThreads, smem, st>>>(a);
+    choose_rows_kernel<D><<<dim3(a.Hkv, (a.nq + kRows - 1) / kRows, a.B), kThreads, smem, st>>>(a);
     e = cudaGetLastError();
   } else {
     const size_t smem = row_words(a.nk, kWarps) * 4;
@@ -1151,7 +1167,7 @@ cudaError_t launch_select_d(const SelectArgs& a, const DevRule& R, cudaStream_t 
     e = cudaLaunchKernelEx(&cfg, choose_kernel<kWarps, D>, a, ranks);
   }
   if (e != cudaSuccess || a.nq == 1) return e;
-  return launch_mask_transpose(R, a.out, st);
+  return launch_mask_columns(a.out, st);
 }
 
 }  // namespace
@@ -1167,8 +1183,8 @@ cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t st) {
   return a.d == 64 ? launch_bounds_d<64>(a, st) : launch_bounds_d<128>(a, st);
 }
 
-cudaError_t launch_select_blocks(const SelectArgs& a, const DevRule& R, cudaStream_t st) {
-  return a.d == 64 ? launch_select_d<64>(a, R, st) : launch_select_d<128>(a, R, st);
+cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t st) {
+  return a.d == 64 ? launch_select_d<64>(a, st) : launch_select_d<128>(a, st);
 }
 
 }  // namespace fa
