@@ -463,8 +463,9 @@ __global__ void __launch_bounds__(kThreads) mask_classify_kernel(DevRule R, Mask
 // the histogram is static shared memory of every CTA of that launch, hence kept small.
 constexpr int kOrderBins = 2049;
 
+template <class LenFn>  // visited length of a row
 __device__ void mask_row_order(const MaskOut& T, int hm, int bm, int* s_cnt /* [kOrderBins] */,
-                               int* s_tmp /* [8] */) {
+                               int* s_tmp /* [8] */, LenFn len) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int nq = T.nq, nk = T.nk;
   const size_t base = ((size_t)bm * T.Hm + hm) * nq;
@@ -473,7 +474,6 @@ __device__ void mask_row_order(const MaskOut& T, int hm, int bm, int* s_cnt /* [
     for (int x = tid; x < nq; x += kThreads) order[x] = nq - 1 - x;
     return;
   }
-  auto len = [&](int r) { return __ldg(T.kv_num + base + r) + __ldg(T.full_kv_num + base + r); };
   for (int x = tid; x <= nk; x += kThreads) s_cnt[x] = 0;
   __syncthreads();
   for (int r = tid; r < nq; r += kThreads) atomicAdd(&s_cnt[nk - len(r)], 1);
@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(kThreads) mask_transpose_kernel(DevRule R, Mas
   __shared__ int s_tmp[8];
   if (c == nk) {  // the extra CTA: the row order
     __shared__ int s_cnt[kOrderBins];
-    mask_row_order(T, hm, bm, s_cnt, s_tmp);
+    const size_t base = ((size_t)bm * T.Hm + hm) * nq;
+    mask_row_order(T, hm, bm, s_cnt, s_tmp, [&](int r) { return __ldg(T.kv_num + base + r) + __ldg(T.full_kv_num + base + r); });
     return;
   }
   __shared__ Hull s_h;  // the query blocks that can reach this KV block; the class matrix is empty elsewhere
@@ -569,10 +570,19 @@ constexpr int kColumns = 8, kColumnRows = 1024;
 __global__ void __launch_bounds__(kThreads) mask_columns_kernel(MaskOut T) {
   constexpr int kWarps = kThreads / 32, kMine = kColumns / kWarps;
   __shared__ int s_tmp[8], s_cnt[kOrderBins];
-  __shared__ uint8_t s_cls[kColumnRows][kColumns + 4];  // rows 12 bytes apart
+  __shared__ __align__(16) uint8_t s_cls[kColumnRows][kColumns + 4];  // rows 12 bytes apart
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nq = T.nq, nk = T.nk;
   if (blockIdx.x == 0) {  // first: it takes longest
-    mask_row_order(T, blockIdx.y, blockIdx.z, s_cnt, s_tmp);
+    const size_t base = ((size_t)blockIdx.z * T.Hm + blockIdx.y) * nq;
+    auto len = [&](int r) { return __ldg(T.kv_num + base + r) + __ldg(T.full_kv_num + base + r); };
+    if (nq <= kColumnRows) {  // the lengths at hand: the rows are placed one 32 after another
+      int* s_len = reinterpret_cast<int*>(&s_cls[0][0]);
+      for (int r = threadIdx.x; r < nq; r += kThreads) s_len[r] = len(r);
+      __syncthreads();
+      mask_row_order(T, blockIdx.y, blockIdx.z, s_cnt, s_tmp, [&](int r) { return s_len[r]; });
+    } else {
+      mask_row_order(T, blockIdx.y, blockIdx.z, s_cnt, s_tmp, len);
+    }
     return;
   }
   const int c0 = ((int)blockIdx.x - 1) * kColumns;
