@@ -1537,7 +1537,8 @@ static int select_blocks_plan(const fa_block_mask* src, int32_t B, int32_t Hq, i
   if (s != FA_OK) return s;
   const size_t rows = (size_t)B * Hkv * src->nq;
   // one query block's sums are split among its heads where there are fewer (request, KV head, query block)s than two for each SM
-  P->parts = src->q_len == 1 ? 0 : rows < 2 * 152 ? Hq / Hkv : 1;
+  // (and among divisions of 8 heads at most)
+  P->parts = src->q_len == 1 ? 0 : rows < 2 * 152 ? Hq / Hkv : (Hq / Hkv + 7) / 8;
   P->off_zone = align256(rows * P->parts * 4 * d * sizeof(float));
   P->total = P->off_zone + align256(rows * src->nk * sizeof(uint64_t));
   return FA_OK;

@@ -268,37 +268,82 @@ __device__ __forceinline__ void add_exact2(uint64_t& s, uint64_t& rest, uint64_t
   s = t;
 }
 
-// Sums of values that stay under a known size: s starts at a power of two C over twice their number times that size, so |s| >= |x| at every
-// step, and what s + x rounds off is x - ((s + x) - s), exactly: four additions where an unknown order of magnitudes takes seven.
-struct LargeSum {
-  float s[8], rest[8];  // of 8 channels
+// Sums of bf16 in whole numbers. For |x| < 2^E, x + C with C = 1.5 * 2^(E + 1) lies in C's binade, so its bits are C's plus x in units of
+// 2^(E - 22): an integer sum of the bits is exact, and with max(x, 0) + C = max(x + C, C) the sum of the positive ones takes two
+// operations more. What x + C rounds off (of magnitudes under 2^(E - 14)) is summed apart, where there is any. At most 256 values a lane.
+struct BitSums {
+  uint32_t all[8], pos[8];        // sums of the bits, C's own left in
+  float rest[8], rest_pos[8];     // what was rounded off
+  float c, under;                 // C and 2^E
+  int n;                          // values so far
   __device__ __forceinline__ void start() {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = rest[i] = 0.f;
+    for (int i = 0; i < 8; ++i) {
+      all[i] = pos[i] = 0u;
+      rest[i] = rest_pos[i] = 0.f;
+    }
+    c = under = 0.f;
+    n = 0;
   }
-  __device__ __forceinline__ void add(int i, float x) {
-    const float t = __fadd_rn(s[i], x);
-    rest[i] = __fadd_rn(rest[i], __fsub_rn(x, __fsub_rn(t, s[i])));
-    s[i] = t;
-  }
-  __device__ __forceinline__ void grow(float was, float c) {  // another C
+  __device__ __forceinline__ float unit() const { return under * 2.384185791015625e-7f; }  // 2^(E - 22)
+  // the sums as whole numbers of units, and another E for values up to `top`
+  __device__ __forceinline__ void grow(float top) {
+    const int ex = min((int)(__float_as_uint(top) >> 23), 251);  // top < 2^(ex - 126)
+    const float to = __uint_as_float((uint32_t)(ex + 2) << 23), u = unit();
+    const int k = min(31, (int)(__float_as_uint(to) >> 23) - (int)(__float_as_uint(under) >> 23));  // units are 2^k of the old ones
+    const uint32_t was = __float_as_uint(c) * (uint32_t)n;
+    under = to;
+    c = 3.f * to;
+    const uint32_t now = __float_as_uint(c) * (uint32_t)n;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float x = s[i] - was;  // exact: s lies within a factor of 2 of C
-      s[i] = c;
-      add(i, x);
+      const int a = (int)(all[i] - was), p = (int)(pos[i] - was);
+      rest[i] += (float)(a - (a >> k << k)) * u;
+      rest_pos[i] += (float)(p - (p >> k << k)) * u;
+      all[i] = (uint32_t)(a >> k) + now;
+      pos[i] = (uint32_t)(p >> k) + now;
     }
+  }
+  __device__ __forceinline__ void add(uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float y[8], t[8];
+    bool off = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = (e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
+      t[e] = __fadd_rn(y[e], c);
+      off = off || __fsub_rn(t[e], c) != y[e];
+      all[e] += __float_as_uint(t[e]);
+      pos[e] += __float_as_uint(fmaxf(t[e], c));
+    }
+    if (off) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float d = __fsub_rn(y[e], __fsub_rn(t[e], c));
+        rest[e] += d;
+        rest_pos[e] += y[e] > 0.f ? d : 0.f;
+      }
+    }
+    ++n;
+  }
+  // sum + rest, of all and of the positive values
+  __device__ __forceinline__ void sums(int i, float& s, float& r, float& sp, float& rp) const {
+    const uint32_t own = __float_as_uint(c) * (uint32_t)n;
+    const int a = (int)(all[i] - own), p = (int)(pos[i] - own);
+    const float u = unit();
+    s = (float)(a >> 8) * (256.f * u);   // 22 + 8 bits: both parts are exact
+    r = rest[i] + (float)(a & 255) * u;
+    sp = (float)(p >> 8) * (256.f * u);
+    rp = rest_pos[i] + (float)(p & 255) * u;
   }
 };
 
-// grid (nq, Hkv * parts, B): Q-, Q+ of one query block over Hq / Hkv / parts heads, in pairs of floats, as the sums of all values and of the
-// positive ones -> pooled [B, Hkv, nq, parts, 2 (sum, rest), 2 D]. Of n values under m in a lane, a sum's error is at most n^2 m 2^-46 (the
-// rounding of the rests' sum), and next to nothing where they lie within 2^16 of each other. Two warps, half of the rows each: long enough a
-// way through memory that the joining at its end costs little.
+// grid (nq, Hkv * parts, B): Q-, Q+ of one query block over at most 8 of a group's heads, in pairs of floats -> pooled [B, Hkv, nq, parts, 2 (sum,
+// rest), 2 D]. Two warps, half of the rows each: long enough a way through memory that the joining at its end costs little.
 constexpr int kPoolThreads = 64, kAhead = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes a row, rows a load
   __shared__ float s_sum[2][2 * D];
   const int r = blockIdx.x, hk = blockIdx.y / a.parts, part = blockIdx.y % a.parts, b = blockIdx.z;
@@ -308,64 +353,48 @@ __global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_con
   const int begin = warp * half + lane / LPR, end = min(rows, warp * half + half);
   const int mine = end > begin ? (end - begin + RPL - 1) / RPL : 0;  // rows of a head that this lane reads
   const int steps = (half + RPL - 1) / RPL;
-  const int shift = 34 - __clz((h1 - h0) * steps);                    // 2^shift >= 4 x the number of values
-  LargeSum all, pos;
-  float big = 0.f, under = 0.f;  // C, and what the values have to stay under
-  all.start();
-  pos.start();
+  BitSums q;
+  q.start();
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.Hq + h0) * a.q_len + i0 + begin) * D) + x;
   for (int h = h0; h < h1; ++h, src += (size_t)a.q_len * LPR) {
     for (int t = 0; t < steps; t += kAhead) {
       uint4 v[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) v[k] = t + k < mine ? __ldg(src + (t + k) * 32) : make_uint4(0, 0, 0, 0);
+      uint32_t top = 0u;  // largest magnitudes, two to a word
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        float y[8], top = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          y[e] = (e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
-          top = fmaxf(top, fabsf(y[e]));
-        }
-        if (top >= under) {  // the first values, and larger ones than those so far
-          const int ex = min((int)(__float_as_uint(top) >> 23), 253 - shift);  // top < 2^(ex - 126)
-          under = __uint_as_float((uint32_t)(ex + 1) << 23);
-          const float c = __uint_as_float((uint32_t)(ex + 1 + shift) << 23);
-          all.grow(big, c);
-          pos.grow(big, c);
-          big = c;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          all.add(e, y[e]);
-          pos.add(e, fmaxf(y[e], 0.f));
-        }
+        top = bits_of(__hmax2(as_bf2(top), __habs2(as_bf2(v[k].x))));
+        top = bits_of(__hmax2(as_bf2(top), __habs2(as_bf2(v[k].y))));
+        top = bits_of(__hmax2(as_bf2(top), __habs2(as_bf2(v[k].z))));
+        top = bits_of(__hmax2(as_bf2(top), __habs2(as_bf2(v[k].w))));
       }
+      const float most = fmaxf(bf_lo(top), bf_hi(top));
+      if (most >= q.under) q.grow(most);
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) q.add(v[k]);
     }
   }
+  float all[8], all_r[8], pos[8], pos_r[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    all.s[e] -= big;
-    pos.s[e] -= big;
-  }
+  for (int e = 0; e < 8; ++e) q.sums(e, all[e], all_r[e], pos[e], pos_r[e]);
 #pragma unroll
   for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float u = __shfl_xor_sync(kAll, all.s[e], o), p = __shfl_xor_sync(kAll, pos.s[e], o);
-      all.rest[e] += __shfl_xor_sync(kAll, all.rest[e], o);
-      pos.rest[e] += __shfl_xor_sync(kAll, pos.rest[e], o);
-      add_exact(all.s[e], all.rest[e], u);
-      add_exact(pos.s[e], pos.rest[e], p);
+      const float u = __shfl_xor_sync(kAll, all[e], o), p = __shfl_xor_sync(kAll, pos[e], o);
+      all_r[e] += __shfl_xor_sync(kAll, all_r[e], o);
+      pos_r[e] += __shfl_xor_sync(kAll, pos_r[e], o);
+      add_exact(all[e], all_r[e], u);
+      add_exact(pos[e], pos_r[e], p);
     }
   if (warp == 1 && lane < LPR) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      s_sum[0][x * 8 + e] = all.s[e];
-      s_sum[1][x * 8 + e] = all.rest[e];
-      s_sum[0][D + x * 8 + e] = pos.s[e];
-      s_sum[1][D + x * 8 + e] = pos.rest[e];
+      s_sum[0][x * 8 + e] = all[e];
+      s_sum[1][x * 8 + e] = all_r[e];
+      s_sum[0][D + x * 8 + e] = pos[e];
+      s_sum[1][D + x * 8 + e] = pos_r[e];
     }
   }
   __syncthreads();
@@ -373,15 +402,15 @@ __global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_con
   float* out = a.pooled + ((((size_t)b * a.Hkv + hk) * a.nq + r) * a.parts + part) * 4 * D + x * 8;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    all.rest[e] += s_sum[1][x * 8 + e];
-    add_exact(all.s[e], all.rest[e], s_sum[0][x * 8 + e]);
-    pos.rest[e] += s_sum[1][D + x * 8 + e];
-    add_exact(pos.s[e], pos.rest[e], s_sum[0][D + x * 8 + e]);
-    all.rest[e] -= pos.rest[e];  // Q- = all - positive
-    add_exact(all.s[e], all.rest[e], -pos.s[e]);
+    all_r[e] += s_sum[1][x * 8 + e];
+    add_exact(all[e], all_r[e], s_sum[0][x * 8 + e]);
+    pos_r[e] += s_sum[1][D + x * 8 + e];
+    add_exact(pos[e], pos_r[e], s_sum[0][D + x * 8 + e]);
+    all_r[e] -= pos_r[e];  // Q- = all - positive
+    add_exact(all[e], all_r[e], -pos[e]);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {  // the rest below the sum's last bit
-      const float s = w ? pos.s[e] : all.s[e], rest = w ? pos.rest[e] : all.rest[e], t = s + rest;
+      const float s = w ? pos[e] : all[e], rest = w ? pos_r[e] : all_r[e], t = s + rest;
       out[w * D + e] = t;
       out[2 * D + w * D + e] = t - t == 0.f ? rest - (t - s) : 0.f;
     }
