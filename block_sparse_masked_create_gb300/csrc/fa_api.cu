@@ -1540,7 +1540,7 @@ static int select_blocks_plan(const fa_block_mask* src, int32_t B, int32_t Hq, i
   // (and among divisions of 8 heads at most)
   P->parts = src->q_len == 1 ? 0 : rows < 2 * 152 ? Hq / Hkv : (Hq / Hkv + 7) / 8;
   P->off_zone = align256(rows * P->parts * 4 * d * sizeof(float));
-  P->total = P->off_zone + align256(rows * src->nk * sizeof(uint64_t));
+  P->total = P->off_zone + (select_needs_zone(src->nq, src->nk) ? align256(rows * src->nk * sizeof(uint64_t)) : 0);
   return FA_OK;
 }
 
@@ -1559,19 +1559,17 @@ fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, c
                                       int32_t keep, int32_t first, int32_t last, void* dev_buf, size_t buf_bytes,
                                       fa_block_mask* out, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                                       fa_stream_t stream) {
-  if (!src || !q || !bounds || !dev_buf || !out || !workspace) return FA_ERR_INVALID_ARG;
+  if (!src || !q || !bounds || !dev_buf || !out) return FA_ERR_INVALID_ARG;
   SelectPlan P;
   int s = select_blocks_plan(src, B, Hq, Hkv, d, &P);
   if (s != FA_OK) return (fa_status)s;
+  if (P.total && !workspace) return FA_ERR_INVALID_ARG;
   if (!src->block_class || keep < 1 || first < 0 || last < 0 || (int64_t)first + last > keep) return FA_ERR_INVALID_ARG;
   if (page_table && (n_pages_total < 1 || max_pages < src->nk)) return FA_ERR_SHAPE;
   if (!aligned16(q) || !aligned16(bounds) || !words_aligned({page_table, dev_status}) ||
       ((reinterpret_cast<uintptr_t>(dev_buf) | reinterpret_cast<uintptr_t>(workspace)) & 255u))
     return FA_ERR_INVALID_ARG;
   if (buf_bytes < P.mask.total || workspace_bytes < P.total) return FA_ERR_BUFFER_TOO_SMALL;
-  DevRule R;
-  s = compile_rule_noexcept(&src->rule, &R);  // the attention entries would refuse it later
-  if (s != FA_OK) return (fa_status)s;
   SelectArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = q;

@@ -230,28 +230,6 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-// a + b of two pairs of floats, a * b + c
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 floats_of(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 // s + rest = s + x (+ rest): what the addition rounds off goes to rest
@@ -260,14 +238,6 @@ __device__ __forceinline__ void add_exact(float& s, float& rest, float x) {
   rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(x, u)));
   s = t;
 }
-// the same for two sums at once
-__device__ __forceinline__ void add_exact2(uint64_t& s, uint64_t& rest, uint64_t x) {
-  constexpr uint64_t kMinus = 0xBF800000BF800000ull;  // (-1, -1): a - b as b * -1 + a
-  const uint64_t t = add2(s, x), u = fma2(s, kMinus, t);
-  rest = add2(rest, add2(fma2(fma2(u, kMinus, t), kMinus, s), fma2(u, kMinus, x)));
-  s = t;
-}
-
 // Sums of bf16 in whole numbers. For |x| < 2^E, x + C with C = 1.5 * 2^(E + 1) lies in C's binade, so its bits are C's plus x in units of
 // 2^(E - 22): an integer sum of the bits is exact, and with max(x, 0) + C = max(x + C, C) the sum of the positive ones takes two
 // operations more. What x + C rounds off (of magnitudes under 2^(E - 14)) is summed apart, where there is any. At most 256 values a lane.
@@ -440,47 +410,34 @@ struct Boxes {
   __device__ __forceinline__ const __nv_bfloat16* at(int id) const { return base + (size_t)id * stride; }
 };
 
-// A warp scores the blocks of its lanes' ids (-1: none), 16 bytes of a block a lane: 8 (d = 64: 16) blocks in flight, whose partial sums
-// meet in a butterfly that halves the blocks a lane still has with every step. q: the lane's 8 terms of Q-, Q+; most: largest magnitudes
-// of its 8 bounds so far. 4 products in a row, 6 sums. AHEAD: the next blocks are loaded before these are summed (a warp that works alone).
-template <int D, bool AHEAD>
-__device__ __forceinline__ float score_lanes(const Boxes<D>& box, int id, const uint64_t (&q)[4], uint32_t (&most)[4]) {
-  constexpr int LPB = D / 4, BPW = 32 / LPB, kStep = 8 * BPW;
-  const int lane = threadIdx.x & 31, x = lane % LPB;
-  const uint32_t have = __ballot_sync(kAll, id >= 0);
-  float out = -INFINITY;
-  uint4 v[8], ahead[AHEAD ? 8 : 1];
-  auto load = [&](int k, uint4* to) {
+// A warp's part in the scores of one row: the lane's 8 terms of Q-, Q+, and the largest magnitudes of its 8 bounds so far. 16 bytes of a block a
+// lane, 8 (d = 64: 16) blocks at a time, whose partial sums meet in a butterfly that halves the blocks a lane still has with every
+// step: 8 products in a row, 5 sums.
+template <int D>
+struct Scorer {
+  static constexpr int LPB = D / 4, BPW = 32 / LPB, kStep = 8 * BPW;  // lanes a block, blocks a load, blocks at a time
+  float q[8];
+  uint32_t most[4];
+  // lane t < kStep: the score of the block that its id names (negative: none)
+  __device__ __forceinline__ float scores(const Boxes<D>& box, int id) {
+    const int lane = threadIdx.x & 31;
+    uint4 v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int w = __shfl_sync(kAll, id, (k + j * BPW + lane / LPB) & 31);
-      to[j] = w >= 0 ? __ldg(reinterpret_cast<const uint4*>(box.at(w)) + x) : make_uint4(0, 0, 0, 0);
-    }
-  };
-  if (AHEAD) load(0, ahead);
-#pragma unroll 1
-  for (int k = 0; k < 32; k += kStep) {
-    if (!AHEAD && !((have >> k) & ((1u << kStep) - 1u))) continue;
-    if (AHEAD) {
-      if (!(have >> k)) break;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = ahead[AHEAD ? j : 0];
-      if (k + kStep < 32) load(k + kStep, ahead);
-    } else {
-      load(k, v);
+      const int w = __shfl_sync(kAll, id, j * BPW + lane / LPB);
+      v[j] = w >= 0 ? __ldg(reinterpret_cast<const uint4*>(box.at(w)) + lane % LPB) : make_uint4(0, 0, 0, 0);
     }
     float s[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const uint32_t t[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-      uint64_t p = 0;
+      s[j] = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        p = fma2(q[i], pair_of(bf_lo(t[i]), bf_hi(t[i])), p);
+        s[j] = fmaf(q[2 * i], bf_lo(t[i]), s[j]);
+        s[j] = fmaf(q[2 * i + 1], bf_hi(t[i]), s[j]);
         most[i] = bits_of(__hmax2(as_bf2(most[i]), __habs2(as_bf2(t[i]))));
       }
-      const float2 f = floats_of(p);
-      s[j] = f.x + f.y;
     }
     constexpr int O = LPB / 2;
 #pragma unroll
@@ -494,13 +451,27 @@ __device__ __forceinline__ float score_lanes(const Boxes<D>& box, int id, const 
     }
 #pragma unroll
     for (int o = O / 8; o > 0; o >>= 1) s[0] += __shfl_xor_sync(kAll, s[0], o);
-    const int t = lane - k, slot = (t / BPW) & 7;
-    const int from = (t % BPW) * LPB + ((slot >> 2) & 1) * O + ((slot >> 1) & 1) * (O / 2) + (slot & 1) * (O / 4);
-    const float mine = __shfl_sync(kAll, s[0], from & 31);
-    if (t >= 0 && t < kStep) out = mine;
+    const int slot = (lane / BPW) & 7;
+    const int from = (lane % BPW) * LPB + ((slot >> 2) & 1) * O + ((slot >> 1) & 1) * (O / 2) + (slot & 1) * (O / 4);
+    return __shfl_sync(kAll, s[0], from);
   }
-  return out;
-}
+  // a bound on the magnitudes that any of the scores so far added up
+  __device__ __forceinline__ float magnitude() const {
+    float err = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      err = fmaf(fabsf(q[2 * i]), bf_lo(most[i]), err);
+      err = fmaf(fabsf(q[2 * i + 1]), bf_hi(most[i]), err);
+    }
+#pragma unroll
+    for (int o = LPB / 2; o > 0; o >>= 1) err += __shfl_xor_sync(kAll, err, o);
+    if (LPB < 32) {
+      const float e = __shfl_xor_sync(kAll, err, LPB & 31);  // the other half's blocks
+      err = e > err || e != e ? e : err;
+    }
+    return err;
+  }
+};
 
 // ------------------------------------------------------------------------------------------------ the choice
 // Order of floats as unsigned numbers, NaN on top, 0 below all of them.
@@ -674,35 +645,37 @@ __device__ __forceinline__ double exact_score(const __nv_bfloat16* box, const Ex
 }
 
 // Chooses among the scored blocks of a row, by W warps: M.key -> M.wx, with the prefix sums and totals that write_row needs. err bounds the
-// magnitudes that a score adds up; exact_q gives the lane's terms of Q-, Q+.
+// magnitudes that a score adds up; exact_q gives the lane's terms of Q-, Q+; zone [nk] is scratch.
 template <int W, int D, class QFn>
-__device__ void search_row(const SelectArgs& a, size_t row, const Boxes<D>& box, const RowMem& M, Zone& Z, float err, QFn exact_q) {
+__device__ void search_row(const SelectArgs& a, uint64_t* zone, const Boxes<D>& box, const RowMem& M, Zone& Z, float err, QFn exact_q) {
   using G = Group<W>;
   G grp{M.red, 0};
   const int lane = threadIdx.x & 31, gw = G::warp(), nk = M.nk, want = a.keep - a.first - a.last;
   const uint32_t below = (1u << lane) - 1u;
   const int n = grp.prefix([&](int i) { return M.wc[i]; }, M.nw, M.pa);
   if (n > a.keep) {
-    for (int i = gw; i < M.nw; i += W) {  // always kept: not among the others
+    // this thread's keys, of columns lane + 32 (gw + j W), in registers, or where there are too many in shared memory
+    constexpr int kHeld = 16;
+    uint32_t held[kHeld];
+    const bool small = nk <= kHeld * 32 * W;
+    auto take = [&](int i) {  // those always kept are marked, and not among the others
       const int c = i * 32 + lane, place = (int)M.pa[i] + __popc(M.wc[i] & below);
+      uint32_t k = c < nk ? M.key[c] : 0u;
       const bool always = ((M.wc[i] >> lane) & 1u) && (place < a.first || place >= n - a.last);
-      if (always) M.key[c] = 0u;
       const uint32_t w = __ballot_sync(kAll, always);
+      if (always) M.key[c] = k = 0u;
       if (lane == 0) M.wx[i] = w;
+      return k;
+    };
+    if (small) {
+#pragma unroll
+      for (int j = 0; j < kHeld; ++j) held[j] = gw + j * W < M.nw ? take(gw + j * W) : 0u;
+    } else {
+#pragma unroll 4
+      for (int i = gw; i < M.nw; i += W) take(i);
     }
     G::sync();
     if (want > 0) {
-      // this thread's keys in registers, or where there are too many in shared memory
-      constexpr int kHeld = 16;
-      uint32_t held[kHeld];
-      const bool small = nk <= kHeld * 32 * W;
-      if (small) {
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j) {
-          const int c = G::tid() + j * 32 * W;
-          held[j] = c < nk ? M.key[c] : 0u;
-        }
-      }
       auto each = [&](auto f) {
         if (small) {
 #pragma unroll
@@ -725,16 +698,22 @@ __device__ void search_row(const SelectArgs& a, size_t row, const Boxes<D>& box,
       bd.left = want - grp.sum(m);
       bd.z = grp.sum(z);
       const bool fits = bd.z == bd.left;
-      for (int i = gw; i < M.nw; i += W) {
-        const int c = i * 32 + lane;
-        const uint32_t k = c < nk ? M.key[c] : 0u, w = __ballot_sync(kAll, bd.sure(k) || (fits && bd.near(k)));
+      auto put = [&](int i, uint32_t k) {
+        const uint32_t w = __ballot_sync(kAll, bd.sure(k) || (fits && bd.near(k)));
         if (lane == 0) M.wx[i] |= w;
+      };
+      if (small) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j)
+          if (gw + j * W < M.nw) put(gw + j * W, held[j]);
+      } else {
+#pragma unroll 4
+        for (int i = gw; i < M.nw; i += W) put(i, i * 32 + lane < nk ? M.key[i * 32 + lane] : 0u);
       }
       if (!fits) {  // 32 bits do not tell which of the blocks near the border are in: their scores exactly, a warp each
         const ExactQ<D> xq = exact_q();
         const bool wide = !(err > 8.7e-19f && err < 1e36f);  // 2^-60: what a product rounds off is a normal number still
         const bool few = bd.z <= kZone;
-        uint64_t* zone = a.zone + row * nk;
         if (G::tid() == 0) Z.n = 0;
         G::sync();
         for (int i = gw; i < M.nw; i += W) {
@@ -833,160 +812,131 @@ __device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const
 // Rows of up to kAlone blocks, whose keys one warp holds in registers, are searched by it alone: the steps are too short for barriers.
 constexpr int kAlone = 512;
 
-// W = 1: a warp a row, 8 rows of one (request, KV head) a CTA, grid (ceil(nq / 8), Hkv, B). W = 8: a cluster of `ranks` CTAs a row, grid
-// (nq * ranks, Hkv, B): each scores its share of the blocks into the first one's shared memory, and that one chooses.
-template <int W, int D>
-__global__ void __launch_bounds__(kThreads, W == 1 ? 2 : 4) choose_kernel(const __grid_constant__ SelectArgs a, int ranks) {
+// A cluster of `ranks` CTAs a row, grid (nq * ranks, Hkv, B): each scores its share of the blocks into the first one's shared memory, and
+// that one chooses. zone_words: shared memory for the scores near the border, or 0 (the workspace).
+constexpr int kZoneBlocks = 2048;  // rows of up to so many keep them in shared memory
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 4) choose_kernel(const __grid_constant__ SelectArgs a, int ranks) {
   namespace cg = cooperative_groups;
-  using G = Group<W>;
-  constexpr int LPB = D / 4, V = ExactQ<D>::V;
-  extern __shared__ uint32_t dyn[];
-  __shared__ Zone s_zone[kWarps / W];
-  __shared__ float s_err[W == 1 ? 1 : 8 * kWarps];
-  __shared__ float s_q[W == 1 ? 1 : 2][W == 1 ? 1 : 2 * D];  // one query: sum and rest
-  const int lane = threadIdx.x & 31, gw = G::warp(), nk = a.nk;
-  const int rank = W == 1 ? 0 : blockIdx.x % ranks, hk = blockIdx.y, b = blockIdx.z;
-  const int r = a.nq - 1 - (W == 1 ? (int)blockIdx.x * kWarps + (int)(threadIdx.x >> 5) : (int)blockIdx.x / ranks);  // causal: long rows first
-  if (W == 1 && r < 0) return;  // no barrier of the CTA from here on for W = 1
-  const bool token = W > 1 && a.q_len == 1;
-  const RowMem M(dyn + (W == 1 ? (threadIdx.x >> 5) * row_words(nk, 1) : 0), nk);
+  using S = Scorer<D>;
+  constexpr int V = ExactQ<D>::V, kPanel = 32 * kWarps;  // columns that a CTA takes at a time
+  extern __shared__ __align__(8) uint32_t dyn[];
+  __shared__ Zone s_zone;
+  __shared__ float s_err[8 * kWarps];
+  __shared__ float s_q[2][2 * D];  // Q-, Q+: sum and rest
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nk = a.nk;
+  const int rank = blockIdx.x % ranks, hk = blockIdx.y, b = blockIdx.z, r = a.nq - 1 - (int)blockIdx.x / ranks;  // causal: long rows first
   const size_t row = ((size_t)b * a.Hkv + hk) * a.nq + r;
+  const bool near_by = nk <= kZoneBlocks;
+  const RowMem M(dyn + (near_by ? 2 * nk : 0), nk);
   const Boxes<D> box(a, b, hk);
   const uint8_t* cls = a.src_class + ((size_t)(a.src_Bm > 1 ? b : 0) * a.nq + r) * nk;
   const int want = a.keep - a.first - a.last, g = a.Hq / a.Hkv;
-  if (W > 1 && ranks > 1) cg::this_cluster().barrier_arrive();  // every CTA of the cluster runs before the first one's memory is written
+  if (ranks > 1) cg::this_cluster().barrier_arrive();  // every CTA of the cluster runs before the first one's memory is written
 
-  // the blocks' ids, the loads of all chunks in flight together (key [c] holds them until the score takes their place)
-  for (int i = rank * W + gw; i < M.nw; i += W * ranks) {
-    const int c = i * 32 + lane, v = c < nk ? cls[c] : 0;
-    const uint32_t some = __ballot_sync(kAll, v != FA_BLOCK_EMPTY), part = __ballot_sync(kAll, v == FA_BLOCK_PARTIAL);
-    const int id = v != FA_BLOCK_EMPTY ? box.id(c) : -2;
-    if (c < nk) M.key[c] = (uint32_t)id;
-    if (lane == 0) {
-      M.wc[i] = M.wx[i] = some;
-      M.wp[i] = part;
-    }
+  // classes and ids of the blocks, the first two panels' loads ahead of the queries'
+  const int i0 = rank * kWarps + warp, step = kWarps * ranks;
+  int cv[2], ci[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = (i0 + j * step) * 32 + lane;
+    cv[j] = c < nk ? cls[c] : 0;
+    ci[j] = c < nk ? box.id(c) : -1;
   }
-  if (W > 1 && ranks > 1 && rank == 0)  // the first CTA needs the bits of the others' blocks too
-    for (int i = gw; i < M.nw; i += W) {
-      if (i / W % ranks == 0) continue;
-      const int c = i * 32 + lane, v = c < nk ? cls[c] : 0;
-      const uint32_t some = __ballot_sync(kAll, v != FA_BLOCK_EMPTY), part = __ballot_sync(kAll, v == FA_BLOCK_PARTIAL);
-      if (lane == 0) {
-        M.wc[i] = M.wx[i] = some;
-        M.wp[i] = part;
-      }
-    }
-
-  // Q-, Q+ of the row: this lane's terms
-  uint64_t q[4];
-  const int e0 = lane % LPB * 8;
-  if (token) {
-    if (threadIdx.x < 2 * D) {
-      const int e = threadIdx.x % D;
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * a.Hq + (size_t)hk * g) * D + e;
-      float s = 0.f, rest = 0.f;
+  if (threadIdx.x < 2 * D) {
+    float s = 0.f, rest = 0.f;
+    if (a.q_len == 1) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + ((size_t)b * a.Hq + (size_t)hk * g) * D + threadIdx.x % D;
 #pragma unroll 4
       for (int h = 0; h < g; ++h) {
         const float x = __bfloat162float(src[(size_t)h * D]);
         add_exact(s, rest, threadIdx.x < D ? min_nan(x, 0.f) : max_nan(x, 0.f));
       }
-      s_q[0][threadIdx.x] = s;
-      s_q[1][threadIdx.x] = rest;
+    } else {
+      for (int p = 0; p < a.parts; ++p) {
+        const float* src = a.pooled + (row * a.parts + p) * 4 * D + threadIdx.x;
+        rest = __fadd_rn(rest, __ldg(src + 2 * D));
+        add_exact(s, rest, __ldg(src));
+      }
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const uint64_t*>(&s_q[0][e0 + 2 * i]);
-  } else {
-    float hi[8], lo[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) hi[i] = lo[i] = 0.f;
-    for (int p = 0; p < a.parts; ++p) {
-      const float4* src = reinterpret_cast<const float4*>(a.pooled + (row * a.parts + p) * 4 * D + e0);
-      const float4 u = __ldg(src), v = __ldg(src + 1);
-      const float t[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) add_exact(hi[i], lo[i], t[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = pair_of(hi[2 * i] + lo[2 * i], hi[2 * i + 1] + lo[2 * i + 1]);
+    s_q[0][threadIdx.x] = s;
+    s_q[1][threadIdx.x] = rest;
   }
+  auto note = [&](int i, int v, int id) {
+    const int c = i * 32 + lane;
+    const uint32_t some = __ballot_sync(kAll, v != FA_BLOCK_EMPTY), part = __ballot_sync(kAll, v == FA_BLOCK_PARTIAL);
+    if (v != FA_BLOCK_EMPTY && id < 0) report(a.status, FA_ERR_DEVICE_CHECK);
+    if (c < nk) M.key[c] = v != FA_BLOCK_EMPTY ? (uint32_t)id : (uint32_t)-2;  // until the score takes its place
+    if (lane == 0) {
+      M.wc[i] = M.wx[i] = some;
+      M.wp[i] = part;
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (i0 + j * step < M.nw) note(i0 + j * step, cv[j], ci[j]);
+  for (int i = i0 + 2 * step; i < M.nw; i += step) {
+    const int c = i * 32 + lane;
+    note(i, c < nk ? cls[c] : 0, c < nk ? box.id(c) : -1);
+  }
+  __syncthreads();
 
-  // the scores
+  // the scores, a panel's steps in turn to the warps
+  S sc;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sc.q[i] = s_q[0][lane % S::LPB * 8 + i];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sc.most[i] = 0u;
   uint32_t* key = M.key;
-  if (W > 1 && ranks > 1) {
+  if (ranks > 1) {
     cg::this_cluster().barrier_wait();
     key = cg::this_cluster().map_shared_rank(M.key, 0);
-  }
-  uint32_t most[4] = {0u, 0u, 0u, 0u};
-  for (int i = rank * W + gw; i < M.nw; i += W * ranks) {
-    const int c = i * 32 + lane, id = c < nk ? (int)M.key[c] : -2;
-    const uint32_t any = __ballot_sync(kAll, id >= 0);
-    if (id == -1) report(a.status, FA_ERR_DEVICE_CHECK);
-    float s = -INFINITY;
-    if (any && want > 0) s = score_lanes<D, W == 1>(box, id, q, most);
-    if (c < nk) key[c] = id == -2 ? 0u : order_of(s);
-  }
-  float err = 0.f;  // a bound on the magnitudes that any of the scores adds up
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = floats_of(q[i]);
-    err = fmaf(fabsf(f.x), bf_lo(most[i]), err);
-    err = fmaf(fabsf(f.y), bf_hi(most[i]), err);
-  }
-#pragma unroll
-  for (int o = LPB / 2; o > 0; o >>= 1) err += __shfl_xor_sync(kAll, err, o);
-  if (LPB < 32) {
-    const float e = __shfl_xor_sync(kAll, err, LPB & 31);  // the other half's blocks
-    err = e > err || e != e ? e : err;
-  }
-  if (W > 1) {
-    if (lane == 0) (ranks > 1 ? cg::this_cluster().map_shared_rank(s_err, 0) : s_err)[rank * W + gw] = err;
-    if (ranks > 1) {
-      cg::this_cluster().sync();
-      if (rank) return;
-    } else {
-      __syncthreads();
+    if (rank) {
+      uint32_t* words = cg::this_cluster().map_shared_rank(M.wc, 0);
+      for (int i = i0; i < M.nw; i += step)
+        if (lane < 3) words[lane * M.nw + i] = M.wc[lane * M.nw + i];  // wc, wp, wx follow one another
     }
   }
+  for (int p0 = rank * kPanel; p0 < nk; p0 += kPanel * ranks) {
+    for (int c0 = p0 + warp * S::kStep; c0 < min(nk, p0 + kPanel); c0 += kWarps * S::kStep) {
+      const int c = c0 + lane;
+      const bool mine = lane < S::kStep && c < nk;
+      const int id = mine ? (int)M.key[c] : -2;
+      float s = -INFINITY;
+      if (want > 0 && __any_sync(kAll, id >= 0)) s = sc.scores(box, id);
+      if (mine) key[c] = id == -2 ? 0u : order_of(id >= 0 ? s : -INFINITY);
+    }
+  }
+  const float err = sc.magnitude();
+  if (lane == 0) (ranks > 1 ? cg::this_cluster().map_shared_rank(s_err, 0) : s_err)[rank * kWarps + warp] = err;
+  if (ranks > 1) {
+    cg::this_cluster().sync();
+    if (rank) return;
+  } else {
+    __syncthreads();
+  }
+
   auto search = [&](auto warps) {
-    float all = err;
-    if (W > 1) {
-      all = 0.f;
-      for (int i = 0; i < ranks * W; ++i) all = s_err[i] > all || s_err[i] != s_err[i] ? s_err[i] : all;
-    }
-    search_row<decltype(warps)::value, D>(a, row, box, M, s_zone[W == 1 ? threadIdx.x >> 5 : 0], all, [&]() {
+    float all = 0.f;
+    for (int i = 0; i < ranks * kWarps; ++i) all = s_err[i] > all || s_err[i] != s_err[i] ? s_err[i] : all;
+    search_row<decltype(warps)::value, D>(a, near_by ? reinterpret_cast<uint64_t*>(dyn) : a.zone + row * nk, box, M, s_zone, all, [&]() {
       ExactQ<D> x;
-      if (token) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          x.hi[e] = s_q[0][lane * V + e];
-          x.lo[e] = s_q[W == 1 ? 0 : 1][lane * V + e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < V; ++e) x.hi[e] = x.lo[e] = 0.f;
-        for (int p = 0; p < a.parts; ++p) {
-          const float* src = a.pooled + (row * a.parts + p) * 4 * D + lane * V;
-#pragma unroll
-          for (int e = 0; e < V; ++e) {
-            x.lo[e] = __fadd_rn(x.lo[e], __ldg(src + 2 * D + e));
-            add_exact(x.hi[e], x.lo[e], __ldg(src + e));
-          }
-        }
+      for (int e = 0; e < V; ++e) {
+        x.hi[e] = s_q[0][lane * V + e];
+        x.lo[e] = s_q[1][lane * V + e];
       }
       return x;
     });
   };
-  if (W == 1) {
-    search(std::integral_constant<int, 1>{});
-  } else if (nk <= kAlone) {
-    if (gw == 0) search(std::integral_constant<int, 1>{});
+  if (nk <= kAlone) {
+    if (warp == 0) search(std::integral_constant<int, 1>{});
     __syncthreads();
   } else {
-    search(std::integral_constant<int, W>{});
+    search(std::integral_constant<int, kWarps>{});
   }
-  write_row<W>(a, row, M);
+  write_row<kWarps>(a, row, M);
 }
 
 // ------------------------------------------------------------------------------------------------ rows of many query blocks
@@ -1128,7 +1078,7 @@ __global__ void __launch_bounds__(kThreads, 2) choose_rows_kernel(const __grid_c
   float err = 0.f;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) err = s_err[w][warp] > err || s_err[w][warp] != s_err[w][warp] ? s_err[w][warp] : err;
-  search_row<1, D>(a, head + r, box, M, s_zone[warp], err, [&]() {
+  search_row<1, D>(a, a.zone + (head + r) * nk, box, M, s_zone[warp], err, [&]() {
     ExactQ<D> x;
 #pragma unroll
     for (int e = 0; e < V; ++e) x.hi[e] = x.lo[e] = 0.f;
@@ -1179,9 +1129,9 @@ cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t st) {
     choose_rows_kernel<D><<<dim3(a.Hkv, (a.nq + kRows - 1) / kRows, a.B), kThreads, smem, st>>>(a);
     e = cudaGetLastError();
   } else {
-    const size_t smem = row_words(a.nk, kWarps) * 4;
+    const size_t smem = (row_words(a.nk, kWarps) + (a.nk <= kZoneBlocks ? 2 * a.nk : 0)) * 4;
     const int ranks = select_ranks(rows, a.nk);
-    if ((e = allow_smem(choose_kernel<kWarps, D>, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(choose_kernel<D>, smem)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.nq * ranks, a.Hkv, a.B);
     cfg.blockDim = dim3(kThreads);
@@ -1193,13 +1143,16 @@ cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t st) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, choose_kernel<kWarps, D>, a, ranks);
+    e = cudaLaunchKernelEx(&cfg, choose_kernel<D>, a, ranks);
   }
   if (e != cudaSuccess || a.nq == 1) return e;
   return launch_mask_columns(a.out, st);
 }
 
 }  // namespace
+
+// whether the choice needs the workspace for scores near the border
+bool select_needs_zone(int32_t nq, int32_t nk) { return nk > kZoneBlocks || (nq > 1 && nk <= kRowsBlocks); }
 
 // CTAs that share the blocks of one row
 int select_ranks(int64_t rows, int32_t nk) {

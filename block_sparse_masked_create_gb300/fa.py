@@ -953,14 +953,14 @@ def select_blocks(src: BlockMask, q: torch.Tensor, bounds: torch.Tensor, keep: i
         src.select = (need, lib.fa_block_mask_select_blocks_bytes(ref, B, Hkv),
                       lib.fa_block_mask_select_blocks_workspace_bytes(ref, B, Hq, Hkv, d))
     _, n, scratch = src.select
-    if workspace is None:
-        size = scratch or 256
+    if workspace is None and scratch:
+        size = scratch
         workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     if out is None or out.buf is buf or out.buf.device != dev or out.buf.numel() < n:
         out = BlockMask(BlockMaskC(), torch.empty(n or 256, dtype=torch.uint8, device=dev))
     buf = out.buf
     _check(_call(dev, lib.fa_block_mask_select_blocks, ref, q.data_ptr(), bounds.data_ptr(), _at(page_table), P, max_pages, B, Hq, Hkv, d,
-                 keep, first, last, buf.data_ptr(), buf.numel(), ctypes.byref(out.c), workspace.data_ptr(), size, _at(status)),
+                 keep, first, last, buf.data_ptr(), buf.numel(), ctypes.byref(out.c), _at(workspace), size, _at(status)),
            "fa_block_mask_select_blocks")
     out.keep = [src]  # its rule's tensors and its document runs stay valid with it
     return out

@@ -86,9 +86,12 @@ def test_select_blocks_refusals(fa):
     wn = lib.fa_block_mask_select_blocks_workspace_bytes(ctypes.byref(c), 2, 4, 2, 64)
     assert n >= 2 * 2 * 2 * 4 * 17 and wn >= 2 * 2 * 2 * 4 * 8
     assert call(n=n - 1) == fa.ERR_BUFFER and call(wn=wn - 1) == fa.ERR_BUFFER
-    many = fa.make_mask_rule([("causal",), ("doc",), ("or",)] + [op for w in (1, 2, 3) for op in (("window", w), ("prefix", w), ("or",), ("and",))])
-    c.rule = many
-    assert call(c=c) in (fa.ERR_INVALID_ARG, fa.ERR_UNSUPPORTED)
+    one = mask(fa, nq=1, bq=1, q_len=1)                                # one query: no workspace, unless its row is very long
+    assert lib.fa_block_mask_select_blocks_workspace_bytes(ctypes.byref(one), 2, 4, 2, 64) == 0
+    assert call(c=one, ws=None, wn=0, n=0) == fa.ERR_BUFFER
+    one = mask(fa, nq=1, bq=1, q_len=1, nk=2049, bk=64, kv_len=2049 * 64)
+    assert lib.fa_block_mask_select_blocks_workspace_bytes(ctypes.byref(one), 2, 4, 2, 64) >= 2 * 2 * 2049 * 8
+    assert call(c=one, ws=None) == fa.ERR_INVALID_ARG
     assert lib.fa_block_mask_select_blocks_bytes(None, 2, 2) == 0
     assert lib.fa_block_mask_select_blocks_workspace_bytes(ctypes.byref(mask(fa)), 2, 3, 2, 64) == 0
 
