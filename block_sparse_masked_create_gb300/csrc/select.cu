@@ -552,6 +552,7 @@ struct Group {
     });
     lo = least(lo);
     uint32_t hi = ~least(top);
+#pragma unroll 1
     while (lo < hi) {
       const uint32_t mid = lo + (hi - lo) / 2 + 1;
       int m = 0;
@@ -654,36 +655,26 @@ __device__ void search_row(const SelectArgs& a, uint64_t* zone, const Boxes<D>& 
   const uint32_t below = (1u << lane) - 1u;
   const int n = grp.prefix([&](int i) { return M.wc[i]; }, M.nw, M.pa);
   if (n > a.keep) {
-    // this thread's keys, of columns lane + 32 (gw + j W), in registers, or where there are too many in shared memory
-    constexpr int kHeld = 16;
-    uint32_t held[kHeld];
-    const bool small = nk <= kHeld * 32 * W;
-    auto take = [&](int i) {  // those always kept are marked, and not among the others
+#pragma unroll 1
+    for (int i = gw; i < M.nw; i += W) {  // always kept: not among the others
       const int c = i * 32 + lane, place = (int)M.pa[i] + __popc(M.wc[i] & below);
-      uint32_t k = c < nk ? M.key[c] : 0u;
       const bool always = ((M.wc[i] >> lane) & 1u) && (place < a.first || place >= n - a.last);
       const uint32_t w = __ballot_sync(kAll, always);
-      if (always) M.key[c] = k = 0u;
+      if (always) M.key[c] = 0u;
       if (lane == 0) M.wx[i] = w;
-      return k;
-    };
-    if (small) {
-#pragma unroll
-      for (int j = 0; j < kHeld; ++j) held[j] = gw + j * W < M.nw ? take(gw + j * W) : 0u;
-    } else {
-#pragma unroll 4
-      for (int i = gw; i < M.nw; i += W) take(i);
     }
     G::sync();
     if (want > 0) {
+      // Short loops over the keys in shared memory, four at a time: unrolled over registers the code is several times as long, and a CTA
+      // that runs it once waits for its instructions (4 x 4096 queries, rows of 32 blocks: the choice took 40 us so, 36 us this way).
       auto each = [&](auto f) {
-        if (small) {
+#pragma unroll 1
+        for (int c = G::tid(); c < nk; c += 128 * W) {
+          uint32_t k[4];
 #pragma unroll
-          for (int j = 0; j < kHeld; ++j)
-            if (j * 32 * W < nk) f(held[j]);
-        } else {
-#pragma unroll 8
-          for (int c = G::tid(); c < nk; c += 32 * W) f(M.key[c]);
+          for (int j = 0; j < 4; ++j) k[j] = c + j * 32 * W < nk ? M.key[c + j * 32 * W] : 0u;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f(k[j]);
         }
       };
       const float t = value_of(grp.kth(each, want));
@@ -698,17 +689,10 @@ __device__ void search_row(const SelectArgs& a, uint64_t* zone, const Boxes<D>& 
       bd.left = want - grp.sum(m);
       bd.z = grp.sum(z);
       const bool fits = bd.z == bd.left;
-      auto put = [&](int i, uint32_t k) {
-        const uint32_t w = __ballot_sync(kAll, bd.sure(k) || (fits && bd.near(k)));
+#pragma unroll 1
+      for (int i = gw; i < M.nw; i += W) {
+        const uint32_t k = i * 32 + lane < nk ? M.key[i * 32 + lane] : 0u, w = __ballot_sync(kAll, bd.sure(k) || (fits && bd.near(k)));
         if (lane == 0) M.wx[i] |= w;
-      };
-      if (small) {
-#pragma unroll
-        for (int j = 0; j < kHeld; ++j)
-          if (gw + j * W < M.nw) put(gw + j * W, held[j]);
-      } else {
-#pragma unroll 4
-        for (int i = gw; i < M.nw; i += W) put(i, i * 32 + lane < nk ? M.key[i * 32 + lane] : 0u);
       }
       if (!fits) {  // 32 bits do not tell which of the blocks near the border are in: their scores exactly, a warp each
         const ExactQ<D> xq = exact_q();
@@ -786,6 +770,7 @@ __device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const
   const uint32_t below = (1u << lane) - 1u;
   const MaskOut& T = a.out;
   int32_t *pi = T.kv_idx + row * nk, *fi = T.full_kv_idx + row * nk;
+#pragma unroll 1
   for (int i = G::warp(); i < M.nw; i += W) {
     const int c = i * 32 + lane;
     if (c >= nk) continue;
@@ -809,8 +794,8 @@ __device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const
   }
 }
 
-// Rows of up to kAlone blocks, whose keys one warp holds in registers, are searched by it alone: the steps are too short for barriers.
-constexpr int kAlone = 512;
+// Rows of up to kAlone blocks are searched by one warp: the steps are too short for barriers.
+constexpr int kAlone = 128;
 
 // A cluster of `ranks` CTAs a row, grid (nq * ranks, Hkv, B): each scores its share of the blocks into the first one's shared memory, and
 // that one chooses. zone_words: shared memory for the scores near the border, or 0 (the workspace).
