@@ -1526,7 +1526,8 @@ static int select_blocks_plan(const fa_block_mask* src, int32_t B, int32_t Hq, i
   if (src->bq < 1 || src->bk < 1 || src->nq != (src->q_len + src->bq - 1) / src->bq ||
       src->nk != (src->kv_len + src->bk - 1) / src->bk)
     return FA_ERR_SHAPE;
-  if (src->Hm != 1 || (d != 64 && d != 128) || src->nk > kSelectMaxBlocks || B > 65535 || Hq > 65535) return FA_ERR_UNSUPPORTED;
+  if (src->Hm != 1 || (d != 64 && d != 128) || src->nk > kSelectMaxBlocks || src->nq > kSelectMaxRows || B > 65535 || Hq > 65535)
+    return FA_ERR_UNSUPPORTED;
   fa_mask_rule r;
   std::memset(&r, 0, sizeof(r));
   r.n_ops = 1;

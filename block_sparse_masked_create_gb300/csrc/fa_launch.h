@@ -254,6 +254,7 @@ struct BoundsArgs {
 cudaError_t launch_bounds(const BoundsArgs& a, cudaStream_t st);
 
 constexpr int kSelectMaxBlocks = 32768;  // key blocks of a row: what the choice keeps of it fits in shared memory
+constexpr int kSelectMaxRows = 8 * 65535;  // query blocks: rows of a grid
 struct SelectArgs {
   const void* q;             // bf16 [B, Hq, q_len, d]
   const void* bounds;        // bf16 [B, Hkv, nk, 2, d], or with a page table [n_pages_total, Hkv, 2, d]

@@ -8,6 +8,7 @@ block_sparse_masked_create_gb300.build``); a missing library is an error, never 
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass, field
@@ -790,6 +791,7 @@ def _outputs(shape, dev, out, lse, out_dtype):
     return out, lse
 
 
+@functools.lru_cache(maxsize=1024)  # sizes alone decide
 def decode_fp8_workspace_bytes(Bz: int, Hq: int, Hkv: int, d: int, max_pages: int, page: int) -> int:
     return int(load().fa_decode_fp8_workspace_bytes(Bz, Hq, Hkv, d, max_pages, page))
 
@@ -955,9 +957,9 @@ def select_blocks(src: BlockMask, q: torch.Tensor, bounds: torch.Tensor, keep: i
     _, n, scratch = src.select
     if workspace is None and scratch:
         size = scratch
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        workspace = buf.new_empty(size)
     if out is None or out.buf is buf or out.buf.device != dev or out.buf.numel() < n:
-        out = BlockMask(BlockMaskC(), torch.empty(n or 256, dtype=torch.uint8, device=dev))
+        out = BlockMask(BlockMaskC(), buf.new_empty(n or 256))
     buf = out.buf
     _check(_call(dev, lib.fa_block_mask_select_blocks, ref, q.data_ptr(), bounds.data_ptr(), _at(page_table), P, max_pages, B, Hq, Hkv, d,
                  keep, first, last, buf.data_ptr(), buf.numel(), ctypes.byref(out.c), _at(workspace), size, _at(status)),

@@ -219,7 +219,7 @@ FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, voi
  *   score(c) = sum over the query block's rows i < Q_LEN and the query heads h of the group, sum over e of
  *              max(q[b,h,i,e] * smallest[c,e], q[b,h,i,e] * largest[c,e]),
  * which bounds the sum of <q, k> over those queries for any choice of keys in the block (scale, score rule and mask rule
- * do not enter). Scores are compared in 64 bits, ties go to the lower column; scores closer than 2^-32 of the magnitudes that they
+ * do not enter). Scores are compared in 64 bits, ties go to the lower column; scores closer than 2^-28 of the magnitudes that they
  * add up may rank either way. A NaN score ranks above all others (a NaN key is not hidden by the choice).
  * The result is src's mask with the other blocks empty: classes, row lists, query-side transpose and row order as
  * fa_create_block_mask would lay them out, with Bm = B, Hm = Hkv, for every attention entry point (fa_flex_decode and
@@ -230,13 +230,13 @@ FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, voi
  *   bounds     page_table NULL: device bf16 [B, Hkv, nk, 2, d] (fa_key_bounds); else device bf16 [n_pages_total, Hkv, 2, d]
  *              (fa_kv_bounds) with key block c of batch row b in page page_table[b * max_pages + c], max_pages >= nk, one page a block
  *   keep       >= 1;  first, last >= 0, first + last <= keep
- *   dev_buf    device buffer of >= fa_block_mask_select_blocks_bytes(src, B, Hkv) bytes, 256-byte aligned
+ *   dev_buf    device buffer of >= fa_block_mask_select_blocks_bytes(src, B, Hkv) bytes, 256-byte aligned; not the one that src lies in
  *   out        host struct, filled with pointers into dev_buf and src's document run arrays; may be src
  *   workspace  device, >= fa_block_mask_select_blocks_workspace_bytes(src, B, Hq, Hkv, d) bytes, 256-byte aligned, for one call at a time
  *              (NULL where that is 0: one query, up to 2048 key blocks)
  *   dev_status a page id of a visited block outside [0, n_pages_total) sets FA_ERR_DEVICE_CHECK; that block ranks lowest
  * Returns FA_ERR_INVALID_ARG (NULL, alignment, keep / first / last), FA_ERR_SHAPE (sizes, src->Bm), FA_ERR_UNSUPPORTED (src->Hm > 1, too
- * many blocks, d not in {64, 128}, B or Hq > 65535), FA_ERR_BUFFER_TOO_SMALL. */
+ * many blocks, more than 524280 query blocks, d not in {64, 128}, B or Hq > 65535), FA_ERR_BUFFER_TOO_SMALL. */
 FA_API size_t fa_block_mask_select_blocks_bytes(const fa_block_mask* src, int32_t B, int32_t Hkv);
 FA_API size_t fa_block_mask_select_blocks_workspace_bytes(const fa_block_mask* src, int32_t B, int32_t Hq, int32_t Hkv, int32_t d);
 FA_API fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, const void* bounds,

@@ -212,6 +212,9 @@ def test_choice_of_one_query(fa, B, lens, Hq, Hkv, d, page, keep, first, last, s
     (1, 300, 3, 3, 128, 7, 5, 11, 2, 1, [("causal",), ("prefix", 33), ("or",)]),
     (2, 640, 16, 2, 64, 128, 64, 2, 0, 0, [("true",)]),
     (3, 130, 2, 2, 64, 128, 128, 1, 0, 0, [("causal",)]),
+    (1, 300, 40, 2, 64, 128, 32, 3, 0, 1, [("causal",)]),        # 20 heads a group, few rows: each head's sums for itself
+    (1, 5000, 20, 2, 128, 16, 128, 6, 1, 1, [("causal",)]),      # 10 heads a group, many rows: divisions of 8 at most
+    (1, 1100, 2, 1, 64, 1, 64, 3, 0, 1, [("causal",)]),          # a query a row
 ])
 def test_choice_of_query_blocks(fa, B, Q, Hq, Hkv, d, bq, bk, keep, first, last, spec):
     rule = fa.make_mask_rule(spec)
@@ -265,6 +268,20 @@ def test_ties_go_to_the_lower_column(fa, Q):
     zero = torch.zeros_like(q)
     bm = fa.select_blocks(src, zero, box, 9, 2, 1)                                  # every score is 0
     same_tables(bm, ref.select(src.tables()["block_class"], zero, ref.Dense(box), 9, 2, 1, 128))
+
+
+@pytest.mark.parametrize("Q,n,Bk", [(1, 300, 16), (1, 2200, 8), (130, 300, 16), (70, 4200, 4), (200, 4200, 4)])
+def test_ties_of_long_rows(fa, Q, n, Bk):
+    # rows that more than one warp searches, with more equal scores than are sorted at hand: in shared memory and in the workspace
+    off = torch.full((1,), n * Bk - Q, dtype=torch.int32, device="cuda")
+    src = fa.create_block_mask(fa.make_mask_rule([("causal",)], q_offset=off), 1, 2, Q, n * Bk, 128, Bk)
+    q = bf((1, 2, Q, 64), 14, spread=False)
+    some = boxes((1, 1, 5, 2, 64), 15)
+    box = some[:, :, torch.arange(n, device="cuda") % 5].contiguous()
+    box[:, :, 17] = some[:, :, 0] * 2
+    for keep in (3, n // 7, n // 2, n - 3):
+        bm = fa.select_blocks(src, q, box, keep, 1, 1)
+        same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Dense(box), keep, 1, 1, 128))
 
 
 @pytest.mark.parametrize("Q", [1, 200])

@@ -79,7 +79,8 @@ def test_select_blocks_refusals(fa):
                 dict(table=P, pages=0, max_pages=4), dict(table=P, pages=8, max_pages=3)):
         assert call(**bad) == fa.ERR_SHAPE, bad
     wide = mask(fa, nk=32769, bk=1, kv_len=32769)
-    for bad in (dict(c=mask(fa, Hm=2)), dict(d=96), dict(c=wide), dict(B=65536), dict(Hq=65536, Hkv=65536)):
+    tall = mask(fa, nq=524281, bq=1, q_len=524281, nk=1, bk=128, kv_len=128)
+    for bad in (dict(c=mask(fa, Hm=2)), dict(d=96), dict(c=wide), dict(c=tall), dict(B=65536), dict(Hq=65536, Hkv=65536)):
         assert call(**bad) == fa.ERR_UNSUPPORTED, bad
     c = mask(fa)
     n = lib.fa_block_mask_select_blocks_bytes(ctypes.byref(c), 2, 2)
