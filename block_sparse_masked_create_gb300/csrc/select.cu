@@ -13,6 +13,7 @@
 // all fit are they scored again in 64 bits.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "fa_launch.h"
@@ -805,7 +806,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 4) choose_kernel(const __grid_constant__ SelectArgs a, int ranks) {
   namespace cg = cooperative_groups;
   using S = Scorer<D>;
-  constexpr int V = ExactQ<D>::V, kPanel = 32 * kWarps;  // columns that a CTA takes at a time
+  constexpr int V = ExactQ<D>::V, kSteps = 32 / S::kStep;  // steps of the scores a word of columns
   extern __shared__ __align__(8) uint32_t dyn[];
   __shared__ Zone s_zone;
   __shared__ float s_err[8 * kWarps];
@@ -820,8 +821,9 @@ __global__ void __launch_bounds__(kThreads, 4) choose_kernel(const __grid_consta
   const int want = a.keep - a.first - a.last, g = a.Hq / a.Hkv;
   if (ranks > 1) cg::this_cluster().barrier_arrive();  // every CTA of the cluster runs before the first one's memory is written
 
-  // classes and ids of the blocks, the first two panels' loads ahead of the queries'
-  const int i0 = rank * kWarps + warp, step = kWarps * ranks;
+  // classes and ids of the blocks, 32 columns (a word) at a time, the words in turn to the CTAs: visited blocks are neighbours, and every CTA
+  // gets its part of them. A warp's first two words' loads go ahead of the queries'.
+  const int i0 = rank + ranks * warp, step = ranks * kWarps;
   int cv[2], ci[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
@@ -851,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 4) choose_kernel(const __grid_consta
   auto note = [&](int i, int v, int id) {
     const int c = i * 32 + lane;
     const uint32_t some = __ballot_sync(kAll, v != FA_BLOCK_EMPTY), part = __ballot_sync(kAll, v == FA_BLOCK_PARTIAL);
-    if (v != FA_BLOCK_EMPTY && id < 0) report(a.status, FA_ERR_DEVICE_CHECK);
+    if (want > 0 && v != FA_BLOCK_EMPTY && id < 0) report(a.status, FA_ERR_DEVICE_CHECK);
     if (c < nk) M.key[c] = v != FA_BLOCK_EMPTY ? (uint32_t)id : (uint32_t)-2;  // until the score takes its place
     if (lane == 0) {
       M.wc[i] = M.wx[i] = some;
@@ -867,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 4) choose_kernel(const __grid_consta
   }
   __syncthreads();
 
-  // the scores, a panel's steps in turn to the warps
+  // the scores, the steps of this CTA's words in turn to the warps
   S sc;
 #pragma unroll
   for (int i = 0; i < 8; ++i) sc.q[i] = s_q[0][lane % S::LPB * 8 + i];
@@ -883,15 +885,14 @@ __global__ void __launch_bounds__(kThreads, 4) choose_kernel(const __grid_consta
         if (lane < 3) words[lane * M.nw + i] = M.wc[lane * M.nw + i];  // wc, wp, wx follow one another
     }
   }
-  for (int p0 = rank * kPanel; p0 < nk; p0 += kPanel * ranks) {
-    for (int c0 = p0 + warp * S::kStep; c0 < min(nk, p0 + kPanel); c0 += kWarps * S::kStep) {
-      const int c = c0 + lane;
-      const bool mine = lane < S::kStep && c < nk;
-      const int id = mine ? (int)M.key[c] : -2;
-      float s = -INFINITY;
-      if (want > 0 && __any_sync(kAll, id >= 0)) s = sc.scores(box, id);
-      if (mine) key[c] = id == -2 ? 0u : order_of(id >= 0 ? s : -INFINITY);
-    }
+  for (int t = warp;; t += kWarps) {
+    const int c = (rank + ranks * (t / kSteps)) * 32 + t % kSteps * S::kStep + lane;
+    if (c - lane >= nk) break;
+    const bool mine = lane < S::kStep && c < nk;
+    const int id = mine ? (int)M.key[c] : -2;
+    float s = -INFINITY;
+    if (want > 0 && __any_sync(kAll, id >= 0)) s = sc.scores(box, id);
+    if (mine) key[c] = id == -2 ? 0u : order_of(id >= 0 ? s : -INFINITY);
   }
   const float err = sc.magnitude();
   if (lane == 0) (ranks > 1 ? cg::this_cluster().map_shared_rank(s_err, 0) : s_err)[rank * kWarps + warp] = err;
@@ -1085,7 +1086,8 @@ cudaError_t launch_bounds_d(const BoundsArgs& a, cudaStream_t st) {
   if (!a.page_table) {
     key_bounds_kernel<D><<<dim3((a.kv_len + a.page - 1) / a.page, a.Hkv, a.B), kBoundThreads, 0, st>>>(a);
   } else {
-    const dim3 grid((unsigned)(((int64_t)a.N + 2 * a.page - 2) / a.page), a.Hkv, a.B);
+    // N tokens reach so many pages at most, wherever they begin
+    const dim3 grid((unsigned)std::min(((int64_t)a.N + 2 * a.page - 2) / a.page, (int64_t)a.max_pages), a.Hkv, a.B);
     if (a.k_scale) kv_bounds_fp8_kernel<D><<<grid, kBound8Threads, 0, st>>>(a);
     else kv_bounds_kernel<D><<<grid, kBoundThreads, 0, st>>>(a);
   }

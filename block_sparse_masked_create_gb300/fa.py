@@ -950,11 +950,11 @@ def select_blocks(src: BlockMask, q: torch.Tensor, bounds: torch.Tensor, keep: i
         _same(status, (1,), torch.int32, dev, "status")
     lib, ref = load(), ctypes.byref(c)
     size = _scratch(workspace, dev)
-    need = (B, Hq, Hkv, d, c.nq, c.nk, n)
+    need = (B, Hq, Hkv, d, c.Bm, c.Hm, n, c.kv_len, c.bq, c.bk)
     if src.select is None or src.select[0] != need:  # a layer's call after another's asks for the same sizes
         src.select = (need, lib.fa_block_mask_select_blocks_bytes(ref, B, Hkv),
                       lib.fa_block_mask_select_blocks_workspace_bytes(ref, B, Hq, Hkv, d))
-    _, n, scratch = src.select
+    _, n, scratch = src.select  # zeros: sizes that the call refuses
     if workspace is None and scratch:
         size = scratch
         workspace = buf.new_empty(size)

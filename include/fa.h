@@ -226,7 +226,8 @@ FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, voi
  * fa_flex_decode_fp8 for one query, the forwards and fa_flex_backward for query blocks). The choice itself has no gradient.
  *   src        host pointer to a mask with Hm = 1, Bm in {1, B} and at most 32768 key blocks
  *   q          device bf16 [B, Hq, Q_LEN, d] (the [Bz, Hq, d] of fa_flex_decode where Q_LEN = 1), 16-byte aligned; magnitudes under 2^110
- *              (else the choice of that query block is any of its candidates)
+ *              (else the choice of that query block is any of its candidates). Rows that pad a shorter request count like others: in a
+ *              query block with rows that matter they have to be zero, which adds nothing
  *   bounds     page_table NULL: device bf16 [B, Hkv, nk, 2, d] (fa_key_bounds); else device bf16 [n_pages_total, Hkv, 2, d]
  *              (fa_kv_bounds) with key block c of batch row b in page page_table[b * max_pages + c], max_pages >= nk, one page a block
  *   keep       >= 1;  first, last >= 0, first + last <= keep
@@ -234,7 +235,8 @@ FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, voi
  *   out        host struct, filled with pointers into dev_buf and src's document run arrays; may be src
  *   workspace  device, >= fa_block_mask_select_blocks_workspace_bytes(src, B, Hq, Hkv, d) bytes, 256-byte aligned, for one call at a time
  *              (NULL where that is 0: one query, up to 2048 key blocks)
- *   dev_status a page id of a visited block outside [0, n_pages_total) sets FA_ERR_DEVICE_CHECK; that block ranks lowest
+ *   dev_status a page id of a visited block outside [0, n_pages_total) sets FA_ERR_DEVICE_CHECK, and that block ranks lowest (page ids
+ *              are looked at where keep > first + last)
  * Returns FA_ERR_INVALID_ARG (NULL, alignment, keep / first / last), FA_ERR_SHAPE (sizes, src->Bm), FA_ERR_UNSUPPORTED (src->Hm > 1, too
  * many blocks, more than 524280 query blocks, d not in {64, 128}, B or Hq > 65535), FA_ERR_BUFFER_TOO_SMALL. */
 FA_API size_t fa_block_mask_select_blocks_bytes(const fa_block_mask* src, int32_t B, int32_t Hkv);

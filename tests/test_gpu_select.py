@@ -146,6 +146,20 @@ def test_page_bounds_out_of_range(fa):
     assert run([0, 0, 0, 0], [0, 0, 0, 0], 30)[0] == fa.OK
 
 
+def test_page_bounds_of_few_where_many_may_be_new(fa):
+    pages, _ = cache(6, 2, 16, 64, 12, False)
+    table = torch.tensor([[0, 1, 2], [5, 4, 3]], dtype=torch.int32, device="cuda")
+    t = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = fa.kv_bounds(pages, torch.zeros(6, 2, 2, 64, dtype=BF, device="cuda"), table, 2**31 - 1, t([40, 10]), t([8, 20]), status)
+    assert fa.check_status(status) == fa.OK
+    want = torch.zeros(6, 2, 2, 64, dtype=torch.float64)
+    for p, n in ((2, 16), (5, 16), (4, 14)):
+        x = pages[p, :, :n].double().cpu()
+        want[p] = torch.stack([x.amin(1), x.amax(1)], 1)
+    same_bounds(out, want)
+
+
 # ---------------------------------------------------------------------------------------------- the choice
 def same_tables(bm, cls):
     got, want = tables_np(bm), ref.tables(cls)
@@ -363,6 +377,25 @@ def test_missing_pages_rank_lowest_and_are_reported(fa, Q):
         bm = fa.select_blocks(src, q, box, keep, 0, 1, page_table=table, status=status)
         assert fa.check_status(status) == fa.ERR_DEVICE_CHECK
         same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Paged(box, table, src.c.nk), keep, 0, 1, src.c.bq))
+
+
+@pytest.mark.parametrize("Q", [1, 100])
+def test_pages_are_not_looked_at_where_nothing_is_scored(fa, Q):
+    src, q, box, table, _ = paged_case(fa, 2, [1000, 900], 4, 2, 64, 64, 42, Q=Q, bq=1 if Q == 1 else 64)
+    bad = torch.full_like(table, 10**6)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    bm = fa.select_blocks(src, q, box, 3, 1, 2, page_table=bad, status=status)
+    assert fa.check_status(status) == fa.OK
+    same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Paged(box, table, src.c.nk), 3, 1, 2, src.c.bq))
+
+
+def test_a_mask_built_anew_for_other_sizes(fa):
+    src = fa.create_block_mask(fa.make_mask_rule([("causal",)]), 1, 4, 512, 512, 64, 64)
+    for n in (512, 300, 129):
+        fa.recreate_block_mask(src, fa.make_mask_rule([("causal",)]), 1, 4, n, n, 64, 64)
+        q, box = bf((3, 4, n, 64), n, spread=False), boxes((3, 2, (n + 63) // 64, 2, 64), n + 1)
+        bm = fa.select_blocks(src, q, box, 3)
+        same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Dense(box), 3, 1, 1, 64))
 
 
 def test_bounds_past_32_bit_offsets(fa):
