@@ -7,10 +7,13 @@
 //            the queries. The sums over queries come first, so a block costs one product of 2 d, however many queries there are.
 //   choice   the first and last few blocks of the mask's row, and of the others those with the largest score, ties to the lower column.
 //
-// The choice is that of scores in 64 bits, but hardly any is computed in 64 bits: this GPU has two FP64 lanes an SM. Q+- are summed in
-// pairs of floats (an error of 2^-48), the scores in 32 bits with a bound e on their error. With T the K-th largest of these, the true
-// K-th largest lies within e of T, so blocks over T + 2 e are in, blocks under T - 2 e are out, and only where those in between do not
-// all fit are they scored again in 64 bits.
+// The choice is that of scores in 64 bits, but hardly any is computed so: this GPU has two FP64 lanes an SM. Q+- are sums of whole numbers
+// or of pairs of floats (an error of 2^-44 of their magnitudes), the scores 32-bit sums with a bound e on their error. With T the K-th
+// largest of these, the true K-th largest lies within e of T, so blocks over T + 2 e are in, blocks under T - 2 e are out, and only where
+// those in between do not all fit are they scored again, in pairs of floats (2^-44), or in 64 bits where those would leave their range.
+//
+// One query a request: choose_kernel alone. Query blocks: pool_kernel (the queries, read once: the bytes of the whole), choose_rows_kernel
+// (scores, search, rows of the table), then the transpose. Times are of one GB300, device time in a captured loop over four inputs.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -32,6 +35,8 @@ __device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v <<
 __device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
 // ------------------------------------------------------------------------------------------------ bounds of bf16 keys
+// A block is at most 128 rows, so every load of a CTA is in flight at once, 16 bytes a lane; two values a comparison. HBM bounds a large call:
+// 4 x 4096 keys, 16 heads, d = 128 (67 MB) in 11.6 us, 5.9 TB/s; 64 requests of one new token (512 pages of 64) 3.1 us, a launch.
 constexpr uint32_t kBfInf2 = 0x7F807F80u, kBfNegInf2 = 0xFF80FF80u;  // NaN keys propagate: min and max of them are NaN
 constexpr int kBoundThreads = 256;
 
@@ -148,7 +153,8 @@ __global__ void __launch_bounds__(kBoundThreads) kv_bounds_kernel(const __grid_c
 
 // ------------------------------------------------------------------------------------------------ bounds of e4m3 keys
 // A warp takes the 32 tokens of a scale: e4m3 orders as it is (in fp16, exactly), one multiplication by the scale at the end, rounded
-// outwards, and outwards again to bf16: with a power-of-two scale nothing is rounded.
+// outwards, and outwards again to bf16: with a power-of-two scale nothing is rounded. 8 x up to 2048 new tokens, 8 heads, pages of 128
+// (12 MB): 5.3 us, a launch and three loads that wait for one another (n_new, page id, keys).
 constexpr int kBound8Threads = 128;
 
 template <int D>
@@ -231,7 +237,7 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32, kPoolThreads = 64;
 
 // s + rest = s + x (+ rest): what the addition rounds off goes to rest
 __device__ __forceinline__ void add_exact(float& s, float& rest, float x) {
@@ -241,17 +247,21 @@ __device__ __forceinline__ void add_exact(float& s, float& rest, float x) {
 }
 // Sums of bf16 in whole numbers. For |x| < 2^E, x + C with C = 1.5 * 2^(E + 1) lies in C's binade, so its bits are C's plus x in units of
 // 2^(E - 22): an integer sum of the bits is exact, and with max(x, 0) + C = max(x + C, C) the sum of the positive ones takes two
-// operations more. What x + C rounds off (of magnitudes under 2^(E - 14)) is summed apart, where there is any. At most 256 values a lane.
+// operations more. What x + C rounds off (of magnitudes under 2^(E - 15)) is summed apart, where there is any. At most 256 values a lane.
+// Sums in pairs of floats took 7 dependent operations a value: 41 us for 4 x 4096 queries' choice against 37, 118 against 114 for 65536.
 struct BitSums {
   uint32_t all[8], pos[8];        // sums of the bits, C's own left in
-  float rest[8], rest_pos[8];     // what was rounded off
+  float* rest;                    // what was rounded off, of all and of the positive ones: [16], kPoolThreads apart. Seldom touched: in shared memory
   float c, under;                 // C and 2^E
   int n;                          // values so far
-  __device__ __forceinline__ void start() {
+  __device__ __forceinline__ float& off_all(int i) const { return rest[i * kPoolThreads]; }
+  __device__ __forceinline__ float& off_pos(int i) const { return rest[(8 + i) * kPoolThreads]; }
+  __device__ __forceinline__ void start(float* mine) {
+    rest = mine;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       all[i] = pos[i] = 0u;
-      rest[i] = rest_pos[i] = 0.f;
+      off_all(i) = off_pos(i) = 0.f;
     }
     c = under = 0.f;
     n = 0;
@@ -260,7 +270,7 @@ struct BitSums {
   // the sums as whole numbers of units, and another E for values up to `top`
   __device__ __forceinline__ void grow(float top) {
     const int ex = min((int)(__float_as_uint(top) >> 23), 251);  // top < 2^(ex - 126)
-    const float to = __uint_as_float((uint32_t)(ex + 2) << 23), u = unit();
+    const float to = __uint_as_float((uint32_t)(ex + 1) << 23), u = unit();
     const int k = min(31, (int)(__float_as_uint(to) >> 23) - (int)(__float_as_uint(under) >> 23));  // units are 2^k of the old ones
     const uint32_t was = __float_as_uint(c) * (uint32_t)n;
     under = to;
@@ -269,33 +279,41 @@ struct BitSums {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int a = (int)(all[i] - was), p = (int)(pos[i] - was);
-      rest[i] += (float)(a - (a >> k << k)) * u;
-      rest_pos[i] += (float)(p - (p >> k << k)) * u;
+      off_all(i) += (float)(a - (a >> k << k)) * u;
+      off_pos(i) += (float)(p - (p >> k << k)) * u;
       all[i] = (uint32_t)(a >> k) + now;
       pos[i] = (uint32_t)(p >> k) + now;
     }
   }
   __device__ __forceinline__ void add(uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float y[8], t[8];
-    bool off = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      y[e] = (e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
-      t[e] = __fadd_rn(y[e], c);
-      off = off || __fsub_rn(t[e], c) != y[e];
-      all[e] += __float_as_uint(t[e]);
-      pos[e] += __float_as_uint(fmaxf(t[e], c));
-    }
-    if (off) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = __fsub_rn(y[e], __fsub_rn(t[e], c));
-        rest[e] += d;
-        rest_pos[e] += y[e] > 0.f ? d : 0.f;
-      }
+      const float t = __fadd_rn((e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]), c);
+      all[e] += __float_as_uint(t);
+      pos[e] += __float_as_uint(fmaxf(t, c));
     }
     ++n;
+  }
+  // Magnitudes from here on, with 8 bits of their own, lose nothing
+  __device__ __forceinline__ float kept() const { return 128.f * unit(); }
+  // what add(v) rounds off
+  __device__ __forceinline__ void add_rest(uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float d[8];
+    bool any = false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = (e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
+      d[e] = __fsub_rn(y, __fsub_rn(__fadd_rn(y, c), c));
+      any = any || d[e] != 0.f;
+    }
+    if (!any) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      off_all(e) += d[e];
+      off_pos(e) += ((e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1])) > 0.f ? d[e] : 0.f;
+    }
   }
   // sum + rest, of all and of the positive values
   __device__ __forceinline__ void sums(int i, float& s, float& r, float& sp, float& rp) const {
@@ -303,20 +321,23 @@ struct BitSums {
     const int a = (int)(all[i] - own), p = (int)(pos[i] - own);
     const float u = unit();
     s = (float)(a >> 8) * (256.f * u);   // 22 + 8 bits: both parts are exact
-    r = rest[i] + (float)(a & 255) * u;
+    r = off_all(i) + (float)(a & 255) * u;
     sp = (float)(p >> 8) * (256.f * u);
-    rp = rest_pos[i] + (float)(p & 255) * u;
+    rp = off_pos(i) + (float)(p & 255) * u;
   }
 };
 
 // grid (nq, Hkv * parts, B): Q-, Q+ of one query block over at most 8 of a group's heads, in pairs of floats -> pooled [B, Hkv, nq, parts, 2 (sum,
-// rest), 2 D]. Two warps, half of the rows each: long enough a way through memory that the joining at its end costs little.
-constexpr int kPoolThreads = 64, kAhead = 8;
+// rest), 2 D]. Two warps, half of the rows each: long enough a way through memory that the joining at its end costs little. Fourteen CTAs an
+// SM: 2048 of them, the two large cases below, are all there at once. HBM and the instructions bound it about alike: 65536 queries of 16 heads
+// (268 MB) in 54 us, 5.0 TB/s, 59 % of the issue slots (the whole choice 109 us; with ten CTAs an SM, the rests in registers, 117).
+constexpr int kAhead = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constant__ SelectArgs a) {
+__global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes a row, rows a load
   __shared__ float s_sum[2][2 * D];
+  __shared__ float s_rest[16 * kPoolThreads];
   const int r = blockIdx.x, hk = blockIdx.y / a.parts, part = blockIdx.y % a.parts, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = lane % LPR;
   const int g = a.Hq / a.Hkv, h0 = hk * g + part * g / a.parts, h1 = hk * g + (part + 1) * g / a.parts;
@@ -325,23 +346,29 @@ __global__ void __launch_bounds__(kPoolThreads) pool_kernel(const __grid_constan
   const int mine = end > begin ? (end - begin + RPL - 1) / RPL : 0;  // rows of a head that this lane reads
   const int steps = (half + RPL - 1) / RPL;
   BitSums q;
-  q.start();
+  q.start(s_rest + tid);
   const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + (((size_t)b * a.Hq + h0) * a.q_len + i0 + begin) * D) + x;
   for (int h = h0; h < h1; ++h, src += (size_t)a.q_len * LPR) {
     for (int t = 0; t < steps; t += kAhead) {
       uint4 v[kAhead];
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) v[k] = t + k < mine ? __ldg(src + (t + k) * 32) : make_uint4(0, 0, 0, 0);
-      uint32_t top = 0u;  // largest magnitudes, two to a word
+      uint32_t top = 0u, low = kBfInf2;  // largest and smallest magnitudes, two to a word
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        top = bits_of(__hmax2(as_bf2(top), __habs2(as_bf2(v[k].x))));
-        top = bits_of(__hmax2(as_bf2(top), __habs2(as_bf2(v[k].y))));
-        top = bits_of(__hmax2(as_bf2(top), __habs2(as_bf2(v[k].z))));
-        top = bits_of(__hmax2(as_bf2(top), __habs2(as_bf2(v[k].w))));
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          top = bits_of(__hmax2(as_bf2(top), __habs2(as_bf2(w[j]))));
+          low = bits_of(__hmin2(as_bf2(low), __habs2(as_bf2(w[j]))));
+        }
       }
       const float most = fmaxf(bf_lo(top), bf_hi(top));
       if (most >= q.under) q.grow(most);
+      if (fminf(bf_lo(low), bf_hi(low)) < q.kept()) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) q.add_rest(v[k]);
+      }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) q.add(v[k]);
     }
@@ -613,7 +640,7 @@ struct ExactQ {
   float hi[V], lo[V];
 };
 
-// Exact score of a block, by a warp: products and sums in pairs of floats (2^-46 of the magnitudes), or where those could overflow or
+// Exact score of a block, by a warp: products and sums in pairs of floats (2^-44 of the magnitudes), or where those could overflow or
 // underflow (`wide`) in 64 bits.
 template <int D>
 __device__ __forceinline__ double exact_score(const __nv_bfloat16* box, const ExactQ<D>& q, bool wide) {
@@ -799,8 +826,10 @@ __device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const
 constexpr int kAlone = 128;
 
 // A cluster of `ranks` CTAs a row, grid (nq * ranks, Hkv, B): each scores its share of the blocks into the first one's shared memory, and
-// that one chooses. zone_words: shared memory for the scores near the border, or 0 (the workspace).
-constexpr int kZoneBlocks = 2048;  // rows of up to so many keep them in shared memory
+// that one chooses. 64 requests of 1k - 32k tokens, 8 KV heads, 32 blocks of up to 512 (76 MB of bounds): 29 us, 9 of them the classes, the
+// tables and the launch, 15 the scores (HBM: 11), 5 the search. Two requests of 131,072 tokens, 64 of 2048 blocks: 18 us with eight CTAs a
+// row (9, 3.5 and 6 of them; 20 with four CTAs); one of 600 tokens: 6 us.
+constexpr int kZoneBlocks = 2048;  // rows of up to so many keep the scores near the border in shared memory, longer ones in the workspace
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 4) choose_kernel(const __grid_constant__ SelectArgs a, int ranks) {
@@ -928,7 +957,8 @@ __global__ void __launch_bounds__(kThreads, 4) choose_kernel(const __grid_consta
 // ------------------------------------------------------------------------------------------------ rows of many query blocks
 // Eight neighbouring rows a CTA: a block's bounds are read and unpacked once for all of them (a lane holds 8 of its 2 d terms, and those of Q for
 // the eight rows), and the partial sums of the eight meet in a butterfly that halves the rows a lane still has with every step. Then a
-// warp a row. A warp for each (row, block) took 2.2 times the instructions.
+// warp a row. A warp for each (row, block) took 2.2 times the instructions. 65536 queries, 4 KV heads, 32 of up to 512 blocks: 47 us, 24 of
+// them the scores, 12 the search: the CTAs of long rows, whose warps wait for loads and for one another, two or one to an SM.
 constexpr int kRows = kWarps;
 
 __host__ __device__ constexpr size_t rows_pitch(int nk) { return row_words(nk, 1) | 1; }  // odd: the rows' keys of a column lie in different banks
