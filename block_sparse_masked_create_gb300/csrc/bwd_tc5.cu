@@ -6,7 +6,7 @@
 //   delta kernel; dV = P^T dO; dP = dO V^T; dS = P (dP - D) g with g = ds'/ds; dQ = scale dS K;
 //   dK = scale dS^T Q; dK and dV summed over the query heads of a KV head, without atomics.
 //
-// dK/dV kernel: one CTA (for chosen blocks, where a few columns are long, up to a cluster of four that share the
+// dK/dV kernel: one CTA (for chosen blocks, where a few columns are long, a cluster of two or four that share the
 // column and add their sums up) per (key block c, KV head, batch row). K_c and V_c stay in shared memory; the CTA
 // walks, for every query head of the group, the column of block c in the query-side transpose (full
 // blocks, then partial ones). Per query block, with the key rows in the TMEM lanes:
@@ -55,6 +55,7 @@ struct BwdTc5 {
   static constexpr int kQSmem = kQOffBar + 256;
   static_assert(kKvSmem <= 232448 && kQSmem <= 232448, "shared memory per CTA");
   static_assert(2 * 128 * (D + 4) * 4 <= kKvOffStat, "a CTA's sums of a shared column");
+  static_assert((kThreads + 1) * 4 <= kKvOffBar - kKvOffStat, "the columns' lengths");
 };
 
 // K-major operand tile (TMA box {64, 128} with the 128-byte swizzle): k-step ks (16 elements) starts at
@@ -142,6 +143,7 @@ __device__ __forceinline__ Bits128 rule_key_bits(const DevRule& R, int64_t j, in
 struct Tc5BwdParams {
   BwdArgs a;
   int ranks;  // dK/dV: CTAs (a cluster) that share a key block's column
+  bool by_length;  // dK/dV: the longest columns first
 };
 
 // The (query head, query block, partial?) of item k of the dK/dV walk over key block c: the query heads
@@ -195,7 +197,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) report(a.status, FA_ERR_DEVICE_CHECK);
     return;
   }
-  const int c = P.ranks > 1 ? blockIdx.x / P.ranks : blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
+  int c = P.ranks > 1 ? blockIdx.x / P.ranks : blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
+  if (P.by_length) {  // the longest columns of all heads, then the next: the t-th CTA (cluster) takes the x-th of its head's columns
+    const int nk = a.mask.nk, heads = a.Hkv * a.B, t = c + nk * (hk + a.Hkv * b), x = t / heads;
+    int* s_len = reinterpret_cast<int*>(smem + C::kKvOffStat);  // [kThreads], and the column
+    hk = t % heads % a.Hkv;
+    b = t % heads / a.Hkv;
+    const int mine = tid < nk ? kv_items(a, b, hk, tid) : 0;
+    s_len[tid] = mine;
+    __syncthreads();
+    if (tid < nk) {
+      int longer = 0;
+      for (int j = 0; j < nk; ++j) longer += s_len[j] > mine || (s_len[j] == mine && j < tid);
+      if (longer == x) s_len[kThreads] = tid;
+    }
+    __syncthreads();
+    c = s_len[kThreads];
+  }
   // this CTA's items of the column: from k_first on, n of them. A cluster's CTAs that the column is too short for leave at once.
   const int n_all = kv_items(a, b, hk, c);
   const int ranks = P.ranks > 1 ? min(P.ranks, max(1, (n_all + kFewItems - 1) / kFewItems)) : 1;
@@ -851,12 +869,22 @@ int launch_tc5(const BwdArgs& a, cudaStream_t st) {
     return FA_ERR_CUDA;
   kq<<<dim3(a.mask.nq, a.Hq, a.B), kThreads, C::kQSmem, st>>>(p, tq, tk, tv, tdo);
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  // Chosen blocks make long columns (the first blocks of a row are in every row). A column is nq * Hq / Hkv items at most, all of them are
-  // about nq * Hq / Hkv * row_max * Hkv * B: where the longest would outlast an SM's share, a cluster shares each column. One sequence of
-  // 8192, 16 / 4 heads, 16 of up to 64 blocks: 595 us with one CTA a column, 445 with two, 425 with three, 380 with four, 468 with eight
-  // (a cluster waits for as many free SMs of one part of the GPU).
-  const int64_t share = (int64_t)a.row_max * a.Hkv * a.B;
-  p.ranks = a.row_max == 0 || share >= 152 ? 1 : share >= 76 ? 2 : 4;
+  // Chosen blocks make long columns (the first blocks of a row are in every row): up to nq * g items, where all columns together are about
+  // nq * g * row_max * Hkv * B. With a CTA's start and end as long as ten items, `part` is an SM's share of all in lengths of the longest:
+  // where that is well under 1, the longest column outlasts the rest, and a cluster shares each column. Times of the whole backward, one /
+  // two / four CTAs a column, d = 128:
+  //   part 1.10  16,384 tokens, 16/8 heads, 16 blocks a row   890 /  988 / 1117 us
+  //   part 0.95    4096 tokens,  8/8 heads,  8 blocks         111 /  119 /  133
+  //   part 0.76  16,384 tokens, 32/8 heads, 12 blocks        1798 / 1611 / 1809
+  //   part 0.49    8192 tokens, 16/4 heads, 16 blocks         740 /  508 /  531
+  //   part 0.38    8192 tokens, 16/4 heads, 12 blocks         714 /  480 /  452
+  //   part 0.30    8192 tokens,  8/2 heads, 20 blocks         664 /  429 /  317
+  // Eight are slower than four (a cluster waits for as many free SMs of one part of the GPU).
+  const int g = a.Hq / a.Hkv;
+  const float part = (a.row_max + 10.f / g) * a.Hkv * a.B / 152.f;
+  p.ranks = a.row_max == 0 || a.mask.nq <= kFewItems / g || part > 0.85f ? 1 : part > 0.42f ? 2 : 4;
+  // The longest columns first, as far as a CTA finds its own with a thread a column (1394 -> 1131 us for 16,384 tokens, 16/8 heads, 24 blocks a row).
+  p.by_length = a.row_max > 0 && a.mask.nk <= kThreads;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.mask.nk * p.ranks, a.Hkv, a.B);
   cfg.blockDim = dim3(kThreads);

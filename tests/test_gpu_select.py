@@ -523,6 +523,40 @@ def test_forward_and_backward_over_the_choice(fa, B, N, Hq, Hkv, d, block, keep,
     assert torch.equal(oh, o.cpu()) and torch.equal(lh, lse.cpu())
 
 
+def blockwise(q, k, v, do, cls, scale):
+    """Gradients in 64 bits of one causal sequence over 128 x 128 blocks, a query block of a head at a time."""
+    g, N = q.shape[0] // k.shape[0], q.shape[1]
+    q, k, v, do = (x.double() for x in (q, k, v, do))
+    dq, dk, dv = (torch.zeros_like(x) for x in (q, k, v))
+    for h in range(q.shape[0]):
+        for r in range(cls.shape[1]):
+            i = torch.arange(r * 128, min(N, r * 128 + 128), device="cuda")
+            j = torch.cat([torch.arange(c * 128, min(N, c * 128 + 128), device="cuda") for c in np.flatnonzero(cls[h // g, r])])
+            kj, vj = k[h // g, j], v[h // g, j]
+            p = (q[h, i] @ kj.T * scale).masked_fill(j[None] > i[:, None], -math.inf).softmax(-1)
+            ds = do[h, i] @ vj.T
+            ds = p * (ds - (p * ds).sum(-1, keepdim=True)) * scale
+            dq[h, i] = ds @ kj
+            dk[h // g, j] += ds.T @ q[h, i]
+            dv[h // g, j] += p.T @ do[h, i]
+    return dq, dk, dv
+
+
+# columns of a key block that four CTAs share, two, none; more key blocks than a CTA puts in order of length
+@pytest.mark.parametrize("N,Hq,Hkv,d,keep", [(6000, 8, 2, 64, 9), (6100, 16, 4, 128, 14), (3000, 8, 8, 64, 8), (41000, 2, 1, 64, 4)])
+def test_gradients_of_long_columns(fa, N, Hq, Hkv, d, keep):
+    src = fa.create_block_mask(fa.make_mask_rule([("causal",)]), 1, Hq, N, N, 128, 128)
+    q, k, v, do = (bf((1, h, N, d), 180 + i, spread=False) for i, h in enumerate((Hq, Hkv, Hkv, Hq)))
+    bm = fa.select_blocks(src, q, fa.key_bounds(k), keep)
+    o, lse = fa.flex_forward(q, k, v, bm)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = fa.flex_backward(q, k, v, o, lse, do, bm, status=status)
+    again = fa.flex_backward(q, k, v, o, lse, do, bm)
+    assert fa.check_status(status) == fa.OK and all(torch.equal(x, y) for x, y in zip(got, again))
+    for x, w in zip(got, blockwise(q[0], k[0], v[0], do[0], bm.tables()["block_class"][0].cpu().numpy(), d**-0.5)):
+        assert float((x[0].double() - w).abs().max()) <= GRAD * float(w.abs().max())
+
+
 def test_gradient_over_the_choice_against_differences(fa):
     # the choice held fixed, as training does: f = sum(dout * O) along a direction
     N, d = 300, 64
