@@ -1127,9 +1127,10 @@ cudaError_t launch_bounds_d(const BoundsArgs& a, cudaStream_t st) {
 // Rows of many query blocks go eight to a CTA, as long as their keys fit in its shared memory; one row, and longer ones, take a CTA or more.
 constexpr int kRowsBlocks = 4096;
 
+// 48 KB without asking, the kernel's own 8 KB at most among them
 template <class K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
-  return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+  return bytes > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
 }
 
 template <int D>

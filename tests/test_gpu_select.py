@@ -298,6 +298,17 @@ def test_ties_of_long_rows(fa, Q, n, Bk):
         same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Dense(box), keep, 1, 1, 128))
 
 
+# rows whose keys fill about 48 KB of shared memory, which a kernel gets without asking, together with what it has of its own
+@pytest.mark.parametrize("Q,n,Bk", [(1, 2500, 8), (1, 9700, 4), (1, 9900, 4), (1, 10100, 4), (130, 1180, 4), (130, 1240, 4), (130, 1290, 4), (130, 1320, 4)])
+def test_rows_that_fill_shared_memory(fa, Q, n, Bk):
+    N = n * Bk
+    off = torch.tensor([N - Q], dtype=torch.int32, device="cuda")
+    src = fa.create_block_mask(fa.make_mask_rule([("causal",)], q_offset=off), 1, 2, Q, N, 1 if Q == 1 else 64, Bk)
+    q, box = bf((1, 2, Q, 64), n, spread=False), boxes((1, 1, n, 2, 64), n + 1)
+    bm = fa.select_blocks(src, q, box, 40)
+    same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Dense(box), 40, 1, 1, src.c.bq))
+
+
 @pytest.mark.parametrize("Q", [1, 200])
 def test_scores_that_32_bits_cannot_tell_apart(fa, Q):
     # large parts that cancel, and a small one that decides: 1 / 65536 of a channel against sums of 2^14
