@@ -1571,6 +1571,8 @@ fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, c
       ((reinterpret_cast<uintptr_t>(dev_buf) | reinterpret_cast<uintptr_t>(workspace)) & 255u))
     return FA_ERR_INVALID_ARG;
   if (buf_bytes < P.mask.total || workspace_bytes < P.total) return FA_ERR_BUFFER_TOO_SMALL;
+  const uintptr_t from = reinterpret_cast<uintptr_t>(dev_buf), cls = reinterpret_cast<uintptr_t>(src->block_class);
+  if (cls < from + P.mask.total && from < cls + (size_t)src->Bm * src->nq * src->nk) return FA_ERR_INVALID_ARG;  // read while dev_buf is written
   SelectArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = q;

@@ -951,10 +951,11 @@ def select_blocks(src: BlockMask, q: torch.Tensor, bounds: torch.Tensor, keep: i
     lib, ref = load(), ctypes.byref(c)
     size = _scratch(workspace, dev)
     need = (B, Hq, Hkv, d, c.Bm, c.Hm, n, c.kv_len, c.bq, c.bk)
-    if src.select is None or src.select[0] != need:  # a layer's call after another's asks for the same sizes
-        src.select = (need, lib.fa_block_mask_select_blocks_bytes(ref, B, Hkv),
-                      lib.fa_block_mask_select_blocks_workspace_bytes(ref, B, Hq, Hkv, d))
-    _, n, scratch = src.select  # zeros: sizes that the call refuses
+    sizes = src.select  # a layer's call after another's asks for the same ones
+    if sizes is None or sizes[0] != need:
+        sizes = src.select = (need, lib.fa_block_mask_select_blocks_bytes(ref, B, Hkv),
+                              lib.fa_block_mask_select_blocks_workspace_bytes(ref, B, Hq, Hkv, d))
+    _, n, scratch = sizes  # zeros: sizes that the call refuses
     if workspace is None and scratch:
         size = scratch
         workspace = buf.new_empty(size)

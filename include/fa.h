@@ -237,7 +237,7 @@ FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, voi
  *              (NULL where that is 0: one query, up to 2048 key blocks)
  *   dev_status a page id of a visited block outside [0, n_pages_total) sets FA_ERR_DEVICE_CHECK, and that block ranks lowest (page ids
  *              are looked at where keep > first + last)
- * Returns FA_ERR_INVALID_ARG (NULL, alignment, keep / first / last), FA_ERR_SHAPE (sizes, src->Bm), FA_ERR_UNSUPPORTED (src->Hm > 1, too
+ * Returns FA_ERR_INVALID_ARG (NULL, alignment, keep / first / last, src's classes in dev_buf), FA_ERR_SHAPE (sizes, src->Bm), FA_ERR_UNSUPPORTED (src->Hm > 1, too
  * many blocks, more than 524280 query blocks, d not in {64, 128}, B or Hq > 65535), FA_ERR_BUFFER_TOO_SMALL. */
 FA_API size_t fa_block_mask_select_blocks_bytes(const fa_block_mask* src, int32_t B, int32_t Hkv);
 FA_API size_t fa_block_mask_select_blocks_workspace_bytes(const fa_block_mask* src, int32_t B, int32_t Hq, int32_t Hkv, int32_t d);

@@ -97,6 +97,17 @@ def test_select_blocks_refusals(fa):
     assert lib.fa_block_mask_select_blocks_workspace_bytes(ctypes.byref(mask(fa)), 2, 3, 2, 64) == 0
 
 
+def test_select_blocks_refuses_the_buffer_that_it_reads(fa):
+    lib = fa.load()
+    c = mask(fa)
+    n = lib.fa_block_mask_select_blocks_bytes(ctypes.byref(c), 2, 2)
+    out = fa.BlockMaskC()
+    for at in (1 << 20, (1 << 20) + n - 1, (1 << 20) - c.Bm * c.nq * c.nk + 1):   # its first byte, its last, and classes that end on its first
+        c.block_class = at
+        assert lib.fa_block_mask_select_blocks(ctypes.byref(c), P, P, None, 0, 0, 2, 4, 2, 64, 3, 1, 1, ctypes.c_void_p(1 << 20), n, ctypes.byref(out),
+                                               ctypes.c_void_p(1 << 30), 1 << 30, None, None) == fa.ERR_INVALID_ARG
+
+
 def test_decode_takes_one_row_for_all_heads_or_one_for_each_kv_head(fa):
     lib = fa.load()
     for hm, code in ((3, fa.ERR_SHAPE), (8, fa.ERR_SHAPE), (2, fa.ERR_BUFFER), (1, fa.ERR_BUFFER)):
