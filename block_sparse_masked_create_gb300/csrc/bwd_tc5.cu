@@ -144,6 +144,7 @@ struct Tc5BwdParams {
   BwdArgs a;
   int ranks;  // dK/dV: CTAs (a cluster) that share a key block's column
   bool by_length;  // dK/dV: the longest columns first
+  bool overlap;    // dK/dV first, and dQ starts as soon as the last of its CTAs has
 };
 
 // The (query head, query block, partial?) of item k of the dK/dV walk over key block c: the query heads
@@ -197,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) report(a.status, FA_ERR_DEVICE_CHECK);
     return;
   }
+  if (P.overlap) cudaTriggerProgrammaticLaunchCompletion();
   int c = P.ranks > 1 ? blockIdx.x / P.ranks : blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
   if (P.by_length) {  // the longest columns of all heads, then the next: the t-th CTA (cluster) takes the x-th of its head's columns
     const int nk = a.mask.nk, heads = a.Hkv * a.B, t = c + nk * (hk + a.Hkv * b), x = t / heads;
@@ -845,6 +847,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc5_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  // dK/dV is done when this kernel is, for what comes after it: its last CTA waits
+  if (P.overlap && blockIdx.x == gridDim.x - 1 && blockIdx.y == gridDim.y - 1 && blockIdx.z == gridDim.z - 1) cudaGridDependencySynchronize();
 }
 
 template <int D, int SK>
@@ -867,36 +871,46 @@ int launch_tc5(const BwdArgs& a, cudaStream_t st) {
   if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kQSmem) != cudaSuccess ||
       cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kKvSmem) != cudaSuccess)
     return FA_ERR_CUDA;
-  kq<<<dim3(a.mask.nq, a.Hq, a.B), kThreads, C::kQSmem, st>>>(p, tq, tk, tv, tdo);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   // Chosen blocks make long columns (the first blocks of a row are in every row): up to nq * g items, where all columns together are about
-  // nq * g * row_max * Hkv * B. With a CTA's start and end as long as ten items, `part` is an SM's share of all in lengths of the longest:
-  // where that is well under 1, the longest column outlasts the rest, and a cluster shares each column. Times of the whole backward, one /
-  // two / four CTAs a column, d = 128:
-  //   part 1.10  16,384 tokens, 16/8 heads, 16 blocks a row   890 /  988 / 1117 us
-  //   part 0.95    4096 tokens,  8/8 heads,  8 blocks         111 /  119 /  133
-  //   part 0.76  16,384 tokens, 32/8 heads, 12 blocks        1798 / 1611 / 1809
-  //   part 0.49    8192 tokens, 16/4 heads, 16 blocks         740 /  508 /  531
-  //   part 0.38    8192 tokens, 16/4 heads, 12 blocks         714 /  480 /  452
-  //   part 0.30    8192 tokens,  8/2 heads, 20 blocks         664 /  429 /  317
-  // Eight are slower than four (a cluster waits for as many free SMs of one part of the GPU).
+  // nq * g * row_max * Hkv * B. So
+  //   - dK/dV goes first, and dQ, which does not need it, starts as soon as the last of its CTAs has: dQ's short CTAs fill the SMs that the
+  //     long columns leave (8192 tokens, 16/4 heads, 16 blocks a row: 508 -> 461 us; 16,384 tokens, 16/8 heads: 890 -> 840);
+  //   - the longest columns go first, as far as a CTA finds its own with a thread a column (16,384 tokens, 16/8 heads, 24 blocks: 1394 -> 1131);
+  //   - a cluster shares each column where the longest would outlast all the rest. With a CTA's start and end as long as ten items, `part` is an
+  //     SM's share of dK/dV in lengths of the longest column. Times of the whole backward, one / two / four CTAs a column, d = 128:
+  //       part 1.10  16,384 tokens, 16/8 heads, 16 blocks a row   840 /  975 / 1104 us
+  //       part 0.76  16,384 tokens, 32/8 heads, 12 blocks        1391 / 1599 / 1795
+  //       part 0.59  16,384 tokens, 16/4 heads, 20 blocks        1193 / 1133 / 1253
+  //       part 0.49    8192 tokens, 16/4 heads, 16 blocks         602 /  460 /  517
+  //       part 0.38    8192 tokens, 16/4 heads, 12 blocks         600 /  387 /  436
+  //       part 0.22  32,768 tokens,  8/1 heads, 32 blocks        3918 / 2178 / 1620
+  //     Eight are slower than four (a cluster waits for as many free SMs of one part of the GPU).
   const int g = a.Hq / a.Hkv;
   const float part = (a.row_max + 10.f / g) * a.Hkv * a.B / 152.f;
-  p.ranks = a.row_max == 0 || a.mask.nq <= kFewItems / g || part > 0.85f ? 1 : part > 0.42f ? 2 : 4;
-  // The longest columns first, as far as a CTA finds its own with a thread a column (1394 -> 1131 us for 16,384 tokens, 16/8 heads, 24 blocks a row).
+  p.ranks = a.row_max == 0 || a.mask.nq <= kFewItems / g || part > 0.65f ? 1 : part > 0.33f ? 2 : 4;
   p.by_length = a.row_max > 0 && a.mask.nk <= kThreads;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.mask.nk * p.ranks, a.Hkv, a.B);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kKvSmem;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = p.ranks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = p.ranks > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kk, p, tq, tk, tv, tdo) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  p.overlap = a.row_max > 0;
+  const auto launch = [&](auto kernel, dim3 grid, int smem, cudaLaunchAttributeID id, int value) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1] = {};
+    at[0].id = id;
+    if (id == cudaLaunchAttributeClusterDimension) at[0].val.clusterDim = {(unsigned)value, 1, 1};
+    else at[0].val.programmaticStreamSerializationAllowed = value;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p, tq, tk, tv, tdo) == cudaSuccess;
+  };
+  const auto launch_kv = [&]() {
+    return launch(kk, dim3(a.mask.nk * p.ranks, a.Hkv, a.B), C::kKvSmem, cudaLaunchAttributeClusterDimension, p.ranks);
+  };
+  const auto launch_q = [&]() {
+    return launch(kq, dim3(a.mask.nq, a.Hq, a.B), C::kQSmem, cudaLaunchAttributeProgrammaticStreamSerialization, p.overlap ? 1 : 0);
+  };
+  return (p.overlap ? launch_kv() && launch_q() : launch_q() && launch_kv()) ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace

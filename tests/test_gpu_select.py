@@ -568,6 +568,34 @@ def test_gradients_of_long_columns(fa, N, Hq, Hkv, d, keep):
         assert float((x[0].double() - w).abs().max()) <= GRAD * float(w.abs().max())
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 16)])
+def test_what_follows_a_backward_reads_whole_gradients(fa, Hq, Hkv):
+    # captured with the copies that follow it, and eagerly on a side stream: dQ's kernel starts before that of dK and dV has ended
+    N, d = 2500, 128
+    src = fa.create_block_mask(fa.make_mask_rule([("causal",)]), 1, Hq, N, N, 128, 128)
+    q, k, v, do = (bf((1, h, N, d), 280 + i, spread=False) for i, h in enumerate((Hq, Hkv, Hkv, Hq)))
+    bm = fa.select_blocks(src, q, fa.key_bounds(k), 5)
+    o, lse = fa.flex_forward(q, k, v, bm)
+    want = fa.flex_backward(q, k, v, o, lse, do, bm)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        for _ in range(3):
+            got = [x.clone() for x in fa.flex_backward(q, k, v, o, lse, do, bm)]
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grads = fa.flex_backward(q, k, v, o, lse, do, bm)
+        copies = [x.clone() for x in grads]
+        for x in grads:
+            x.fill_(math.nan)               # the next replay has to write all of them again
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(copies, want))
+
+
 def test_gradient_over_the_choice_against_differences(fa):
     # the choice held fixed, as training does: f = sum(dout * O) along a direction
     N, d = 300, 64
