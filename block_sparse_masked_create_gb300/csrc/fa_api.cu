@@ -1541,7 +1541,7 @@ static int select_blocks_plan(const fa_block_mask* src, int32_t B, int32_t Hq, i
   // (and among divisions of 8 heads at most)
   P->parts = src->q_len == 1 ? 0 : rows < 2 * 152 ? Hq / Hkv : (Hq / Hkv + 7) / 8;
   P->off_zone = align256(rows * P->parts * 4 * d * sizeof(float));
-  P->total = P->off_zone + (select_needs_zone(src->nq, src->nk) ? align256(rows * src->nk * sizeof(uint64_t)) : 0);
+  P->total = P->off_zone + (select_needs_zone((int64_t)rows, src->nq, src->nk) ? align256(rows * src->nk * sizeof(uint64_t)) : 0);
   return FA_OK;
 }
 

@@ -270,7 +270,7 @@ struct SelectArgs {
   uint64_t* zone;            // [B, Hkv, nq, nk]
   int32_t* status;
 };
-bool select_needs_zone(int32_t nq, int32_t nk);
+bool select_needs_zone(int64_t rows, int32_t nq, int32_t nk);
 int select_ranks(int64_t rows, int32_t nk);
 cudaError_t launch_select_blocks(const SelectArgs& a, cudaStream_t st);
 

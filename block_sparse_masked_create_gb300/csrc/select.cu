@@ -12,8 +12,8 @@
 // largest of these, the true K-th largest lies within e of T, so blocks over T + 2 e are in, blocks under T - 2 e are out, and only where
 // those in between do not all fit are they scored again, in pairs of floats (2^-44), or in 64 bits where those would leave their range.
 //
-// One query a request: choose_kernel alone. Query blocks: pool_kernel (the queries, read once: the bytes of the whole), choose_rows_kernel
-// (scores, search, rows of the table), then the transpose. Times are of one GB300, device time in a captured loop over four inputs.
+// One query a request: choose_kernel alone. Query blocks: pool_kernel (the queries, read once: the bytes of the whole), choose_kernel or, for many
+// rows, choose_rows_kernel (scores, search, rows of the table), then the transpose. Times are of one GB300, device time in a captured loop over four inputs.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -822,7 +822,8 @@ __device__ __forceinline__ void write_row(const SelectArgs& a, size_t row, const
   }
 }
 
-// Rows of up to kAlone blocks are searched by one warp: the steps are too short for barriers.
+// Rows of up to kAlone blocks are searched by one warp: the steps are too short for barriers (one request of 600 tokens: 6.0 us, by all eight warps 6.4; 64
+// requests, rows of up to 512 blocks: 32.4 us by one warp, 29.4 by eight).
 constexpr int kAlone = 128;
 
 // A cluster of `ranks` CTAs a row, grid (nq * ranks, Hkv, B): each scores its share of the blocks into the first one's shared memory, and
@@ -1124,8 +1125,15 @@ cudaError_t launch_bounds_d(const BoundsArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-// Rows of many query blocks go eight to a CTA, as long as their keys fit in its shared memory; one row, and longer ones, take a CTA or more.
-constexpr int kRowsBlocks = 4096;
+// Rows of query blocks go eight to a CTA, as long as their keys fit in its shared memory and there are more rows than CTAs with one each would
+// run at once (four an SM); fewer or longer ones take a CTA or more each. The whole choice, one row / eight rows a CTA, d = 128:
+//   256 rows of up to  64 blocks (8192 queries, 4 KV heads)     20.2 / 24.1 us
+//   512 rows of up to 256 blocks (32,768 queries, 2 KV heads)   36.6 / 45.2
+//  1024 rows of up to 128 blocks (16,384 queries, 8 KV heads)   35.6 / 32.5
+//  2048 rows of up to  32 blocks (4 x 4096 queries, 16 heads)   44.5 / 34.7
+//  2048 rows of up to 512 blocks (65,536 queries, 4 KV heads)    125 / 109
+constexpr int kRowsBlocks = 4096, kAtOnce = 4 * 152;
+bool rows_together(int64_t rows, int32_t nq, int32_t nk) { return nq > 1 && nk <= kRowsBlocks && rows > kAtOnce; }
 
 // 48 KB without asking, the kernel's own 8 KB at most among them
 template <class K>
@@ -1141,7 +1149,7 @@ cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t st) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const int64_t rows = (int64_t)a.B * a.Hkv * a.nq;
-  if (a.nq > 1 && a.nk <= kRowsBlocks) {
+  if (rows_together(rows, a.nq, a.nk)) {
     const size_t smem = kRows * rows_pitch(a.nk) * 4;
     if ((e = allow_smem(choose_rows_kernel<D>, smem)) != cudaSuccess) return e;
     choose_rows_kernel<D><<<dim3(a.Hkv, (a.nq + kRows - 1) / kRows, a.B), kThreads, smem, st>>>(a);
@@ -1170,12 +1178,13 @@ cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t st) {
 }  // namespace
 
 // whether the choice needs the workspace for scores near the border
-bool select_needs_zone(int32_t nq, int32_t nk) { return nk > kZoneBlocks || (nq > 1 && nk <= kRowsBlocks); }
+bool select_needs_zone(int64_t rows, int32_t nq, int32_t nk) { return nk > kZoneBlocks || rows_together(rows, nq, nk); }
 
-// CTAs that share the blocks of one row
+// CTAs that share the blocks of one row: as many as run at once, each with a step of the scores for every warp. 512 rows of up to 512 blocks: 29 us with
+// one CTA each, 37 with two, which take two rounds; 16 rows of 2048 blocks: 18.3 us with eight, 19.7 with four.
 int select_ranks(int64_t rows, int32_t nk) {
   int n = 1;
-  while (n < 8 && 2 * n * rows <= 4 * 152 && nk >= 128 * n) n *= 2;
+  while (n < 8 && 2 * n * rows <= kAtOnce && nk >= 128 * n) n *= 2;
   return n;
 }
 
