@@ -1567,6 +1567,8 @@ fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, c
   if (P.total && !workspace) return FA_ERR_INVALID_ARG;
   if (!src->block_class || keep < 1 || first < 0 || last < 0 || (int64_t)first + last > keep) return FA_ERR_INVALID_ARG;
   if (page_table && (n_pages_total < 1 || max_pages < src->nk)) return FA_ERR_SHAPE;
+  // one offset for all batch rows: the result has a row set for each, and its offsets would be read for each
+  if (src->rule.q_offset && src->Bm == 1 && B > 1) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(bounds) || !words_aligned({page_table, dev_status}) ||
       ((reinterpret_cast<uintptr_t>(dev_buf) | reinterpret_cast<uintptr_t>(workspace)) & 255u))
     return FA_ERR_INVALID_ARG;

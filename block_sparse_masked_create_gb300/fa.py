@@ -919,7 +919,7 @@ def select_blocks_workspace_bytes(src: BlockMask, B: int, Hq: int, Hkv: int, d: 
 def select_blocks(src: BlockMask, q: torch.Tensor, bounds: torch.Tensor, keep: int, first: int = 1, last: int = 1,
                   page_table: Optional[torch.Tensor] = None, out: Optional[BlockMask] = None,
                   workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None) -> BlockMask:
-    """fa_block_mask_select_blocks: from each row of src (Hm = 1), for each request and KV head, at most `keep` of the blocks it visits:
+    """fa_block_mask_select_blocks: from each row of src (Hm = 1; with a q_offset Bm = B), for each request and KV head, at most `keep` of the blocks it visits:
     the first `first`, the last `last`, and of the others those with the largest bound on <q, k>, summed over the query block's rows
     and the heads of the group. q [B,Hq,Q_LEN,d] bf16 (or [B,Hq,d] for one query); bounds [B,Hkv,nk,2,d] of key_bounds, or with a
     page_table int32 [B,max_pages] (one page a block) [P,Hkv,2,d] of kv_bounds. Returns a mask with Bm = B, Hm = Hkv for flex_decode,

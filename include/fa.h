@@ -224,7 +224,8 @@ FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, voi
  * The result is src's mask with the other blocks empty: classes, row lists, query-side transpose and row order as
  * fa_create_block_mask would lay them out, with Bm = B, Hm = Hkv, for every attention entry point (fa_flex_decode and
  * fa_flex_decode_fp8 for one query, the forwards and fa_flex_backward for query blocks). The choice itself has no gradient.
- *   src        host pointer to a mask with Hm = 1, Bm in {1, B} and at most 32768 key blocks
+ *   src        host pointer to a mask with Hm = 1, Bm in {1, B} and at most 32768 key blocks. With a q_offset in its rule Bm = B: the
+ *              result reads q_offset[b] for each b
  *   q          device bf16 [B, Hq, Q_LEN, d] (the [Bz, Hq, d] of fa_flex_decode where Q_LEN = 1), 16-byte aligned; magnitudes under 2^110
  *              (else the choice of that query block is any of its candidates). Rows that pad a shorter request count like others: in a
  *              query block with rows that matter they have to be zero, which adds nothing
@@ -237,8 +238,8 @@ FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, voi
  *              (NULL where that is 0: one query, up to 2048 key blocks)
  *   dev_status a page id of a visited block outside [0, n_pages_total) sets FA_ERR_DEVICE_CHECK, and that block ranks lowest (page ids
  *              are looked at where keep > first + last)
- * Returns FA_ERR_INVALID_ARG (NULL, alignment, keep / first / last, src's classes in dev_buf), FA_ERR_SHAPE (sizes, src->Bm), FA_ERR_UNSUPPORTED (src->Hm > 1, too
- * many blocks, more than 524280 query blocks, d not in {64, 128}, B or Hq > 65535), FA_ERR_BUFFER_TOO_SMALL. */
+ * Returns FA_ERR_INVALID_ARG (NULL, alignment, keep / first / last, src's classes in dev_buf, a q_offset where src->Bm = 1 < B), FA_ERR_SHAPE
+ * (sizes, src->Bm), FA_ERR_UNSUPPORTED (src->Hm > 1, too many blocks, more than 524280 query blocks, d not in {64, 128}, B or Hq > 65535), FA_ERR_BUFFER_TOO_SMALL. */
 FA_API size_t fa_block_mask_select_blocks_bytes(const fa_block_mask* src, int32_t B, int32_t Hkv);
 FA_API size_t fa_block_mask_select_blocks_workspace_bytes(const fa_block_mask* src, int32_t B, int32_t Hq, int32_t Hkv, int32_t d);
 FA_API fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, const void* bounds,

@@ -1,0 +1,27 @@
+"""Source masks and buffers that the choice of blocks refuses. No GPU is needed."""
+import ctypes
+
+import pytest
+
+from test_select_abi import P, fa, mask  # noqa: F401 (fa is a fixture)
+
+BIG = ctypes.c_void_p(1 << 20)
+
+
+def choose(fa, c, B=2, buf=BIG, n=1 << 40):  # noqa: F811
+    out = fa.BlockMaskC()
+    return fa.load().fa_block_mask_select_blocks(ctypes.byref(c), P, P, None, 0, 0, B, 4, 2, 64, 3, 1, 1, buf, n, ctypes.byref(out), BIG, 1 << 40, None, None)
+
+
+@pytest.mark.parametrize("q_len,nq,bq", [(256, 2, 128), (1, 1, 1)])
+def test_one_offset_for_several_batch_rows(fa, q_len, nq, bq):  # noqa: F811
+    # the result would have a row set for each batch row and read an offset for each: there is one
+    c = mask(fa, nq=nq, q_len=q_len, bq=bq)
+    c.rule.q_offset = 4096
+    for B in (2, 4, 65535):
+        assert choose(fa, c, B) == fa.ERR_INVALID_ARG, B
+    # one batch row, and an offset for each: the next check answers
+    assert choose(fa, c, 1, n=0) == fa.ERR_BUFFER
+    c = mask(fa, nq=nq, q_len=q_len, bq=bq, Bm=2)
+    c.rule.q_offset = 4096
+    assert choose(fa, c, 2, n=0) == fa.ERR_BUFFER
