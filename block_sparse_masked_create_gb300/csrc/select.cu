@@ -333,6 +333,9 @@ struct BitSums {
 // (268 MB) in 54 us, 5.0 TB/s, 59 % of the issue slots (the whole choice 109 us; with ten CTAs an SM, the rests in registers, 117).
 constexpr int kAhead = 8;
 
+// the first of a group's g heads that division `part` takes: part * g passes 32 bits for groups of 46,341 heads and more
+__device__ __forceinline__ int first_head(int part, int g, int parts) { return (int)((int64_t)part * g / parts); }
+
 template <int D>
 __global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes a row, rows a load
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_con
   __shared__ float s_rest[16 * kPoolThreads];
   const int r = blockIdx.x, hk = blockIdx.y / a.parts, part = blockIdx.y % a.parts, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = lane % LPR;
-  const int g = a.Hq / a.Hkv, h0 = hk * g + part * g / a.parts, h1 = hk * g + (part + 1) * g / a.parts;
+  const int g = a.Hq / a.Hkv, h0 = hk * g + first_head(part, g, a.parts), h1 = hk * g + first_head(part + 1, g, a.parts);
   const int i0 = r * a.bq, rows = min(a.bq, a.q_len - i0), half = (rows + 1) / 2;
   const int begin = warp * half + lane / LPR, end = min(rows, warp * half + half);
   const int mine = end > begin ? (end - begin + RPL - 1) / RPL : 0;  // rows of a head that this lane reads
