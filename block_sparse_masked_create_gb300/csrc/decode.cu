@@ -59,8 +59,9 @@ __global__ void __launch_bounds__(kDecWarps * 32)
   const DevMask& M = a.mask;
   const int bm = M.Bm > 1 ? b : 0;
   const size_t mrow = (size_t)bm * M.Hm + (M.Hm > 1 ? hk : 0);  // Hm is 1 or Hkv, nq == 1
-  const int n_full = __ldg(M.full_kv_num + mrow), n_part = __ldg(M.kv_num + mrow);
-  const int n_vis = n_full + n_part;
+  const int n_full = __ldg(M.full_kv_num + mrow), listed = n_full + __ldg(M.kv_num + mrow);
+  const int n_vis = min(listed, a.n_splits * a.pages_per_split);  // a row may not list more than the mask's row_max says
+  if (listed > n_vis && s == 0 && tid == 0) report(a.status, FA_ERR_DEVICE_CHECK);
   const int e0 = s * a.pages_per_split;
   const size_t hq0 = (size_t)b * a.Hq + (size_t)hk * g;
   if (e0 >= n_vis) {  // nothing here: the combine never reads it, and a request without any key is written by split 0
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const __grid_consta
   const int hq = blockIdx.x, b = blockIdx.y;
   const DevMask& M = a.mask;
   const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, hq);
-  const int n_vis = __ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow);
+  const int n_vis = min(__ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow), a.n_splits * a.pages_per_split);
   if (n_vis <= a.pages_per_split) return;  // written by its one split
   const int ns = (n_vis + a.pages_per_split - 1) / a.pages_per_split;
   const size_t base = ((size_t)b * a.Hq + hq) * (size_t)a.n_splits;

@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(kWarps * 32, Cfg<D>::kCtas)
   const DevMask& M = a.mask;
   const int bm = M.Bm > 1 ? b : 0;
   const size_t mrow = (size_t)bm * M.Hm + (M.Hm > 1 ? hk : 0);  // Hm is 1 or Hkv, nq == 1
-  const int n_full = __ldg(M.full_kv_num + mrow), n_vis = n_full + __ldg(M.kv_num + mrow);
+  const int n_full = __ldg(M.full_kv_num + mrow), listed = n_full + __ldg(M.kv_num + mrow);
+  const int n_vis = min(listed, a.n_splits * a.pages_per_split);  // a row may not list more than the mask's row_max or its rule says
+  if (listed > n_vis && s == 0 && tid == 0) report(a.status, FA_ERR_DEVICE_CHECK);
   const int e0 = s * a.pages_per_split;
   const size_t hq0 = (size_t)b * a.Hq + (size_t)hk * g;
   if (e0 >= n_vis) {  // nothing here: the join never reads it, and a request without any key is written by span 0
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(kJoin * D) decode_fp8_join_kernel(const __grid
   const int hq = blockIdx.x, b = blockIdx.y, col = threadIdx.x % D, part = threadIdx.x / D;
   const DevMask& M = a.mask;
   const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, hq);
-  const int n_vis = __ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow);
+  const int n_vis = min(__ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow), a.n_splits * a.pages_per_split);
   if (n_vis <= a.pages_per_split) return;
   const int ns = (n_vis + a.pages_per_split - 1) / a.pages_per_split;
   const size_t base = ((size_t)b * a.Hq + hq) * (size_t)a.n_splits, obase = ((size_t)b * a.Hq + hq) * D;

@@ -139,7 +139,9 @@ typedef struct {
                                dQ kernel take their query blocks in this order. NULL (one row per table):
                                rows nq-1 .. 0. Tables of more than 2048 key blocks keep nq-1 .. 0 too. */
   fa_mask_rule rule;
-  int32_t row_max;          /* the most blocks a row lists, where the builder knows (fa_block_mask_select_blocks); 0: not known */
+  int32_t row_max;          /* the most blocks a row lists, where the builder knows (fa_block_mask_select_blocks); 0: not known. The
+                               decodes lay out their work by it: of a row that lists more they leave out blocks, and set
+                               FA_ERR_DEVICE_CHECK. Whoever changes tables by hand sets it to 0 */
 } fa_block_mask;
 
 /* Bytes of device buffer fa_create_block_mask needs for these sizes (0 on invalid arguments). */
