@@ -535,6 +535,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   }
+  // All of an SM's tensor memory goes back before this CTA waits for others of its cluster: one of them may wait for the tensor memory of an SM that
+  // a CTA of another cluster holds, which in turn waits for one here.
+  tc5_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc5_fence_after();
+    tmem_dealloc(tmem, C::kTmemCols);
+  }
   if (ranks > 1) {
     // the cluster's shares added up in the order of the ranks, a part of the key rows by each
     namespace cg = cooperative_groups;
@@ -561,12 +569,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
     cl.sync();  // no CTA leaves while another reads its shared memory
-  }
-  tc5_fence_before();
-  __syncthreads();
-  if (warp == kMmaWarp) {
-    tc5_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
