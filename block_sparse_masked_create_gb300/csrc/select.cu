@@ -271,7 +271,8 @@ struct BitSums {
   __device__ __forceinline__ void grow(float top) {
     const int ex = min((int)(__float_as_uint(top) >> 23), 251);  // top < 2^(ex - 126)
     const float to = __uint_as_float((uint32_t)(ex + 1) << 23), u = unit();
-    const int k = min(31, (int)(__float_as_uint(to) >> 23) - (int)(__float_as_uint(under) >> 23));  // units are 2^k of the old ones
+    const int jump = (int)(__float_as_uint(to) >> 23) - (int)(__float_as_uint(under) >> 23);  // units are 2^jump of the old ones
+    const int k = min(31, jump);
     const uint32_t was = __float_as_uint(c) * (uint32_t)n;
     under = to;
     c = 3.f * to;
@@ -279,10 +280,11 @@ struct BitSums {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int a = (int)(all[i] - was), p = (int)(pos[i] - was);
-      off_all(i) += (float)(a - (a >> k << k)) * u;
-      off_pos(i) += (float)(p - (p >> k << k)) * u;
-      all[i] = (uint32_t)(a >> k) + now;
-      pos[i] = (uint32_t)(p >> k) + now;
+      const int a_up = jump > 31 ? 0 : a >> k, p_up = jump > 31 ? 0 : p >> k;  // past 31 a sum, of either sign, is less than one unit: all of it is rest
+      off_all(i) += (float)(a - (a_up << k)) * u;
+      off_pos(i) += (float)(p - (p_up << k)) * u;
+      all[i] = (uint32_t)a_up + now;
+      pos[i] = (uint32_t)p_up + now;
     }
   }
   __device__ __forceinline__ void add(uint4 v) {
