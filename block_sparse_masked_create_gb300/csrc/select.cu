@@ -245,6 +245,17 @@ __device__ __forceinline__ void add_exact(float& s, float& rest, float x) {
   rest = __fadd_rn(rest, __fadd_rn(__fsub_rn(s, __fsub_rn(t, u)), __fsub_rn(x, u)));
   s = t;
 }
+// The same, with s the sum rounded once however many terms there were: the scores in 32 bits take s alone, and their bound counts one rounding. (A
+// running s is off by half a step for each term, and what rest itself rounds off grows with their number squared.)
+__device__ __forceinline__ void add_joined(float& s, float& rest, float x) {
+  add_exact(s, rest, x);
+  float t = s, off = 0.f;
+  add_exact(t, off, rest);
+  if (t - t == 0.f) {  // infinities and NaN stay as they are
+    s = t;
+    rest = off;
+  }
+}
 // Sums of bf16 in whole numbers. For |x| < 2^E, x + C with C = 1.5 * 2^(E + 1) lies in C's binade, so its bits are C's plus x in units of
 // 2^(E - 22): an integer sum of the bits is exact, and with max(x, 0) + C = max(x + C, C) the sum of the positive ones takes two
 // operations more. What x + C rounds off (of magnitudes under 2^(E - 15)) is summed apart, where there is any. At most 256 values a lane.
@@ -711,7 +722,7 @@ __device__ void search_row(const SelectArgs& a, uint64_t* zone, const Boxes<D>& 
         }
       };
       const float t = value_of(grp.kth(each, want));
-      // Q rounded (twice), a product in 13 steps; the rest is for the rounding of the bound itself
+      // Q rounded (its parts and their sum), a product in 13 steps; the rest is for the rounding of the bound itself
       const float e2 = 2.f * fmaf(17.f * 5.9604644775390625e-8f, err, 1e-42f);
       Border bd{t + e2, t - e2, 0, 0};
       int m = 0, z = 0;
@@ -873,13 +884,13 @@ __global__ void __launch_bounds__(kThreads, 4) choose_kernel(const __grid_consta
 #pragma unroll 4
       for (int h = 0; h < g; ++h) {
         const float x = __bfloat162float(src[(size_t)h * D]);
-        add_exact(s, rest, threadIdx.x < D ? min_nan(x, 0.f) : max_nan(x, 0.f));
+        add_joined(s, rest, threadIdx.x < D ? min_nan(x, 0.f) : max_nan(x, 0.f));
       }
     } else {
       for (int p = 0; p < a.parts; ++p) {
         const float* src = a.pooled + (row * a.parts + p) * 4 * D + threadIdx.x;
         rest = __fadd_rn(rest, __ldg(src + 2 * D));
-        add_exact(s, rest, __ldg(src));
+        add_joined(s, rest, __ldg(src));
       }
     }
     s_q[0][threadIdx.x] = s;
@@ -1008,10 +1019,8 @@ __global__ void __launch_bounds__(kThreads, 2) choose_rows_kernel(const __grid_c
         const float4 u = __ldg(src), v = __ldg(src + 1);
         const float t[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) add_exact(q[k][e], lo[e], t[e]);
+        for (int e = 0; e < 8; ++e) add_joined(q[k][e], lo[e], t[e]);
       }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[k][e] += lo[e];
     }
   }
   const int slot = ((lane & O) ? 4 : 0) + ((lane & (O / 2)) ? 2 : 0) + ((lane & (O / 4)) ? 1 : 0);  // the row whose sum ends up here
@@ -1109,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, 2) choose_rows_kernel(const __grid_c
 #pragma unroll
       for (int e = 0; e < V; ++e) {
         x.lo[e] = __fadd_rn(x.lo[e], __ldg(src + 2 * D + e));
-        add_exact(x.hi[e], x.lo[e], __ldg(src + e));
+        add_joined(x.hi[e], x.lo[e], __ldg(src + e));
       }
     }
     return x;

@@ -58,3 +58,24 @@ def test_small_queries_before_large_ones(fa, where, Q, d, D, sign):  # noqa: F81
     for keep in (2, 7, 20):
         bm = fa.select_blocks(src, q, box, keep, 0, 1)
         same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Dense(box), keep, 0, 1, block_of(Q)))
+
+
+@pytest.mark.parametrize("g", [2, 6, 128, 600])
+@pytest.mark.parametrize("Q", [1, 2, MANY])
+def test_wide_groups_lose_nothing(fa, Q, g):  # noqa: F811
+    # channel 0: 1 from one head and a little under 2^-24 from each other one, which a running 32-bit sum never takes up. A block with a bound of 1 there is ahead of a
+    # rival with 1 in channel 1 and 2^-24 times two thirds of the heads in channel 2
+    nk, d = 9, 64
+    src = source(fa, 1, g, Q, nk)
+    q = torch.zeros(1, g, Q, d, device="cuda")
+    q[0, 1:, 0, 0] = 0.99 * 2.0**-24
+    q[0, 0, 0, 0] = q[0, 0, 0, 1] = 1
+    q[0, 0, 0, 2] = 2.0**-10
+    q = q.to(BF)
+    for ahead, rival in ((3, 5), (5, 3)):
+        box = torch.zeros(1, 1, nk, 2, d, device="cuda")
+        box[0, 0, ahead, 1, 0] = box[0, 0, rival, 1, 1] = 1
+        box[0, 0, rival, 1, 2] = g * 2 / 3 * 2.0**-14
+        box = box.to(BF)
+        bm = fa.select_blocks(src, q, box, 2, 0, 1)
+        same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Dense(box), 2, 0, 1, block_of(Q)))
