@@ -258,21 +258,28 @@ __device__ __forceinline__ void add_joined(float& s, float& rest, float x) {
 }
 // Sums of bf16 in whole numbers. For |x| < 2^E, x + C with C = 1.5 * 2^(E + 1) lies in C's binade, so its bits are C's plus x in units of
 // 2^(E - 22): an integer sum of the bits is exact, and with max(x, 0) + C = max(x + C, C) the sum of the positive ones takes two
-// operations more. What x + C rounds off (of magnitudes under 2^(E - 15)) is summed apart, where there is any. At most 256 values a lane.
+// operations more. What x + C rounds off (of magnitudes under 2^(E - 15)) is summed apart, where there is any, in pairs of floats: E is that of eight channels
+// together, and one of them may hold nothing but such rests. At most 256 values a lane.
 // Sums in pairs of floats took 7 dependent operations a value: 41 us for 4 x 4096 queries' choice against 37, 118 against 114 for 65536.
 struct BitSums {
   uint32_t all[8], pos[8];        // sums of the bits, C's own left in
-  float* rest;                    // what was rounded off, of all and of the positive ones: [16], kPoolThreads apart. Seldom touched: in shared memory
+  float* rest;                    // what was rounded off, of all and of the positive ones, sums and their rests: [2][16], kPoolThreads apart. Seldom touched: in shared memory
   float c, under;                 // C and 2^E
   int n;                          // values so far
-  __device__ __forceinline__ float& off_all(int i) const { return rest[i * kPoolThreads]; }
-  __device__ __forceinline__ float& off_pos(int i) const { return rest[(8 + i) * kPoolThreads]; }
+  __device__ __forceinline__ float& off(int i, int part) const { return rest[(part * 16 + i) * kPoolThreads]; }  // channel i of all, 8 + i of the positive ones
+  __device__ __forceinline__ void add_off(int i, float x) { add_exact(off(i, 0), off(i, 1), x); }
+  // v units, of up to 31 bits
+  __device__ __forceinline__ void add_off(int i, int v, float u) {
+    const float f = (float)(v & ~255);
+    add_off(i, f * u);
+    add_off(i, (float)(v & 255) * u);
+  }
   __device__ __forceinline__ void start(float* mine) {
     rest = mine;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       all[i] = pos[i] = 0u;
-      off_all(i) = off_pos(i) = 0.f;
+      off(i, 0) = off(i, 1) = off(8 + i, 0) = off(8 + i, 1) = 0.f;
     }
     c = under = 0.f;
     n = 0;
@@ -292,8 +299,8 @@ struct BitSums {
     for (int i = 0; i < 8; ++i) {
       const int a = (int)(all[i] - was), p = (int)(pos[i] - was);
       const int a_up = jump > 31 ? 0 : a >> k, p_up = jump > 31 ? 0 : p >> k;  // past 31 a sum, of either sign, is less than one unit: all of it is rest
-      off_all(i) += (float)(a - (a_up << k)) * u;
-      off_pos(i) += (float)(p - (p_up << k)) * u;
+      add_off(i, a - (a_up << k), u);
+      add_off(8 + i, p - (p_up << k), u);
       all[i] = (uint32_t)a_up + now;
       pos[i] = (uint32_t)p_up + now;
     }
@@ -313,19 +320,13 @@ struct BitSums {
   // what add(v) rounds off
   __device__ __forceinline__ void add_rest(uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    float d[8];
-    bool any = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float y = (e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]);
-      d[e] = __fsub_rn(y, __fsub_rn(__fadd_rn(y, c), c));
-      any = any || d[e] != 0.f;
-    }
-    if (!any) return;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      off_all(e) += d[e];
-      off_pos(e) += ((e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1])) > 0.f ? d[e] : 0.f;
+      const float y = (e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]), d = __fsub_rn(y, __fsub_rn(__fadd_rn(y, c), c));
+      if (d != 0.f) {
+        add_off(e, d);
+        if (y > 0.f) add_off(8 + e, d);
+      }
     }
   }
   // sum + rest, of all and of the positive values
@@ -334,9 +335,13 @@ struct BitSums {
     const int a = (int)(all[i] - own), p = (int)(pos[i] - own);
     const float u = unit();
     s = (float)(a >> 8) * (256.f * u);   // 22 + 8 bits: both parts are exact
-    r = off_all(i) + (float)(a & 255) * u;
+    r = off(i, 1);
+    add_joined(s, r, (float)(a & 255) * u);
+    add_joined(s, r, off(i, 0));
     sp = (float)(p >> 8) * (256.f * u);
-    rp = off_pos(i) + (float)(p & 255) * u;
+    rp = off(8 + i, 1);
+    add_joined(sp, rp, (float)(p & 255) * u);
+    add_joined(sp, rp, off(8 + i, 0));
   }
 };
 
@@ -353,7 +358,7 @@ template <int D>
 __global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_constant__ SelectArgs a) {
   constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes a row, rows a load
   __shared__ float s_sum[2][2 * D];
-  __shared__ float s_rest[16 * kPoolThreads];
+  __shared__ float s_rest[32 * kPoolThreads];
   const int r = blockIdx.x, hk = blockIdx.y / a.parts, part = blockIdx.y % a.parts, b = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = lane % LPR;
   const int g = a.Hq / a.Hkv, h0 = hk * g + first_head(part, g, a.parts), h1 = hk * g + first_head(part + 1, g, a.parts);
@@ -391,17 +396,17 @@ __global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_con
   }
   float all[8], all_r[8], pos[8], pos_r[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q.sums(e, all[e], all_r[e], pos[e], pos_r[e]);
+  for (int e = 0; e < 8; ++e) {
+    q.sums(e, all[e], all_r[e], pos[e], pos_r[e]);
 #pragma unroll
-  for (int o = LPR; o < 32; o <<= 1)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int o = LPR; o < 32; o <<= 1) {
       const float u = __shfl_xor_sync(kAll, all[e], o), p = __shfl_xor_sync(kAll, pos[e], o);
       all_r[e] += __shfl_xor_sync(kAll, all_r[e], o);
       pos_r[e] += __shfl_xor_sync(kAll, pos_r[e], o);
       add_exact(all[e], all_r[e], u);
       add_exact(pos[e], pos_r[e], p);
     }
+  }
   if (warp == 1 && lane < LPR) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {

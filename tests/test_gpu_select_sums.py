@@ -79,3 +79,30 @@ def test_wide_groups_lose_nothing(fa, Q, g):  # noqa: F811
         box = box.to(BF)
         bm = fa.select_blocks(src, q, box, 2, 0, 1)
         same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Dense(box), 2, 0, 1, block_of(Q)))
+
+
+# Channel 0 far below its neighbour: 2^-40 in the first of the queries that a lane reads and a little under 2^-64 in all others, which a running
+# 32-bit sum of them never takes up. A block whose bound there is 2^40 is ahead of a rival that takes channel 2, half as much above the large ones.
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("Q,g", [(128, 1), (256, 2), (MANY, 8)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_channel_beside_a_large_one(fa, Q, g, d, sign):  # noqa: F811
+    nk = 9
+    src = source(fa, 1, g, Q, nk)
+    r = torch.arange(Q, device="cuda") % 64
+    first = (torch.arange(g, device="cuda")[:, None] == 0) & ((r < 256 // d) | (Q == MANY))     # the rows of a lane's first load
+    q = torch.zeros(1, g, Q, d, device="cuda")
+    q[0, :, :, 0] = torch.where(first, 2.0**-40, 0.99 * 2.0**-64)
+    q[0, :, :, 1] = 1
+    q[0, :, :, 2] = torch.where(first, 1.0, 0.0)
+    q[0, :, :, 3] = torch.where(first, 0.0, 2.0**-10)
+    q = (q * torch.where(torch.arange(d, device="cuda") == 1, 1.0, sign)).to(BF)
+    for ahead, rival in ((3, 5), (5, 3)):
+        box = torch.zeros(1, 1, nk, 2, d, device="cuda")
+        at = 0 if sign < 0 else 1
+        box[0, 0, ahead, at, 0] = sign * 2.0**40
+        box[0, 0, rival, at, 2] = sign
+        box[0, 0, rival, at, 3] = sign * 2.0**-15                       # 2^-25 a query
+        box = box.to(BF)
+        bm = fa.select_blocks(src, q, box, 2, 0, 1)
+        same_tables(bm, ref.select(src.tables()["block_class"], q, ref.Dense(box), 2, 0, 1, block_of(Q)))
