@@ -1154,10 +1154,15 @@ cudaError_t launch_bounds_d(const BoundsArgs& a, cudaStream_t st) {
 constexpr int kRowsBlocks = 4096, kAtOnce = 4 * 152;
 bool rows_together(int64_t rows, int32_t nq, int32_t nk) { return nq > 1 && nk <= kRowsBlocks && rows > kAtOnce; }
 
-// 48 KB without asking, the kernel's own 8 KB at most among them
+// What a launch's rows need, and what the longest rows that its kernel takes would
+size_t choose_smem(int nk) { return (row_words(nk, kWarps) + (nk <= kZoneBlocks ? 2 * nk : 0)) * 4; }
+size_t rows_smem(int nk) { return kRows * rows_pitch(nk) * 4; }
+
+// 48 KB without asking, the kernel's own 8 KB at most among them; more always as `most`: the limit is the function's, for all threads' launches, and one
+// that another call lowered between here and the launch would refuse it
 template <class K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-  return bytes > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) : cudaSuccess;
+cudaError_t allow_smem(K kernel, size_t bytes, size_t most) {
+  return bytes > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) : cudaSuccess;
 }
 
 template <int D>
@@ -1169,14 +1174,14 @@ cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t st) {
   }
   const int64_t rows = (int64_t)a.B * a.Hkv * a.nq;
   if (rows_together(rows, a.nq, a.nk)) {
-    const size_t smem = kRows * rows_pitch(a.nk) * 4;
-    if ((e = allow_smem(choose_rows_kernel<D>, smem)) != cudaSuccess) return e;
+    const size_t smem = rows_smem(a.nk);
+    if ((e = allow_smem(choose_rows_kernel<D>, smem, rows_smem(kRowsBlocks))) != cudaSuccess) return e;
     choose_rows_kernel<D><<<dim3(a.Hkv, (a.nq + kRows - 1) / kRows, a.B), kThreads, smem, st>>>(a);
     e = cudaGetLastError();
   } else {
-    const size_t smem = (row_words(a.nk, kWarps) + (a.nk <= kZoneBlocks ? 2 * a.nk : 0)) * 4;
+    const size_t smem = choose_smem(a.nk);
     const int ranks = select_ranks(rows, a.nk);
-    if ((e = allow_smem(choose_kernel<D>, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(choose_kernel<D>, smem, std::max(choose_smem(kSelectMaxBlocks), choose_smem(kZoneBlocks)))) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.nq * ranks, a.Hkv, a.B);
     cfg.blockDim = dim3(kThreads);
