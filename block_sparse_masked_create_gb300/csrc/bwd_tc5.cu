@@ -870,8 +870,8 @@ int launch_tc5(const BwdArgs& a, cudaStream_t st) {
   p.a = a;
   auto kq = bwd_q_tc5_kernel<D, SK>;
   auto kk = bwd_kv_tc5_kernel<D, SK>;
-  if (cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kQSmem) != cudaSuccess ||
-      cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kKvSmem) != cudaSuccess)
+  if (taken(cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kQSmem)) != cudaSuccess ||
+      taken(cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kKvSmem)) != cudaSuccess)
     return FA_ERR_CUDA;
   // Chosen blocks make long columns (the first blocks of a row are in every row): up to nq * g items, where all columns together are about
   // nq * g * row_max * Hkv * B. So
@@ -904,7 +904,7 @@ int launch_tc5(const BwdArgs& a, cudaStream_t st) {
     else at[0].val.programmaticStreamSerializationAllowed = value;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p, tq, tk, tv, tdo) == cudaSuccess;
+    return taken(cudaLaunchKernelEx(&cfg, kernel, p, tq, tk, tv, tdo)) == cudaSuccess;
   };
   const auto launch_kv = [&]() {
     return launch(kk, dim3(a.mask.nk * p.ranks, a.Hkv, a.B), C::kKvSmem, cudaLaunchAttributeClusterDimension, p.ranks);

@@ -9,6 +9,13 @@
 
 namespace fa {
 
+// What a launch or a function's attribute came to. The runtime keeps the error of a refused one for the thread's next cudaGetLastError, which would take
+// it for its own launch's: it is taken out here.
+inline cudaError_t taken(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
 // Table pointers and geometry of a BlockMask, as the kernels read it.
 struct DevMask {
   int32_t Bm, Hm, q_len, kv_len, bq, bk, nq, nk;

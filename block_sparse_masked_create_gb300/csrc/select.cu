@@ -1162,7 +1162,7 @@ size_t rows_smem(int nk) { return kRows * rows_pitch(nk) * 4; }
 // that another call lowered between here and the launch would refuse it
 template <class K>
 cudaError_t allow_smem(K kernel, size_t bytes, size_t most) {
-  return bytes > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) : cudaSuccess;
+  return bytes > 40 * 1024 ? taken(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most)) : cudaSuccess;
 }
 
 template <int D>
@@ -1193,7 +1193,7 @@ cudaError_t launch_select_d(const SelectArgs& a, cudaStream_t st) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, choose_kernel<D>, a, ranks);
+    e = taken(cudaLaunchKernelEx(&cfg, choose_kernel<D>, a, ranks));
   }
   if (e != cudaSuccess || a.nq == 1) return e;
   return launch_mask_columns(a.out, st);
