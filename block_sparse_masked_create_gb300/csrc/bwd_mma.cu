@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_dq_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = h / (a.Hq / a.Hkv);
   const DevMask& M = a.mask;
-  const int bm = M.Bm > 1 ? b : 0, hm = mask_head(M, a.Hq, h);
+  const int bm = M.Bm > 1 ? b : 0, hm = mask_head(M, h);
   const size_t mrow = ((size_t)bm * M.Hm + hm) * M.nq + r;
   const int n_full = __ldg(M.full_kv_num + mrow), n_vis = n_full + __ldg(M.kv_num + mrow);
   const int32_t* full_idx = M.full_kv_idx + mrow * M.nk;
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kBwdThreads) bwd_dkdv_kernel(const __grid_cons
 
   for (int gi = 0; gi < g; ++gi) {
     const int h = hk * g + gi;
-    const int hm = mask_head(M, a.Hq, h);
+    const int hm = mask_head(M, h);
     const size_t mcol = ((size_t)bm * M.Hm + hm) * M.nk + c;
     const int n_full = __ldg(M.full_q_num + mcol), n_vis = n_full + __ldg(M.q_num + mcol);
     const int32_t* full_idx = M.full_q_idx + mcol * M.nq;

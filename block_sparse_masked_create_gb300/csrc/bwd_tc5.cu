@@ -155,7 +155,7 @@ __device__ __forceinline__ void kv_item(const BwdArgs& a, int b, int hk, int c, 
   const int bm = M.Bm > 1 ? b : 0;
   for (int gi = 0; gi < g; ++gi) {
     const int hh = hk * g + gi;
-    const int hm = mask_head(M, a.Hq, hh);
+    const int hm = mask_head(M, hh);
     const size_t col = ((size_t)bm * M.Hm + hm) * M.nk + c;
     const int nf = __ldg(M.full_q_num + col), np = __ldg(M.q_num + col);
     if (k < nf + np) {
@@ -177,7 +177,7 @@ __device__ __forceinline__ int kv_items(const BwdArgs& a, int b, int hk, int c) 
   const int bm = M.Bm > 1 ? b : 0;
   int n = 0;
   for (int gi = 0; gi < g; ++gi) {
-    const int hm = mask_head(M, a.Hq, hk * g + gi);
+    const int hm = mask_head(M, hk * g + gi);
     const size_t col = ((size_t)bm * M.Hm + hm) * M.nk + c;
     n += __ldg(M.full_q_num + col) + __ldg(M.q_num + col);
   }
@@ -588,12 +588,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const DevMask& M = a.mask;
   const int h = blockIdx.y, b = blockIdx.z;
-  // long rows first: the mask's row order (causal: nq-1 .. 0)
-  const int r = M.row_order
-                    ? __ldg(M.row_order + ((size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, h)) * M.nq + blockIdx.x)
-                    : M.nq - 1 - (int)blockIdx.x;
   const int hk = h / (a.Hq / a.Hkv);
-  const size_t mrow = ((size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, h)) * M.nq + r;
+  const size_t mhead = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, h);
+  // long rows first: the mask's row order (causal: nq-1 .. 0)
+  const int r = M.row_order ? __ldg(M.row_order + mhead * M.nq + blockIdx.x) : M.nq - 1 - (int)blockIdx.x;
+  const size_t mrow = mhead * M.nq + r;
   const int nf = __ldg(M.full_kv_num + mrow), n = nf + __ldg(M.kv_num + mrow);
   const int32_t* full_idx = M.full_kv_idx + mrow * M.nk;
   const int32_t* part_idx = M.kv_idx + mrow * M.nk;

@@ -365,7 +365,7 @@ template <int D>
 __global__ void __launch_bounds__(128) decode_combine_kernel(const __grid_constant__ DecArgs a) {
   const int hq = blockIdx.x, b = blockIdx.y;
   const DevMask& M = a.mask;
-  const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, hq);
+  const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + (M.Hm > 1 ? hq / (a.Hq / a.Hkv) : 0);
   const int n_vis = min(__ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow), a.n_splits * a.pages_per_split);
   if (n_vis <= a.pages_per_split) return;  // written by its one split
   const int ns = (n_vis + a.pages_per_split - 1) / a.pages_per_split;

@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kJoin * D) decode_fp8_join_kernel(const __grid
   __shared__ float s_u[kJoin][D], s_red[kJoin * D / 32], s_l[kJoin];
   const int hq = blockIdx.x, b = blockIdx.y, col = threadIdx.x % D, part = threadIdx.x / D;
   const DevMask& M = a.mask;
-  const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, hq);
+  const size_t mrow = (size_t)(M.Bm > 1 ? b : 0) * M.Hm + (M.Hm > 1 ? hq / (a.Hq / a.Hkv) : 0);
   const int n_vis = min(__ldg(M.full_kv_num + mrow) + __ldg(M.kv_num + mrow), a.n_splits * a.pages_per_split);
   if (n_vis <= a.pages_per_split) return;
   const int ns = (n_vis + a.pages_per_split - 1) / a.pages_per_split;

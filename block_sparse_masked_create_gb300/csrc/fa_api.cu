@@ -118,7 +118,14 @@ static DevScore make_score(const fa_score_rule* s, int kv_len) {
   return d;
 }
 
-static DevMask dev_mask(const fa_block_mask* m) {
+// which of the mask's rows each of Hq query heads (packed ones as one) reads
+static void set_heads(DevMask* m, int Hq) {
+  const int64_t g = Hq / m->Hm;
+  m->head_step = m->Hm > 1 && g == 1;
+  m->head_mul = m->Hm > 1 && g > 1 ? (uint32_t)(((int64_t(1) << 32) + g - 1) / g) : 0u;
+}
+
+static DevMask dev_mask(const fa_block_mask* m, int Hq) {
   DevMask d;
   d.Bm = m->Bm;
   d.Hm = m->Hm;
@@ -137,6 +144,7 @@ static DevMask dev_mask(const fa_block_mask* m) {
   d.full_q_num = m->full_q_num;
   d.full_q_idx = m->full_q_idx;
   d.row_order = m->row_order;
+  set_heads(&d, Hq);
   return d;
 }
 
@@ -277,6 +285,7 @@ static int check_forward(const void* q, const void* k, const void* v, const fa_b
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (bm->q_len != Q_LEN || bm->kv_len != KV_LEN) return FA_ERR_SHAPE;  // never trimmed silently
   if (!(bm->Bm == 1 || bm->Bm == B) || !(bm->Hm == 1 || bm->Hm == Hq || bm->Hm == Hkv)) return FA_ERR_SHAPE;
+  if (bm->Hm > 1 && (int64_t)Hq * (Hq / bm->Hm) >= (int64_t(1) << 32)) return FA_ERR_UNSUPPORTED;  // see set_heads
   if (bm->nq != (Q_LEN + bm->bq - 1) / bm->bq || bm->nk != (KV_LEN + bm->bk - 1) / bm->bk) return FA_ERR_SHAPE;
   auto okb = [](int x) { return x == 16 || x == 32 || x == 64 || x == 128; };
   if (!okb(bm->bq) || !okb(bm->bk)) return FA_ERR_UNSUPPORTED;
@@ -332,7 +341,7 @@ static int forward_impl(bool force_mma, const void* q, const void* k, const void
   a.d = d;
   a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   a.score = make_score(score, KV_LEN);
-  a.mask = dev_mask(bm);
+  a.mask = dev_mask(bm, Hq);
   a.status = dev_status;
   a.counters = dev_counters;
   a.timeout_ns = g_timeout_ns.load();
@@ -344,6 +353,7 @@ static int forward_impl(bool force_mma, const void* q, const void* k, const void
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (split) {  // the tcgen05 kernel over the derived tables, writing each entry's O and LSE
     a.mask = split->mask;
+    set_heads(&a.mask, Hq);
     a.split_ncm = split->ncm;
     a.out_q_len = split->mask.nq * 128;
     a.out = split->o_part;
@@ -395,7 +405,7 @@ static int backward_impl(const void* q, const void* k, const void* v, const void
   a.d = d;
   a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   a.score = make_score(score, KV_LEN);
-  a.mask = dev_mask(bm);
+  a.mask = dev_mask(bm, Hq);
   a.row_max = bm->row_max;
   a.status = dev_status;
   a.timeout_ns = g_timeout_ns.load();
@@ -848,7 +858,7 @@ fa_status fa_flex_decode(const void* q, const void* k_pages, const void* v_pages
   a.max_pages = max_pages;
   a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   a.score = make_score(score_rule, bm->kv_len);
-  a.mask = dev_mask(bm);
+  a.mask = dev_mask(bm, Hq);
   a.pages_per_split = decode_pages_per_split(page, max_pages);
   a.n_splits = (max_pages + a.pages_per_split - 1) / a.pages_per_split;
   if (bm->row_max > 0 && bm->row_max < max_pages) {  // rows known to be short
@@ -1263,7 +1273,7 @@ fa_status fa_flex_decode_fp8(const void* q, const void* k_pages, const void* v_p
   a.max_pages = max_pages;
   a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   a.score = make_score(score_rule, bm->kv_len);
-  a.mask = dev_mask(bm);
+  a.mask = dev_mask(bm, Hq);
   a.pages_per_split = P.pages_per_split;
   a.n_splits = P.n_splits;
   uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -1384,7 +1394,7 @@ fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const vo
     e.kv_len = KV_LEN;
     e.d = d;
     e.rule = rule;
-    e.mask = dev_mask(bm);
+    e.mask = dev_mask(bm, Hq);
     e.status = dev_status;
     if (launch_expand_fp8(e, st) != cudaSuccess) return FA_ERR_CUDA;
     if (P.chunk)
@@ -1411,7 +1421,7 @@ fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const vo
   a.scale = scale > 0.f ? scale : 1.0f / std::sqrt((float)d);
   a.rule = rule;
   a.score = make_score(score_rule, KV_LEN);
-  a.mask = dev_mask(bm);
+  a.mask = dev_mask(bm, Hq);
   a.status = dev_status;
   a.timeout_ns = g_timeout_ns.load();
   a.page_table = page_table;
@@ -1437,6 +1447,7 @@ fa_status fa_flex_forward_paged_fp8(const void* q, const void* k_pages, const vo
     a.out_f32 = 1;
     a.lse = S.lse_part;
   }
+  set_heads(&a.mask, a.Hq);
   if ((int64_t)B * a.mask.nq * a.Hq > INT_MAX) return FA_ERR_UNSUPPORTED;  // grid size
   s = launch_fwd_fp8(f, st);
   if (s != FA_OK || !P.chunk) return (fa_status)s;

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(MmaCfg<D, BQ, BK>::kThreads)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = a.Hq / a.Hkv, hk = h / g;
   const DevMask& M = a.mask;
-  const int bm = M.Bm > 1 ? b : 0, hm = mask_head(M, a.Hq, h);
+  const int bm = M.Bm > 1 ? b : 0, hm = mask_head(M, h);
   const size_t mrow = ((size_t)bm * M.Hm + hm) * M.nq + r;
   const int n_full = __ldg(M.full_kv_num + mrow), n_part = __ldg(M.kv_num + mrow);
   const int n_vis = n_full + n_part;

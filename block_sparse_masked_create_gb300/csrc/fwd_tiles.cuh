@@ -33,7 +33,7 @@ __device__ __forceinline__ Tile make_tile(const FwdArgs& a, int b, int h, int r)
   T.r = T.valid ? r : 0;
   T.rq = a.split_ncm > 1 ? T.r / a.split_ncm : T.r;
   T.hk = T.h / (a.Hq / a.Hkv);
-  const int bm = M.Bm > 1 ? b : 0, hm = mask_head(M, a.Hq, T.h);
+  const int bm = M.Bm > 1 ? b : 0, hm = mask_head(M, T.h);
   const size_t mrow = ((size_t)bm * M.Hm + hm) * M.nq + T.r;
   T.n_full = T.valid ? __ldg(M.full_kv_num + mrow) : 0;
   T.n_part = T.valid ? __ldg(M.kv_num + mrow) : 0;
@@ -156,8 +156,7 @@ __device__ __forceinline__ void work_item(const FwdArgs& a, int pair_rows, int g
   b = unit / HP;
   const DevMask& M = a.mask;
   const int hm_head = pair_rows ? hu : 2 * hu;
-  const int32_t* ro = M.row_order ? M.row_order + ((size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, a.Hq, hm_head)) * nq
-                                  : nullptr;
+  const int32_t* ro = M.row_order ? M.row_order + ((size_t)(M.Bm > 1 ? b : 0) * M.Hm + mask_head(M, hm_head)) * nq : nullptr;
   auto row = [&](int i) { return ro ? __ldg(ro + i) : nq - 1 - i; };
   if (pair_rows) {
     h0 = h1 = hu;

@@ -261,7 +261,8 @@ typedef enum { FA_OUT_BF16 = 0, FA_OUT_F32 = 1 } fa_out_dtype;
  *   q            device bf16 [B, Hq, Q_LEN, d]
  *   k, v         device bf16 [B, Hkv, KV_LEN, d]; query head h reads KV head floor(h / (Hq/Hkv))
  *   block_mask   host pointer to a mask made by fa_create_block_mask with q_len == Q_LEN, kv_len ==
- *                KV_LEN, Bm in {1, B}, Hm in {1, Hkv, Hq} (a length mismatch is an error, never trimmed)
+ *                KV_LEN, Bm in {1, B}, Hm in {1, Hkv, Hq}, Hq (Hq / Hm) < 2^32 where Hm > 1 (a length
+ *                mismatch is an error, never trimmed)
  *   score_rule   host pointer or NULL (no score rule)
  *   scale        > 0, or <= 0 for 1/sqrt(d)
  *   out          device [B, Hq, Q_LEN, d] of type out_dtype;  lse  device fp32 [B, Hq, Q_LEN] (natural log)

@@ -25,3 +25,11 @@ def test_one_offset_for_several_batch_rows(fa, q_len, nq, bq):  # noqa: F811
     c = mask(fa, nq=nq, q_len=q_len, bq=bq, Bm=2)
     c.rule.q_offset = 4096
     assert choose(fa, c, 2, n=0) == fa.ERR_BUFFER
+
+
+def test_more_heads_than_a_row_set_is_found_for(fa):  # noqa: F811
+    # the row set of a query head is found by a product that is exact for Hq times the group's heads under 2^32
+    lib = fa.load()
+    c = mask(fa, Hm=2)
+    for Hq, code in ((2**17, fa.ERR_UNSUPPORTED), (2**16, fa.ERR_INVALID_ARG)):
+        assert lib.fa_flex_forward(P, P, P, ctypes.byref(c), None, 0.0, ctypes.c_void_p(4104), 0, P, 1, Hq, 2, 256, 256, 64, None, None, None) == code
