@@ -1584,8 +1584,15 @@ fa_status fa_block_mask_select_blocks(const fa_block_mask* src, const void* q, c
       ((reinterpret_cast<uintptr_t>(dev_buf) | reinterpret_cast<uintptr_t>(workspace)) & 255u))
     return FA_ERR_INVALID_ARG;
   if (buf_bytes < P.mask.total || workspace_bytes < P.total) return FA_ERR_BUFFER_TOO_SMALL;
-  const uintptr_t from = reinterpret_cast<uintptr_t>(dev_buf), cls = reinterpret_cast<uintptr_t>(src->block_class);
-  if (cls < from + P.mask.total && from < cls + (size_t)src->Bm * src->nq * src->nk) return FA_ERR_INVALID_ARG;  // read while dev_buf is written
+  // read while dev_buf is written, or (document runs, which may lie in the buffer of the mask that src was chosen from) kept in the result
+  const auto overlaps = [&](const void* p, size_t bytes) {
+    const uintptr_t from = reinterpret_cast<uintptr_t>(dev_buf), at = reinterpret_cast<uintptr_t>(p);
+    return p && at < from + P.mask.total && from < at + bytes;
+  };
+  const size_t doc_batch = src->rule.doc_batch > 0 ? src->rule.doc_batch : 0, doc_len = src->rule.doc_len > 0 ? src->rule.doc_len : 0;
+  if (overlaps(src->block_class, (size_t)src->Bm * src->nq * src->nk) || overlaps(src->doc_run, doc_batch * 2 * doc_len * sizeof(int32_t)) ||
+      overlaps(src->doc_sorted, doc_batch * sizeof(int32_t)))
+    return FA_ERR_INVALID_ARG;
   SelectArgs a;
   std::memset(&a, 0, sizeof(a));
   a.q = q;

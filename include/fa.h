@@ -234,13 +234,14 @@ FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, voi
  *   bounds     page_table NULL: device bf16 [B, Hkv, nk, 2, d] (fa_key_bounds); else device bf16 [n_pages_total, Hkv, 2, d]
  *              (fa_kv_bounds) with key block c of batch row b in page page_table[b * max_pages + c], max_pages >= nk, one page a block
  *   keep       >= 1;  first, last >= 0, first + last <= keep
- *   dev_buf    device buffer of >= fa_block_mask_select_blocks_bytes(src, B, Hkv) bytes, 256-byte aligned; not the one that src lies in
+ *   dev_buf    device buffer of >= fa_block_mask_select_blocks_bytes(src, B, Hkv) bytes, 256-byte aligned; not the one that src lies in, nor
+ *              one that holds its document run arrays (that of the mask that src was chosen from)
  *   out        host struct, filled with pointers into dev_buf and src's document run arrays; may be src
  *   workspace  device, >= fa_block_mask_select_blocks_workspace_bytes(src, B, Hq, Hkv, d) bytes, 256-byte aligned, for one call at a time
  *              (NULL where that is 0: one query, up to 2048 key blocks)
  *   dev_status a page id of a visited block outside [0, n_pages_total) sets FA_ERR_DEVICE_CHECK, and that block ranks lowest (page ids
  *              are looked at where keep > first + last)
- * Returns FA_ERR_INVALID_ARG (NULL, alignment, keep / first / last, src's classes in dev_buf, a q_offset where src->Bm = 1 < B), FA_ERR_SHAPE
+ * Returns FA_ERR_INVALID_ARG (NULL, alignment, keep / first / last, src's classes or document runs in dev_buf, a q_offset where src->Bm = 1 < B), FA_ERR_SHAPE
  * (sizes, src->Bm), FA_ERR_UNSUPPORTED (src->Hm > 1, too many blocks, more than 524280 query blocks, d not in {64, 128}, B or Hq > 65535), FA_ERR_BUFFER_TOO_SMALL. */
 FA_API size_t fa_block_mask_select_blocks_bytes(const fa_block_mask* src, int32_t B, int32_t Hkv);
 FA_API size_t fa_block_mask_select_blocks_workspace_bytes(const fa_block_mask* src, int32_t B, int32_t Hq, int32_t Hkv, int32_t d);

@@ -33,3 +33,16 @@ def test_more_heads_than_a_row_set_is_found_for(fa):  # noqa: F811
     c = mask(fa, Hm=2)
     for Hq, code in ((2**17, fa.ERR_UNSUPPORTED), (2**16, fa.ERR_INVALID_ARG)):
         assert lib.fa_flex_forward(P, P, P, ctypes.byref(c), None, 0.0, ctypes.c_void_p(4104), 0, P, 1, Hq, 2, 256, 256, 64, None, None, None) == code
+
+
+def test_a_buffer_that_holds_the_document_runs(fa):  # noqa: F811
+    # a choice keeps the runs of the mask that it was made from: a choice from it must not be laid out over them
+    c = mask(fa)
+    c.rule.doc_batch, c.rule.doc_len = 1, 256
+    n = fa.load().fa_block_mask_select_blocks_bytes(ctypes.byref(c), 2, 2)
+    at = BIG.value
+    for name, size in (("doc_run", 2 * 256 * 4), ("doc_sorted", 4)):
+        for start, code in ((at, fa.ERR_INVALID_ARG), (at + n - 4, fa.ERR_INVALID_ARG), (at - size + 4, fa.ERR_INVALID_ARG)):
+            setattr(c, name, start)
+            assert choose(fa, c, buf=BIG, n=n) == code, (name, start)
+        setattr(c, name, None)
