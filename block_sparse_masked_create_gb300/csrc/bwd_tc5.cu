@@ -20,6 +20,7 @@
 // a wait that runs out sets FA_ERR_TIMEOUT and the CTA drains its copies and MMAs before it exits.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <cstring>
 
 #include "fa_launch.h"
@@ -873,22 +874,30 @@ int launch_tc5(const BwdArgs& a, cudaStream_t st) {
       taken(cudaFuncSetAttribute(kk, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kKvSmem)) != cudaSuccess)
     return FA_ERR_CUDA;
   // Chosen blocks make long columns (the first blocks of a row are in every row): up to nq * g items, where all columns together are about
-  // nq * g * row_max * Hkv * B. So
+  // nq * g * row_max * Hkv * B. Under a window no key block is in more rows than see it (col_max). So
   //   - dK/dV goes first, and dQ, which does not need it, starts as soon as the last of its CTAs has: dQ's short CTAs fill the SMs that the
-  //     long columns leave (8192 tokens, 16/4 heads, 16 blocks a row: 508 -> 461 us; 16,384 tokens, 16/8 heads: 890 -> 840);
-  //   - the longest columns go first, as far as a CTA finds its own with a thread a column (16,384 tokens, 16/8 heads, 24 blocks: 1394 -> 1131);
+  //     long columns leave (8192 tokens, 16/4 heads, 16 blocks a row: 508 -> 461 us; 16,384 tokens, 16/8 heads: 890 -> 840, both with divisions in the
+  //     walk over a column that are gone since);
+  //   - the longest columns go first, as far as a CTA finds its own with a thread a column (16,384 tokens, 16/8 heads, 24 blocks: 1394 -> 1131, so too);
   //   - a cluster shares each column where the longest would outlast all the rest. With a CTA's start and end as long as ten items, `part` is an
   //     SM's share of dK/dV in lengths of the longest column. Times of the whole backward, one / two / four CTAs a column, d = 128:
-  //       part 1.10  16,384 tokens, 16/8 heads, 16 blocks a row   840 /  975 / 1104 us
-  //       part 0.76  16,384 tokens, 32/8 heads, 12 blocks        1391 / 1599 / 1795
-  //       part 0.59  16,384 tokens, 16/4 heads, 20 blocks        1193 / 1133 / 1253
-  //       part 0.49    8192 tokens, 16/4 heads, 16 blocks         602 /  460 /  517
-  //       part 0.38    8192 tokens, 16/4 heads, 12 blocks         600 /  387 /  436
-  //       part 0.22  32,768 tokens,  8/1 heads, 32 blocks        3918 / 2178 / 1620
+  //       part 3.84  16,384 tokens, 16/4 heads, 64 blocks a row, window 2048       794 /  863 /  949 us
+  //       part 1.96  16,384 tokens, 16/4 heads,  8 blocks, window 2048             479 /  561 /  633
+  //       part 1.11  16,384 tokens, 16/8 heads, 16 blocks                          784 /  897 / 1016
+  //       part 1.09    8192 tokens, 16/4 heads,  4 blocks, window 1024             167 /  208 /  237
+  //       part 0.85  32,768 tokens,  8/1 heads, 16 blocks, window 4096             798 /  878 /  956
+  //       part 0.76  16,384 tokens, 32/8 heads, 12 blocks                         1249 / 1389 / 1530
+  //       part 0.59  16,384 tokens, 16/4 heads, 20 blocks                         1013 /  975 / 1066
+  //       part 0.49    8192 tokens, 16/4 heads, 16 blocks                          480 /  403 /  445
+  //       part 0.33    2 x 8192 tokens, 8/2 heads, 10 blocks                       489 /  303 /  334
+  //       part 0.28  16,384 tokens, 16/4 heads,  8 blocks                         1002 /  569 /  603
+  //       part 0.28  the same, window 2048 or the first 128 tokens                1059 /  567 /  618
+  //       part 0.23    8192 tokens, 16/2 heads,  8 blocks, window 4096             548 /  319 /  291
+  //       part 0.22  32,768 tokens,  8/1 heads, 32 blocks                         3982 / 2220 / 1627
   //     Eight are slower than four (a cluster waits for as many free SMs of one part of the GPU).
   const int g = a.Hq / a.Hkv;
-  const float part = (a.row_max + 10.f / g) * a.Hkv * a.B / 152.f;
-  p.ranks = a.row_max == 0 || a.mask.nq <= kFewItems / g || part > 0.65f ? 1 : part > 0.33f ? 2 : 4;
+  const float part = (std::min(a.row_max, a.col_max) + 10.f / g) * a.Hkv * a.B / 152.f * a.mask.nq / a.col_max;
+  p.ranks = a.row_max == 0 || a.mask.nq <= kFewItems / g || part > 0.65f ? 1 : part > 0.25f ? 2 : 4;
   p.by_length = a.row_max > 0 && a.mask.nk <= kThreads;
   p.overlap = a.row_max > 0;
   const auto launch = [&](auto kernel, dim3 grid, int smem, cudaLaunchAttributeID id, int value) {

@@ -368,6 +368,16 @@ static int forward_impl(bool force_mma, const void* q, const void* k, const void
   return launch_fwd_mma(a, st) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// The most query blocks that see one key block: under a causal window of W those that W + bk - 1 neighbouring queries lie in, under any other term all.
+static int32_t most_rows(const DevRule& R, int32_t nq, int32_t bq, int32_t bk) {
+  int64_t n = 0;
+  for (int t = 0; t < R.n_terms; ++t) {
+    const bool near = R.t[t].causal && R.t[t].win < (int64_t)nq * bq;
+    n += near ? std::min<int64_t>(nq, (std::max<int64_t>(R.t[t].win, 1) + bk + bq - 3) / bq + 1) : nq;
+  }
+  return (int32_t)std::min<int64_t>(std::max<int64_t>(n, 1), nq);
+}
+
 static int backward_impl(const void* q, const void* k, const void* v, const void* out, int32_t out_dtype,
                          const void* dout, const float* lse, const fa_block_mask* bm, const fa_score_rule* score,
                          float scale, float* dq, float* dk, float* dv, float* delta, int32_t B, int32_t Hq,
@@ -407,6 +417,7 @@ static int backward_impl(const void* q, const void* k, const void* v, const void
   a.score = make_score(score, KV_LEN);
   a.mask = dev_mask(bm, Hq);
   a.row_max = bm->row_max;
+  a.col_max = most_rows(a.rule, bm->nq, bm->bq, bm->bk);
   a.status = dev_status;
   a.timeout_ns = g_timeout_ns.load();
   if ((long long)B * Hq > 65535LL * 65535LL || Hq > 65535 || B > 65535) return FA_ERR_UNSUPPORTED;

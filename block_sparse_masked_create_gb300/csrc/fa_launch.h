@@ -136,6 +136,7 @@ struct BwdArgs {
   DevScore score;
   DevMask mask;
   int32_t row_max;      // the most blocks a row lists; 0: not known
+  int32_t col_max;      // the most query blocks that a key block can be listed by
   int32_t* status;
   uint64_t timeout_ns;  // bound of every in-kernel wait (tcgen05 kernels)
 };
