@@ -8,7 +8,7 @@
 //   choice   the first and last few blocks of the mask's row, and of the others those with the largest score, ties to the lower column.
 //
 // The choice is that of scores in 64 bits, but hardly any is computed so: this GPU has two FP64 lanes an SM. Q+- are sums of whole numbers
-// or of pairs of floats (an error of 2^-44 of their magnitudes), the scores 32-bit sums with a bound e on their error. With T the K-th
+// or of pairs of floats (an error of 2^-44 of their magnitudes, mostly none), the scores 32-bit sums with a bound e on their error. With T the K-th
 // largest of these, the true K-th largest lies within e of T, so blocks over T + 2 e are in, blocks under T - 2 e are out, and only where
 // those in between do not all fit are they scored again, in pairs of floats (2^-44), or in 64 bits where those would leave their range.
 //
@@ -268,12 +268,6 @@ struct BitSums {
   int n;                          // values so far
   __device__ __forceinline__ float& off(int i, int part) const { return rest[(part * 16 + i) * kPoolThreads]; }  // channel i of all, 8 + i of the positive ones
   __device__ __forceinline__ void add_off(int i, float x) { add_exact(off(i, 0), off(i, 1), x); }
-  // v units, of up to 31 bits
-  __device__ __forceinline__ void add_off(int i, int v, float u) {
-    const float f = (float)(v & ~255);
-    add_off(i, f * u);
-    add_off(i, (float)(v & 255) * u);
-  }
   __device__ __forceinline__ void start(float* mine) {
     rest = mine;
 #pragma unroll
@@ -295,12 +289,18 @@ struct BitSums {
     under = to;
     c = 3.f * to;
     const uint32_t now = __float_as_uint(c) * (uint32_t)n;
+    if (n == 0) return;  // nothing yet: all and pos are 0
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int a = (int)(all[i] - was), p = (int)(pos[i] - was);
       const int a_up = jump > 31 ? 0 : a >> k, p_up = jump > 31 ? 0 : p >> k;  // past 31 a sum, of either sign, is less than one unit: all of it is rest
-      add_off(i, a - (a_up << k), u);
-      add_off(8 + i, p - (p_up << k), u);
+      const int a_low = a - (a_up << k), p_low = p - (p_up << k);
+      if (jump > 24) {  // of up to 31 bits: a float takes 24
+        off(i, 1) += (float)(a_low & 255) * u;
+        off(8 + i, 1) += (float)(p_low & 255) * u;
+      }
+      add_off(i, (float)(jump > 24 ? a_low & ~255 : a_low) * u);
+      add_off(8 + i, (float)(jump > 24 ? p_low & ~255 : p_low) * u);
       all[i] = (uint32_t)a_up + now;
       pos[i] = (uint32_t)p_up + now;
     }
@@ -317,16 +317,20 @@ struct BitSums {
   }
   // Magnitudes from here on, with 8 bits of their own, lose nothing
   __device__ __forceinline__ float kept() const { return 128.f * unit(); }
-  // what add(v) rounds off
+  // what add(v) rounds off: looked for first, as it is seldom more than one value's, and one after another
   __device__ __forceinline__ void add_rest(uint4 v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    auto off_by = [&](float y) { return __fsub_rn(y, __fsub_rn(__fadd_rn(y, c), c)); };
+    uint32_t some = 0u;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float y = (e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1]), d = __fsub_rn(y, __fsub_rn(__fadd_rn(y, c), c));
-      if (d != 0.f) {
-        add_off(e, d);
-        if (y > 0.f) add_off(8 + e, d);
-      }
+    for (int e = 0; e < 8; ++e) some |= (off_by((e & 1) ? bf_hi(w[e >> 1]) : bf_lo(w[e >> 1])) != 0.f ? 1u : 0u) << e;
+#pragma unroll 1
+    for (; some; some &= some - 1) {
+      const int e = __ffs(some) - 1;
+      const uint32_t two = e < 4 ? (e < 2 ? v.x : v.y) : (e < 6 ? v.z : v.w);
+      const float y = (e & 1) ? bf_hi(two) : bf_lo(two), d = off_by(y);
+      add_off(e, d);
+      if (y > 0.f) add_off(8 + e, d);
     }
   }
   // sum + rest, of all and of the positive values
@@ -334,21 +338,33 @@ struct BitSums {
     const uint32_t own = __float_as_uint(c) * (uint32_t)n;
     const int a = (int)(all[i] - own), p = (int)(pos[i] - own);
     const float u = unit();
-    s = (float)(a >> 8) * (256.f * u);   // 22 + 8 bits: both parts are exact
-    r = off(i, 1);
-    add_joined(s, r, (float)(a & 255) * u);
-    add_joined(s, r, off(i, 0));
-    sp = (float)(p >> 8) * (256.f * u);
-    rp = off(8 + i, 1);
-    add_joined(sp, rp, (float)(p & 255) * u);
-    add_joined(sp, rp, off(8 + i, 0));
+    s = (float)a * u;  // of up to 30 bits the upper 24; the others go apart
+    r = off(i, 1) + (float)(a - (int)(float)a) * u;
+    add_exact(s, r, off(i, 0));
+    sp = (float)p * u;
+    rp = off(8 + i, 1) + (float)(p - (int)(float)p) * u;
+    add_exact(sp, rp, off(8 + i, 0));
   }
 };
+
+// The bits of the least magnitude among eight values that is not 0 (2^16: there is none). Volatile: what it shares with other minima is made anew, not
+// kept in registers
+__device__ __forceinline__ uint32_t least_of(uint4 v) {
+  uint32_t m;
+  asm volatile(
+      "{\n\t.reg .b32 a, b, c, d, e;\n\tmov.b32 e, 0xFFFFFFFF;\n\t"
+      "and.b32 a, %1, 0x7FFF7FFF;\n\tand.b32 b, %2, 0x7FFF7FFF;\n\tand.b32 c, %3, 0x7FFF7FFF;\n\tand.b32 d, %4, 0x7FFF7FFF;\n\t"
+      "add.u16x2 a, a, e;\n\tadd.u16x2 b, b, e;\n\tadd.u16x2 c, c, e;\n\tadd.u16x2 d, d, e;\n\t"  // less 1: a 0 is the largest
+      "min.u16x2 a, a, b;\n\tmin.u16x2 c, c, d;\n\tmin.u16x2 %0, a, c;\n\t}"
+      : "=r"(m)
+      : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+  return min(m & 0xFFFFu, m >> 16) + 1u;
+}
 
 // grid (nq, Hkv * parts, B): Q-, Q+ of one query block over at most 8 of a group's heads, in pairs of floats -> pooled [B, Hkv, nq, parts, 2 (sum,
 // rest), 2 D]. Two warps, half of the rows each: long enough a way through memory that the joining at its end costs little. Fourteen CTAs an
 // SM: 2048 of them, the two large cases below, are all there at once. HBM and the instructions bound it about alike: 65536 queries of 16 heads
-// (268 MB) in 54 us, 5.0 TB/s, 59 % of the issue slots (the whole choice 109 us; with ten CTAs an SM, the rests in registers, 117).
+// (268 MB) in 54 us, 5.0 TB/s, 59 % of the issue slots (the whole choice 110 us; with ten CTAs an SM, the rests in registers, 117).
 constexpr int kAhead = 8;
 
 // the first of a group's g heads that division `part` takes: part * g passes 32 bits for groups of 46,341 heads and more
@@ -387,8 +403,23 @@ __global__ void __launch_bounds__(kPoolThreads, 14) pool_kernel(const __grid_con
       const float most = fmaxf(bf_lo(top), bf_hi(top));
       if (most >= q.under) q.grow(most);
       if (fminf(bf_lo(low), bf_hi(low)) < q.kept()) {
+        // Short: which rows hold such a value, and these one after another. Unrolled over the rows, what add_rest does is longer than all of the rest (the whole
+        // choice of 65536 queries took 143 us so, 121 with these rows read again, 110 this way). Queries whose magnitudes span 2^60 at random take
+        // it for nearly every value: 281 us for 32,768 queries of 16 heads where N(0, 1) takes 66
+        uint32_t some = 0u;
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) q.add_rest(v[k]);
+        for (int k = 0; k < kAhead; ++k) {
+          some |= (least_of(v[k]) < __float_as_uint(q.kept()) >> 16 ? 1u : 0u) << k;
+        }
+#pragma unroll 1
+        for (; some; some &= some - 1) {
+          const int k = __ffs(some) - 1;
+          uint4 r = v[0];
+#pragma unroll
+          for (int x = 1; x < kAhead; ++x)
+            if (k == x) r = v[x];
+          q.add_rest(r);
+        }
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) q.add(v[k]);
