@@ -1176,7 +1176,8 @@ cudaError_t launch_bounds_d(const BoundsArgs& a, cudaStream_t st) {
 }
 
 // Rows of query blocks go eight to a CTA, as long as their keys fit in its shared memory and there are more rows than CTAs with one each would
-// run at once (four an SM); fewer or longer ones take a CTA or more each. The whole choice, one row / eight rows a CTA, d = 128:
+// run at once (four an SM); fewer or longer ones take a CTA or more each. The whole choice, one row / eight rows a CTA, d = 128 (with rests in single
+// floats: the sums take 1 % more now on both sides):
 //   256 rows of up to  64 blocks (8192 queries, 4 KV heads)     20.2 / 24.1 us
 //   512 rows of up to 256 blocks (32,768 queries, 2 KV heads)   36.6 / 45.2
 //  1024 rows of up to 128 blocks (16,384 queries, 8 KV heads)   35.6 / 32.5

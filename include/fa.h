@@ -222,7 +222,7 @@ FA_API fa_status fa_kv_bounds_fp8(const void* k_pages, const float* k_scale, voi
  *              max(q[b,h,i,e] * smallest[c,e], q[b,h,i,e] * largest[c,e]),
  * which bounds the sum of <q, k> over those queries for any choice of keys in the block (scale, score rule and mask rule
  * do not enter). Scores are compared in 64 bits, ties go to the lower column; scores closer than 2^-28 of the magnitudes that they
- * add up may rank either way. A NaN score ranks above all others (a NaN key is not hidden by the choice).
+ * add up (|q| times the larger of |smallest| and |largest|) may rank either way. A NaN score ranks above all others (a NaN key is not hidden by the choice).
  * The result is src's mask with the other blocks empty: classes, row lists, query-side transpose and row order as
  * fa_create_block_mask would lay them out, with Bm = B, Hm = Hkv, for every attention entry point (fa_flex_decode and
  * fa_flex_decode_fp8 for one query, the forwards and fa_flex_backward for query blocks). The choice itself has no gradient.
